@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(_HERE, "libmigemm.so")
@@ -29,7 +30,7 @@ VARIANT_AUTO, NAIVE, LDS_TILED, REGTILE_VALU, REGTILE_MFMA, MFMA16, MFMA_I8 = -1
 EXPORTS = ("migemm_gemm", "migemm_gemm_variant", "migemm_gemm_ex", "migemm_gemm_ex_variant",
            "migemm_gemm_ws", "migemm_gemm_noalloc", "migemm_workspace_size", "migemm_describe",
            "migemm_describe_ex",
-           "migemm_convert",
+           "migemm_convert", "migemm_quantize_mx", "migemm_dequantize_mx", "migemm_gemm_mx",
            "migemm_variant_count", "migemm_variant_name",
            "migemm_variant_supports", "migemm_config_count", "migemm_config_name",
            "migemm_select", "migemm_status_string", "migemm_last_hip_error", "migemm_version")
@@ -83,6 +84,13 @@ def lib():
     L.migemm_describe_ex.restype = i32
     L.migemm_convert.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp]
     L.migemm_convert.restype = i32
+    L.migemm_quantize_mx.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.migemm_quantize_mx.restype = i32
+    L.migemm_dequantize_mx.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.migemm_dequantize_mx.restype = i32
+    L.migemm_gemm_mx.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, f32, f32, i32,
+                                 vp, i64, vp]
+    L.migemm_gemm_mx.restype = i32
     L.migemm_variant_count.argtypes = []
     L.migemm_variant_count.restype = i32
     L.migemm_variant_name.argtypes = [i32]
@@ -185,6 +193,24 @@ def describe(*args, **kw) -> dict:
 
 def migemm_convert(src_dtype, dst_dtype, rows, cols, src, lds, dst, ldd, stream=None) -> int:
     return lib().migemm_convert(src_dtype, dst_dtype, rows, cols, src, lds, dst, ldd, stream)
+
+
+def migemm_quantize_mx(src_dtype, op, rows, cols, src, lds, data, ldd, scales, ldsc,
+                       stream=None) -> int:
+    return lib().migemm_quantize_mx(src_dtype, op, rows, cols, src, lds, data, ldd, scales, ldsc,
+                                    stream)
+
+
+def migemm_dequantize_mx(dst_dtype, rows, cols, data, ldd, scales, ldsc, dst, ld,
+                         stream=None) -> int:
+    return lib().migemm_dequantize_mx(dst_dtype, rows, cols, data, ldd, scales, ldsc, dst, ld,
+                                      stream)
+
+
+def migemm_gemm_mx(M, N, K, A, lda, a_scales, ldas, B, ldb, b_scales, ldbs, alpha, beta, c_dtype,
+                   C, ldc, stream=None) -> int:
+    return lib().migemm_gemm_mx(M, N, K, A, lda, a_scales, ldas, B, ldb, b_scales, ldbs, alpha,
+                                beta, c_dtype, C, ldc, stream)
 
 
 def migemm_variant_count() -> int:
@@ -354,4 +380,149 @@ def gemm(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=Non
                         ws.numel() if ws is not None else 0, stream)
     if st != OK:
         raise MigemmError(st, "migemm_gemm_ws")
+    return out
+
+
+# ---------------------------------------------------------------------- MXFP4
+
+class MxMatrix(NamedTuple):
+    """A matrix in microscaled 4-bit floating point (the format is described in
+    ``include/migemm.h``).
+
+    ``data``: uint8 CUDA tensor, rows x (16 bytes or more per block of 32
+    elements); ``scales``: uint8, rows x (1 byte or more per block); both with unit
+    column stride, 16-byte aligned rows and row strides a multiple of 16.
+    ``cols``: elements per row (not bytes)."""
+    data: "torch.Tensor"  # noqa: F821
+    scales: "torch.Tensor"  # noqa: F821
+    cols: int
+
+    @property
+    def shape(self):
+        return self.data.shape[0], self.cols
+
+    @property
+    def device(self):
+        return self.data.device
+
+
+def _mx_operand(name, m, device):
+    """(data pointer, ldd, scales pointer, ldsc) of an MxMatrix, checked."""
+    import torch
+    data, scales, cols = m
+    rows, blocks = data.shape[0], (cols + 31) // 32
+    for what, t, need in (("data", data, 16 * blocks), ("scales", scales, blocks)):
+        _check_device(f"{name}.{what}", t, device)
+        if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < need:
+            raise ValueError(f"{name}.{what} must be a uint8 matrix of {rows} rows of at least "
+                             f"{need} bytes (got {t.dtype}, {tuple(t.shape)})")
+        # a row occupies its whole stride, the last one too
+        if rows and t.untyped_storage().nbytes() - t.storage_offset() < rows * _ld(t):
+            raise ValueError(f"{name}.{what}: the storage ends inside the last row's stride")
+    return data.data_ptr() or None, _ld(data), scales.data_ptr() or None, _ld(scales)
+
+
+def _stream_of(stream, device):
+    """(stream handle, whether it is another one than torch's current stream)."""
+    import torch
+    current = torch.cuda.current_stream(device).cuda_stream
+    return (current, False) if stream is None else (stream, stream != current)
+
+
+def _used_on(stream, device, *tensors):
+    """Keeps tensors that torch allocated for its current stream from being reused
+    before the work queued on `stream` has finished."""
+    import torch
+    s = torch.cuda.ExternalStream(stream, device=device)
+    for t in tensors:
+        t.record_stream(s)
+
+
+def quantize_mx(src, *, out=None, stream=None):
+    """``src`` (a 2-D CUDA tensor, float32/float16/bfloat16, row-major or a
+    transposed view of row-major storage, read as stored) quantised to MXFP4 along
+    its rows, as an ``MxMatrix`` (``out``, if given).  Quantise a weight stored K x N
+    for ``gemm_mx`` as ``quantize_mx(w.t())``.  Does not synchronise."""
+    import torch
+    device = src.device
+    _check_device("src", src, device)
+    op, lds = _operand(src)
+    rows, cols = src.shape
+    blocks = (cols + 31) // 32
+    with torch.cuda.device(device):
+        stream, other = _stream_of(stream, device)
+        fresh = out is None
+        if fresh:
+            out = MxMatrix(torch.empty((rows, 16 * max(blocks, 1)), dtype=torch.uint8,
+                                       device=device),
+                           torch.empty((rows, max(16, (blocks + 15) // 16 * 16)), dtype=torch.uint8,
+                                       device=device), cols)
+        elif out.shape != (rows, cols):
+            raise ValueError("out must have src's shape")
+        data, ldd, scales, ldsc = _mx_operand("out", out, device)
+        st = migemm_quantize_mx(_dtype_code(src), op, rows, cols, src.data_ptr() or None, lds,
+                                data, ldd, scales, ldsc, stream)
+        if st != OK:
+            raise MigemmError(st, "migemm_quantize_mx")
+        if fresh and other:
+            _used_on(stream, device, out.data, out.scales)
+    return out
+
+
+def dequantize_mx(m, dtype, out=None, *, stream=None):
+    """The values of an ``MxMatrix`` as a row-major ``dtype`` tensor (float32,
+    float16 or bfloat16; ``out``, if given).  Does not synchronise."""
+    import torch
+    device = m.device
+    rows, cols = m.shape
+    data, ldd, scales, ldsc = _mx_operand("m", m, device)
+    with torch.cuda.device(device):
+        stream, other = _stream_of(stream, device)
+        fresh = out is None
+        if fresh:
+            out = torch.empty((rows, cols), dtype=dtype, device=device)
+        else:
+            _check_device("out", out, device)
+            if out.dtype != dtype or tuple(out.shape) != (rows, cols):
+                raise ValueError("out must have m's shape and the requested dtype")
+        st = migemm_dequantize_mx(_dtype_code(out), rows, cols, data, ldd, scales, ldsc,
+                                  out.data_ptr() or None, _ld(out), stream)
+        if st != OK:
+            raise MigemmError(st, "migemm_dequantize_mx")
+        if fresh and other:
+            _used_on(stream, device, out)
+    return out
+
+
+def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=None,
+            stream=None):
+    """out = alpha * (A x B^T) + beta * out for two ``MxMatrix`` operands: ``a`` is
+    M x K, ``b`` N x K (quantised along k).  ``out`` (M x N, row-major, float32,
+    float16 or bfloat16) is allocated with ``out_dtype`` (default float32) if not
+    given, which beta == 0 requires.  Does not synchronise."""
+    import torch
+    device = a.device
+    (M, K), (N, K2) = a.shape, b.shape
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {a.shape} x {b.shape} transposed")
+    pa, lda, psa, ldsa = _mx_operand("a", a, device)
+    pb, ldb, psb, ldsb = _mx_operand("b", b, device)
+    with torch.cuda.device(device):
+        stream, other = _stream_of(stream, device)
+        fresh = out is None
+        if fresh:
+            if beta != 0.0:
+                raise ValueError("beta != 0 needs an existing out")
+            out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=device)
+        else:
+            _check_device("out", out, device)
+            if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
+                raise ValueError("out must have shape (M, N) (and out_dtype, if given)")
+        st = migemm_gemm_mx(M, N, (K + 31) // 32 * 32, pa, lda, psa, ldsa, pb, ldb, psb, ldsb,
+                            float(alpha), float(beta), _dtype_code(out), out.data_ptr() or None,
+                            _ld(out), stream)
+        if st != OK:
+            raise MigemmError(st, "migemm_gemm_mx")
+        if fresh and other:
+            _used_on(stream, device, out)
     return out

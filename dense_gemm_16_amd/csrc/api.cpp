@@ -19,12 +19,40 @@
 #include "migemm.h"
 
 namespace migemm {
+
+int elem_size(int dtype) {
+    return (dtype == MIGEMM_F32 || dtype == MIGEMM_I32) ? 4 : dtype == MIGEMM_I8 ? 1 : 2;
+}
+
+// Byte range [lo, hi) touched by a rows x cols row-major operand (rows, cols >= 1)
+// with leading dimension ld.  False when the range does not fit the address
+// space: (rows - 1) ld + cols reaches 2^63 at the size limits, so the bytes are
+// counted in 128 bits.
+bool extent(const void* p, int64_t rows, int64_t cols, int64_t ld, int es, uintptr_t& lo,
+            uintptr_t& hi) {
+    lo = reinterpret_cast<uintptr_t>(p);
+    const unsigned __int128 bytes =
+        (static_cast<unsigned __int128>(rows - 1) * static_cast<unsigned __int128>(ld) +
+         static_cast<unsigned __int128>(cols)) * static_cast<unsigned __int128>(es);
+    if (bytes > static_cast<unsigned __int128>(UINTPTR_MAX - lo)) return false;
+    hi = lo + static_cast<uintptr_t>(bytes);
+    return true;
+}
+
+bool overlaps(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a0 < b1 && b0 < a1; }
+
+bool known_dtype(int d) { return d == MIGEMM_F32 || d == MIGEMM_F16 || d == MIGEMM_BF16; }
+
+thread_local int g_last_hip_error = 0;
+
+int hip_status(hipError_t err) {
+    if (err == hipSuccess) return MIGEMM_OK;
+    g_last_hip_error = static_cast<int>(err);
+    return MIGEMM_ERR_HIP;
+}
+
 namespace {
 
-// Sizes are limited so that every index product fits in 64 bits:
-// a dimension below 2^31 times a leading dimension below 2^32.
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxLd = int64_t(1) << 32;  // leading dimensions must be below this
 // M * N * K from which a 16-bit product the direct kernel cannot read in place
 // is run on packed copies (pack.hip) rather than by the register-staged kernel.
 constexpr double kPackMinWork = 134217728.0;  // 2^27, e.g. 512^3
@@ -73,34 +101,10 @@ const Variant kVariants[] = {
 };
 constexpr int kNumVariants = sizeof(kVariants) / sizeof(kVariants[0]);
 
-thread_local int g_last_hip_error = 0;
-
-int elem_size(int dtype) {
-    return (dtype == MIGEMM_F32 || dtype == MIGEMM_I32) ? 4 : dtype == MIGEMM_I8 ? 1 : 2;
-}
-
 // INT8: each product is at most 2^14 in magnitude ((-128)(-128)), so sums of at
 // most 2^17 - 1 of them stay below 2^31 and fit INT32 exactly.
 constexpr int64_t kMaxKi8 = (int64_t(1) << 17) - 1;
 
-// Byte range [lo, hi) touched by a rows x cols row-major operand (rows, cols >= 1)
-// with leading dimension ld.  False when the range does not fit the address
-// space: (rows - 1) ld + cols reaches 2^63 at the size limits, so the bytes are
-// counted in 128 bits.
-bool extent(const void* p, int64_t rows, int64_t cols, int64_t ld, int es, uintptr_t& lo,
-            uintptr_t& hi) {
-    lo = reinterpret_cast<uintptr_t>(p);
-    const unsigned __int128 bytes =
-        (static_cast<unsigned __int128>(rows - 1) * static_cast<unsigned __int128>(ld) +
-         static_cast<unsigned __int128>(cols)) * static_cast<unsigned __int128>(es);
-    if (bytes > static_cast<unsigned __int128>(UINTPTR_MAX - lo)) return false;
-    hi = lo + static_cast<uintptr_t>(bytes);
-    return true;
-}
-
-bool overlaps(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) { return a0 < b1 && b0 < a1; }
-
-bool known_dtype(int d) { return d == MIGEMM_F32 || d == MIGEMM_F16 || d == MIGEMM_BF16; }
 bool known_input(int d) { return known_dtype(d) || d == MIGEMM_I8; }
 bool known_output(int d) { return known_dtype(d) || d == MIGEMM_I32; }
 
@@ -450,12 +454,7 @@ int run_gemm(int variant, int config, int op_a, int op_b, int64_t M, int64_t N, 
     const int st = prepare(variant, config, op_a, op_b, M, N, K, dtype, A, lda, B, ldb, alpha,
                            beta, c_dtype, C, ldc, ws, ws_bytes, stream, true, g);
     if (st != MIGEMM_OK) return st;
-    const hipError_t err = launch(g, variant, config);
-    if (err != hipSuccess) {
-        g_last_hip_error = static_cast<int>(err);
-        return MIGEMM_ERR_HIP;
-    }
-    return MIGEMM_OK;
+    return hip_status(launch(g, variant, config));
 }
 
 int workspace_bytes(int variant, int config, int op_a, int op_b, int64_t M, int64_t N,
@@ -555,13 +554,8 @@ int migemm_convert(int src_dtype, int dst_dtype, int64_t rows, int64_t cols, con
     extent(src, rows, cols, lds, elem_size(src_dtype), s0, s1);
     extent(dst, rows, cols, ldd, elem_size(dst_dtype), d0, d1);
     if (overlaps(s0, s1, d0, d1)) return MIGEMM_ERR_INVALID_ARG;
-    const hipError_t err = launch_convert(src_dtype, dst_dtype, rows, cols, src, lds, dst, ldd,
-                                          static_cast<hipStream_t>(stream));
-    if (err != hipSuccess) {
-        g_last_hip_error = static_cast<int>(err);
-        return MIGEMM_ERR_HIP;
-    }
-    return MIGEMM_OK;
+    return hip_status(launch_convert(src_dtype, dst_dtype, rows, cols, src, lds, dst, ldd,
+                                     static_cast<hipStream_t>(stream)));
 }
 
 int migemm_variant_count(void) { return kNumVariants; }
@@ -607,7 +601,8 @@ const char* migemm_status_string(int status) {
         case MIGEMM_ERR_UNSUPPORTED: return "variant does not support this dtype";
         case MIGEMM_ERR_HIP: return "HIP runtime error";
         case MIGEMM_ERR_WORKSPACE:
-            return "the product needs more scratch memory than the allocation-free entry point holds";
+            return "the call needs more scratch memory than it was lent (or than the "
+                   "allocation-free entry point holds)";
         default: return "unknown status";
     }
 }

@@ -315,6 +315,43 @@ hipError_t launch_empty_product(const GemmArgs& a);
 hipError_t launch_convert(int src_dtype, int dst_dtype, int64_t rows, int64_t cols,
                           const void* src, int64_t lds, void* dst, int64_t ldd, hipStream_t s);
 
+// MXFP4 (mx.hip, mx_gemm.hip): quantisation (trans: the source holds k as its
+// row index), decoding, and the product C = alpha A B + beta C of A (M x K) and
+// B given transposed (N x K); element and scale rows 16-byte aligned.
+hipError_t launch_quantize_mx(int dtype, bool trans, int64_t rows, int64_t cols, const void* src,
+                              int64_t lds, uint8_t* data, int64_t ldd, uint8_t* scales,
+                              int64_t ldsc, hipStream_t s);
+hipError_t launch_dequantize_mx(int dtype, int64_t rows, int64_t cols, const uint8_t* data,
+                                int64_t ldd, const uint8_t* scales, int64_t ldsc, void* dst,
+                                int64_t ld, hipStream_t s);
+struct MxArgs {
+    int64_t M, N, K;
+    const uint8_t* A;
+    int64_t lda;
+    const uint8_t* sa;
+    int64_t ldsa;
+    const uint8_t* B;
+    int64_t ldb;
+    const uint8_t* sb;
+    int64_t ldsb;
+    Epi out;
+    hipStream_t stream;
+};
+hipError_t launch_gemm_mx(const MxArgs& p);
+
+// Argument checks shared by the entry points (api.cpp).  Sizes are limited so
+// that every index product fits in 64 bits: a dimension below 2^31 times a
+// leading dimension below 2^32.
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxLd = int64_t(1) << 32;  // leading dimensions must be below this
+int elem_size(int dtype);
+bool known_dtype(int dtype);  // FP32, FP16 or BF16
+bool extent(const void* p, int64_t rows, int64_t cols, int64_t ld, int es, uintptr_t& lo,
+            uintptr_t& hi);
+bool overlaps(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1);
+// MIGEMM_OK, or MIGEMM_ERR_HIP with the error kept for migemm_last_hip_error.
+int hip_status(hipError_t err);
+
 // The C ABI's common path (api.cpp): validates one call, selects its variant
 // and configuration (variant -1: the selection table's; config -1: the table's
 // choice for the variant), and launches it with the workspace lent (ws may be

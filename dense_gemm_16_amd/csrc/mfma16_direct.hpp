@@ -351,11 +351,14 @@ __device__ __forceinline__ void wait_then_barrier() {
 // the rest, see splitk_slice) and writes its sums (FP32, INT32 for 8-bit
 // inputs), plain, to that slice's M x N block of out.C (leading dimension N):
 // the partial products that a reduction then sums.
+// Out: Epi, the output step of a product (GEN: the general one), or a type
+// derived from it whose `store` takes the wave's accumulators instead (the
+// softmax losses of a product's rows, linear_loss.hpp).
 template <class Cfg, bool GEN, bool TA, bool TB, bool KTAIL = false, bool KHEAD = false,
-          bool SPLITK = false>
+          bool SPLITK = false, class Out = Epi>
 __global__ __launch_bounds__(Cfg::NT) void mfma16_direct_kernel(
     int64_t M, int64_t N, int64_t K, const typename Cfg::E* __restrict__ A, int64_t lda,
-    const typename Cfg::E* __restrict__ B, int64_t ldb, Epi out, int tiles_m, int tiles_n) {
+    const typename Cfg::E* __restrict__ B, int64_t ldb, Out out, int tiles_m, int tiles_n) {
     int tile = blockIdx.x;
     if constexpr (SPLITK) {
         const int tiles = tiles_m * tiles_n;
@@ -813,7 +816,13 @@ __global__ __launch_bounds__(Cfg::NT) void mfma16_direct_kernel(
         // 4-byte accesses in 32- or 64-byte row pieces (the 16x16 accumulator
         // layout: four rows of one column per lane).
         constexpr bool kLdsEpilogue = GEN && MF == 16 && Cfg::WTN == 64 && EB != 1;
-        if constexpr (kLdsEpilogue) {
+        if constexpr (!std::is_same_v<Out, Epi>) {
+            // every wave's fragment reads are done before its LDS is reused (as
+            // in lds_epilogue)
+            if constexpr (Cfg::SCHED != 4) __syncthreads();
+            out.template store<Cfg>(acc, (MIGEMM_LDS char*)smem, m0 + wm0, n0 + wn0, wave, lane,
+                                    M, N);
+        } else if constexpr (kLdsEpilogue) {
             lds_epilogue();
         } else if constexpr (!GEN) {
 #pragma unroll

@@ -1,0 +1,261 @@
+// mx.hip -- quantisation of FP32, FP16 and BF16 matrices to microscaled 4-bit
+// floating point (MXFP4), and its decoding.
+//
+// The format.  A row is cut into blocks of 32 elements along k.  A block has
+// one scale byte b, the power of two 2^(b - 127) (255: the block is NaN), and
+// 32 four-bit elements: sign, two exponent bits, one mantissa bit, the values
+// 0, 0.5, 1, 1.5, 2, 3, 4 and 6 and their negatives (codes 0 to 7, sign 8).  Two
+// elements share a byte, the even one in the low half; a block is 16 bytes.
+//
+// The rule.  With m the largest magnitude of a block, the scale is 2^e with
+// e = floor(log2 m) - 2 (the largest element, 6 = 1.5 x 2^2, then covers m up to
+// a quarter of a step), at least -127; every element is x 2^-e rounded to the
+// nearest of the values above, midpoints to the even code, magnitudes past 6 to
+// 6.  In bits: for FP32 m with biased exponent field E, b = max(E - 2, 0), and
+// x 2^-e = x 2^(127 - b) is a product by a normal FP32 power of two, exact.  A
+// block that holds an infinity or a NaN has no such scale and becomes NaN
+// (b = 255, all codes 0); an all-zero one has b = 0.
+#include "common.hpp"
+
+namespace migemm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The four-bit code of |y| < 8 (sign 0): below 2 the values are multiples of
+// 0.5, below 4 of 1, above of 2, so one rounding to the nearest even integer in
+// that unit gives the code's offset in its binade.
+__device__ __forceinline__ uint32_t fp4_code(float y) {
+    const float a = fabsf(y);
+    const float unit = a < 2.0f ? 2.0f : a < 4.0f ? 1.0f : 0.5f;
+    const int base = a < 2.0f ? 0 : a < 4.0f ? 2 : 4;
+    const int n = static_cast<int>(rintf(a * unit)) + base;
+    return static_cast<uint32_t>(min(n, 7)) | ((__float_as_uint(y) >> 28) & 8u);
+}
+
+// The scale byte of a block whose largest magnitude has the FP32 bits `m` (sign
+// cleared; infinities and NaN are 0x7f800000 and above).
+__device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
+    const int e = static_cast<int>(m >> 23);
+    return e == 255 ? 255u : static_cast<uint32_t>(max(e - 2, 0));
+}
+
+// 2^(127 - b), the factor that brings a block of scale byte b to element units;
+// 0 for a NaN block, whose codes are 0 (its elements are dropped by the caller).
+__device__ __forceinline__ float unscale(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+
+// Eight consecutive elements from column c of a row, zeros past cols.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* __restrict__ row, int64_t c, int64_t cols,
+                                      float (&v)[8]) {
+    if (VEC && c + 8 <= cols) {
+        u32x4 raw[sizeof(T) / 2];
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            raw[i] = reinterpret_cast<const u32x4*>(row + c)[i];
+        T e[8];
+        __builtin_memcpy(e, raw, sizeof(e));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_f32(row[c + i]) : 0.0f;
+    }
+}
+
+// Rows along k (OP_N).  Four lanes share a block, eight elements each, so loads
+// are 16 bytes per lane and contiguous over a wavefront.  A workgroup takes
+// kThreads / lpr rows (lpr lanes each, a power of two) of one segment of columns.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
+    int64_t rows, int64_t cols, const T* __restrict__ src, int64_t lds, uint8_t* __restrict__ data,
+    int64_t ldd, uint8_t* __restrict__ scales, int64_t ldsc, int lpr, int64_t segs) {
+    const int64_t group = blockIdx.x / segs, seg = blockIdx.x % segs;
+    const int64_t row = group * (kThreads / lpr) + threadIdx.x / lpr;
+    const int64_t piece = seg * lpr + threadIdx.x % lpr;  // of eight elements
+    const int64_t blocks = ceil_div(cols, 32);
+    // whole groups of four lanes leave together
+    if (row >= rows || piece / 4 >= blocks) return;
+    float v[8];
+    load8<T, VEC>(src + row * lds, piece * 8, cols, v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1)));
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 2)));
+    const uint32_t b = scale_byte(m);
+    const float f = unscale(b);
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= fp4_code(v[i] * f) << (4 * i);
+    if (b == 255u) w = 0;
+    *reinterpret_cast<uint32_t*>(data + row * ldd + piece * 4) = w;
+    if (piece % 4 == 0) scales[row * ldsc + piece / 4] = static_cast<uint8_t>(b);
+}
+
+// k as the row index of the source (OP_T): a workgroup takes 64 rows of the
+// result by 8 blocks; a lane owns one row and one block at a time, so loads are
+// contiguous over a wavefront, and the packed blocks go through LDS (the 16-byte
+// slot XORed by the row, which spreads a wavefront's writes over the banks) to
+// be written 128 bytes to a row.
+constexpr int kRows = 64, kBlocks = 8;
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void quantize_cols_kernel(
+    int64_t rows, int64_t cols, const T* __restrict__ src, int64_t lds, uint8_t* __restrict__ data,
+    int64_t ldd, uint8_t* __restrict__ scales, int64_t ldsc, int64_t tiles_k) {
+    __shared__ __attribute__((aligned(16))) u32x4 out[kRows][kBlocks];
+    __shared__ uint8_t sc[kRows][kBlocks];
+    const int64_t r0 = blockIdx.x / tiles_k * kRows, b0 = blockIdx.x % tiles_k * kBlocks;
+    const int64_t blocks = ceil_div(cols, 32);
+    const int lane = threadIdx.x % kWave;
+    const int64_t row = r0 + lane;
+    for (int blk = threadIdx.x / kWave; blk < kBlocks; blk += kThreads / kWave) {
+        const int64_t k0 = (b0 + blk) * 32;
+        float v[32];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v[i] = row < rows && k0 + i < cols ? to_f32(src[(k0 + i) * lds + row]) : 0.0f;
+            m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        }
+        const uint32_t b = scale_byte(m);
+        const float f = unscale(b);
+        u32x4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i / 8] |= fp4_code(v[i] * f) << (4 * (i % 8));
+        if (b == 255u) w = u32x4{0u, 0u, 0u, 0u};
+        out[lane][blk ^ (lane & 7)] = w;
+        sc[lane][blk] = static_cast<uint8_t>(b);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * kBlocks; i += kThreads) {
+        const int r = i / kBlocks, blk = i % kBlocks;
+        if (r0 + r >= rows || b0 + blk >= blocks) continue;
+        *reinterpret_cast<u32x4*>(data + (r0 + r) * ldd + (b0 + blk) * 16) = out[r][blk ^ (r & 7)];
+        scales[(r0 + r) * ldsc + b0 + blk] = sc[r][blk];
+    }
+}
+
+// The value of a four-bit code.
+__device__ __forceinline__ float fp4_value(uint32_t code) {
+    // codes 0 and 1 are 0 and 0.5; from 2 on, exponent field code / 2 over 1 / 2,
+    // mantissa bit code % 2: the code placed at FP32 bit 22, bias 126
+    const uint32_t mag = code & 7u;
+    const float a = mag < 2u ? 0.5f * static_cast<float>(mag)
+                             : __uint_as_float((mag << 22) + (126u << 23));
+    return code & 8u ? -a : a;
+}
+
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ _Float16 from_f32<_Float16>(float x) {
+    return static_cast<_Float16>(x);
+}
+template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float x) {
+    return bf16_t{f32_to_bf16_bits(x)};
+}
+
+// Eight elements per lane, as in quantize_rows_kernel.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(
+    int64_t rows, int64_t cols, const uint8_t* __restrict__ data, int64_t ldd,
+    const uint8_t* __restrict__ scales, int64_t ldsc, T* __restrict__ dst, int64_t ld, int lpr,
+    int64_t segs) {
+    const int64_t group = blockIdx.x / segs, seg = blockIdx.x % segs;
+    const int64_t row = group * (kThreads / lpr) + threadIdx.x / lpr;
+    const int64_t piece = seg * lpr + threadIdx.x % lpr;
+    const int64_t c = piece * 8;
+    if (row >= rows || c >= cols) return;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(data + row * ldd + piece * 4);
+    const uint32_t b = scales[row * ldsc + piece / 4];
+    const float s = b == 255u ? __uint_as_float(0x7fc00000u)
+                              : __uint_as_float(b == 0u ? 0x00400000u : b << 23);
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = from_f32<T>(fp4_value((w >> (4 * i)) & 15u) * s);
+    T* const p = dst + row * ld + c;
+    if (VEC && c + 8 <= cols) {
+        u32x4 raw[sizeof(T) / 2];
+        __builtin_memcpy(raw, v, sizeof(v));
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            reinterpret_cast<u32x4*>(p)[i] = raw[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols) p[i] = v[i];
+    }
+}
+
+// Lanes per row (a power of two, 4 to 256) and column segments for rows of
+// `pieces` eight-element pieces.
+void row_shape(int64_t pieces, int& lpr, int64_t& segs) {
+    lpr = 4;
+    while (lpr < kThreads && lpr < pieces) lpr *= 2;
+    segs = ceil_div(pieces, lpr);
+}
+
+template <typename T>
+hipError_t quantize_typed(bool trans, int64_t rows, int64_t cols, const void* src, int64_t lds,
+                          uint8_t* data, int64_t ldd, uint8_t* scales, int64_t ldsc,
+                          hipStream_t s) {
+    const T* p = static_cast<const T*>(src);
+    if (trans) {
+        const int64_t tiles_k = ceil_div(ceil_div(cols, 32), kBlocks);
+        const int64_t grid = ceil_div(rows, kRows) * tiles_k;
+        if (grid > 0x7fffffff) return hipErrorInvalidValue;
+        quantize_cols_kernel<T><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
+            rows, cols, p, lds, data, ldd, scales, ldsc, tiles_k);
+        return hipGetLastError();
+    }
+    int lpr;
+    int64_t segs;
+    row_shape(4 * ceil_div(cols, 32), lpr, segs);
+    const int64_t grid = ceil_div(rows, kThreads / lpr) * segs;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    const bool vec = aligned16(src) && (lds * static_cast<int64_t>(sizeof(T))) % 16 == 0;
+    auto* const fn = vec ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>;
+    fn<<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(rows, cols, p, lds, data, ldd,
+                                                                   scales, ldsc, lpr, segs);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t dequantize_typed(int64_t rows, int64_t cols, const uint8_t* data, int64_t ldd,
+                            const uint8_t* scales, int64_t ldsc, void* dst, int64_t ld,
+                            hipStream_t s) {
+    int lpr;
+    int64_t segs;
+    row_shape(ceil_div(cols, 8), lpr, segs);
+    const int64_t grid = ceil_div(rows, kThreads / lpr) * segs;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    const bool vec = aligned16(dst) && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0;
+    auto* const fn = vec ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
+    fn<<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
+        rows, cols, data, ldd, scales, ldsc, static_cast<T*>(dst), ld, lpr, segs);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_mx(int dtype, bool trans, int64_t rows, int64_t cols, const void* src,
+                              int64_t lds, uint8_t* data, int64_t ldd, uint8_t* scales,
+                              int64_t ldsc, hipStream_t s) {
+    if (dtype == 0)
+        return quantize_typed<float>(trans, rows, cols, src, lds, data, ldd, scales, ldsc, s);
+    if (dtype == 1)
+        return quantize_typed<_Float16>(trans, rows, cols, src, lds, data, ldd, scales, ldsc, s);
+    return quantize_typed<bf16_t>(trans, rows, cols, src, lds, data, ldd, scales, ldsc, s);
+}
+
+hipError_t launch_dequantize_mx(int dtype, int64_t rows, int64_t cols, const uint8_t* data,
+                                int64_t ldd, const uint8_t* scales, int64_t ldsc, void* dst,
+                                int64_t ld, hipStream_t s) {
+    if (dtype == 0) return dequantize_typed<float>(rows, cols, data, ldd, scales, ldsc, dst, ld, s);
+    if (dtype == 1)
+        return dequantize_typed<_Float16>(rows, cols, data, ldd, scales, ldsc, dst, ld, s);
+    return dequantize_typed<bf16_t>(rows, cols, data, ldd, scales, ldsc, dst, ld, s);
+}
+
+}  // namespace migemm

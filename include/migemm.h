@@ -94,8 +94,8 @@ typedef enum {
     MIGEMM_ERR_UNSUPPORTED = 2, /* a forced variant that does not take this dtype */
     MIGEMM_ERR_HIP = 3,         /* the HIP runtime reported an error at launch
                                    (see migemm_last_hip_error) */
-    MIGEMM_ERR_WORKSPACE = 4    /* the product needs more scratch memory than the
-                                   allocation-free entry point holds */
+    MIGEMM_ERR_WORKSPACE = 4    /* the call needs more scratch memory than it was lent, or
+                                   than the allocation-free entry point holds */
 } migemm_status;
 
 /*
@@ -315,6 +315,76 @@ int migemm_describe_ex(int variant, int config, int op_a, int op_b,
  */
 int migemm_convert(int src_dtype, int dst_dtype, int64_t rows, int64_t cols,
                    const void* src, int64_t lds, void* dst, int64_t ldd, void* stream);
+
+/*
+ * Microscaled 4-bit floating point (MXFP4).
+ *
+ * A rows x cols matrix in MXFP4 is two row-major byte arrays.  Each row is cut
+ * into ceil(cols / 32) blocks of 32 elements:
+ *
+ *   scales  one byte b per block, block c of row i at scales[i * ldsc + c]: the
+ *           power of two 2^(b - 127); 255 makes every element of the block NaN;
+ *   data    16 bytes per block, block c of row i from data[i * ldd + 16 c] on,
+ *           two elements to a byte, the even one in the low half.  An element is
+ *           a sign bit, two exponent bits and a mantissa bit: codes 0 to 7 are
+ *           0, 0.5, 1, 1.5, 2, 3, 4, 6, codes 8 to 15 their negatives.
+ *
+ * An element's value is its code's value times its block's scale.  Where cols is
+ * not a multiple of 32 the last block's elements past cols are 0 (codes 0 or 8).
+ * Both arrays start at 16-byte boundaries, and ldd and ldsc (bytes) are multiples of
+ * 16 with ldd >= 16 ceil(cols / 32) and ldsc >= ceil(cols / 32); each row, the last
+ * one included, occupies its whole ldd or ldsc bytes.  The bytes of a row past
+ * its last block are never written, and their values never matter.
+ */
+
+/*
+ * Quantisation along rows: dst (MXFP4, rows x cols) from a source of src_dtype
+ * (MIGEMM_F32, MIGEMM_F16 or MIGEMM_BF16).  op: MIGEMM_OP_N, element (i, k) at
+ * src[i * lds + k], lds >= max(1, cols); MIGEMM_OP_T, the source is stored
+ * transposed (a K x N weight of a product, k as its row index): element (i, k) at
+ * src[k * lds + i], lds >= max(1, rows).
+ *
+ * With m the largest magnitude of a block, its scale is 2^e, e = floor(log2 m) -
+ * 2 but at least -127 (b = 0 for an all-zero block), and each element is x / 2^e
+ * rounded to the nearest code, midpoints to the even code, magnitudes above 6 to
+ * 6.  A block with an infinity or a NaN gets scale byte 255 and codes 0.
+ *
+ * Any alignment of src (16-byte aligned rows take the vector path).  data and
+ * scales must not overlap src or each other.  Misaligned or too narrow outputs
+ * are MIGEMM_ERR_INVALID_ARG; the pointer, stream, ownership and error rules are
+ * migemm_gemm's; rows == 0 or cols == 0 is a no-op.
+ */
+int migemm_quantize_mx(int src_dtype, int op, int64_t rows, int64_t cols, const void* src,
+                       int64_t lds, void* data, int64_t ldd, void* scales, int64_t ldsc,
+                       void* stream);
+
+/*
+ * Decoding: dst (dst_dtype, rows x cols, row-major, leading dimension ld
+ * elements) = the values of an MXFP4 matrix, rounded to nearest even into
+ * dst_dtype where it does not hold them exactly.  Same rules as above.
+ */
+int migemm_dequantize_mx(int dst_dtype, int64_t rows, int64_t cols, const void* data, int64_t ldd,
+                         const void* scales, int64_t ldsc, void* dst, int64_t ld, void* stream);
+
+/*
+ * The product of two MXFP4 matrices:
+ *
+ *     C[i][j] = alpha * (sum_{k=0}^{K-1} A[i][k] * B[j][k]) + beta * C[i][j]
+ *
+ * A is M x K; B is given transposed, N x K (each of its rows quantised along k:
+ * a weight stored output-major, or a K x N one quantised with MIGEMM_OP_T).
+ * K counts whole blocks and must be a multiple of 32 (a matrix with other cols
+ * is multiplied with K rounded up: its padding elements are 0).  Products and
+ * scales are exact, sums are FP32, and the output step is migemm_gemm_ex's:
+ * c_dtype MIGEMM_F32, MIGEMM_F16 or MIGEMM_BF16, beta == 0 leaves C unread,
+ * M == 0 or N == 0 is a no-op and K == 0 gives C = beta * C.  A NaN scale makes
+ * every sum it takes part in NaN.  C must not overlap the operands.  Same
+ * pointer, stream, ownership and error rules as migemm_gemm.
+ */
+int migemm_gemm_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                   const void* a_scales, int64_t ldas, const void* B, int64_t ldb,
+                   const void* b_scales, int64_t ldbs, float alpha, float beta, int c_dtype,
+                   void* C, int64_t ldc, void* stream);
 
 /* Number of variants (they are numbered 0 .. count-1). */
 int migemm_variant_count(void);
