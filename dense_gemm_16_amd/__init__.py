@@ -31,6 +31,8 @@ EXPORTS = ("migemm_gemm", "migemm_gemm_variant", "migemm_gemm_ex", "migemm_gemm_
            "migemm_gemm_ws", "migemm_gemm_noalloc", "migemm_workspace_size", "migemm_describe",
            "migemm_describe_ex",
            "migemm_convert", "migemm_quantize_mx", "migemm_dequantize_mx", "migemm_gemm_mx",
+           "migemm_linear_loss_workspace_size", "migemm_linear_ce_forward",
+           "migemm_linear_ce_backward", "migemm_linear_kd_forward", "migemm_linear_kd_backward",
            "migemm_variant_count", "migemm_variant_name",
            "migemm_variant_supports", "migemm_config_count", "migemm_config_name",
            "migemm_select", "migemm_status_string", "migemm_last_hip_error", "migemm_version")
@@ -91,6 +93,19 @@ def lib():
     L.migemm_gemm_mx.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, f32, f32, i32,
                                  vp, i64, vp]
     L.migemm_gemm_mx.restype = i32
+    layer = [i64, i64, i64, i32, vp, i64, vp, i64]  # T, V, D, dtype, X, ldx, W, ldw
+    kd = [i64, i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp, i64, f32]
+    L.migemm_linear_loss_workspace_size.argtypes = [i32, i64, i64, i64, i64, i32, vp, i64, vp, i64,
+                                                    ctypes.POINTER(i64)]
+    L.migemm_linear_loss_workspace_size.restype = i32
+    L.migemm_linear_ce_forward.argtypes = layer + [vp, i64, vp, vp, vp, i64, vp]
+    L.migemm_linear_ce_forward.restype = i32
+    L.migemm_linear_ce_backward.argtypes = layer + [vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp]
+    L.migemm_linear_ce_backward.restype = i32
+    L.migemm_linear_kd_forward.argtypes = kd + [vp, vp, vp, i64, vp, i64, vp]
+    L.migemm_linear_kd_forward.restype = i32
+    L.migemm_linear_kd_backward.argtypes = kd + [vp, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp]
+    L.migemm_linear_kd_backward.restype = i32
     L.migemm_variant_count.argtypes = []
     L.migemm_variant_count.restype = i32
     L.migemm_variant_name.argtypes = [i32]
@@ -211,6 +226,44 @@ def migemm_gemm_mx(M, N, K, A, lda, a_scales, ldas, B, ldb, b_scales, ldbs, alph
                    C, ldc, stream=None) -> int:
     return lib().migemm_gemm_mx(M, N, K, A, lda, a_scales, ldas, B, ldb, b_scales, ldbs, alpha,
                                 beta, c_dtype, C, ldc, stream)
+
+
+def migemm_linear_loss_workspace_size(backward, T, V, D, top, dtype, X, ldx, W, ldw):
+    """(status, bytes) of the workspace a loss's pass needs."""
+    n = ctypes.c_int64(-1)
+    st = lib().migemm_linear_loss_workspace_size(backward, T, V, D, top, dtype, X, ldx, W, ldw,
+                                                 ctypes.byref(n))
+    return st, n.value
+
+
+def migemm_linear_ce_forward(T, V, D, dtype, X, ldx, W, ldw, target, ignore_index, loss, lse,
+                             workspace, workspace_bytes, stream=None) -> int:
+    return lib().migemm_linear_ce_forward(T, V, D, dtype, X, ldx, W, ldw, target, ignore_index,
+                                          loss, lse, workspace, workspace_bytes, stream)
+
+
+def migemm_linear_ce_backward(T, V, D, dtype, X, ldx, W, ldw, target, ignore_index, lse, grad, dX,
+                              lddx, dW, lddw, workspace, workspace_bytes, stream=None) -> int:
+    return lib().migemm_linear_ce_backward(T, V, D, dtype, X, ldx, W, ldw, target, ignore_index,
+                                           lse, grad, dX, lddx, dW, lddw, workspace,
+                                           workspace_bytes, stream)
+
+
+def migemm_linear_kd_forward(T, V, D, top, dtype, X, ldx, W, ldw, teacher_dtype, teacher, ldt,
+                             index, ldi, temperature, loss, lse, student, lds, workspace,
+                             workspace_bytes, stream=None) -> int:
+    return lib().migemm_linear_kd_forward(T, V, D, top, dtype, X, ldx, W, ldw, teacher_dtype,
+                                          teacher, ldt, index, ldi, temperature, loss, lse, student,
+                                          lds, workspace, workspace_bytes, stream)
+
+
+def migemm_linear_kd_backward(T, V, D, top, dtype, X, ldx, W, ldw, teacher_dtype, teacher, ldt,
+                              index, ldi, temperature, lse, student, lds, grad, dX, lddx, dW, lddw,
+                              workspace, workspace_bytes, stream=None) -> int:
+    return lib().migemm_linear_kd_backward(T, V, D, top, dtype, X, ldx, W, ldw, teacher_dtype,
+                                           teacher, ldt, index, ldi, temperature, lse, student, lds,
+                                           grad, dX, lddx, dW, lddw, workspace, workspace_bytes,
+                                           stream)
 
 
 def migemm_variant_count() -> int:
@@ -526,3 +579,195 @@ def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=
         if fresh and other:
             _used_on(stream, device, out)
     return out
+
+
+# ------------------------------------------------------- output-layer losses
+
+def _layer(x, w):
+    """(device, T, V, D, dtype code, (x pointer, ldx, w pointer, ldw)) of an output
+    layer's operands, checked."""
+    device = x.device
+    _check_device("x", x, device)
+    _check_device("w", w, device)
+    if x.dtype != w.dtype:
+        raise ValueError(f"dtype mismatch: {x.dtype} vs {w.dtype}")
+    dt, ldx, ldw = _dtype_code(x), _ld(x), _ld(w)
+    (T, D), (V, D2) = x.shape, w.shape
+    if D != D2:
+        raise ValueError(f"x has rows of {D}, w of {D2}")
+    return device, T, V, D, dt, (x.data_ptr() or None, ldx, w.data_ptr() or None, ldw)
+
+
+def _row_vector(name, t, device, dtype, rows):
+    """Pointer of a contiguous vector of one value per row, checked."""
+    _check_device(name, t, device)
+    if t.dtype != dtype or tuple(t.shape) != (rows,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector of {rows} (got {t.dtype}, "
+                         f"{tuple(t.shape)}, strides {t.stride()})")
+    return t.data_ptr() or None
+
+
+def _row_gradient(grad, device, rows):
+    """`grad` as one float32 per row: a number, a 0-d tensor or a vector."""
+    import torch
+    if not isinstance(grad, torch.Tensor):
+        return torch.full((rows,), float(grad), dtype=torch.float32, device=device)
+    _check_device("grad", grad, device)
+    if grad.dim() > 1 or (grad.dim() == 1 and grad.shape[0] != rows):
+        raise ValueError(f"grad must be a number or a vector of {rows}")
+    return grad.to(torch.float32).expand(rows).contiguous()
+
+
+def _gradient(name, wanted, given, like):
+    """The tensor a gradient is written to: `given` (checked), a new one, or None."""
+    import torch
+    if given is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device) if wanted else None
+    _check_device(name, given, like.device)
+    if given.dtype != like.dtype or given.shape != like.shape:
+        raise ValueError(f"{name} must have the shape and dtype of what it is the gradient of")
+    return given
+
+
+def _loss_workspace(backward, T, V, D, top, dt, ptrs, device):
+    import torch
+    st, n = migemm_linear_loss_workspace_size(backward, T, V, D, top, dt, *ptrs)
+    if st != OK:
+        raise MigemmError(st, "migemm_linear_loss_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _teacher(logits, index, T, device):
+    """(dtype code, pointer, ldt, index pointer, ldi, entries per row), checked."""
+    import torch
+    _check_device("teacher_logits", logits, device)
+    _check_device("teacher_index", index, device)
+    if logits.dim() != 2 or logits.shape[0] != T or index.shape != logits.shape:
+        raise ValueError(f"teacher_logits and teacher_index must both be {T} x entries")
+    if index.dtype != torch.int64:
+        raise ValueError("teacher_index must be int64")
+    return (_dtype_code(logits), logits.data_ptr() or None, _ld(logits), index.data_ptr() or None,
+            _ld(index)), logits.shape[1]
+
+
+def linear_cross_entropy(x, w, target, *, ignore_index: int = -100, stream=None):
+    """(loss, lse): per row of ``x`` (T x D) the softmax cross entropy of the logits
+    ``x @ w.t()`` (``w``: V x D) against ``target`` (int64, T), and the logits'
+    log-sum-exp, which ``linear_cross_entropy_backward`` takes; both float32.  The
+    logits are never stored.  Rows whose target is ``ignore_index`` have loss 0; a
+    target outside the vocabulary gives NaN.  ``x`` and ``w``: CUDA tensors of one
+    dtype (float32, float16, bfloat16), unit column stride.  Runs on ``stream``
+    (default: torch's current stream) without synchronising."""
+    import torch
+    device, T, V, D, dt, ptrs = _layer(x, w)
+    pt = _row_vector("target", target, device, torch.int64, T)
+    with torch.cuda.device(device):
+        stream, other = _stream_of(stream, device)
+        loss = torch.empty(T, dtype=torch.float32, device=device)
+        lse = torch.empty(T, dtype=torch.float32, device=device)
+        ws = _loss_workspace(0, T, V, D, 0, dt, ptrs, device)
+        if other:
+            _used_on(stream, device, loss, lse, ws)
+        st = migemm_linear_ce_forward(T, V, D, dt, *ptrs, pt, ignore_index, loss.data_ptr() or None,
+                                      lse.data_ptr() or None, ws.data_ptr() or None, ws.numel(),
+                                      stream)
+    if st != OK:
+        raise MigemmError(st, "migemm_linear_ce_forward")
+    return loss, lse
+
+
+def linear_cross_entropy_backward(x, w, target, lse, grad, *, ignore_index: int = -100, dx=None,
+                                  dw=None, need_dx: bool = True, need_dw: bool = True,
+                                  stream=None):
+    """(dx, dw): the gradients of ``linear_cross_entropy``'s losses to ``x`` and ``w``
+    in their dtype, for the upstream gradient ``grad`` of each row's loss (a number
+    or a vector of T).  ``dx`` and ``dw`` are written into if given; one that is
+    neither given nor needed is None."""
+    import torch
+    device, T, V, D, dt, ptrs = _layer(x, w)
+    pt = _row_vector("target", target, device, torch.int64, T)
+    pl = _row_vector("lse", lse, device, torch.float32, T)
+    with torch.cuda.device(device):
+        stream, other = _stream_of(stream, device)
+        grad = _row_gradient(grad, device, T)
+        dx, dw = _gradient("dx", need_dx, dx, x), _gradient("dw", need_dw, dw, w)
+        ws = _loss_workspace(1, T, V, D, 0, dt, ptrs, device)
+        if other:
+            _hand_over(stream, device)
+            _used_on(stream, device, grad, ws, *(t for t in (dx, dw) if t is not None))
+        st = migemm_linear_ce_backward(
+            T, V, D, dt, *ptrs, pt, ignore_index, pl, grad.data_ptr() or None, *_out_matrix(dx),
+            *_out_matrix(dw), ws.data_ptr() or None, ws.numel(), stream)
+    if st != OK:
+        raise MigemmError(st, "migemm_linear_ce_backward")
+    return dx, dw
+
+
+def _out_matrix(t):
+    return (None, 1) if t is None else (t.data_ptr() or None, _ld(t))
+
+
+def _hand_over(stream, device):
+    """`stream` waits for what this call has queued on torch's current stream (the
+    upstream gradient, brought into one float32 per row there)."""
+    import torch
+    torch.cuda.ExternalStream(stream, device=device).wait_stream(torch.cuda.current_stream(device))
+
+
+def linear_distillation(x, w, teacher_logits, teacher_index, *, temperature: float = 1.0,
+                        stream=None):
+    """(loss, lse, student): per row of ``x`` (T x D) temperature^2 times the
+    divergence of the student's softmax (logits ``x @ w.t()``, ``w``: V x D, never
+    stored) from the softmax of the teacher's top logits (``teacher_logits``, T x
+    entries, at the vocabulary indices ``teacher_index``, int64; a negative index
+    marks an entry that is not held), both at ``temperature``.  ``lse`` and
+    ``student`` (the student's logits at the indices) are what
+    ``linear_distillation_backward`` takes.  All float32.  A row that holds no entry
+    has loss 0.  Otherwise as ``linear_cross_entropy``."""
+    import torch
+    device, T, V, D, dt, ptrs = _layer(x, w)
+    teacher, top = _teacher(teacher_logits, teacher_index, T, device)
+    with torch.cuda.device(device):
+        stream, other = _stream_of(stream, device)
+        loss = torch.empty(T, dtype=torch.float32, device=device)
+        lse = torch.empty(T, dtype=torch.float32, device=device)
+        student = torch.empty((T, top), dtype=torch.float32, device=device)
+        ws = _loss_workspace(0, T, V, D, top, dt, ptrs, device)
+        if other:
+            _used_on(stream, device, loss, lse, student, ws)
+        st = migemm_linear_kd_forward(
+            T, V, D, top, dt, *ptrs, *teacher, float(temperature), loss.data_ptr() or None,
+            lse.data_ptr() or None, student.data_ptr() or None, max(1, top), ws.data_ptr() or None,
+            ws.numel(), stream)
+    if st != OK:
+        raise MigemmError(st, "migemm_linear_kd_forward")
+    return loss, lse, student
+
+
+def linear_distillation_backward(x, w, teacher_logits, teacher_index, lse, student, grad, *,
+                                 temperature: float = 1.0, dx=None, dw=None, need_dx: bool = True,
+                                 need_dw: bool = True, stream=None):
+    """(dx, dw): the gradients of ``linear_distillation``'s losses to ``x`` and ``w``;
+    arguments as in ``linear_cross_entropy_backward``."""
+    import torch
+    device, T, V, D, dt, ptrs = _layer(x, w)
+    teacher, top = _teacher(teacher_logits, teacher_index, T, device)
+    pl = _row_vector("lse", lse, device, torch.float32, T)
+    _check_device("student", student, device)
+    if student.dtype != torch.float32 or tuple(student.shape) != (T, top):
+        raise ValueError(f"student must be float32, {T} x {top}")
+    with torch.cuda.device(device):
+        stream, other = _stream_of(stream, device)
+        grad = _row_gradient(grad, device, T)
+        dx, dw = _gradient("dx", need_dx, dx, x), _gradient("dw", need_dw, dw, w)
+        ws = _loss_workspace(1, T, V, D, top, dt, ptrs, device)
+        if other:
+            _hand_over(stream, device)
+            _used_on(stream, device, grad, ws, *(t for t in (dx, dw) if t is not None))
+        st = migemm_linear_kd_backward(
+            T, V, D, top, dt, *ptrs, *teacher, float(temperature), pl, student.data_ptr() or None,
+            _ld(student), grad.data_ptr() or None, *_out_matrix(dx), *_out_matrix(dw),
+            ws.data_ptr() or None, ws.numel(), stream)
+    if st != OK:
+        raise MigemmError(st, "migemm_linear_kd_backward")
+    return dx, dw

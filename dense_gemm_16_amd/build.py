@@ -30,7 +30,7 @@ RESOURCES = os.path.join(PKG, "kernel_resources.json")
 SOURCES = ["api.cpp", "mfma16.hip", "mfma_i8.hip", "regtile_mfma.hip", "naive.hip",
            "lds_tiled.hip", "regtile_valu.hip", "fill.hip", "convert.hip", "pack.hip",
            "noalloc.hip", "skinny.hip", "split.cpp", "splitk.hip", "mx.hip", "mx_gemm.hip",
-           "mx_api.cpp"]
+           "mx_api.cpp", "linear_loss.hip", "linear_loss_api.cpp"]
 # The configuration tables' kernels are built from *_part.hip sources, once per
 # configuration (and element type and output form), so that the compiles run in
 # parallel and a change rebuilds only what it touches.
@@ -43,7 +43,11 @@ PARTS = ([("mfma16_part.hip", f"mfma16_{et}_{'gen' if gen else 'plain'}_{c}",
          [("regtile_mfma_part.hip", f"regtile_mfma_{'gen' if gen else 'plain'}_{c}",
            [f"-DMIGEMM_PART_GEN={'true' if gen else 'false'}", f"-DMIGEMM_PART_C={c}"])
           for gen in (False, True) for c in range(12)] +
-         [("mfma_i8_part.hip", f"mfma_i8_{c}", [f"-DMIGEMM_PART_C={c}"]) for c in (0, 1, 2, 3, 4, 6)])
+         [("mfma_i8_part.hip", f"mfma_i8_{c}", [f"-DMIGEMM_PART_C={c}"]) for c in (0, 1, 2, 3, 4, 6)] +
+         [("linear_loss_part.hip", f"linear_loss_{et}_{c}",
+           [f"-DMIGEMM_PART_E={e}", f"-DMIGEMM_PART_C={c}"])
+          for et, e, n in (("f32", "float", 2), ("f16", "_Float16", 4), ("bf16", "bf16_t", 4))
+          for c in range(n)])
 # Units that take longest, started first (measured compile times, seconds).
 SLOW_FIRST = ("mfma16_f16_gen_14", "mfma16_bf16_gen_14", "mfma_i8_4", "mfma16_f16_gen_4",
               "mfma16_f16_gen_15", "mfma16_f16_gen_1", "mfma16_bf16_gen_15",

@@ -1,0 +1,395 @@
+// linear_loss.hip -- the row kernels of the output-layer losses
+// (linear_loss.hpp): joining the forward statistics, the logits that a loss
+// names, the losses; and the backward pass's row data, its scattered entries and
+// its conversions.
+#include "linear_loss.hpp"
+
+namespace migemm {
+namespace {
+
+constexpr int kThreads = 256, kRowWaves = kThreads / kWave;
+constexpr int kMaxTop = 1024;
+
+// Joins two pairs (largest, sum) of base-2 statistics.  An empty pair has sum 0.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+    if (s2 == 0.0f) return;
+    if (s == 0.0f) {
+        m = m2;
+        s = s2;
+        return;
+    }
+    const float hi = fmaxf(m, m2);
+    // equal maxima (infinite ones too) keep their sums as they are
+    s = s * (m == hi ? 1.0f : exp2_of(m - hi)) + s2 * (m2 == hi ? 1.0f : exp2_of(m2 - hi));
+    m = hi;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// The dot product of two rows of `depth` elements (whole 16-byte chunks), over a
+// wavefront, in FP32.
+template <typename E>
+__device__ __forceinline__ float row_dot(const E* __restrict__ x, const E* __restrict__ w,
+                                         int64_t depth, int lane) {
+    constexpr int EPC = 16 / sizeof(E);
+    float s = 0.0f;
+    for (int64_t c = static_cast<int64_t>(lane) * EPC; c < depth; c += kWave * EPC) {
+        const u32x4 xr = *reinterpret_cast<const u32x4*>(x + c);
+        const u32x4 wr = *reinterpret_cast<const u32x4*>(w + c);
+        E xe[EPC], we[EPC];
+        __builtin_memcpy(xe, &xr, 16);
+        __builtin_memcpy(we, &wr, 16);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) s = fmaf(to_f32(xe[e]), to_f32(we[e]), s);
+    }
+    return wave_sum(s);
+}
+
+// Teacher logit j of a row, in the teacher's type.
+__device__ __forceinline__ float teacher_logit(const LossArgs& a, int64_t row, int64_t j) {
+    const int64_t i = row * a.ldt + j;
+    if (a.t_dtype == 0) return static_cast<const float*>(a.t_logits)[i];
+    if (a.t_dtype == 1) return to_f32(static_cast<const _Float16*>(a.t_logits)[i]);
+    return to_f32(static_cast<const bf16_t*>(a.t_logits)[i]);
+}
+
+// The teacher's distribution over a row's held entries (index >= 0), by one
+// wavefront: p_j = 2^(scale (t_j - largest)) / sum.  held: a held entry with a
+// logit above -infinity exists; bad: an index at or past V.
+struct Teacher {
+    float largest, sum;
+    bool held, bad;
+};
+__device__ __forceinline__ Teacher teacher_row(const LossArgs& a, int64_t row, int lane) {
+    const float scale = kLog2e / a.tau;
+    Teacher t{-INFINITY, 0.0f, false, false};
+    int bad = 0, nan = 0;
+    for (int64_t j = lane; j < a.top; j += kWave) {
+        const int64_t v = a.t_index[row * a.ldi + j];
+        if (v < 0) continue;
+        if (v >= a.V) bad = 1;
+        const float x = teacher_logit(a, row, j);
+        if (x != x) nan = 1;
+        t.largest = fmaxf(t.largest, x);
+    }
+    t.largest = wave_max(t.largest);
+    t.bad = __any(bad);
+    // a NaN beside nothing else must not look like an empty row
+    t.held = t.largest > -INFINITY || __any(nan);
+    float s = 0.0f;
+    for (int64_t j = lane; j < a.top; j += kWave)
+        if (a.t_index[row * a.ldi + j] >= 0)
+            s += exp2_of(scale * (teacher_logit(a, row, j) - t.largest));
+    t.sum = wave_sum(s);
+    return t;
+}
+
+// One workgroup per row: its log-sum-exp from the chunks' statistics, the logits
+// at its target or at the teacher's indices, and its loss.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E* __restrict__ X,
+                                                             int64_t ldx, const E* __restrict__ W,
+                                                             int64_t ldw, int64_t depth,
+                                                             const RowStat* __restrict__ part,
+                                                             int64_t chunks,
+                                                             float* __restrict__ loss,
+                                                             float* __restrict__ lse_out) {
+    __shared__ RowStat stat[kRowWaves];
+    __shared__ float logit[kMaxTop];
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    float m = -INFINITY, s = 0.0f;
+    for (int64_t c = threadIdx.x; c < chunks; c += kThreads) {
+        const RowStat r = part[row * chunks + c];
+        join(m, s, r.largest, r.sum);
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+        const float m2 = __shfl_xor(m, d), s2 = __shfl_xor(s, d);
+        join(m, s, m2, s2);
+    }
+    if (lane == 0) stat[wave] = RowStat{m, s};
+    const E* const x = X + row * ldx;
+    if (a.top == 0) {
+        const int64_t y = a.target[row];
+        if (wave == 0 && y >= 0 && y < a.V && y != a.ignore) {
+            const float z = row_dot(x, W + y * ldw, depth, lane);
+            if (lane == 0) logit[0] = z;
+        }
+    } else {
+        for (int64_t j = wave; j < a.top; j += kRowWaves) {
+            const int64_t v = a.t_index[row * a.ldi + j];
+            const float z = v >= 0 && v < a.V ? row_dot(x, W + v * ldw, depth, lane) : 0.0f;
+            if (lane == 0) {
+                logit[j] = z;
+                a.student[row * a.lds + j] = z;
+            }
+        }
+    }
+    __syncthreads();
+    if (wave != 0) return;
+    m = stat[0].largest;
+    s = stat[0].sum;
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w) join(m, s, stat[w].largest, stat[w].sum);
+    const float lse = (m + log2f(s)) * kLn2;
+    float out = 0.0f;
+    if (a.top == 0) {
+        const int64_t y = a.target[row];
+        if (y != a.ignore) out = y >= 0 && y < a.V ? lse - logit[0] : NAN;
+    } else {
+        const Teacher t = teacher_row(a, row, lane);
+        if (t.held) {
+            const float log_sum = log2f(t.sum) * kLn2, inv = 1.0f / a.tau;
+            float terms = 0.0f;
+            for (int64_t j = lane; j < a.top; j += kWave) {
+                if (a.t_index[row * a.ldi + j] < 0) continue;
+                const float log_p = (teacher_logit(a, row, j) - t.largest) * inv - log_sum;
+                const float p = exp2_of(log_p * kLog2e);
+                // no weight, no term: log p may be -infinity there
+                if (p != 0.0f) terms = fmaf(p, log_p - logit[j] * inv + lse, terms);
+            }
+            out = a.tau * a.tau * wave_sum(terms);
+        }
+        if (t.bad) out = NAN;
+    }
+    if (lane == 0) {
+        loss[row] = out;
+        lse_out[row] = lse;
+    }
+}
+
+// Row data of the backward pass, and X's row into the padded copy.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void loss_prepare_kernel(
+    LossArgs a, const float* __restrict__ lse, const float* __restrict__ grad,
+    LossRow* __restrict__ info, E* __restrict__ copy, int64_t rows, int64_t ldc,
+    float* __restrict__ tp, bool vec) {
+    constexpr int EPC = 16 / sizeof(E);
+    __shared__ float shared_coef;
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x % kWave;
+    if (threadIdx.x < kWave) {
+        LossRow r{0.0f, 0.0f, -1, 0.0f};
+        if (row < a.T) {
+            r.lse2 = lse[row] * kLog2e;
+            if (a.top == 0) {
+                const int64_t y = a.target[row];
+                if (y != a.ignore) {
+                    const bool known = y >= 0 && y < a.V;
+                    r.coef = known ? grad[row] : NAN;
+                    r.target = known ? static_cast<int32_t>(y) : -1;
+                }
+            } else {
+                const Teacher t = teacher_row(a, row, lane);
+                if (t.held) r.coef = a.tau * grad[row];
+                if (t.bad) r.coef = NAN;
+                const float scale = kLog2e / a.tau;
+                for (int64_t j = lane; j < a.top; j += kWave) {
+                    float p = 0.0f;
+                    if (r.coef != 0.0f && a.t_index[row * a.ldi + j] >= 0)
+                        p = exp2_of(scale * (teacher_logit(a, row, j) - t.largest)) / t.sum;
+                    tp[row * a.top + j] = r.coef * p;
+                }
+            }
+        }
+        if (lane == 0) {
+            info[row] = r;
+            shared_coef = r.coef;
+        }
+    }
+    __syncthreads();
+    if (row >= rows) return;
+    const bool live = row < a.T && shared_coef != 0.0f;
+    const E* const x = static_cast<const E*>(a.X) + row * a.ldx;
+    for (int64_t c = static_cast<int64_t>(threadIdx.x) * EPC; c < ldc; c += kThreads * EPC) {
+        u32x4 w = {0u, 0u, 0u, 0u};
+        if (live && vec && c + EPC <= a.D) {
+            w = *reinterpret_cast<const u32x4*>(x + c);
+        } else if (live) {
+            E v[EPC];
+            __builtin_memcpy(v, &w, 16);
+#pragma unroll
+            for (int e = 0; e < EPC; ++e)
+                if (c + e < a.D) v[e] = x[c + e];
+            __builtin_memcpy(&w, v, 16);
+        }
+        *reinterpret_cast<u32x4*>(copy + row * ldc + c) = w;
+    }
+}
+
+// One workgroup.  Non-finite coefficients do not count.
+__global__ __launch_bounds__(1024) void loss_factor_kernel(const LossRow* __restrict__ info,
+                                                           int64_t rows,
+                                                           float* __restrict__ factor) {
+    __shared__ float part[16];
+    float m = 0.0f;
+    for (int64_t i = threadIdx.x; i < rows; i += 1024) {
+        const float c = fabsf(info[i].coef);
+        if (c < INFINITY) m = fmaxf(m, c);
+    }
+    m = wave_max(m);
+    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = m;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < 16; ++w) m = fmaxf(m, part[w]);
+    // exponent of m: m in [2^e, 2^(e+1)); factor 2^(13 - e), within +-100
+    int e = m > 0.0f ? ilogbf(m) : 13;
+    e = min(max(13 - e, -100), 100);
+    factor[0] = ldexpf(1.0f, e);
+    factor[1] = ldexpf(1.0f, -e);
+}
+
+// A wavefront per row: dz at the indices inside [v0, v1).  An index that a row
+// names more than once gets the sum of its weights, written by each of them.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void loss_scatter_kernel(
+    LossArgs a, const LossRow* __restrict__ info, const float* __restrict__ tp,
+    const float* __restrict__ factor, E* __restrict__ dz, int64_t ldz, int64_t v0, int64_t v1) {
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWaves + threadIdx.x / kWave;
+    const int lane = threadIdx.x % kWave;
+    if (row >= a.T) return;
+    const LossRow r = info[row];
+    if (r.coef == 0.0f) return;  // the whole row is 0 already
+    const float f = factor ? *factor : 1.0f, scale = kLog2e / a.tau;
+    const int64_t* const index = a.t_index + row * a.ldi;
+    for (int64_t j = lane; j < a.top; j += kWave) {
+        const int64_t v = index[j];
+        if (v < v0 || v >= v1) continue;
+        float weight = 0.0f;
+        for (int64_t i = 0; i < a.top; ++i)
+            if (index[i] == v) weight += tp[row * a.top + i];
+        const float q = exp2_of(fmaf(a.student[row * a.lds + j], scale, -r.lse2));
+        dz[row * ldz + (v - v0)] = narrow<E>((r.coef * q - weight) * f);
+    }
+}
+
+// 16 bytes of dst per lane.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void pad_copy_kernel(int64_t rows, int64_t cols,
+                                                            const E* __restrict__ src, int64_t lds,
+                                                            E* __restrict__ dst, int64_t pieces,
+                                                            int64_t ldd) {
+    constexpr int EPC = 16 / sizeof(E);
+    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < pieces;
+         p += static_cast<int64_t>(gridDim.x) * kThreads) {
+        const int64_t r = p / (ldd / EPC), c = p % (ldd / EPC) * EPC;
+        E v[EPC];
+        u32x4 w = {0u, 0u, 0u, 0u};
+        __builtin_memcpy(v, &w, 16);
+        if (r < rows) {
+#pragma unroll
+            for (int e = 0; e < EPC; ++e)
+                if (c + e < cols) v[e] = src[r * lds + c + e];
+        }
+        __builtin_memcpy(&w, v, 16);
+        *reinterpret_cast<u32x4*>(dst + r * ldd + c) = w;
+    }
+}
+
+// Four columns per lane; src rows 16-byte aligned.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void scaled_convert_kernel(
+    int64_t rows, int64_t cols, const float* __restrict__ src, int64_t lds,
+    const float* __restrict__ factor, E* __restrict__ dst, int64_t ldd) {
+    const float f = factor ? *factor : 1.0f;
+    const int64_t per = ceil_div(cols, 4), pieces = rows * per;
+    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < pieces;
+         p += static_cast<int64_t>(gridDim.x) * kThreads) {
+        const int64_t r = p / per, c = p % per * 4;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(src + r * lds + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < cols) dst[r * ldd + c + e] = narrow<E>(v[e] * f);
+    }
+}
+
+unsigned grid_for(int64_t items) {
+    const int64_t g = ceil_div(items, kThreads);
+    return static_cast<unsigned>(g < 16384 ? g : 16384);
+}
+
+template <typename F>
+hipError_t by_type(int dtype, F f) {
+    if (dtype == 0) return f(float{});
+    if (dtype == 1) return f(_Float16{});
+    return f(bf16_t{});
+}
+
+}  // namespace
+
+hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const void* W,
+                            int64_t ldw, int64_t depth, const RowStat* part, int64_t chunks,
+                            float* loss, float* lse) {
+    return by_type(a.dtype, [&](auto tag) {
+        using E = decltype(tag);
+        loss_rows_kernel<E><<<dim3(static_cast<unsigned>(a.T)), dim3(kThreads), 0, a.stream>>>(
+            a, static_cast<const E*>(X), ldx, static_cast<const E*>(W), ldw, depth, part, chunks,
+            loss, lse);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_loss_prepare(const LossArgs& a, const float* lse, const float* grad,
+                               LossRow* info, int64_t rows_info, void* copy, int64_t rows,
+                               int64_t ldc, float* tp) {
+    return by_type(a.dtype, [&](auto tag) {
+        using E = decltype(tag);
+        const bool vec = aligned16(a.X) && (a.ldx * static_cast<int64_t>(sizeof(E))) % 16 == 0;
+        loss_prepare_kernel<E>
+            <<<dim3(static_cast<unsigned>(rows_info)), dim3(kThreads), 0, a.stream>>>(
+                a, lse, grad, info, static_cast<E*>(copy), rows, ldc, tp, vec);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_loss_factor(const LossRow* info, int64_t rows, float* factor, hipStream_t s) {
+    loss_factor_kernel<<<dim3(1), dim3(1024), 0, s>>>(info, rows, factor);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_scatter(const LossArgs& a, const LossRow* info, const float* tp,
+                               const float* factor, void* dz, int64_t ldz, int64_t v0,
+                               int64_t v1) {
+    return by_type(a.dtype, [&](auto tag) {
+        using E = decltype(tag);
+        const unsigned grid = static_cast<unsigned>(ceil_div(a.T, kRowWaves));
+        loss_scatter_kernel<E><<<dim3(grid), dim3(kThreads), 0, a.stream>>>(
+            a, info, tp, factor, static_cast<E*>(dz), ldz, v0, v1);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_pad_copy(int dtype, int64_t rows, int64_t cols, const void* src, int64_t lds,
+                           void* dst, int64_t rows_out, int64_t ldd, hipStream_t s) {
+    return by_type(dtype, [&](auto tag) {
+        using E = decltype(tag);
+        const int64_t pieces = rows_out * (ldd * static_cast<int64_t>(sizeof(E)) / 16);
+        pad_copy_kernel<E><<<dim3(grid_for(pieces)), dim3(kThreads), 0, s>>>(
+            rows, cols, static_cast<const E*>(src), lds, static_cast<E*>(dst), pieces, ldd);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_scaled_convert(int dtype, int64_t rows, int64_t cols, const float* src,
+                                 int64_t lds, const float* factor, void* dst, int64_t ldd,
+                                 hipStream_t s) {
+    return by_type(dtype, [&](auto tag) {
+        using E = decltype(tag);
+        scaled_convert_kernel<E>
+            <<<dim3(grid_for(rows * ceil_div(cols, 4))), dim3(kThreads), 0, s>>>(
+                rows, cols, src, lds, factor, static_cast<E*>(dst), ldd);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace migemm

@@ -1,0 +1,472 @@
+// linear_loss_api.cpp -- the output-layer losses' entry points: argument checks,
+// the plan of a call (what is copied, the pieces of the vocabulary, where each
+// scratch array lies in the lent workspace) and its launches.
+#include <math.h>
+
+#include "linear_loss.hpp"
+#include "migemm.h"
+
+namespace migemm {
+
+// 256x256 tiles from half a round of them on, else 128x128 from half a round,
+// else 64x64; the ping-pong schedule where every tile and k-tile is whole.
+LossShape loss_shape(int dtype, int64_t M, int64_t N, int64_t K) {
+    auto tiles = [&](int64_t b) { return ceil_div(M, b) * ceil_div(N, b); };
+    const bool f32 = dtype == MIGEMM_F32;
+    if (!f32 && M > 128 && tiles(256) >= 128)
+        return {M % 256 == 0 && N % 256 == 0 && K % 64 == 0 ? 3 : 2, 64, 256};
+    if (M > 64 && tiles(128) >= 128) return {1, 32, 128};
+    return {0, 16, 64};
+}
+
+hipError_t launch_loss(const LossTile& t, int config) {
+    if (t.dtype == MIGEMM_F32)
+        return config == 1 ? launch_loss_tile<float, 1>(t) : launch_loss_tile<float, 0>(t);
+#define MIGEMM_LOSS(E)                                        \
+    switch (config) {                                         \
+        case 0: return launch_loss_tile<E, 0>(t);             \
+        case 1: return launch_loss_tile<E, 1>(t);             \
+        case 2: return launch_loss_tile<E, 2>(t);             \
+        default: return launch_loss_tile<E, 3>(t);            \
+    }
+    if (t.dtype == MIGEMM_F16) {
+        MIGEMM_LOSS(_Float16)
+    }
+    MIGEMM_LOSS(bf16_t)
+#undef MIGEMM_LOSS
+}
+
+namespace {
+
+constexpr int64_t kMaxTop = 1024;
+// Entries of dz in one piece of the vocabulary: 2^28, 512 MiB in 16 bits.
+constexpr int64_t kPieceEntries = int64_t(1) << 28;
+
+int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
+
+// What one call copies and where its scratch arrays lie (byte offsets into the
+// workspace, 256-byte aligned).
+struct Plan {
+    bool copy_x = false, copy_w = false, wide = false;
+    int64_t depth = 0;   // k of the logits' product
+    int64_t ld_copy = 0; // leading dimension of copies
+    int64_t bytes = 0;
+    int64_t x = 0, w = 0;
+    // forward
+    int64_t part = 0, chunks = 0;
+    // backward
+    int64_t t_pad = 0, piece = 0, pieces = 0, ldz = 0, cols = 0;
+    bool dx_acc = false, dw_acc = false, tail_w = false;
+    int64_t info = 0, factor = 0, dz = 0, acc_x = 0, acc_w = 0, tail = 0, tp = 0, gemm = 0,
+            gemm_bytes = 0;
+    int64_t take(int64_t n) {
+        const int64_t at = bytes;
+        bytes += round_up(n, 256);
+        return at;
+    }
+};
+
+// Rows that the direct kernels read in place: 16-byte aligned, in whole chunks,
+// within their offset limit.
+bool rows_ok(const void* p, int64_t ld, int64_t epc) {
+    return aligned16(p) && ld % epc == 0 && ld < (int64_t(1) << 21);
+}
+
+Plan make_plan(const LossArgs& a, bool backward) {
+    Plan p;
+    const int64_t es = elem_size(a.dtype), epc = 16 / es;
+    const bool whole = a.D % epc == 0;
+    p.ld_copy = round_up(a.D, 64);
+    p.copy_w = !whole || !rows_ok(a.W, a.ldw, epc);
+    // the backward pass always copies x: its rows without a loss become 0, so
+    // that whatever they hold (NaN from a masked position) stays out of dw
+    p.copy_x = backward || !whole || !rows_ok(a.X, a.ldx, epc);
+    p.depth = p.copy_w && p.copy_x ? p.ld_copy : a.D;
+    if (p.copy_w) p.w = p.take(round_up(a.V, 64) * p.ld_copy * es);
+    if (!backward) {
+        if (p.copy_x) p.x = p.take(a.T * p.ld_copy * es);
+        const LossShape s = loss_shape(a.dtype, a.T, a.V, p.depth);
+        p.chunks = ceil_div(a.V, s.bn) * (s.bn / s.chunk);
+        p.part = p.take(a.T * p.chunks * static_cast<int64_t>(sizeof(RowStat)));
+        return p;
+    }
+    p.t_pad = round_up(a.T, 64);
+    p.x = p.take(p.t_pad * p.ld_copy * es);
+    const int64_t fit = kPieceEntries / p.t_pad / 256 * 256;
+    p.piece = fit < 2048 ? 2048 : fit;
+    if (p.piece > a.V) p.piece = a.V;
+    p.pieces = ceil_div(a.V, p.piece);
+    p.ldz = round_up(p.piece, 64);
+    // FP16 gradients go through FP32 with the factor that keeps dz normal taken
+    // out again, and rows that end inside a chunk through FP32 rows of whole ones
+    p.wide = a.dtype == MIGEMM_F16 || !whole;
+    p.cols = whole ? a.D : p.ld_copy;
+    p.dw_acc = p.wide;
+    p.dx_acc = p.wide || (a.dtype != MIGEMM_F32 && p.pieces > 1);
+    p.tail_w = !p.copy_w && a.V % epc != 0;
+    p.info = p.take(round_up(a.T, 256) * static_cast<int64_t>(sizeof(LossRow)));
+    p.factor = p.take(256);
+    p.dz = p.take(p.t_pad * p.ldz * es);
+    if (p.dx_acc) p.acc_x = p.take(a.T * p.cols * 4);
+    if (p.dw_acc) p.acc_w = p.take(p.piece * p.cols * 4);
+    const int64_t last = a.V - (p.pieces - 1) * p.piece;
+    if (p.tail_w) p.tail = p.take(round_up(last, 64) * p.ld_copy * es);
+    if (a.top) p.tp = p.take(a.T * a.top * 4);
+    // what the two products ask for, for a full piece and the last one (their
+    // operands are aligned; NULL stands for that)
+    for (int64_t n : {p.piece, last}) {
+        int64_t b = 0;
+        const int64_t k = n % epc == 0 ? n : round_up(n, 64);
+        if (workspace_bytes(-1, -1, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, k, a.dtype, nullptr,
+                            p.ldz, nullptr, p.copy_w || k != n ? p.ld_copy : a.ldw, &b) ==
+                MIGEMM_OK &&
+            b > p.gemm_bytes)
+            p.gemm_bytes = b;
+        const int64_t m = n / epc * epc;
+        if (m > 0 && workspace_bytes(-1, -1, MIGEMM_OP_T, MIGEMM_OP_N, m, p.cols, p.t_pad, a.dtype,
+                                     nullptr, p.ldz, nullptr, p.ld_copy, &b) == MIGEMM_OK &&
+            b > p.gemm_bytes)
+            p.gemm_bytes = b;
+    }
+    p.gemm = p.take(p.gemm_bytes);
+    return p;
+}
+
+char* at(void* ws, int64_t offset) { return static_cast<char*>(ws) + offset; }
+
+// X or W as the products read them: in place, or the copy made here.
+hipError_t operand(const LossArgs& a, bool copy, const void* src, int64_t lds, int64_t rows,
+                   int64_t rows_out, const Plan& p, void* to, const void** out, int64_t* ld) {
+    *out = copy ? to : src;
+    *ld = copy ? p.ld_copy : lds;
+    if (!copy) return hipSuccess;
+    return launch_pad_copy(a.dtype, rows, a.D, src, lds, to, rows_out, p.ld_copy, a.stream);
+}
+
+int forward(const LossArgs& a, float* loss, float* lse, void* ws) {
+    const Plan p = make_plan(a, false);
+    const void *x, *w;
+    int64_t ldx, ldw;
+    int st = hip_status(operand(a, p.copy_x, a.X, a.ldx, a.T, a.T, p, at(ws, p.x), &x, &ldx));
+    if (st != MIGEMM_OK) return st;
+    st = hip_status(operand(a, p.copy_w, a.W, a.ldw, a.V, round_up(a.V, 64), p, at(ws, p.w), &w,
+                            &ldw));
+    if (st != MIGEMM_OK) return st;
+    LseOut out{};
+    out.part = reinterpret_cast<RowStat*>(at(ws, p.part));
+    out.chunks = p.chunks;
+    out.scale = kLog2e / a.tau;
+    const LossTile t{a.T, a.V, p.depth, a.dtype, x, ldx, w, ldw, a.stream, &out, nullptr};
+    st = hip_status(launch_loss(t, loss_shape(a.dtype, a.T, a.V, p.depth).config));
+    if (st != MIGEMM_OK) return st;
+    return hip_status(
+        launch_loss_rows(a, x, ldx, w, ldw, p.depth, out.part, p.chunks, loss, lse));
+}
+
+template <typename E>
+hipError_t launch_dz(const LossArgs& a, const Plan& p, const void* x, const void* w, int64_t ldw,
+                     int64_t v0, int64_t n, void* ws, const float* factor) {
+    DzOut<E> out{};
+    out.dz = reinterpret_cast<E*>(at(ws, p.dz));
+    out.ldz = round_up(n, 64);
+    out.rows = p.t_pad;
+    out.v0 = v0;
+    out.info = reinterpret_cast<const LossRow*>(at(ws, p.info));
+    out.factor = factor;
+    out.scale = kLog2e / a.tau;
+    const LossTile t{a.T, n, p.depth, a.dtype, x, p.ld_copy, w, ldw, a.stream, nullptr, &out};
+    return launch_loss(t, loss_shape(a.dtype, a.T, n, p.depth).config);
+}
+
+int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, int64_t lddx,
+             void* dw, int64_t lddw, void* ws) {
+    const Plan p = make_plan(a, true);
+    const int64_t es = elem_size(a.dtype), epc = 16 / es;
+    LossRow* const info = reinterpret_cast<LossRow*>(at(ws, p.info));
+    float* const tp = a.top ? reinterpret_cast<float*>(at(ws, p.tp)) : nullptr;
+    void* const x = at(ws, p.x);
+    void* const dz = at(ws, p.dz);
+    void* const gws = p.gemm_bytes ? at(ws, p.gemm) : nullptr;
+    const void* w;
+    int64_t ldw;
+#define MIGEMM_TRY(call)                                       \
+    do {                                                       \
+        const int st_ = (call);                                \
+        if (st_ != MIGEMM_OK) return st_;                      \
+    } while (0)
+    MIGEMM_TRY(hip_status(operand(a, p.copy_w, a.W, a.ldw, a.V, round_up(a.V, 64), p, at(ws, p.w),
+                                  &w, &ldw)));
+    MIGEMM_TRY(hip_status(launch_loss_prepare(a, lse, grad, info, round_up(a.T, 256), x, p.t_pad,
+                                              p.ld_copy, tp)));
+    float* factor = nullptr;
+    if (a.dtype == MIGEMM_F16) {
+        factor = reinterpret_cast<float*>(at(ws, p.factor));
+        MIGEMM_TRY(hip_status(launch_loss_factor(info, a.T, factor, a.stream)));
+    }
+    const float* const inverse = factor ? factor + 1 : nullptr;
+    for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
+        const int64_t n = a.V - v0 < p.piece ? a.V - v0 : p.piece, ldz = round_up(n, 64);
+        const char* const wp = static_cast<const char*>(w) + v0 * ldw * es;
+        hipError_t e;
+        if (a.dtype == MIGEMM_F32)
+            e = launch_dz<float>(a, p, x, wp, ldw, v0, n, ws, factor);
+        else if (a.dtype == MIGEMM_F16)
+            e = launch_dz<_Float16>(a, p, x, wp, ldw, v0, n, ws, factor);
+        else
+            e = launch_dz<bf16_t>(a, p, x, wp, ldw, v0, n, ws, factor);
+        MIGEMM_TRY(hip_status(e));
+        if (a.top)
+            MIGEMM_TRY(
+                hip_status(launch_loss_scatter(a, info, tp, factor, dz, ldz, v0, v0 + n)));
+        if (dx) {
+            // k: the piece's columns, in whole chunks; past them dz is 0, and the
+            // rows of w read there must exist and be finite: the copies' zeros
+            const void* wk = wp;
+            int64_t ldk = ldw, k = n;
+            if (n % epc != 0) {
+                k = ldz;
+                if (p.tail_w) {
+                    wk = at(ws, p.tail);
+                    ldk = p.ld_copy;
+                    MIGEMM_TRY(hip_status(launch_pad_copy(a.dtype, n, a.D, wp, ldw,
+                                                          at(ws, p.tail), ldz, ldk, a.stream)));
+                }
+            }
+            void* const c = p.dx_acc ? at(ws, p.acc_x) : dx;
+            const int ct = p.dx_acc ? MIGEMM_F32 : a.dtype;
+            MIGEMM_TRY(run_gemm(-1, -1, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, k, a.dtype, dz, ldz,
+                                wk, ldk, 1.0f, v0 ? 1.0f : 0.0f, ct, c, p.dx_acc ? p.cols : lddx,
+                                gws, p.gemm_bytes, a.stream));
+        }
+        if (dw) {
+            char* const to = static_cast<char*>(dw) + v0 * lddw * es;
+            char* const c = p.dw_acc ? at(ws, p.acc_w) : to;
+            const int ct = p.dw_acc ? MIGEMM_F32 : a.dtype;
+            const int64_t ldc = p.dw_acc ? p.cols : lddw, m = n / epc * epc;
+            if (m > 0)
+                MIGEMM_TRY(run_gemm(-1, -1, MIGEMM_OP_T, MIGEMM_OP_N, m, p.cols, p.t_pad, a.dtype,
+                                    dz, ldz, x, p.ld_copy, 1.0f, 0.0f, ct, c, ldc, gws,
+                                    p.gemm_bytes, a.stream));
+            if (m < n) {
+                // the last rows, fewer than a chunk
+                GemmArgs g{n - m, p.cols, p.t_pad, a.dtype, true, false,
+                           static_cast<const char*>(dz) + m * es, ldz, x, p.ld_copy,
+                           Epi{c + m * ldc * elem_size(ct), ldc, 1.0f, 0.0f, ct}, a.stream};
+                MIGEMM_TRY(hip_status(launch_skinny(g)));
+            }
+            if (p.dw_acc)
+                MIGEMM_TRY(hip_status(launch_scaled_convert(a.dtype, n, a.D,
+                                                            reinterpret_cast<float*>(c), p.cols,
+                                                            inverse, to, lddw, a.stream)));
+        }
+    }
+    if (dx && p.dx_acc)
+        MIGEMM_TRY(hip_status(launch_scaled_convert(a.dtype, a.T, a.D,
+                                                    reinterpret_cast<float*>(at(ws, p.acc_x)),
+                                                    p.cols, inverse, dx, lddx, a.stream)));
+#undef MIGEMM_TRY
+    return MIGEMM_OK;
+}
+
+bool ld_ok(int64_t ld, int64_t cols) { return ld >= (cols > 1 ? cols : 1) && ld < kMaxLd; }
+
+// Sizes and leading dimensions that both passes share.
+bool shape_ok(const LossArgs& a, bool kd) {
+    if (!known_dtype(a.dtype) || a.T < 0 || a.V < 1 || a.D < 1 || a.T > kMaxDim || a.V > kMaxDim ||
+        a.D > kMaxDim || !ld_ok(a.ldx, a.D) || !ld_ok(a.ldw, a.D))
+        return false;
+    // copies and the products' offsets: rows of fewer than 2^21 - 64 elements
+    if (a.D > (int64_t(1) << 21) - 64) return false;
+    return !kd || (a.top >= 1 && a.top <= kMaxTop);
+}
+
+bool kd_ok(const LossArgs& a) {
+    return known_dtype(a.t_dtype) && ld_ok(a.ldt, a.top) && ld_ok(a.ldi, a.top) &&
+           ld_ok(a.lds, a.top) && a.tau > 0.0f && a.tau < INFINITY;
+}
+
+struct Range {
+    uintptr_t lo, hi;
+};
+
+// Adds the range of a rows x cols array; false for NULL or one past the address space.
+bool add(Range* list, int& count, const void* p, int64_t rows, int64_t cols, int64_t ld, int es) {
+    Range r;
+    if (!p || !extent(p, rows, cols, ld, es, r.lo, r.hi)) return false;
+    list[count++] = r;
+    return true;
+}
+
+// No output meets an input or another output.
+bool disjoint(const Range* in, int n_in, const Range* out, int n_out) {
+    for (int i = 0; i < n_out; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlaps(out[i].lo, out[i].hi, in[j].lo, in[j].hi)) return false;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i].lo, out[i].hi, out[j].lo, out[j].hi)) return false;
+    }
+    return true;
+}
+
+int check_workspace(const Plan& p, const void* ws, int64_t ws_bytes) {
+    if (ws_bytes < 0) return MIGEMM_ERR_INVALID_ARG;
+    if (p.bytes == 0) return MIGEMM_OK;
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % kWorkspaceAlign != 0 || ws_bytes < p.bytes)
+        return MIGEMM_ERR_WORKSPACE;
+    return MIGEMM_OK;
+}
+
+// The inputs of a pass (T >= 1): x, w and what names the targets.
+bool add_inputs(const LossArgs& a, Range* in, int& n) {
+    const int es = elem_size(a.dtype);
+    if (!add(in, n, a.X, a.T, a.D, a.ldx, es) || !add(in, n, a.W, a.V, a.D, a.ldw, es))
+        return false;
+    if (a.top == 0) return add(in, n, a.target, 1, a.T, a.T, 8);
+    return add(in, n, a.t_logits, a.T, a.top, a.ldt, elem_size(a.t_dtype)) &&
+           add(in, n, a.t_index, a.T, a.top, a.ldi, 8);
+}
+
+int run_forward(const LossArgs& a, float* loss, float* lse, void* ws, int64_t ws_bytes) {
+    if (a.T == 0) return ws_bytes < 0 ? MIGEMM_ERR_INVALID_ARG : MIGEMM_OK;
+    Range in[8], out[8];
+    int n_in = 0, n_out = 0;
+    if (!add_inputs(a, in, n_in) || !add(out, n_out, loss, 1, a.T, a.T, 4) ||
+        !add(out, n_out, lse, 1, a.T, a.T, 4))
+        return MIGEMM_ERR_INVALID_ARG;
+    if (a.top && !add(out, n_out, a.student, a.T, a.top, a.lds, 4)) return MIGEMM_ERR_INVALID_ARG;
+    const Plan p = make_plan(a, false);
+    const int st = check_workspace(p, ws, ws_bytes);
+    if (st != MIGEMM_OK) return st;
+    if (p.bytes > 0 && !add(out, n_out, ws, 1, p.bytes, p.bytes, 1)) return MIGEMM_ERR_INVALID_ARG;
+    if (!disjoint(in, n_in, out, n_out)) return MIGEMM_ERR_INVALID_ARG;
+    return forward(a, loss, lse, ws);
+}
+
+int run_backward(const LossArgs& a, const float* lse, const float* grad, void* dx, int64_t lddx,
+                 void* dw, int64_t lddw, void* ws, int64_t ws_bytes) {
+    if ((dx && !ld_ok(lddx, a.D)) || (dw && !ld_ok(lddw, a.D)) || ws_bytes < 0)
+        return MIGEMM_ERR_INVALID_ARG;
+    const int es = elem_size(a.dtype);
+    if (a.T == 0) {
+        // no rows: dw = 0
+        if (!dw) return MIGEMM_OK;
+        uintptr_t lo, hi;
+        if (!extent(dw, a.V, a.D, lddw, es, lo, hi)) return MIGEMM_ERR_INVALID_ARG;
+        return run_gemm(-1, -1, MIGEMM_OP_N, MIGEMM_OP_N, a.V, a.D, 0, a.dtype, nullptr, 1,
+                        nullptr, a.D, 1.0f, 0.0f, a.dtype, dw, lddw, nullptr, 0, a.stream);
+    }
+    Range in[8], out[8];
+    int n_in = 0, n_out = 0;
+    if (!add_inputs(a, in, n_in) || !add(in, n_in, lse, 1, a.T, a.T, 4) ||
+        !add(in, n_in, grad, 1, a.T, a.T, 4))
+        return MIGEMM_ERR_INVALID_ARG;
+    if (a.top && !add(in, n_in, a.student, a.T, a.top, a.lds, 4)) return MIGEMM_ERR_INVALID_ARG;
+    if (dx && !add(out, n_out, dx, a.T, a.D, lddx, es)) return MIGEMM_ERR_INVALID_ARG;
+    if (dw && !add(out, n_out, dw, a.V, a.D, lddw, es)) return MIGEMM_ERR_INVALID_ARG;
+    const Plan p = make_plan(a, true);
+    const int st = check_workspace(p, ws, ws_bytes);
+    if (st != MIGEMM_OK) return st;
+    if (!add(out, n_out, ws, 1, p.bytes, p.bytes, 1)) return MIGEMM_ERR_INVALID_ARG;
+    if (!disjoint(in, n_in, out, n_out)) return MIGEMM_ERR_INVALID_ARG;
+    if (!dx && !dw) return MIGEMM_OK;
+    return backward(a, lse, grad, dx, lddx, dw, lddw, ws);
+}
+
+LossArgs layer(int64_t T, int64_t V, int64_t D, int dtype, const void* X, int64_t ldx,
+               const void* W, int64_t ldw, void* stream) {
+    LossArgs a{};
+    a.T = T;
+    a.V = V;
+    a.D = D;
+    a.dtype = dtype;
+    a.X = X;
+    a.ldx = ldx;
+    a.W = W;
+    a.ldw = ldw;
+    a.tau = 1.0f;
+    a.stream = static_cast<hipStream_t>(stream);
+    return a;
+}
+
+}  // namespace
+}  // namespace migemm
+
+using namespace migemm;
+
+extern "C" {
+
+int migemm_linear_loss_workspace_size(int backward, int64_t T, int64_t V, int64_t D, int64_t top,
+                                      int dtype, const void* X, int64_t ldx, const void* W,
+                                      int64_t ldw, int64_t* bytes) {
+    LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, nullptr);
+    a.top = top;
+    if (!bytes || !shape_ok(a, top != 0)) return MIGEMM_ERR_INVALID_ARG;
+    *bytes = T == 0 ? 0 : make_plan(a, backward != 0).bytes;
+    return MIGEMM_OK;
+}
+
+int migemm_linear_ce_forward(int64_t T, int64_t V, int64_t D, int dtype, const void* X,
+                             int64_t ldx, const void* W, int64_t ldw, const int64_t* target,
+                             int64_t ignore_index, float* loss, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+    LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, stream);
+    a.target = target;
+    a.ignore = ignore_index;
+    if (!shape_ok(a, false)) return MIGEMM_ERR_INVALID_ARG;
+    return run_forward(a, loss, lse, workspace, workspace_bytes);
+}
+
+int migemm_linear_ce_backward(int64_t T, int64_t V, int64_t D, int dtype, const void* X,
+                              int64_t ldx, const void* W, int64_t ldw, const int64_t* target,
+                              int64_t ignore_index, const float* lse, const float* grad, void* dX,
+                              int64_t lddx, void* dW, int64_t lddw, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+    LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, stream);
+    a.target = target;
+    a.ignore = ignore_index;
+    if (!shape_ok(a, false)) return MIGEMM_ERR_INVALID_ARG;
+    return run_backward(a, lse, grad, dX, lddx, dW, lddw, workspace, workspace_bytes);
+}
+
+int migemm_linear_kd_forward(int64_t T, int64_t V, int64_t D, int64_t top, int dtype,
+                             const void* X, int64_t ldx, const void* W, int64_t ldw,
+                             int teacher_dtype, const void* teacher, int64_t ldt,
+                             const int64_t* index, int64_t ldi, float temperature, float* loss,
+                             float* lse, float* student, int64_t lds, void* workspace,
+                             int64_t workspace_bytes, void* stream) {
+    LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, stream);
+    a.top = top;
+    a.t_dtype = teacher_dtype;
+    a.t_logits = teacher;
+    a.ldt = ldt;
+    a.t_index = index;
+    a.ldi = ldi;
+    a.tau = temperature;
+    a.student = student;
+    a.lds = lds;
+    if (!shape_ok(a, true) || !kd_ok(a)) return MIGEMM_ERR_INVALID_ARG;
+    return run_forward(a, loss, lse, workspace, workspace_bytes);
+}
+
+int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int dtype,
+                              const void* X, int64_t ldx, const void* W, int64_t ldw,
+                              int teacher_dtype, const void* teacher, int64_t ldt,
+                              const int64_t* index, int64_t ldi, float temperature,
+                              const float* lse, const float* student, int64_t lds,
+                              const float* grad, void* dX, int64_t lddx, void* dW, int64_t lddw,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
+    LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, stream);
+    a.top = top;
+    a.t_dtype = teacher_dtype;
+    a.t_logits = teacher;
+    a.ldt = ldt;
+    a.t_index = index;
+    a.ldi = ldi;
+    a.tau = temperature;
+    a.student = const_cast<float*>(student);
+    a.lds = lds;
+    if (!shape_ok(a, true) || !kd_ok(a)) return MIGEMM_ERR_INVALID_ARG;
+    return run_backward(a, lse, grad, dX, lddx, dW, lddw, workspace, workspace_bytes);
+}
+
+}  // extern "C"

@@ -386,6 +386,89 @@ int migemm_gemm_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                    const void* b_scales, int64_t ldbs, float alpha, float beta, int c_dtype,
                    void* C, int64_t ldc, void* stream);
 
+/*
+ * The losses of an output layer, without its logits.
+ *
+ * X (T x D) holds T tokens, W (V x D) the layer's weight, one row per entry of the
+ * vocabulary; both row-major of `dtype` (MIGEMM_F32, MIGEMM_F16, MIGEMM_BF16).
+ * The logits z = X W^T are formed tile by tile and never stored; sums, softmax
+ * statistics and losses are FP32.  The backward passes recompute the logits in
+ * pieces of the vocabulary and write the gradients of X (dX, T x D) and W (dW,
+ * V x D) in `dtype`; either may be NULL.  grad (T floats) is the upstream gradient
+ * of each row's loss: 1 / n for the mean over n rows, 1 for the sum.  The
+ * derivative of the loss to each logit is rounded to `dtype` once, for the
+ * matrix cores; FP16 derivatives are held at a power of two of their size chosen
+ * from the largest grad, so small ones do not vanish.
+ *
+ * Rows.  T may be 0 (losses: a no-op; dW = 0).  A row without a loss (below) has
+ * loss 0, a zero row of dX, and adds nothing to dW, whatever its row of X holds;
+ * so has a row whose grad is 0, except for its loss.  V and D are at least 1, D at
+ * most 2^21 - 64.
+ *
+ * Any alignment and leading dimension: rows off 16-byte boundaries, or D not a
+ * whole number of 16-byte chunks, are first copied into the workspace.  lse (T
+ * floats) is written by a forward pass (the natural log of the sum of exp(z /
+ * temperature)) and read by its backward pass.  The workspace
+ * (migemm_linear_loss_workspace_size bytes for the same arguments, device
+ * memory, 256-byte aligned) is lent for the call as in migemm_gemm_ws; NULL, a
+ * misaligned or a smaller one is MIGEMM_ERR_WORKSPACE.  Outputs and workspace must not
+ * overlap each other or the inputs.  Results do not depend on timing: no atomics.
+ * The pointer, stream, ownership and error rules are migemm_gemm's.
+ */
+
+/*
+ * Bytes of workspace for a forward (backward == 0) or backward pass: top == 0 for
+ * cross entropy, else distillation's entries per row.  Pointers are only inspected
+ * for alignment (NULL: aligned).
+ */
+int migemm_linear_loss_workspace_size(int backward, int64_t T, int64_t V, int64_t D, int64_t top,
+                                      int dtype, const void* X, int64_t ldx, const void* W,
+                                      int64_t ldw, int64_t* bytes);
+
+/*
+ * Softmax cross entropy: loss[t] = lse[t] - z[t][target[t]].
+ * A row whose target is ignore_index has no loss.  Any other target outside 0 .. V
+ * - 1 makes its row's loss and gradients NaN (nothing is read for it).
+ */
+int migemm_linear_ce_forward(int64_t T, int64_t V, int64_t D, int dtype, const void* X,
+                             int64_t ldx, const void* W, int64_t ldw, const int64_t* target,
+                             int64_t ignore_index, float* loss, float* lse, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+int migemm_linear_ce_backward(int64_t T, int64_t V, int64_t D, int dtype, const void* X,
+                              int64_t ldx, const void* W, int64_t ldw, const int64_t* target,
+                              int64_t ignore_index, const float* lse, const float* grad, void* dX,
+                              int64_t lddx, void* dW, int64_t lddw, void* workspace,
+                              int64_t workspace_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits.  Row t of the teacher holds `top` (1
+ * to 1024) logits (teacher_dtype MIGEMM_F32, MIGEMM_F16 or MIGEMM_BF16, leading
+ * dimension ldt) and their vocabulary indices (ldi).  With p the softmax of the
+ * held logits / temperature and q the softmax of z[t] / temperature over the whole
+ * vocabulary,
+ *
+ *     loss[t] = temperature^2 * sum_j p_j (log p_j - log q[index_j])
+ *
+ * A negative index marks an entry that is not held; a row that holds none, or only
+ * logits of -infinity, has no loss.  An index of V or more makes its row's loss and
+ * gradients NaN.  An index named twice counts with the sum of its weights.
+ * student (T x top, leading dimension lds) is written by the forward pass (z at
+ * the indices) and read by the backward pass.  temperature is positive and finite.
+ */
+int migemm_linear_kd_forward(int64_t T, int64_t V, int64_t D, int64_t top, int dtype,
+                             const void* X, int64_t ldx, const void* W, int64_t ldw,
+                             int teacher_dtype, const void* teacher, int64_t ldt,
+                             const int64_t* index, int64_t ldi, float temperature, float* loss,
+                             float* lse, float* student, int64_t lds, void* workspace,
+                             int64_t workspace_bytes, void* stream);
+int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int dtype,
+                              const void* X, int64_t ldx, const void* W, int64_t ldw,
+                              int teacher_dtype, const void* teacher, int64_t ldt,
+                              const int64_t* index, int64_t ldi, float temperature,
+                              const float* lse, const float* student, int64_t lds,
+                              const float* grad, void* dX, int64_t lddx, void* dW, int64_t lddw,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Number of variants (they are numbered 0 .. count-1). */
 int migemm_variant_count(void);
 
