@@ -336,6 +336,7 @@ struct MxArgs {
     int64_t ldsb;
     Epi out;
     hipStream_t stream;
+    bool whole_lines;  // c_whole_lines(out)
 };
 hipError_t launch_gemm_mx(const MxArgs& p);
 

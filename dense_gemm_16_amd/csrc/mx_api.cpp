@@ -96,7 +96,8 @@ int migemm_gemm_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
     MxArgs p{M, N, K,
              static_cast<const uint8_t*>(A), lda, static_cast<const uint8_t*>(a_scales), ldas,
              static_cast<const uint8_t*>(B), ldb, static_cast<const uint8_t*>(b_scales), ldbs,
-             Epi{C, ldc, alpha, beta, c_dtype}, static_cast<hipStream_t>(stream)};
+             Epi{C, ldc, alpha, beta, c_dtype}, static_cast<hipStream_t>(stream), false};
+    p.whole_lines = c_whole_lines(p.out);
     return hip_status(launch_gemm_mx(p));
 }
 

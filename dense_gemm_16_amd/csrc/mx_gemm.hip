@@ -12,83 +12,517 @@
 // to the last one (their outputs are never stored); chunks past K read as zero
 // elements with scale byte 0, so whatever lies in a scale row's padding is
 // not used.
-#include "mfma_gemm.hpp"
+//
+// Two kernels:
+// * mx_tile_kernel: tiles of C through LDS, ping-pong wave groups;
+// * mx_rows_kernel: few rows of A, bound by reading B once.
+#include "mfma16_direct.hpp"
 
 namespace migemm {
 namespace {
 
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
-// c += A B for one 16 x 16 x 128 block: 16 bytes of elements and one scale byte
-// per lane and operand (the low byte of sa and sb).
+// c += A B for one 16 x 16 x 128 block: 16 bytes of elements per lane and
+// operand, and one scale byte, byte SEL of sa and sb.
+template <int SEL>
 __device__ __forceinline__ void mfma_mx(f32x4& c, u32x4 a, u32x4 b, uint32_t sa, uint32_t sb) {
     const i32x4 ai = __builtin_bit_cast(i32x4, a), bi = __builtin_bit_cast(i32x4, b);
     const i32x8 a8 = __builtin_shufflevector(ai, ai, 0, 1, 2, 3, -1, -1, -1, -1);
     const i32x8 b8 = __builtin_shufflevector(bi, bi, 0, 1, 2, 3, -1, -1, -1, -1);
-    c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, 0, static_cast<int>(sa),
-                                                         0, static_cast<int>(sb));
+    c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        a8, b8, c, 4, 4, SEL, static_cast<int>(sa), SEL, static_cast<int>(sb));
 }
 
-// The plain kernel: fragments straight from global memory.  Four waves, each
-// TM x TN blocks of 16 x 16.
-template <int TM, int TN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * kWave) void mx_plain_kernel(MxArgs p) {
-    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const int r = lane % 16, g = lane / 16;
-    const int64_t tiles_n = ceil_div(p.N, 16 * TN * WN);
-    const int64_t m0 = (blockIdx.x / tiles_n * WM + wave / WN) * (16 * TM);
-    const int64_t n0 = (blockIdx.x % tiles_n * WN + wave % WN) * (16 * TN);
-    const int64_t chunks = p.K / 32;
-    f32x4 acc[TM][TN] = {};
-    for (int64_t c0 = 0; c0 < chunks; c0 += 4) {
-        const int64_t c = c0 + g;
-        u32x4 a[TM], b[TN];
-        uint32_t sa[TM], sb[TN];
+// ------------------------------------------------------------------ tiles of C
+//
+// The ping-pong schedule of mfma16_direct.hpp (two groups of four waves take
+// turns on each SIMD, one running a k-tile of matrix instructions while the other
+// reads its next k-tile of fragments), for operands with k contiguous on both
+// sides.  A k-tile is 128 bytes per row, 256 elements.  What differs:
+//
+// * Scales.  Two k-tiles' scales of a row are 16 bytes, so every second k-tile a
+//   direct load per 64 rows brings them into LDS as they lie in memory: 8 KiB per
+//   pair of k-tiles beside 128 KiB of elements.  A fragment's lane (r, g) needs
+//   bytes g and 4 + g of its row's eight for the k-tile's two slabs: one 8-byte
+//   LDS read and one byte permute, and the two instructions select the byte.
+// * LDS.  The scales leave no room for a third stage of B, so the direct loads of
+//   both operands are issued by group X in its reading turn, right after group Y
+//   has read the stage that they fill, and land during the following turn.
+// * Ragged sizes run on the same kernel: every load's row is clamped on the
+//   spot (the address arithmetic hides in the reading turn), and a last k-tile
+//   that K ends inside (TAIL) has A's chunks past K and both operands' scales
+//   past K zeroed in LDS once it has landed.
+template <int B_> struct MxTile {
+    static constexpr int BX = B_;                        // the tile is BX x BX
+    static constexpr int WTM = BX / 2, WTN = BX / 4;     // a wave's part
+    static constexpr int TM = WTM / 16, TN = WTN / 16;
+    static constexpr int STAGE = BX * 128;               // one operand's k-tile
+    static constexpr int A0 = 0, B0 = 2 * STAGE, S0 = 4 * STAGE;
+    static constexpr int SCALES = 2 * BX * 16;           // a pair of k-tiles, A's rows then B's
+    static constexpr int LDS_BYTES = S0 + 2 * SCALES;
+    static constexpr int PW = BX / 8 / 4;                // element loads per X wave and operand
+    static constexpr int NS = 2 * BX / 64;               // scale loads per pair, over the X waves
+    static constexpr int GM = 4;
+    static_assert(LDS_BYTES <= 160 * 1024, "stages and scales fit");
+};
+
+template <int BX, bool TAIL>
+__global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int tiles_n) {
+    using T = MxTile<BX>;
+    constexpr int TM = T::TM, TN = T::TN, PW = T::PW;
+    __shared__ __attribute__((aligned(1024))) char smem[T::LDS_BYTES];
+    MIGEMM_LDS char* const lds = (MIGEMM_LDS char*)smem;
+    const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wx = wave & 3;
+    const bool gx = wave < 4;
+    const int wm0 = (wave >> 2) * T::WTM, wn0 = wx * T::WTN;
+
+    int pm, pn;
+    tile_coords<T::GM>(blockIdx.x, tiles_m, tiles_n, pm, pn);
+    const int64_t m0 = static_cast<int64_t>(pm) * BX, n0 = static_cast<int64_t>(pn) * BX;
+    const int chunks = static_cast<int>(p.K / 32), KT = (chunks + 7) / 8;
+    const int left = TAIL ? chunks % 8 : 8;  // chunks in the last k-tile (TAIL: 1 to 7)
+
+    // Element loads.  One covers eight rows; load q of wave wx rows 8 (wx + 4 q) +
+    // lane / 8.  The swizzle depends on the row modulo 16, so a lane's logical
+    // chunk is the same in all its loads.
+    const int r0 = 8 * wx + lane / 8;
+    const int logical = (lane % 8) ^ swz_a<8>(r0);
+    const uint32_t c16 = 16 * logical, c16_last = 16 * min(logical, left - 1);
+    const int last_m = static_cast<int>(min(p.M - m0, int64_t(BX))) - 1;
+    const int last_n = static_cast<int>(min(p.N - n0, int64_t(BX))) - 1;
+    const uint32_t lda = static_cast<uint32_t>(p.lda), ldb = static_cast<uint32_t>(p.ldb);
+    const uint8_t* const a_tile = p.A + m0 * p.lda;
+    const uint8_t* const b_tile = p.B + n0 * p.ldb;
+    auto load_a = [&](int kt, int q) __attribute__((always_inline)) {
+        const uint32_t row = min(r0 + 32 * q, last_m);
+        dma16(lds_addr + T::A0 + (kt & 1) * T::STAGE + (wx + 4 * q) * 1024,
+              a_tile + static_cast<int64_t>(kt) * 128,
+              __umul24(row, lda) + (TAIL && kt == KT - 1 ? c16_last : c16));
+    };
+    auto load_b = [&](int kt, int q) __attribute__((always_inline)) {
+        const uint32_t row = min(r0 + 32 * q, last_n);
+        dma16(lds_addr + T::B0 + (kt & 1) * T::STAGE + (wx + 4 * q) * 1024,
+              b_tile + static_cast<int64_t>(kt) * 128,
+              __umul24(row, ldb) + (TAIL && kt == KT - 1 ? c16_last : c16));
+    };
+    // Scale load j (0 .. NS - 1) of pair `pair`: 64 rows of A, or of B.
+    auto load_scales = [&](int pair, int j) __attribute__((always_inline)) {
+        const bool of_a = j < T::NS / 2;
+        const int row = 64 * (of_a ? j : j - T::NS / 2) + lane;
+        const uint8_t* const base = of_a ? p.sa + m0 * p.ldsa : p.sb + n0 * p.ldsb;
+        const uint32_t ld = static_cast<uint32_t>(of_a ? p.ldsa : p.ldsb);
+        dma16(lds_addr + T::S0 + (pair & 1) * T::SCALES + j * 1024,
+              base + static_cast<int64_t>(pair) * 16,
+              __umul24(static_cast<uint32_t>(min(row, of_a ? last_m : last_n)), ld));
+    };
+    auto load_pair = [&](int pair) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int64_t row = min(m0 + 16 * i + r, p.M - 1);
-            a[i] = u32x4{0u, 0u, 0u, 0u};
-            sa[i] = 0;
-            if (c < chunks) {
-                a[i] = *reinterpret_cast<const u32x4*>(p.A + row * p.lda + 16 * c);
-                sa[i] = p.sa[row * p.ldsa + c];
+        for (int j = 0; j < T::NS; j += 4)
+            if (j + wx < T::NS) load_scales(pair, j + wx);
+    };
+    // Zeroes what the last k-tile's loads of this wave brought from past K (each
+    // lane its own LDS slots), once they have landed.
+    auto zero_tail = [&]() __attribute__((always_inline)) {
+        if constexpr (TAIL) {
+            if (logical >= left) {
+#pragma unroll
+                for (int q = 0; q < PW; ++q)
+                    *(MIGEMM_LDS u32x4*)(lds + T::A0 + ((KT - 1) & 1) * T::STAGE +
+                                         (wx + 4 * q) * 1024 + 16 * lane) = u32x4{0u, 0u, 0u, 0u};
             }
+            const int pair = (KT - 1) / 2, valid = chunks - 16 * pair;  // 1 .. 15 bytes
+#pragma unroll
+            for (int j = 0; j < T::NS; j += 4)
+                if (j + wx < T::NS) {
+                    MIGEMM_LDS u32x4* const s = (MIGEMM_LDS u32x4*)(lds + T::S0 +
+                        (pair & 1) * T::SCALES + (j + wx) * 1024 + 16 * lane);
+                    u32x4 v = *s;
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        const int n = valid - 4 * d;  // valid bytes of this word
+                        v[d] &= n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+                    }
+                    *s = v;
+                }
         }
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t row = min(n0 + 16 * j + r, p.N - 1);
-            b[j] = u32x4{0u, 0u, 0u, 0u};
-            sb[j] = 0;
-            if (c < chunks) {
-                b[j] = *reinterpret_cast<const u32x4*>(p.B + row * p.ldb + 16 * c);
-                sb[j] = p.sb[row * p.ldsb + c];
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) mfma_mx(acc[i][j], a[i], b[j], sa[i], sb[j]);
-    }
-    using L = AccLayout<16>;
+    };
+
+    f32x4 acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // accumulators in AGPRs (see mfma16_direct.hpp)
+    float agpr_hint = 0.0f;
+    asm volatile("" : "+a"(agpr_hint));
+
+    const int ar = lane % 16, ag = lane / 16;
+    const uint32_t pick = 0x0c0c0400u + 0x0101u * static_cast<uint32_t>(ag);
+    u32x4 fa[2][TM], fb[2][TN];
+    uint32_t sa[TM], sb[TN];
+    // A k-tile of fragments and scales; with LOADS the direct loads of k-tile
+    // kt_load, one after every few reads.
+    auto read_ktile = [&](int kt, auto loads, int kt_load) __attribute__((always_inline)) {
+        constexpr bool LOADS = decltype(loads)::value;
+        constexpr int kReads = 2 * (TM + TN), EVERY = kReads / (2 * PW) > 0 ? kReads / (2 * PW) : 1;
+        int r = 0, q = 0;
+        if (LOADS && (kt_load & 1) == 0) load_pair(kt_load >> 1);
+        auto one_load = [&]() __attribute__((always_inline)) {
+            if (q & 1)
+                load_b(kt_load, q >> 1);
+            else
+                load_a(kt_load, q >> 1);
+            ++q;
+        };
+        auto after_read = [&]() __attribute__((always_inline)) {
+            ++r;
+            if (LOADS && r % EVERY == 0 && q < 2 * PW) one_load();
+        };
+        int st = (kt & 1) * T::STAGE, sc = T::S0 + ((kt >> 1) & 1) * T::SCALES + (kt & 1) * 8;
+        asm("" : "+s"(st), "+s"(sc));
+        const MIGEMM_LDS char* const ia = lds + T::A0 + st;
+        const MIGEMM_LDS char* const ib = lds + T::B0 + st;
+        const MIGEMM_LDS char* const is = lds + sc;
+        auto scale = [&](int row) __attribute__((always_inline)) {
+            const u32x2 v = *(const MIGEMM_LDS u32x2*)(is + row * 16);
+            return __builtin_amdgcn_perm(v[1], v[0], pick);
+        };
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int64_t row = m0 + 16 * i + L::row(lane, e), col = n0 + 16 * j + L::col(lane);
-                if (row < p.M && col < p.N)
-                    store_out<true>(p.out, row * p.out.ldc + col, acc[i][j][e]);
+        for (int s = 0; s < 2; ++s) {
+            const int chunk = (4 * s + ag) ^ swz_a<8>(ar);
+            auto read_a = [&](int i) __attribute__((always_inline)) {
+                fa[s][i] = *(const MIGEMM_LDS u32x4*)(ia + (wm0 + ar) * 128 + chunk * 16 + i * 2048);
+                if (s == 0) sa[i] = scale(wm0 + ar + 16 * i);
+                after_read();
+            };
+            auto read_b = [&](int j) __attribute__((always_inline)) {
+                fb[s][j] = *(const MIGEMM_LDS u32x4*)(ib + (wn0 + ar) * 128 + chunk * 16 + j * 2048);
+                if (s == 0) sb[j] = scale(BX + wn0 + ar + 16 * j);
+                after_read();
+            };
+            read_a(0);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) read_b(j);
+#pragma unroll
+            for (int i = 1; i < TM; ++i) read_a(i);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * PW; ++i)
+            if (LOADS && i >= q) one_load();
+    };
+    // A k-tile of matrix instructions; BAR 1 (X: its loads have landed, then the
+    // barrier; 2: also zeroing what lies past K) or 3 (Y: the barrier), met a few
+    // instructions before the last one as in mfma16_direct.hpp.
+    constexpr int kMfma = 2 * TM * TN, kEarly = kMfma > 16 ? 8 : kMfma / 2;
+    auto run_ktile = [&](auto bar) __attribute__((always_inline)) {
+        constexpr int BAR = decltype(bar)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        int n = 0;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    if (s == 0)
+                        mfma_mx<0>(acc[i][j], fa[0][i], fb[0][j], sa[i], sb[j]);
+                    else
+                        mfma_mx<1>(acc[i][j], fa[1][i], fb[1][j], sa[i], sb[j]);
+                    if (BAR && n == kMfma - 1 - kEarly) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        __builtin_amdgcn_s_setprio(1);
+                        if constexpr (BAR == 1) wait_then_barrier<0>();
+                        if constexpr (BAR == 2) {
+                            vm_wait<0>();
+                            zero_tail();
+                            lds_wait_then_barrier();
+                        }
+                        if constexpr (BAR == 3) lds_wait_then_barrier();
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    ++n;
+                }
+        __builtin_amdgcn_sched_barrier(0);
+        if (BAR) __builtin_amdgcn_s_setprio(0);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    using NoBarrier = std::integral_constant<int, 0>;
+    using XBarrier = std::integral_constant<int, 1>;
+    using XTail = std::integral_constant<int, TAIL ? 2 : 1>;
+    using YBarrier = std::integral_constant<int, 3>;
+
+    // Prologue: k-tiles 0 and 1 (X loads A and the first scales, Y loads B).
+    if (gx) {
+        load_pair(0);
+#pragma unroll
+        for (int q = 0; q < PW; ++q) load_a(0, q);
+        if (KT > 1)
+#pragma unroll
+            for (int q = 0; q < PW; ++q) load_a(1, q);
+    } else {
+#pragma unroll
+        for (int q = 0; q < PW; ++q) load_b(0, q);
+        if (KT > 1)
+#pragma unroll
+            for (int q = 0; q < PW; ++q) load_b(1, q);
+    }
+    if (KT > 1) {
+        vm_wait<PW>();
+    } else {
+        vm_wait<0>();
+        if (gx) zero_tail();
+    }
+    lds_wait_then_barrier();
+    if (gx) {
+        read_ktile(0, No{}, 0);
+        lds_wait_then_barrier();
+        for (int kt = 0; kt + 2 < KT; ++kt) {
+            run_ktile(XBarrier{});
+            read_ktile(kt + 1, Yes{}, kt + 2);
+            lds_wait_then_barrier();
+        }
+        if (KT >= 2) {
+            run_ktile(XTail{});
+            read_ktile(KT - 1, No{}, 0);
+            lds_wait_then_barrier();
+        }
+        run_ktile(XBarrier{});
+    } else {
+        lds_wait_then_barrier();
+        for (int kt = 0; kt + 1 < KT; ++kt) {
+            read_ktile(kt, No{}, 0);
+            // the prologue's B of k-tile 1 has landed (later ones are X's)
+            wait_then_barrier<0>();
+            run_ktile(YBarrier{});
+        }
+        read_ktile(KT - 1, No{}, 0);
+        wait_then_barrier<0>();
+        run_ktile(NoBarrier{});
+    }
+
+    // Output.  Every fragment read is done; each wave sends its accumulators, one
+    // 16-row block at a time, through LDS of its own, so that C is read (beta) and
+    // written 16 bytes per lane in whole row pieces.  The 16-byte chunk index of
+    // the block's rows is XORed by (row >> 2), which spreads the accumulator writes
+    // over the banks.
+    constexpr int WTN = T::WTN;
+    MIGEMM_LDS float* const scr = (MIGEMM_LDS float*)(lds + wave * (16 * WTN * 4));
+    const Epi out = p.out;
+    const bool rd = out.beta != 0.0f;
+    const bool lines = p.whole_lines;
+    const int64_t mw = m0 + wm0, nw = n0 + wn0;
+    auto store = [&](auto half_tag) __attribute__((always_inline)) {
+        constexpr bool HALF = decltype(half_tag)::value;
+        constexpr int VE = HALF ? 8 : 4, ES = HALF ? 2 : 4, PIECES = WTN / VE;
+        constexpr int kXor = (WTN / 4 - 1) & 3;  // 16-byte chunks of FP32 in a row, at most 4 used
+        const bool vec = (out.ldc * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(out.C) & 15) == 0;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int c = 16 * j + ar;
+                    scr[(4 * ag + r) * WTN + ((((c >> 2) ^ (ag & kXor)) << 2) | (c & 3))] =
+                        acc[i][j][r];
+                }
+            asm volatile("" : : : "memory");
+#pragma unroll
+            for (int q = 0; q < (16 * PIECES + kWave - 1) / kWave; ++q) {
+                const int piece = lane + q * kWave, row = piece / PIECES, c0 = piece % PIECES * VE;
+                if (16 * PIECES % kWave != 0 && piece >= 16 * PIECES) continue;
+                const int64_t grow = mw + 16 * i + row, gcol = nw + c0;
+                float v[VE];
+#pragma unroll
+                for (int h = 0; h < VE / 4; ++h) {
+                    const int ch = ((c0 >> 2) + h) ^ ((row >> 2) & kXor);
+                    const f32x4 x = *(const MIGEMM_LDS f32x4*)(scr + row * WTN + 4 * ch);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
+                }
+                if (grow >= p.M || gcol >= p.N) continue;
+                const int64_t idx = grow * out.ldc + gcol;
+                if (vec && gcol + VE <= p.N) {
+                    u32x4* const dst =
+                        reinterpret_cast<u32x4*>(static_cast<char*>(out.C) + idx * ES);
+                    u32x4 old = {0u, 0u, 0u, 0u}, w = {0u, 0u, 0u, 0u};
+                    if (rd) old = *dst;
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        float prev;
+                        if constexpr (HALF) {
+                            const uint32_t bits = (old[e / 2] >> (16 * (e % 2))) & 0xffffu;
+                            prev = out.c_dtype == 1
+                                       ? static_cast<float>(__builtin_bit_cast(
+                                             _Float16, static_cast<uint16_t>(bits)))
+                                       : __uint_as_float(bits << 16);
+                        } else {
+                            prev = __uint_as_float(old[e]);
+                        }
+                        const float res =
+                            rd ? fmaf(out.alpha, v[e], out.beta * prev) : out.alpha * v[e];
+                        if constexpr (HALF) {
+                            const uint32_t b =
+                                out.c_dtype == 1
+                                    ? static_cast<uint32_t>(__builtin_bit_cast(
+                                          uint16_t, static_cast<_Float16>(res)))
+                                    : static_cast<uint32_t>(f32_to_bf16_bits(res));
+                            w[e / 2] |= b << (16 * (e % 2));
+                        } else {
+                            w[e] = __float_as_uint(res);
+                        }
+                    }
+                    if (lines)
+                        __builtin_nontemporal_store(w, dst);
+                    else
+                        *dst = w;
+                } else {
+                    // edges and unaligned C, an element at a time
+#pragma unroll
+                    for (int e = 0; e < VE; ++e)
+                        if (gcol + e < p.N)
+                            store_update<false>(out, idx + e, v[e],
+                                                rd ? load_prev(out, idx + e) : 0.0f);
+                }
             }
+            asm volatile("" : : : "memory");
+        }
+    };
+    if (out.c_dtype == 0)
+        store(No{});
+    else
+        store(Yes{});
+}
+
+// ------------------------------------------------------------------ few rows of A
+//
+// M of at most 16 TM rows: nothing is reused but A, which the caches hold, so the
+// time is that of reading B once.  A workgroup takes 16 rows of B (columns of C);
+// its waves split k in groups of 16 chunks (512 elements: four matrix
+// instructions, and the 16 scale bytes of a row in one load), taken in turn, and
+// add their sums through LDS in wave order, so the result does not depend on
+// timing.  A 64-column tile would leave most CUs idle at N = 8192 and walk all of
+// K in each.
+template <int TM, int WAVES>
+__global__ __launch_bounds__(WAVES * kWave) void mx_rows_kernel(MxArgs p) {
+    __shared__ f32x4 part[WAVES][TM][kWave];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int r = lane % 16, g = lane / 16;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const int64_t nrow = min(n0 + r, p.N - 1);
+    const uint8_t* const b_row = p.B + nrow * p.ldb;
+    const uint8_t* const sb_row = p.sb + nrow * p.ldsb;
+    const int64_t chunks = p.K / 32, groups = ceil_div(chunks, 16);
+    f32x4 acc[TM] = {};
+    for (int64_t k = wave; k < groups; k += WAVES) {
+        u32x4 b[4], a[TM][4];
+        const u32x4 wb = *reinterpret_cast<const u32x4*>(sb_row + 16 * k);
+        u32x4 wa[TM];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int64_t c = 16 * k + 4 * s + g;
+            b[s] = u32x4{0u, 0u, 0u, 0u};
+            if (c < chunks) b[s] = *reinterpret_cast<const u32x4*>(b_row + 16 * c);
+        }
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int64_t mrow = min(int64_t(16 * i + r), p.M - 1);
+            wa[i] = *reinterpret_cast<const u32x4*>(p.sa + mrow * p.ldsa + 16 * k);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int64_t c = 16 * k + 4 * s + g;
+                a[i][s] = u32x4{0u, 0u, 0u, 0u};
+                if (c < chunks)
+                    a[i][s] = *reinterpret_cast<const u32x4*>(p.A + mrow * p.lda + 16 * c);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            // byte g of the four blocks' scales; 0 past K
+            const bool in = 16 * k + 4 * s + g < chunks;
+            const uint32_t sb = in ? wb[s] >> (8 * g) : 0u;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                mfma_mx<0>(acc[i], a[i][s], b[s], in ? wa[i][s] >> (8 * g) : 0u, sb);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    using L = AccLayout<16>;
+    for (int i = wave; i < TM; i += WAVES) {
+        f32x4 sum = part[0][i][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) {
+            const f32x4 q = part[w][i][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += q[e];
+        }
+        const int64_t col = n0 + L::col(lane);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t row = 16 * i + L::row(lane, e);
+            if (row < p.M && col < p.N)
+                store_out<true>(p.out, row * p.out.ldc + col, sum[e]);
+        }
+    }
+}
+
+template <int BX>
+hipError_t launch_tile(const MxArgs& p) {
+    const int64_t tm = ceil_div(p.M, BX), tn = ceil_div(p.N, BX);
+    if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+    auto* const fn =
+        p.K % 256 != 0 ? mx_tile_kernel<BX, true> : mx_tile_kernel<BX, false>;
+    fn<<<dim3(static_cast<unsigned>(tm * tn)), dim3(512), 0, p.stream>>>(
+        p, static_cast<int>(tm), static_cast<int>(tn));
+    return hipGetLastError();
+}
+
+template <int TM>
+hipError_t launch_rows(const MxArgs& p) {
+    mx_rows_kernel<TM, 8><<<dim3(static_cast<unsigned>(ceil_div(p.N, 16))), dim3(8 * kWave), 0,
+                            p.stream>>>(p);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gemm_mx(const MxArgs& p) {
-    const int64_t grid = ceil_div(p.M, 64) * ceil_div(p.N, 64);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    mx_plain_kernel<2, 2, 2, 2><<<dim3(static_cast<unsigned>(grid)), dim3(256), 0, p.stream>>>(p);
-    return hipGetLastError();
+    if (p.K == 0) {
+        GemmArgs g{};
+        g.M = p.M;
+        g.N = p.N;
+        g.out = p.out;
+        g.stream = p.stream;
+        return launch_empty_product(g);
+    }
+    if (p.M <= 16) return launch_rows<1>(p);
+    if (p.M <= 32) return launch_rows<2>(p);
+    if (p.M <= 64) return launch_rows<4>(p);
+    // the tile kernel's load offsets are 32 bits, 255 rows: longer rows 64 at a time
+    const int64_t far = int64_t(1) << 23;
+    if (p.lda >= far || p.ldb >= far || p.ldsa >= far || p.ldsb >= far) {
+        for (int64_t m = 0; m < p.M; m += 64) {
+            MxArgs q = p;
+            q.M = p.M - m < 64 ? p.M - m : 64;
+            q.A = p.A + m * p.lda;
+            q.sa = p.sa + m * p.ldsa;
+            q.out.C = static_cast<char*>(p.out.C) + m * p.out.ldc * (p.out.c_dtype == 0 ? 4 : 2);
+            const hipError_t e = launch_rows<4>(q);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
+    auto tiles = [&](int64_t b) { return ceil_div(p.M, b) * ceil_div(p.N, b); };
+    if (tiles(256) >= 128) return launch_tile<256>(p);
+    if (tiles(128) >= 128) return launch_tile<128>(p);
+    return launch_tile<64>(p);
 }
 
 }  // namespace migemm
