@@ -39,16 +39,23 @@ __device__ __forceinline__ void mfma_mx(f32x4& c, u32x4 a, u32x4 b, uint32_t sa,
 // The ping-pong schedule of mfma16_direct.hpp (two groups of four waves take
 // turns on each SIMD, one running a k-tile of matrix instructions while the other
 // reads its next k-tile of fragments), for operands with k contiguous on both
-// sides.  A k-tile is 128 bytes per row, 256 elements.  What differs:
+// sides.  A k-tile is 128 bytes per row, 256 elements, 8 blocks.  What differs:
 //
 // * Scales.  Two k-tiles' scales of a row are 16 bytes, so every second k-tile a
-//   direct load per 64 rows brings them into LDS as they lie in memory: 8 KiB per
-//   pair of k-tiles beside 128 KiB of elements.  A fragment's lane (r, g) needs
-//   bytes g and 4 + g of its row's eight for the k-tile's two slabs: one 8-byte
-//   LDS read and one byte permute, and the two instructions select the byte.
-// * LDS.  The scales leave no room for a third stage of B, so the direct loads of
-//   both operands are issued by group X in its reading turn, right after group Y
-//   has read the stage that they fill, and land during the following turn.
+//   direct load per 64 rows brings them into LDS as they lie in memory.  The
+//   order of k within a sum is free as long as A and B agree, so lane group g
+//   takes blocks 2 g and 2 g + 1 of the k-tile (in its first and second slab)
+//   rather than g and 4 + g: its two scale bytes are then neighbours, one 2-byte
+//   LDS read per fragment and k-tile, and the two instructions select the byte.
+//   (Reading eight bytes and permuting g and 4 + g together cost twice the LDS
+//   time and a wait per permute.)
+// * LDS.  Two stages of A, two and a half of B and two pairs of scales fill the 160
+//   KiB of the 256 x 256 tile.  B moves in halves of the tile's columns, half h of
+//   k-tile kt in slot (2 kt + h) mod 5.  While Y reads k-tile kt, four slots hold
+//   k-tiles kt and kt + 1 and Y fills the fifth with the first half of kt + 2; once
+//   it has read, X fills kt's first slot with the second half, and A's stage, in
+//   its own reading turn.  Loading all of B there instead (two whole stages) made
+//   X's reading turn longer than a turn of matrix instructions.
 // * Ragged sizes run on the same kernel: every load's row is clamped on the
 //   spot (the address arithmetic hides in the reading turn), and a last k-tile
 //   that K ends inside (TAIL) has A's chunks past K and both operands' scales
@@ -58,19 +65,21 @@ template <int B_> struct MxTile {
     static constexpr int WTM = BX / 2, WTN = BX / 4;     // a wave's part
     static constexpr int TM = WTM / 16, TN = WTN / 16;
     static constexpr int STAGE = BX * 128;               // one operand's k-tile
-    static constexpr int A0 = 0, B0 = 2 * STAGE, S0 = 4 * STAGE;
+    static constexpr int HALF = STAGE / 2;
+    static constexpr int A0 = 0, B0 = 2 * STAGE, S0 = B0 + 5 * HALF;
     static constexpr int SCALES = 2 * BX * 16;           // a pair of k-tiles, A's rows then B's
     static constexpr int LDS_BYTES = S0 + 2 * SCALES;
-    static constexpr int PW = BX / 8 / 4;                // element loads per X wave and operand
+    static constexpr int PA = BX / 8 / 4;                // A's loads per X wave and k-tile
+    static constexpr int PB = PA / 2;                    // loads per wave and half of B
     static constexpr int NS = 2 * BX / 64;               // scale loads per pair, over the X waves
     static constexpr int GM = 4;
-    static_assert(LDS_BYTES <= 160 * 1024, "stages and scales fit");
+    static_assert(LDS_BYTES <= 160 * 1024 && PB >= 1, "stages and scales fit");
 };
 
 template <int BX, bool TAIL>
 __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int tiles_n) {
     using T = MxTile<BX>;
-    constexpr int TM = T::TM, TN = T::TN, PW = T::PW;
+    constexpr int TM = T::TM, TN = T::TN, PA = T::PA, PB = T::PB;
     __shared__ __attribute__((aligned(1024))) char smem[T::LDS_BYTES];
     MIGEMM_LDS char* const lds = (MIGEMM_LDS char*)smem;
     const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
@@ -78,7 +87,7 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wx = wave & 3;
     const bool gx = wave < 4;
-    const int wm0 = (wave >> 2) * T::WTM, wn0 = wx * T::WTN;
+    const int wm0 = (wave >> 2) * T::WTM;
 
     int pm, pn;
     tile_coords<T::GM>(blockIdx.x, tiles_m, tiles_n, pm, pn);
@@ -87,8 +96,8 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
     const int left = TAIL ? chunks % 8 : 8;  // chunks in the last k-tile (TAIL: 1 to 7)
 
     // Element loads.  One covers eight rows; load q of wave wx rows 8 (wx + 4 q) +
-    // lane / 8.  The swizzle depends on the row modulo 16, so a lane's logical
-    // chunk is the same in all its loads.
+    // lane / 8 of the image.  The swizzle depends on the row modulo 16, so a
+    // lane's logical chunk is the same in all its loads.
     const int r0 = 8 * wx + lane / 8;
     const int logical = (lane % 8) ^ swz_a<8>(r0);
     const uint32_t c16 = 16 * logical, c16_last = 16 * min(logical, left - 1);
@@ -97,22 +106,26 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
     const uint32_t lda = static_cast<uint32_t>(p.lda), ldb = static_cast<uint32_t>(p.ldb);
     const uint8_t* const a_tile = p.A + m0 * p.lda;
     const uint8_t* const b_tile = p.B + n0 * p.ldb;
-    auto load_a = [&](int kt, int q) __attribute__((always_inline)) {
-        const uint32_t row = min(r0 + 32 * q, last_m);
+    // r: r0, made opaque once per k-tile, or the compiler keeps all of a wave's
+    // row offsets in registers for the whole loop and spills others to memory
+    auto load_a = [&](int kt, int q, int r) __attribute__((always_inline)) {
+        const uint32_t row = min(r + 32 * q, last_m);
         dma16(lds_addr + T::A0 + (kt & 1) * T::STAGE + (wx + 4 * q) * 1024,
               a_tile + static_cast<int64_t>(kt) * 128,
               __umul24(row, lda) + (TAIL && kt == KT - 1 ? c16_last : c16));
     };
-    auto load_b = [&](int kt, int q) __attribute__((always_inline)) {
-        const uint32_t row = min(r0 + 32 * q, last_n);
-        dma16(lds_addr + T::B0 + (kt & 1) * T::STAGE + (wx + 4 * q) * 1024,
+    // Load q of half h of B's k-tile kt, into slot `slot`.
+    auto load_b = [&](int kt, int h, int slot, int q, int r) __attribute__((always_inline)) {
+        const uint32_t row = min(r + 32 * q + h * (BX / 2), last_n);
+        dma16(lds_addr + T::B0 + slot * T::HALF + (wx + 4 * q) * 1024,
               b_tile + static_cast<int64_t>(kt) * 128,
               __umul24(row, ldb) + (TAIL && kt == KT - 1 ? c16_last : c16));
     };
     // Scale load j (0 .. NS - 1) of pair `pair`: 64 rows of A, or of B.
     auto load_scales = [&](int pair, int j) __attribute__((always_inline)) {
         const bool of_a = j < T::NS / 2;
-        const int row = 64 * (of_a ? j : j - T::NS / 2) + lane;
+        int row = 64 * (of_a ? j : j - T::NS / 2) + lane;
+        asm volatile("" : "+v"(row));
         const uint8_t* const base = of_a ? p.sa + m0 * p.ldsa : p.sb + n0 * p.ldsb;
         const uint32_t ld = static_cast<uint32_t>(of_a ? p.ldsa : p.ldsb);
         dma16(lds_addr + T::S0 + (pair & 1) * T::SCALES + j * 1024,
@@ -124,13 +137,14 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
         for (int j = 0; j < T::NS; j += 4)
             if (j + wx < T::NS) load_scales(pair, j + wx);
     };
-    // Zeroes what the last k-tile's loads of this wave brought from past K (each
-    // lane its own LDS slots), once they have landed.
+    // Zeroes what the last k-tile's loads of this wave (group X) brought from past
+    // K (each lane its own LDS slots), once they have landed: A's elements, so
+    // that B's do not matter, and both operands' scales, so that no NaN one does.
     auto zero_tail = [&]() __attribute__((always_inline)) {
         if constexpr (TAIL) {
             if (logical >= left) {
 #pragma unroll
-                for (int q = 0; q < PW; ++q)
+                for (int q = 0; q < PA; ++q)
                     *(MIGEMM_LDS u32x4*)(lds + T::A0 + ((KT - 1) & 1) * T::STAGE +
                                          (wx + 4 * q) * 1024 + 16 * lane) = u32x4{0u, 0u, 0u, 0u};
             }
@@ -161,47 +175,60 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
     asm volatile("" : "+a"(agpr_hint));
 
     const int ar = lane % 16, ag = lane / 16;
-    const uint32_t pick = 0x0c0c0400u + 0x0101u * static_cast<uint32_t>(ag);
+    // this wave's columns: rows wb0 .. of half wh of B's image
+    const int wh = wx >> 1, wb0 = (wx & 1) * T::WTN;
     u32x4 fa[2][TM], fb[2][TN];
     uint32_t sa[TM], sb[TN];
-    // A k-tile of fragments and scales; with LOADS the direct loads of k-tile
-    // kt_load, one after every few reads.
-    auto read_ktile = [&](int kt, auto loads, int kt_load) __attribute__((always_inline)) {
-        constexpr bool LOADS = decltype(loads)::value;
-        constexpr int kReads = 2 * (TM + TN), EVERY = kReads / (2 * PW) > 0 ? kReads / (2 * PW) : 1;
+    auto wrap = [](int slot) { return slot >= 5 ? slot - 5 : slot; };
+    // A k-tile of fragments and scales, its B half in slot `slot` + wh (mod 5),
+    // interleaved with direct loads of k-tile kt + ahead: LOADS 1 (X) A, the second
+    // half of B and, for an even k-tile, the scales; 2 (Y) the first half of B.
+    auto read_ktile = [&](int kt, int slot, auto loads, int kt_load)
+        __attribute__((always_inline)) {
+        constexpr int LOADS = decltype(loads)::value;
+        constexpr int kLoads = LOADS == 1 ? PA + PB : LOADS == 2 ? PB : 0;
+        constexpr int kReads = 2 * (TM + TN);
+        constexpr int EVERY = kLoads && kReads / kLoads > 0 ? kReads / kLoads : 1;
         int r = 0, q = 0;
-        if (LOADS && (kt_load & 1) == 0) load_pair(kt_load >> 1);
+        if (LOADS == 1 && (kt_load & 1) == 0) load_pair(kt_load >> 1);
+        int r_now = r0;
+        asm volatile("" : "+v"(r_now));
         auto one_load = [&]() __attribute__((always_inline)) {
-            if (q & 1)
-                load_b(kt_load, q >> 1);
-            else
-                load_a(kt_load, q >> 1);
+            if constexpr (LOADS == 1) {
+                // kt_load = kt + 1: its second half goes where the first half of
+                // k-tile kt_load - 2 was
+                if (q % 3 == 2)
+                    load_b(kt_load, 1, wrap(slot + 3), q / 3, r_now);
+                else
+                    load_a(kt_load, q - q / 3, r_now);
+            }
+            if constexpr (LOADS == 2) load_b(kt_load, 0, wrap(slot + 4), q, r_now);
             ++q;
         };
         auto after_read = [&]() __attribute__((always_inline)) {
             ++r;
-            if (LOADS && r % EVERY == 0 && q < 2 * PW) one_load();
+            if (LOADS && r % EVERY == 0 && q < kLoads) one_load();
         };
-        int st = (kt & 1) * T::STAGE, sc = T::S0 + ((kt >> 1) & 1) * T::SCALES + (kt & 1) * 8;
-        asm("" : "+s"(st), "+s"(sc));
+        int st = (kt & 1) * T::STAGE, sh = wrap(slot + wh) * T::HALF;
+        int sc = T::S0 + ((kt >> 1) & 1) * T::SCALES + (kt & 1) * 8;
+        asm("" : "+s"(st), "+s"(sc), "+s"(sh));
         const MIGEMM_LDS char* const ia = lds + T::A0 + st;
-        const MIGEMM_LDS char* const ib = lds + T::B0 + st;
+        const MIGEMM_LDS char* const ib = lds + T::B0 + sh;
         const MIGEMM_LDS char* const is = lds + sc;
-        auto scale = [&](int row) __attribute__((always_inline)) {
-            const u32x2 v = *(const MIGEMM_LDS u32x2*)(is + row * 16);
-            return __builtin_amdgcn_perm(v[1], v[0], pick);
-        };
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int chunk = (4 * s + ag) ^ swz_a<8>(ar);
+            const int chunk = (2 * ag + s) ^ swz_a<8>(ar);
             auto read_a = [&](int i) __attribute__((always_inline)) {
                 fa[s][i] = *(const MIGEMM_LDS u32x4*)(ia + (wm0 + ar) * 128 + chunk * 16 + i * 2048);
-                if (s == 0) sa[i] = scale(wm0 + ar + 16 * i);
+                if (s == 0)
+                    sa[i] = *(const MIGEMM_LDS uint16_t*)(is + (wm0 + ar + 16 * i) * 16 + 2 * ag);
                 after_read();
             };
             auto read_b = [&](int j) __attribute__((always_inline)) {
-                fb[s][j] = *(const MIGEMM_LDS u32x4*)(ib + (wn0 + ar) * 128 + chunk * 16 + j * 2048);
-                if (s == 0) sb[j] = scale(BX + wn0 + ar + 16 * j);
+                fb[s][j] = *(const MIGEMM_LDS u32x4*)(ib + (wb0 + ar) * 128 + chunk * 16 + j * 2048);
+                if (s == 0)
+                    sb[j] = *(const MIGEMM_LDS uint16_t*)(
+                        is + (BX + wx * T::WTN + ar + 16 * j) * 16 + 2 * ag);
                 after_read();
             };
             read_a(0);
@@ -211,8 +238,8 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
             for (int i = 1; i < TM; ++i) read_a(i);
         }
 #pragma unroll
-        for (int i = 0; i < 2 * PW; ++i)
-            if (LOADS && i >= q) one_load();
+        for (int i = 0; i < kLoads; ++i)
+            if (i >= q) one_load();
     };
     // A k-tile of matrix instructions; BAR 1 (X: its loads have landed, then the
     // barrier; 2: also zeroing what lies past K) or 3 (Y: the barrier), met a few
@@ -249,58 +276,70 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
         __builtin_amdgcn_sched_barrier(0);
         if (BAR) __builtin_amdgcn_s_setprio(0);
     };
-    using Yes = std::true_type;
-    using No = std::false_type;
     using NoBarrier = std::integral_constant<int, 0>;
     using XBarrier = std::integral_constant<int, 1>;
     using XTail = std::integral_constant<int, TAIL ? 2 : 1>;
     using YBarrier = std::integral_constant<int, 3>;
+    using NoLoads = std::integral_constant<int, 0>;
+    using XLoads = std::integral_constant<int, 1>;
+    using YLoads = std::integral_constant<int, 2>;
 
     // Prologue: k-tiles 0 and 1 (X loads A and the first scales, Y loads B).
     if (gx) {
         load_pair(0);
 #pragma unroll
-        for (int q = 0; q < PW; ++q) load_a(0, q);
+        for (int q = 0; q < PA; ++q) load_a(0, q, r0);
         if (KT > 1)
 #pragma unroll
-            for (int q = 0; q < PW; ++q) load_a(1, q);
+            for (int q = 0; q < PA; ++q) load_a(1, q, r0);
     } else {
 #pragma unroll
-        for (int q = 0; q < PW; ++q) load_b(0, q);
+        for (int q = 0; q < 2 * PB; ++q) load_b(0, q / PB, q / PB, q % PB, r0);
         if (KT > 1)
 #pragma unroll
-            for (int q = 0; q < PW; ++q) load_b(1, q);
+            for (int q = 0; q < 2 * PB; ++q) load_b(1, q / PB, 2 + q / PB, q % PB, r0);
     }
     if (KT > 1) {
-        vm_wait<PW>();
+        vm_wait<PA>();
     } else {
         vm_wait<0>();
         if (gx) zero_tail();
     }
     lds_wait_then_barrier();
+    // slot of B's first half of the k-tile being read: 2 kt mod 5
+    int slot = 0;
     if (gx) {
-        read_ktile(0, No{}, 0);
+        read_ktile(0, 0, NoLoads{}, 0);
         lds_wait_then_barrier();
         for (int kt = 0; kt + 2 < KT; ++kt) {
             run_ktile(XBarrier{});
-            read_ktile(kt + 1, Yes{}, kt + 2);
+            slot = wrap(slot + 2);
+            read_ktile(kt + 1, slot, XLoads{}, kt + 2);
             lds_wait_then_barrier();
         }
         if (KT >= 2) {
             run_ktile(XTail{});
-            read_ktile(KT - 1, No{}, 0);
+            slot = wrap(slot + 2);
+            read_ktile(KT - 1, slot, NoLoads{}, 0);
             lds_wait_then_barrier();
         }
         run_ktile(XBarrier{});
     } else {
         lds_wait_then_barrier();
-        for (int kt = 0; kt + 1 < KT; ++kt) {
-            read_ktile(kt, No{}, 0);
-            // the prologue's B of k-tile 1 has landed (later ones are X's)
+        for (int kt = 0; kt + 2 < KT; ++kt) {
+            read_ktile(kt, slot, YLoads{}, kt + 2);
+            // the B half of k-tile kt + 1 has landed; that of kt + 2 may still fly
+            wait_then_barrier<PB>();
+            run_ktile(YBarrier{});
+            slot = wrap(slot + 2);
+        }
+        if (KT >= 2) {
+            read_ktile(KT - 2, slot, NoLoads{}, 0);
             wait_then_barrier<0>();
             run_ktile(YBarrier{});
+            slot = wrap(slot + 2);
         }
-        read_ktile(KT - 1, No{}, 0);
+        read_ktile(KT - 1, slot, NoLoads{}, 0);
         wait_then_barrier<0>();
         run_ktile(NoBarrier{});
     }
@@ -309,15 +348,15 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
     // 16-row block at a time, through LDS of its own, so that C is read (beta) and
     // written 16 bytes per lane in whole row pieces.  The 16-byte chunk index of
     // the block's rows is XORed by (row >> 2), which spreads the accumulator writes
-    // over the banks.
+    // over the banks.  CT: C's type; RD: beta != 0.  One branch picks the form, so
+    // the code that runs is short and straight.
     constexpr int WTN = T::WTN;
     MIGEMM_LDS float* const scr = (MIGEMM_LDS float*)(lds + wave * (16 * WTN * 4));
     const Epi out = p.out;
-    const bool rd = out.beta != 0.0f;
-    const bool lines = p.whole_lines;
-    const int64_t mw = m0 + wm0, nw = n0 + wn0;
-    auto store = [&](auto half_tag) __attribute__((always_inline)) {
-        constexpr bool HALF = decltype(half_tag)::value;
+    const int64_t mw = m0 + wm0, nw = n0 + wx * WTN;
+    auto store = [&](auto ct_tag, auto rd_tag) __attribute__((always_inline)) {
+        constexpr int CT = decltype(ct_tag)::value;
+        constexpr bool RD = decltype(rd_tag)::value, HALF = CT != 0;
         constexpr int VE = HALF ? 8 : 4, ES = HALF ? 2 : 4, PIECES = WTN / VE;
         constexpr int kXor = (WTN / 4 - 1) & 3;  // 16-byte chunks of FP32 in a row, at most 4 used
         const bool vec = (out.ldc * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(out.C) & 15) == 0;
@@ -337,66 +376,81 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
                 const int piece = lane + q * kWave, row = piece / PIECES, c0 = piece % PIECES * VE;
                 if (16 * PIECES % kWave != 0 && piece >= 16 * PIECES) continue;
                 const int64_t grow = mw + 16 * i + row, gcol = nw + c0;
-                float v[VE];
-#pragma unroll
-                for (int h = 0; h < VE / 4; ++h) {
-                    const int ch = ((c0 >> 2) + h) ^ ((row >> 2) & kXor);
-                    const f32x4 x = *(const MIGEMM_LDS f32x4*)(scr + row * WTN + 4 * ch);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
-                }
+                const int x4 = (row >> 2) & kXor;
                 if (grow >= p.M || gcol >= p.N) continue;
                 const int64_t idx = grow * out.ldc + gcol;
                 if (vec && gcol + VE <= p.N) {
                     u32x4* const dst =
                         reinterpret_cast<u32x4*>(static_cast<char*>(out.C) + idx * ES);
                     u32x4 old = {0u, 0u, 0u, 0u}, w = {0u, 0u, 0u, 0u};
-                    if (rd) old = *dst;
+                    if constexpr (RD) old = *dst;
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        float prev;
-                        if constexpr (HALF) {
-                            const uint32_t bits = (old[e / 2] >> (16 * (e % 2))) & 0xffffu;
-                            prev = out.c_dtype == 1
-                                       ? static_cast<float>(__builtin_bit_cast(
-                                             _Float16, static_cast<uint16_t>(bits)))
-                                       : __uint_as_float(bits << 16);
-                        } else {
-                            prev = __uint_as_float(old[e]);
-                        }
-                        const float res =
-                            rd ? fmaf(out.alpha, v[e], out.beta * prev) : out.alpha * v[e];
-                        if constexpr (HALF) {
-                            const uint32_t b =
-                                out.c_dtype == 1
-                                    ? static_cast<uint32_t>(__builtin_bit_cast(
-                                          uint16_t, static_cast<_Float16>(res)))
-                                    : static_cast<uint32_t>(f32_to_bf16_bits(res));
-                            w[e / 2] |= b << (16 * (e % 2));
-                        } else {
-                            w[e] = __float_as_uint(res);
+                    for (int h = 0; h < VE / 4; ++h) {
+                        const f32x4 x = *(const MIGEMM_LDS f32x4*)(scr + row * WTN +
+                                                                   4 * (((c0 >> 2) + h) ^ x4));
+#pragma unroll
+                        for (int e4 = 0; e4 < 4; ++e4) {
+                            const int e = 4 * h + e4;
+                            float prev = 0.0f;
+                            if constexpr (RD && HALF) {
+                                const uint32_t bits = (old[e / 2] >> (16 * (e % 2))) & 0xffffu;
+                                prev = CT == 1 ? static_cast<float>(__builtin_bit_cast(
+                                                     _Float16, static_cast<uint16_t>(bits)))
+                                               : __uint_as_float(bits << 16);
+                            } else if constexpr (RD) {
+                                prev = __uint_as_float(old[e]);
+                            }
+                            const float res = RD ? fmaf(out.alpha, x[e4], out.beta * prev)
+                                                 : out.alpha * x[e4];
+                            if constexpr (HALF) {
+                                const uint32_t b =
+                                    CT == 1 ? static_cast<uint32_t>(__builtin_bit_cast(
+                                                  uint16_t, static_cast<_Float16>(res)))
+                                            : static_cast<uint32_t>(f32_to_bf16_bits(res));
+                                w[e / 2] |= b << (16 * (e % 2));
+                            } else {
+                                w[e] = __float_as_uint(res);
+                            }
                         }
                     }
-                    if (lines)
+                    if (p.whole_lines)
                         __builtin_nontemporal_store(w, dst);
                     else
                         *dst = w;
                 } else {
-                    // edges and unaligned C, an element at a time
-#pragma unroll
+                    // edges and unaligned C, an element at a time (a rolled loop
+                    // keeps this small)
+#pragma nounroll
                     for (int e = 0; e < VE; ++e)
                         if (gcol + e < p.N)
-                            store_update<false>(out, idx + e, v[e],
-                                                rd ? load_prev(out, idx + e) : 0.0f);
+                            store_update<false>(
+                                out, idx + e,
+                                scr[row * WTN + 4 * (((c0 + e) >> 2) ^ x4) + ((c0 + e) & 3)],
+                                RD ? load_prev(out, idx + e) : 0.0f);
                 }
             }
             asm volatile("" : : : "memory");
         }
     };
-    if (out.c_dtype == 0)
-        store(No{});
-    else
-        store(Yes{});
+    using Yes = std::true_type;
+    using No = std::false_type;
+    using F32 = std::integral_constant<int, 0>;
+    using F16 = std::integral_constant<int, 1>;
+    using BF16 = std::integral_constant<int, 2>;
+    if (out.beta != 0.0f) {
+        if (out.c_dtype == 0)
+            store(F32{}, Yes{});
+        else if (out.c_dtype == 1)
+            store(F16{}, Yes{});
+        else
+            store(BF16{}, Yes{});
+    } else if (out.c_dtype == 0) {
+        store(F32{}, No{});
+    } else if (out.c_dtype == 1) {
+        store(F16{}, No{});
+    } else {
+        store(BF16{}, No{});
+    }
 }
 
 // ------------------------------------------------------------------ few rows of A
