@@ -96,10 +96,14 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
     const int left = TAIL ? chunks % 8 : 8;  // chunks in the last k-tile (TAIL: 1 to 7)
 
     // Element loads.  One covers eight rows; load q of wave wx rows 8 (wx + 4 q) +
-    // lane / 8 of the image.  The swizzle depends on the row modulo 16, so a
-    // lane's logical chunk is the same in all its loads.
+    // lane / 8 of the image.  Block 2 g + s of a row lies at chunk (4 s + g) ^
+    // swizzle: neighbouring lane groups, which share a cycle of a 16-byte LDS read,
+    // then differ in the lowest chunk bit, as the swizzle needs (with the blocks in
+    // order they differ in the next one and meet on the same banks).  The swizzle
+    // depends on the row modulo 16, so a lane's block is the same in all its loads.
     const int r0 = 8 * wx + lane / 8;
-    const int logical = (lane % 8) ^ swz_a<8>(r0);
+    const int at_chunk = (lane % 8) ^ swz_a<8>(r0);
+    const int logical = (at_chunk & 3) * 2 + (at_chunk >> 2);
     const uint32_t c16 = 16 * logical, c16_last = 16 * min(logical, left - 1);
     const int last_m = static_cast<int>(min(p.M - m0, int64_t(BX))) - 1;
     const int last_n = static_cast<int>(min(p.N - n0, int64_t(BX))) - 1;
@@ -217,7 +221,7 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
         const MIGEMM_LDS char* const is = lds + sc;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int chunk = (2 * ag + s) ^ swz_a<8>(ar);
+            const int chunk = (4 * s + ag) ^ swz_a<8>(ar);
             auto read_a = [&](int i) __attribute__((always_inline)) {
                 fa[s][i] = *(const MIGEMM_LDS u32x4*)(ia + (wm0 + ar) * 128 + chunk * 16 + i * 2048);
                 if (s == 0)
