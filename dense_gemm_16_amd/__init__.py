@@ -310,14 +310,19 @@ def migemm_version() -> int:
 
 # ---------------------------------------------------------- torch convenience
 
+_codes = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16, torch.int8: I8,
-             torch.int32: I32}
-    if t.dtype not in codes:
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16,
+                       torch.int8: I8, torch.int32: I32})
+    code = _codes.get(t.dtype)
+    if code is None:
         raise ValueError(f"unsupported dtype {t.dtype}; expected float32, float16, bfloat16, "
                          "int8 (operands) or int32 (output of an int8 product)")
-    return codes[t.dtype]
+    return code
 
 
 def _ld(t) -> int:
@@ -463,22 +468,44 @@ def _mx_operand(name, m, device):
     """(data pointer, ldd, scales pointer, ldsc) of an MxMatrix, checked."""
     import torch
     data, scales, cols = m
-    rows, blocks = data.shape[0], (cols + 31) // 32
+    u8, blocks = torch.uint8, (cols + 31) // 32
     for what, t, need in (("data", data, 16 * blocks), ("scales", scales, blocks)):
-        _check_device(f"{name}.{what}", t, device)
-        if t.dtype != torch.uint8 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < need:
-            raise ValueError(f"{name}.{what} must be a uint8 matrix of {rows} rows of at least "
-                             f"{need} bytes (got {t.dtype}, {tuple(t.shape)})")
-        # a row occupies its whole stride, the last one too
-        if rows and t.untyped_storage().nbytes() - t.storage_offset() < rows * _ld(t):
-            raise ValueError(f"{name}.{what}: the storage ends inside the last row's stride")
-    return data.data_ptr() or None, _ld(data), scales.data_ptr() or None, _ld(scales)
+        if not t.is_cuda or t.device != device:
+            _check_device(f"{name}.{what}", t, device)
+        if t.dtype != u8 or t.dim() != 2 or t.shape[0] != data.shape[0] or t.shape[1] < need:
+            raise ValueError(f"{name}.{what} must be a uint8 matrix of {data.shape[0]} rows of at "
+                             f"least {need} bytes (got {t.dtype}, {tuple(t.shape)})")
+    ldd, ldsc, rows = _ld(data), _ld(scales), data.shape[0]
+    # a row occupies its whole stride, the last one too
+    if (data.untyped_storage().nbytes() - data.storage_offset() < rows * ldd or
+            scales.untyped_storage().nbytes() - scales.storage_offset() < rows * ldsc):
+        raise ValueError(f"{name}: the storage ends inside the last row's stride")
+    return data.data_ptr() or None, ldd, scales.data_ptr() or None, ldsc
+
+
+class _DeviceOf:
+    """Makes a tensor's device torch's current one for a call, where it is not."""
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        import torch
+        self.guard = None
+        if torch.cuda.current_device() != device.index:
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
 
 
 def _stream_of(stream, device):
     """(stream handle, whether it is another one than torch's current stream)."""
     import torch
-    current = torch.cuda.current_stream(device).cuda_stream
+    current = torch._C._cuda_getCurrentRawStream(device.index)
     return (current, False) if stream is None else (stream, stream != current)
 
 
@@ -502,17 +529,18 @@ def quantize_mx(src, *, out=None, stream=None):
     op, lds = _operand(src)
     rows, cols = src.shape
     blocks = (cols + 31) // 32
-    with torch.cuda.device(device):
+    with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
         fresh = out is None
         if fresh:
-            out = MxMatrix(torch.empty((rows, 16 * max(blocks, 1)), dtype=torch.uint8,
-                                       device=device),
-                           torch.empty((rows, max(16, (blocks + 15) // 16 * 16)), dtype=torch.uint8,
-                                       device=device), cols)
-        elif out.shape != (rows, cols):
-            raise ValueError("out must have src's shape")
-        data, ldd, scales, ldsc = _mx_operand("out", out, device)
+            ldd, ldsc = 16 * max(blocks, 1), max(16, (blocks + 15) // 16 * 16)
+            out = MxMatrix(torch.empty((rows, ldd), dtype=torch.uint8, device=device),
+                           torch.empty((rows, ldsc), dtype=torch.uint8, device=device), cols)
+            data, scales = out.data.data_ptr() or None, out.scales.data_ptr() or None
+        else:
+            if out.shape != (rows, cols):
+                raise ValueError("out must have src's shape")
+            data, ldd, scales, ldsc = _mx_operand("out", out, device)
         st = migemm_quantize_mx(_dtype_code(src), op, rows, cols, src.data_ptr() or None, lds,
                                 data, ldd, scales, ldsc, stream)
         if st != OK:
@@ -529,7 +557,7 @@ def dequantize_mx(m, dtype, out=None, *, stream=None):
     device = m.device
     rows, cols = m.shape
     data, ldd, scales, ldsc = _mx_operand("m", m, device)
-    with torch.cuda.device(device):
+    with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
         fresh = out is None
         if fresh:
@@ -560,7 +588,7 @@ def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=
         raise ValueError(f"inner dimensions differ: {a.shape} x {b.shape} transposed")
     pa, lda, psa, ldsa = _mx_operand("a", a, device)
     pb, ldb, psb, ldsb = _mx_operand("b", b, device)
-    with torch.cuda.device(device):
+    with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
         fresh = out is None
         if fresh:
@@ -613,6 +641,8 @@ def _row_gradient(grad, device, rows):
     if not isinstance(grad, torch.Tensor):
         return torch.full((rows,), float(grad), dtype=torch.float32, device=device)
     _check_device("grad", grad, device)
+    if grad.dtype == torch.float32 and tuple(grad.shape) == (rows,) and grad.is_contiguous():
+        return grad
     if grad.dim() > 1 or (grad.dim() == 1 and grad.shape[0] != rows):
         raise ValueError(f"grad must be a number or a vector of {rows}")
     return grad.to(torch.float32).expand(rows).contiguous()
@@ -661,7 +691,7 @@ def linear_cross_entropy(x, w, target, *, ignore_index: int = -100, stream=None)
     import torch
     device, T, V, D, dt, ptrs = _layer(x, w)
     pt = _row_vector("target", target, device, torch.int64, T)
-    with torch.cuda.device(device):
+    with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
         loss = torch.empty(T, dtype=torch.float32, device=device)
         lse = torch.empty(T, dtype=torch.float32, device=device)
@@ -687,7 +717,7 @@ def linear_cross_entropy_backward(x, w, target, lse, grad, *, ignore_index: int 
     device, T, V, D, dt, ptrs = _layer(x, w)
     pt = _row_vector("target", target, device, torch.int64, T)
     pl = _row_vector("lse", lse, device, torch.float32, T)
-    with torch.cuda.device(device):
+    with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
         grad = _row_gradient(grad, device, T)
         dx, dw = _gradient("dx", need_dx, dx, x), _gradient("dw", need_dw, dw, w)
@@ -727,7 +757,7 @@ def linear_distillation(x, w, teacher_logits, teacher_index, *, temperature: flo
     import torch
     device, T, V, D, dt, ptrs = _layer(x, w)
     teacher, top = _teacher(teacher_logits, teacher_index, T, device)
-    with torch.cuda.device(device):
+    with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
         loss = torch.empty(T, dtype=torch.float32, device=device)
         lse = torch.empty(T, dtype=torch.float32, device=device)
@@ -756,7 +786,7 @@ def linear_distillation_backward(x, w, teacher_logits, teacher_index, lse, stude
     _check_device("student", student, device)
     if student.dtype != torch.float32 or tuple(student.shape) != (T, top):
         raise ValueError(f"student must be float32, {T} x {top}")
-    with torch.cuda.device(device):
+    with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
         grad = _row_gradient(grad, device, T)
         dx, dw = _gradient("dx", need_dx, dx, x), _gradient("dw", need_dw, dw, w)

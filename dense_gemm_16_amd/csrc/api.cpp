@@ -226,7 +226,11 @@ void select(const GemmArgs& g, bool aligned, int& variant, int& config) {
         // against 66 TFLOPS at 1024^3 (64x64 tiles, 8 waves) and 142 against 124
         // at 4096^3 (128x128 tiles).  Other operands stage through registers.
         variant = MIGEMM_REGTILE_MFMA;
-        const bool direct = aligned && K % 4 == 0 && (tb || N % 4 == 0) && (!ta || M % 4 == 0);
+        // (pad_a: A is zero-filled to whole chunks, and K may end anywhere where B
+        // holds k as its row index)
+        const bool k_whole = K % 4 == 0 || (g.pad_a && !ta && !tb);
+        const bool direct = aligned && k_whole && (tb || N % 4 == 0) &&
+                            (!ta || M % 4 == 0 || g.pad_a);
         // split-K (configuration 12): at most half a round of 64x64 tiles, where a
         // workspace for the slices' sums is lent
         const bool splitk = direct && tiles(64, 64) <= 128 && K >= kSplitKMinK32 &&
@@ -257,7 +261,11 @@ void select(const GemmArgs& g, bool aligned, int& variant, int& config) {
     // register-staged kernel otherwise.  Other operands are packed into
     // zero-padded copies for the direct kernel once the product is large
     // enough for the extra copy launch to pay.
-    const bool direct = aligned && K % 8 == 0 && (tb || N % 8 == 0) && (!ta || M % 8 == 0);
+    // pad_a: A is zero-filled to whole chunks, and K may end anywhere where B holds
+    // k as its row index (configuration 10's partial first k-tile excepted).
+    const bool chunks = K % 8 == 0;
+    const bool direct = aligned && (chunks || (g.pad_a && !ta && !tb)) && (tb || N % 8 == 0) &&
+                        (!ta || M % 8 == 0 || g.pad_a);
     const bool ktiles = K % 64 == 0;
     const double work = static_cast<double>(M) * static_cast<double>(N) * static_cast<double>(K);
     const int pc = tiles(256, 256) >= 256 ? 11 : 12;  // packed copies, then config 14/10 or 7
@@ -294,7 +302,7 @@ void select(const GemmArgs& g, bool aligned, int& variant, int& config) {
         config = small_whole;
     else if (direct && ktiles && tiles(256, 256) >= 256 && whole256)
         config = 14;  // direct 256x256x64, ping-pong wave groups (whole tiles only)
-    else if (direct && tiles(256, 256) >= 256)
+    else if (direct && chunks && tiles(256, 256) >= 256)
         config = 10;  // direct 256x256x64, 8 waves, 16x16x32, AGPR accumulators, early loads
                       // (a K that ends inside a k-tile: the partial k-tile first)
     else if (direct && ktiles && tiles(128, 256) >= 256 && M % 128 == 0 && N % 256 == 0)
@@ -323,7 +331,7 @@ void select(const GemmArgs& g, bool aligned, int& variant, int& config) {
 int prepare(int& variant, int& config, int op_a, int op_b, int64_t M, int64_t N, int64_t K,
             int dtype, const void* A, int64_t lda, const void* B, int64_t ldb, float alpha,
             float beta, int c_dtype, void* C, int64_t ldc, void* ws, int64_t ws_bytes,
-            void* stream, bool need_ptrs, GemmArgs& g) {
+            void* stream, bool need_ptrs, GemmArgs& g, bool pad_a = false) {
     if (!known_op(op_a) || !known_op(op_b)) return MIGEMM_ERR_INVALID_ARG;
     const bool ta = op_a == MIGEMM_OP_T, tb = op_b == MIGEMM_OP_T;
     int st = check_args(M, N, K, dtype, ta, tb, A, lda, B, ldb, C, ldc, c_dtype, need_ptrs);
@@ -342,6 +350,7 @@ int prepare(int& variant, int& config, int op_a, int op_b, int64_t M, int64_t N,
                  Epi{C, ldc, alpha, beta, c_dtype}, static_cast<hipStream_t>(stream)};
     g.ws = ws;
     g.ws_bytes = ws ? ws_bytes : 0;
+    g.pad_a = pad_a;
     const bool aligned = operands_aligned(A, lda, B, ldb, dtype);
     if (variant == MIGEMM_VARIANT_AUTO) {
         if (config != -1) return MIGEMM_ERR_INVALID_ARG;
@@ -449,24 +458,24 @@ int write_text(const std::string& text, char* buf, int buflen) {
 int run_gemm(int variant, int config, int op_a, int op_b, int64_t M, int64_t N, int64_t K,
              int dtype, const void* A, int64_t lda, const void* B, int64_t ldb, float alpha,
              float beta, int c_dtype, void* C, int64_t ldc, void* ws, int64_t ws_bytes,
-             void* stream) {
+             void* stream, bool pad_a) {
     GemmArgs g{};
     const int st = prepare(variant, config, op_a, op_b, M, N, K, dtype, A, lda, B, ldb, alpha,
-                           beta, c_dtype, C, ldc, ws, ws_bytes, stream, true, g);
+                           beta, c_dtype, C, ldc, ws, ws_bytes, stream, true, g, pad_a);
     if (st != MIGEMM_OK) return st;
     return hip_status(launch(g, variant, config));
 }
 
 int workspace_bytes(int variant, int config, int op_a, int op_b, int64_t M, int64_t N,
                     int64_t K, int dtype, const void* A, int64_t lda, const void* B,
-                    int64_t ldb, int64_t* bytes) {
+                    int64_t ldb, int64_t* bytes, bool pad_a) {
     if (!bytes) return MIGEMM_ERR_INVALID_ARG;
     GemmArgs g{};
     // as if an unbounded workspace were lent, so the selection may pick the packed path
     const int c_dtype = dtype == MIGEMM_I8 ? MIGEMM_I32 : MIGEMM_F32;
     const int st = prepare(variant, config, op_a, op_b, M, N, K, dtype, A, lda, B, ldb, 1.0f,
                            0.0f, c_dtype, nullptr, N > 1 ? N : 1, nullptr, INT64_MAX, nullptr,
-                           false, g);
+                           false, g, pad_a);
     if (st != MIGEMM_OK) return st;
     *bytes = config_workspace_bytes(g, variant, config);
     return MIGEMM_OK;

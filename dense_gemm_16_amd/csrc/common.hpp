@@ -356,15 +356,16 @@ int hip_status(hipError_t err);
 // The C ABI's common path (api.cpp): validates one call, selects its variant
 // and configuration (variant -1: the selection table's; config -1: the table's
 // choice for the variant), and launches it with the workspace lent (ws may be
-// NULL).  Returns a migemm_status.
+// NULL).  Returns a migemm_status.  pad_a: A's contiguous side is zero-filled up to
+// a whole 16-byte chunk inside its leading dimension (GemmArgs::pad_a).
 int run_gemm(int variant, int config, int op_a, int op_b, int64_t M, int64_t N, int64_t K,
              int dtype, const void* A, int64_t lda, const void* B, int64_t ldb, float alpha,
              float beta, int c_dtype, void* C, int64_t ldc, void* ws, int64_t ws_bytes,
-             void* stream);
+             void* stream, bool pad_a = false);
 // The workspace bytes such a call uses when lent enough (api.cpp).
 int workspace_bytes(int variant, int config, int op_a, int op_b, int64_t M, int64_t N,
                     int64_t K, int dtype, const void* A, int64_t lda, const void* B,
-                    int64_t ldb, int64_t* bytes);
+                    int64_t ldb, int64_t* bytes, bool pad_a = false);
 
 // Configuration tables, one per variant (names, and the count).
 int naive_config_count();

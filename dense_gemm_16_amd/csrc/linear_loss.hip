@@ -242,11 +242,12 @@ __global__ __launch_bounds__(1024) void loss_factor_kernel(const LossRow* __rest
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int w = 1; w < 16; ++w) m = fmaxf(m, part[w]);
-    // exponent of m: m in [2^e, 2^(e+1)); factor 2^(13 - e), within +-100
-    int e = m > 0.0f ? ilogbf(m) : 13;
-    e = min(max(13 - e, -100), 100);
-    factor[0] = ldexpf(1.0f, e);
-    factor[1] = ldexpf(1.0f, -e);
+    // 2^14 / m, within 2^+-100.  Not a power of two: where all rows weigh the same
+    // (a mean), c (q - 1) lies just below 2^14, where FP16's steps are finest
+    // relative to it, and c itself is exact.
+    const float f = fminf(fmaxf(m > 0.0f ? 16384.0f / m : 1.0f, 0x1p-100f), 0x1p100f);
+    factor[0] = f;
+    factor[1] = 1.0f / f;
 }
 
 // A wavefront per row: dz at the indices inside [v0, v1).  An index that a row

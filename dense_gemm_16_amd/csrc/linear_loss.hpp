@@ -130,7 +130,7 @@ struct DzOut : Epi {
     E* dz;
     int64_t ldz, rows, v0;
     const LossRow* info;  // padded to whole tiles of rows
-    const float* factor;  // NULL, or a power of two that keeps FP16 derivatives normal
+    const float* factor;  // NULL, or what brings FP16 derivatives to the top of their range
     float scale;          // s
     template <class Cfg, class Acc>
     __device__ __forceinline__ void store(const Acc (&acc)[Cfg::TM][Cfg::TN],
@@ -186,8 +186,68 @@ struct DzOut : Epi {
     }
 };
 
-// One product X W^T (M x N, K deep) with either output step.  A and B are
-// 16-byte aligned with leading dimensions and K in whole 16-byte chunks.
+// Output step of dw = dz^T x where the products' own does not do: the sums times
+// *factor (FP16: taking out the factor that dz holds), rounded into the
+// operands' type, columns below `cols` only (x is a copy padded to whole chunks).
+// As DzOut, through LDS into 16-byte row pieces.
+template <typename E>
+struct GradOut : Epi {
+    E* grad;
+    int64_t ldg, cols;
+    const float* factor;
+    template <class Cfg, class Acc>
+    __device__ __forceinline__ void store(const Acc (&acc)[Cfg::TM][Cfg::TN],
+                                          MIGEMM_LDS char* smem, int64_t m, int64_t n, int wave,
+                                          int lane, int64_t M, int64_t) const {
+        constexpr int TM = Cfg::TM, TN = Cfg::TN, WTN = Cfg::WTN;
+        constexpr int ES = sizeof(E), VE = 16 / ES, PIECES = WTN / VE;
+        using Bits = std::conditional_t<ES == 4, uint32_t, uint16_t>;
+        constexpr int kBytes = 16 * WTN * ES;
+        static_assert(Cfg::MF == 16 && Cfg::NW * kBytes <= Cfg::LDS_BYTES, "scratch fits");
+        MIGEMM_LDS char* const scr = smem + wave * kBytes;
+        const float f = factor ? *factor : 1.0f;
+        const bool vec = (ldg * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(grad) & 15) == 0;
+        const int g = lane >> 4, lj = lane & 15;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int r = 4 * g + e, c = 16 * j + lj;
+                    const int piece = (c / VE) ^ ((g << 1) & (PIECES - 1));
+                    *(MIGEMM_LDS Bits*)(scr + (r * WTN + piece * VE + c % VE) * ES) =
+                        __builtin_bit_cast(Bits, narrow<E>(acc[i][j][e] * f));
+                }
+            asm volatile("" : : : "memory");
+#pragma unroll
+            for (int q = 0; q < (16 * PIECES + kWave - 1) / kWave; ++q) {
+                const int p = lane + q * kWave, r = p / PIECES, c = p % PIECES;
+                if (16 * PIECES % kWave != 0 && p >= 16 * PIECES) continue;
+                const int phys = c ^ (((r >> 2) << 1) & (PIECES - 1));
+                const MIGEMM_LDS char* const from = scr + (r * WTN + phys * VE) * ES;
+                const int64_t grow = m + 16 * i + r, gcol = n + c * VE;
+                if (grow >= M || gcol >= cols) continue;
+                E* const to = grad + grow * ldg + gcol;
+                if (vec && gcol + VE <= cols) {
+                    *reinterpret_cast<u32x4*>(to) = *(const MIGEMM_LDS u32x4*)from;
+                } else {
+#pragma nounroll
+                    for (int e = 0; e < VE; ++e)
+                        if (gcol + e < cols)
+                            reinterpret_cast<Bits*>(to)[e] =
+                                *(const MIGEMM_LDS Bits*)(from + e * ES);
+                }
+            }
+            asm volatile("" : : : "memory");
+        }
+    }
+};
+
+// One product with one of the output steps: X W^T (M x N, K deep) with lse or dz,
+// or dz^T X (A stored K x M, zero-filled to whole chunks, B stored K x N) with
+// grad.  A and B are 16-byte aligned with leading dimensions in whole 16-byte
+// chunks, and so are K (lse, dz) or N (grad).
 struct LossTile {
     int64_t M, N, K;
     int dtype;
@@ -196,8 +256,9 @@ struct LossTile {
     const void* B;
     int64_t ldb;
     hipStream_t stream;
-    const LseOut* lse;  // the forward step, or
-    const void* dz;     // the backward one (DzOut of the type)
+    const LseOut* lse;
+    const void* dz;    // DzOut of the type
+    const void* grad;  // GradOut of the type
 };
 
 // The tile configuration for a product of these sizes, its chunk width (columns
@@ -245,8 +306,7 @@ hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const
 hipError_t launch_loss_prepare(const LossArgs& a, const float* lse, const float* grad,
                                LossRow* info, int64_t rows_info, void* copy, int64_t rows,
                                int64_t ldc, float* tp);
-// factor[0] = a power of two that brings the largest |coef| into [2^13, 2^14),
-// factor[1] its inverse.
+// factor[0] = what brings the largest |coef| to 2^14, factor[1] its inverse.
 hipError_t launch_loss_factor(const LossRow* info, int64_t rows, float* factor, hipStream_t s);
 // Overwrites the entries of dz that distillation's indices name.
 hipError_t launch_loss_scatter(const LossArgs& a, const LossRow* info, const float* tp,

@@ -56,9 +56,8 @@ struct Plan {
     int64_t part = 0, chunks = 0;
     // backward
     int64_t t_pad = 0, piece = 0, pieces = 0, ldz = 0, cols = 0;
-    bool dx_acc = false, dw_acc = false, tail_w = false;
-    int64_t info = 0, factor = 0, dz = 0, acc_x = 0, acc_w = 0, tail = 0, tp = 0, gemm = 0,
-            gemm_bytes = 0;
+    bool dx_acc = false;
+    int64_t info = 0, factor = 0, dz = 0, acc_x = 0, tp = 0, gemm = 0, gemm_bytes = 0;
     int64_t take(int64_t n) {
         const int64_t at = bytes;
         bytes += round_up(n, 256);
@@ -97,34 +96,28 @@ Plan make_plan(const LossArgs& a, bool backward) {
     if (p.piece > a.V) p.piece = a.V;
     p.pieces = ceil_div(a.V, p.piece);
     p.ldz = round_up(p.piece, 64);
-    // FP16 gradients go through FP32 with the factor that keeps dz normal taken
-    // out again, and rows that end inside a chunk through FP32 rows of whole ones
+    // FP16: dz holds a factor that the gradients' output steps take out again; and
+    // rows that end inside a chunk are computed as whole ones
     p.wide = a.dtype == MIGEMM_F16 || !whole;
     p.cols = whole ? a.D : p.ld_copy;
-    p.dw_acc = p.wide;
     p.dx_acc = p.wide || (a.dtype != MIGEMM_F32 && p.pieces > 1);
-    p.tail_w = !p.copy_w && a.V % epc != 0;
     p.info = p.take(round_up(a.T, 256) * static_cast<int64_t>(sizeof(LossRow)));
     p.factor = p.take(256);
     p.dz = p.take(p.t_pad * p.ldz * es);
     if (p.dx_acc) p.acc_x = p.take(a.T * p.cols * 4);
-    if (p.dw_acc) p.acc_w = p.take(p.piece * p.cols * 4);
     const int64_t last = a.V - (p.pieces - 1) * p.piece;
-    if (p.tail_w) p.tail = p.take(round_up(last, 64) * p.ld_copy * es);
     if (a.top) p.tp = p.take(a.T * a.top * 4);
     // what the two products ask for, for a full piece and the last one (their
     // operands are aligned; NULL stands for that)
     for (int64_t n : {p.piece, last}) {
         int64_t b = 0;
-        const int64_t k = n % epc == 0 ? n : round_up(n, 64);
-        if (workspace_bytes(-1, -1, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, k, a.dtype, nullptr,
-                            p.ldz, nullptr, p.copy_w || k != n ? p.ld_copy : a.ldw, &b) ==
-                MIGEMM_OK &&
+        if (workspace_bytes(-1, -1, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, n, a.dtype, nullptr,
+                            p.ldz, nullptr, p.copy_w ? p.ld_copy : a.ldw, &b, true) == MIGEMM_OK &&
             b > p.gemm_bytes)
             p.gemm_bytes = b;
-        const int64_t m = n / epc * epc;
-        if (m > 0 && workspace_bytes(-1, -1, MIGEMM_OP_T, MIGEMM_OP_N, m, p.cols, p.t_pad, a.dtype,
-                                     nullptr, p.ldz, nullptr, p.ld_copy, &b) == MIGEMM_OK &&
+        if (!p.wide &&
+            workspace_bytes(-1, -1, MIGEMM_OP_T, MIGEMM_OP_N, n, p.cols, p.t_pad, a.dtype, nullptr,
+                            p.ldz, nullptr, p.ld_copy, &b, true) == MIGEMM_OK &&
             b > p.gemm_bytes)
             p.gemm_bytes = b;
     }
@@ -156,7 +149,7 @@ int forward(const LossArgs& a, float* loss, float* lse, void* ws) {
     out.part = reinterpret_cast<RowStat*>(at(ws, p.part));
     out.chunks = p.chunks;
     out.scale = kLog2e / a.tau;
-    const LossTile t{a.T, a.V, p.depth, a.dtype, x, ldx, w, ldw, a.stream, &out, nullptr};
+    const LossTile t{a.T, a.V, p.depth, a.dtype, x, ldx, w, ldw, a.stream, &out, nullptr, nullptr};
     st = hip_status(launch_loss(t, loss_shape(a.dtype, a.T, a.V, p.depth).config));
     if (st != MIGEMM_OK) return st;
     return hip_status(
@@ -174,14 +167,41 @@ hipError_t launch_dz(const LossArgs& a, const Plan& p, const void* x, const void
     out.info = reinterpret_cast<const LossRow*>(at(ws, p.info));
     out.factor = factor;
     out.scale = kLog2e / a.tau;
-    const LossTile t{a.T, n, p.depth, a.dtype, x, p.ld_copy, w, ldw, a.stream, nullptr, &out};
+    const LossTile t{a.T, n, p.depth, a.dtype, x, p.ld_copy, w, ldw, a.stream, nullptr, &out,
+                     nullptr};
     return launch_loss(t, loss_shape(a.dtype, a.T, n, p.depth).config);
+}
+
+// dw's rows of one piece, through the factor and the column limit.  Columns past
+// whole 256-wide tiles, where few, take narrow tiles of their own: a 256-wide one
+// for eight columns would cost as much as one for 256.
+template <typename E>
+hipError_t launch_grad(const LossArgs& a, const Plan& p, const void* dz, int64_t ldz,
+                       const void* x, int64_t n, const float* factor, void* dw, int64_t lddw) {
+    GradOut<E> out{};
+    out.grad = static_cast<E*>(dw);
+    out.ldg = lddw;
+    out.cols = a.D;
+    out.factor = factor;
+    LossTile t{n, p.cols, p.t_pad, a.dtype, dz, ldz, x, p.ld_copy, a.stream, nullptr, nullptr,
+               &out};
+    const LossShape s = loss_shape(a.dtype, n, p.cols, p.t_pad);
+    const int64_t rest = p.cols % 256;
+    if (s.bn != 256 || p.cols < 256 || rest == 0 || rest > 64) return launch_loss(t, s.config);
+    t.N -= rest;
+    const hipError_t e = launch_loss(t, loss_shape(a.dtype, n, t.N, p.t_pad).config);
+    if (e != hipSuccess) return e;
+    t.B = static_cast<const E*>(x) + t.N;
+    out.grad += t.N;
+    out.cols -= t.N;
+    t.N = rest;
+    return launch_loss(t, 0);
 }
 
 int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, int64_t lddx,
              void* dw, int64_t lddw, void* ws) {
     const Plan p = make_plan(a, true);
-    const int64_t es = elem_size(a.dtype), epc = 16 / es;
+    const int64_t es = elem_size(a.dtype);
     LossRow* const info = reinterpret_cast<LossRow*>(at(ws, p.info));
     float* const tp = a.top ? reinterpret_cast<float*>(at(ws, p.tp)) : nullptr;
     void* const x = at(ws, p.x);
@@ -219,45 +239,26 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
             MIGEMM_TRY(
                 hip_status(launch_loss_scatter(a, info, tp, factor, dz, ldz, v0, v0 + n)));
         if (dx) {
-            // k: the piece's columns, in whole chunks; past them dz is 0, and the
-            // rows of w read there must exist and be finite: the copies' zeros
-            const void* wk = wp;
-            int64_t ldk = ldw, k = n;
-            if (n % epc != 0) {
-                k = ldz;
-                if (p.tail_w) {
-                    wk = at(ws, p.tail);
-                    ldk = p.ld_copy;
-                    MIGEMM_TRY(hip_status(launch_pad_copy(a.dtype, n, a.D, wp, ldw,
-                                                          at(ws, p.tail), ldz, ldk, a.stream)));
-                }
-            }
             void* const c = p.dx_acc ? at(ws, p.acc_x) : dx;
             const int ct = p.dx_acc ? MIGEMM_F32 : a.dtype;
-            MIGEMM_TRY(run_gemm(-1, -1, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, k, a.dtype, dz, ldz,
-                                wk, ldk, 1.0f, v0 ? 1.0f : 0.0f, ct, c, p.dx_acc ? p.cols : lddx,
-                                gws, p.gemm_bytes, a.stream));
+            MIGEMM_TRY(run_gemm(-1, -1, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, n, a.dtype, dz, ldz,
+                                wp, ldw, 1.0f, v0 ? 1.0f : 0.0f, ct, c, p.dx_acc ? p.cols : lddx,
+                                gws, p.gemm_bytes, a.stream, true));
         }
         if (dw) {
             char* const to = static_cast<char*>(dw) + v0 * lddw * es;
-            char* const c = p.dw_acc ? at(ws, p.acc_w) : to;
-            const int ct = p.dw_acc ? MIGEMM_F32 : a.dtype;
-            const int64_t ldc = p.dw_acc ? p.cols : lddw, m = n / epc * epc;
-            if (m > 0)
-                MIGEMM_TRY(run_gemm(-1, -1, MIGEMM_OP_T, MIGEMM_OP_N, m, p.cols, p.t_pad, a.dtype,
-                                    dz, ldz, x, p.ld_copy, 1.0f, 0.0f, ct, c, ldc, gws,
-                                    p.gemm_bytes, a.stream));
-            if (m < n) {
-                // the last rows, fewer than a chunk
-                GemmArgs g{n - m, p.cols, p.t_pad, a.dtype, true, false,
-                           static_cast<const char*>(dz) + m * es, ldz, x, p.ld_copy,
-                           Epi{c + m * ldc * elem_size(ct), ldc, 1.0f, 0.0f, ct}, a.stream};
-                MIGEMM_TRY(hip_status(launch_skinny(g)));
-            }
-            if (p.dw_acc)
-                MIGEMM_TRY(hip_status(launch_scaled_convert(a.dtype, n, a.D,
-                                                            reinterpret_cast<float*>(c), p.cols,
-                                                            inverse, to, lddw, a.stream)));
+            if (!p.wide)
+                MIGEMM_TRY(run_gemm(-1, -1, MIGEMM_OP_T, MIGEMM_OP_N, n, p.cols, p.t_pad, a.dtype,
+                                    dz, ldz, x, p.ld_copy, 1.0f, 0.0f, a.dtype, to, lddw, gws,
+                                    p.gemm_bytes, a.stream, true));
+            else if (a.dtype == MIGEMM_F32)
+                MIGEMM_TRY(hip_status(launch_grad<float>(a, p, dz, ldz, x, n, inverse, to, lddw)));
+            else if (a.dtype == MIGEMM_F16)
+                MIGEMM_TRY(
+                    hip_status(launch_grad<_Float16>(a, p, dz, ldz, x, n, inverse, to, lddw)));
+            else
+                MIGEMM_TRY(
+                    hip_status(launch_grad<bf16_t>(a, p, dz, ldz, x, n, inverse, to, lddw)));
         }
     }
     if (dx && p.dx_acc)

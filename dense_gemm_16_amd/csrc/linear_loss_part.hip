@@ -29,14 +29,15 @@ template <> struct Tile<float, 1> {
     using Cfg = DirectCfg<float, 128, 128, 2, 4, 16, 4, 32, 4, 2, 48>;
 };
 
-template <class Cfg, class Out>
+template <class Cfg, bool TRANS, class Out>
 hipError_t launch_with(const LossTile& t, const Out& out) {
     using E = typename Cfg::E;
     GemmArgs g{};
+    g.ta = g.pad_a = TRANS;
     g.M = t.M;
     g.N = t.N;
     g.K = t.K;
-    g.tb = true;
+    g.tb = !TRANS;
     g.A = t.A;
     g.lda = t.lda;
     g.B = t.B;
@@ -48,15 +49,19 @@ hipError_t launch_with(const LossTile& t, const Out& out) {
     const dim3 grid(static_cast<unsigned>(tm * tn)), block(Cfg::NT);
     const E* A = static_cast<const E*>(g.A);
     const E* B = static_cast<const E*>(g.B);
-    constexpr bool kTail = (Cfg::FLAGS & 32) != 0, kHead = (Cfg::FLAGS & 64) != 0;
     const int itm = static_cast<int>(tm), itn = static_cast<int>(tn);
-    if ((kTail || kHead) && g.K % Cfg::BK != 0)
-        return launch_kernel(
-            g, mfma16_direct_kernel<Cfg, false, false, true, kTail, kHead, false, Out>, grid,
-            block, g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
-    return launch_kernel(g,
-                         mfma16_direct_kernel<Cfg, false, false, true, false, false, false, Out>,
-                         grid, block, g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
+    if constexpr (TRANS) {
+        if (g.K % Cfg::BK != 0) return hipErrorInvalidValue;  // K is padded to whole k-tiles
+    } else {
+        constexpr bool kTail = (Cfg::FLAGS & 32) != 0, kHead = (Cfg::FLAGS & 64) != 0;
+        if ((kTail || kHead) && g.K % Cfg::BK != 0)
+            return launch_kernel(
+                g, mfma16_direct_kernel<Cfg, false, false, true, kTail, kHead, false, Out>, grid,
+                block, g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
+    }
+    return launch_kernel(
+        g, mfma16_direct_kernel<Cfg, false, TRANS, !TRANS, false, false, false, Out>, grid, block,
+        g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
 }
 
 }  // namespace
@@ -64,8 +69,9 @@ hipError_t launch_with(const LossTile& t, const Out& out) {
 template <typename E, int C>
 hipError_t launch_loss_tile(const LossTile& t) {
     using Cfg = typename Tile<E, C>::Cfg;
-    if (t.lse) return launch_with<Cfg>(t, *t.lse);
-    return launch_with<Cfg>(t, *static_cast<const DzOut<E>*>(t.dz));
+    if (t.lse) return launch_with<Cfg, false>(t, *t.lse);
+    if (t.dz) return launch_with<Cfg, false>(t, *static_cast<const DzOut<E>*>(t.dz));
+    return launch_with<Cfg, true>(t, *static_cast<const GradOut<E>*>(t.grad));
 }
 
 #if defined(MIGEMM_PART_E) && defined(MIGEMM_PART_C)

@@ -142,7 +142,7 @@ SplitKPlan splitk16_plan(const GemmArgs& g) {
     const int64_t t128 = ceil_div(g.M, 128) * ceil_div(g.N, 128);
     const int64_t t256 = ceil_div(g.M, 256) * ceil_div(g.N, 256);
     const int64_t s128 = round_slices(t128);
-    if (t256 >= 16) {
+    if (t256 >= 16 && g.K % 8 == 0) {  // (configuration 10 takes whole chunks of k)
         const int64_t ks = splitk_slice(g.K, round_slices(t256));
         if (ks >= kMinSlice256 || (t128 * s128 > 256 && ks >= kMinSlice256Overshoot))
             return SplitKPlan{10, ceil_div(g.K, ks)};
@@ -241,7 +241,7 @@ hipError_t launch_splitk16(const GemmArgs& g) {
         return hipErrorInvalidValue;
     // the slices run on the direct kernel only; operands it cannot read in
     // place take the ordinary 128x128 path instead
-    if (!direct_ok(g, 8, true, 8) || g.K % 8 != 0) return launch_mfma16(g, 7);
+    if (!direct_ok(g, 8, true, 8) || (g.K % 8 != 0 && !g.pad_a)) return launch_mfma16(g, 7);
     GemmArgs p = g;
     p.splitk = static_cast<int>(S);
     p.out = Epi{g.ws, g.N, 1.0f, 0.0f, 0};  // FP32 slice sums, plain, leading dimension N

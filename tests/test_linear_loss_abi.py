@@ -104,9 +104,7 @@ def test_workspace_size():
     assert ws_bytes(1, top=8)[1] >= backward + T * 8 * 4
     # a misaligned weight is copied: V rounded up to 64 rows more
     assert ws_bytes(0, W=W + 2)[1] >= forward + 320 * 64 * 2
-    # (a vocabulary that ends inside a chunk has its last piece copied in any case)
-    assert ws_bytes(1, ldw=D + 1)[1] == backward
-    assert ws_bytes(1, V=304, ldw=D + 1)[1] >= ws_bytes(1, V=304)[1] + 320 * 64 * 2
+    assert ws_bytes(1, ldw=D + 1)[1] >= backward + 320 * 64 * 2
     assert ws_bytes(0, T=0) == (mg.OK, 0)
     for kw in ({"T": -1}, {"V": 0}, {"D": 0}, {"dtype": mg.I32}, {"ldx": 1}, {"top": 1025},
                {"top": -1}):
