@@ -42,6 +42,7 @@ __device__ __forceinline__ float row_dot(const E* __restrict__ x, const E* __res
                                          int64_t depth, int lane) {
     constexpr int EPC = 16 / sizeof(E);
     float s = 0.0f;
+#pragma unroll 4
     for (int64_t c = static_cast<int64_t>(lane) * EPC; c < depth; c += kWave * EPC) {
         const u32x4 xr = *reinterpret_cast<const u32x4*>(x + c);
         const u32x4 wr = *reinterpret_cast<const u32x4*>(w + c);
@@ -108,9 +109,20 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     float m = -INFINITY, s = 0.0f;
-    for (int64_t c = threadIdx.x; c < chunks; c += kThreads) {
-        const RowStat r = part[row * chunks + c];
-        join(m, s, r.largest, r.sum);
+    // eight chunks at a time, their loads in flight together (a row of 8192 chunks
+    // joined one by one took 25 us)
+    constexpr int kAhead = 8;
+    const RowStat* const stats = part + row * chunks;
+    for (int64_t c = threadIdx.x; c < chunks; c += kAhead * kThreads) {
+        RowStat r[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t at = c + i * kThreads;
+            r[i] = stats[at < chunks ? at : c];
+            if (at >= chunks) r[i].sum = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) join(m, s, r[i].largest, r[i].sum);
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) {

@@ -22,27 +22,34 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The four-bit code of |y| < 8 (sign 0): below 2 the values are multiples of
-// 0.5, below 4 of 1, above of 2, so one rounding to the nearest even integer in
-// that unit gives the code's offset in its binade.
-__device__ __forceinline__ uint32_t fp4_code(float y) {
-    const float a = fabsf(y);
-    const float unit = a < 2.0f ? 2.0f : a < 4.0f ? 1.0f : 0.5f;
-    const int base = a < 2.0f ? 0 : a < 4.0f ? 2 : 4;
-    const int n = static_cast<int>(rintf(a * unit)) + base;
-    return static_cast<uint32_t>(min(n, 7)) | ((__float_as_uint(y) >> 28) & 8u);
+// The larger of m and |x|, NaN if either is (v_maximum3_f32 takes two elements).
+__device__ __forceinline__ float largest_of(float m, float x) {
+    return __builtin_elementwise_maximum(m, fabsf(x));
 }
 
-// The scale byte of a block whose largest magnitude has the FP32 bits `m` (sign
-// cleared; infinities and NaN are 0x7f800000 and above).
-__device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
-    const int e = static_cast<int>(m >> 23);
-    return e == 255 ? 255u : static_cast<uint32_t>(max(e - 2, 0));
+// The scale byte of a block whose largest magnitude is m.
+__device__ __forceinline__ uint32_t scale_byte(float m) {
+    const int e = static_cast<int>(__float_as_uint(m) >> 23);  // sign 0
+    return e >= 255 ? 255u : static_cast<uint32_t>(max(e - 2, 0));
 }
 
 // 2^(127 - b), the factor that brings a block of scale byte b to element units;
-// 0 for a NaN block, whose codes are 0 (its elements are dropped by the caller).
-__device__ __forceinline__ float unscale(uint32_t b) { return __uint_as_float((254u - b) << 23); }
+// 0 for a NaN block, whose codes are dropped by the caller.
+__device__ __forceinline__ float unscale(uint32_t b) {
+    return b == 255u ? 0.0f : __uint_as_float((254u - b) << 23);
+}
+
+// The codes of eight values in element units: the hardware rounds to the nearest
+// code, midpoints to the even one, larger magnitudes to 6 (its own scale operand
+// stays 1: a block's 2^e may be subnormal).  Spelled out in integer arithmetic the
+// rounding took 12 instructions an element and bounded the kernel.
+__device__ __forceinline__ uint32_t fp4_codes(const float (&y)[8]) {
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[0], y[1], 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[2], y[3], 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[4], y[5], 1.0f, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[6], y[7], 1.0f, 3);
+}
 
 // Eight consecutive elements from column c of a row, zeros past cols.
 template <typename T, bool VEC>
@@ -78,61 +85,89 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
     if (row >= rows || piece / 4 >= blocks) return;
     float v[8];
     load8<T, VEC>(src + row * lds, piece * 8, cols, v);
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 1)));
-    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 2)));
+    for (int i = 0; i < 8; ++i) m = largest_of(m, v[i]);
+    m = largest_of(m, __shfl_xor(m, 1));
+    m = largest_of(m, __shfl_xor(m, 2));
     const uint32_t b = scale_byte(m);
     const float f = unscale(b);
-    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w |= fp4_code(v[i] * f) << (4 * i);
-    if (b == 255u) w = 0;
+    for (int i = 0; i < 8; ++i) v[i] *= f;
+    const uint32_t w = b == 255u ? 0u : fp4_codes(v);
     *reinterpret_cast<uint32_t*>(data + row * ldd + piece * 4) = w;
     if (piece % 4 == 0) scales[row * ldsc + piece / 4] = static_cast<uint8_t>(b);
 }
 
-// k as the row index of the source (OP_T): a workgroup takes 64 rows of the
-// result by 8 blocks; a lane owns one row and one block at a time, so loads are
-// contiguous over a wavefront, and the packed blocks go through LDS (the 16-byte
-// slot XORed by the row, which spreads a wavefront's writes over the banks) to
-// be written 128 bytes to a row.
-constexpr int kRows = 64, kBlocks = 8;
+// k as the row index of the source (OP_T): a lane owns a few neighbouring rows of
+// the result (8 bytes of a source row) and one block at a time, so that a
+// wavefront's loads are 512 bytes of one source row; a workgroup takes its rows by
+// 8 blocks, and the packed blocks go through LDS (the 16-byte slot XORed by the
+// lane, which spreads a wavefront's writes over the banks) to be written 128 bytes
+// to a row.
+//
+// HOW 0: an element at a time (a source off 8-byte boundaries, and the edges); 1:
+// 8-byte loads; 2: the same, non-temporal, for a source that the 256 MB last-level
+// cache cannot hold beside the result (8192 x 8192 FP32, 268 MB: 53.7 us, 5.7 TB/s,
+// and 104 with the decoding after it, against 65.0 and 138 for HOW 1; one that
+// still lies in the cache is read faster with HOW 1, BF16 of that size 34.2 us
+// against 37.2).  One row per lane, 256 bytes of an FP32 source row, took 102.
+constexpr int kBlocks = 8;
+template <typename T> constexpr int kPerLane = 8 / sizeof(T);
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void quantize_cols_kernel(
+template <typename T, int HOW>
+__global__ __launch_bounds__(kBlocks * kWave) void quantize_cols_kernel(
     int64_t rows, int64_t cols, const T* __restrict__ src, int64_t lds, uint8_t* __restrict__ data,
     int64_t ldd, uint8_t* __restrict__ scales, int64_t ldsc, int64_t tiles_k) {
+    constexpr int P = kPerLane<T>, kRows = kWave * P;
     __shared__ __attribute__((aligned(16))) u32x4 out[kRows][kBlocks];
     __shared__ uint8_t sc[kRows][kBlocks];
     const int64_t r0 = blockIdx.x / tiles_k * kRows, b0 = blockIdx.x % tiles_k * kBlocks;
     const int64_t blocks = ceil_div(cols, 32);
     const int lane = threadIdx.x % kWave;
-    const int64_t row = r0 + lane;
-    for (int blk = threadIdx.x / kWave; blk < kBlocks; blk += kThreads / kWave) {
-        const int64_t k0 = (b0 + blk) * 32;
-        float v[32];
-        uint32_t m = 0;
+    const int64_t row = r0 + lane * P;
+    const int blk = threadIdx.x / kWave;
+    const int64_t k0 = (b0 + blk) * 32;
+    if (k0 < cols) {
+        T v[32][P];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            v[i] = row < rows && k0 + i < cols ? to_f32(src[(k0 + i) * lds + row]) : 0.0f;
-            m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-        }
-        const uint32_t b = scale_byte(m);
-        const float f = unscale(b);
-        u32x4 w = {0u, 0u, 0u, 0u};
+            const T* const p = src + (k0 + i) * lds + row;
+            if (k0 + i < cols && HOW != 0 && row + P <= rows) {
+                const u32x2* const q = reinterpret_cast<const u32x2*>(p);
+                const u32x2 w = HOW == 2 ? __builtin_nontemporal_load(q) : *q;
+                __builtin_memcpy(v[i], &w, sizeof(v[i]));
+            } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) w[i / 8] |= fp4_code(v[i] * f) << (4 * (i % 8));
-        if (b == 255u) w = u32x4{0u, 0u, 0u, 0u};
-        out[lane][blk ^ (lane & 7)] = w;
-        sc[lane][blk] = static_cast<uint8_t>(b);
+                for (int c = 0; c < P; ++c)
+                    v[i][c] = k0 + i < cols && row + c < rows ? p[c] : ZeroOf<T>::get();
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m = largest_of(m, to_f32(v[i][c]));
+            const uint32_t b = scale_byte(m);
+            const float f = unscale(b);
+            u32x4 w = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = to_f32(v[8 * q + i][c]) * f;
+                w[q] = b == 255u ? 0u : fp4_codes(y);
+            }
+            out[lane * P + c][blk ^ (lane & 7)] = w;
+            sc[lane * P + c][blk] = static_cast<uint8_t>(b);
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kRows * kBlocks; i += kThreads) {
+    for (int i = threadIdx.x; i < kRows * kBlocks; i += kBlocks * kWave) {
         const int r = i / kBlocks, blk = i % kBlocks;
         if (r0 + r >= rows || b0 + blk >= blocks) continue;
-        *reinterpret_cast<u32x4*>(data + (r0 + r) * ldd + (b0 + blk) * 16) = out[r][blk ^ (r & 7)];
+        *reinterpret_cast<u32x4*>(data + (r0 + r) * ldd + (b0 + blk) * 16) =
+            out[r][blk ^ ((r / P) & 7)];
         scales[(r0 + r) * ldsc + b0 + blk] = sc[r][blk];
     }
 }
@@ -203,9 +238,15 @@ hipError_t quantize_typed(bool trans, int64_t rows, int64_t cols, const void* sr
     const T* p = static_cast<const T*>(src);
     if (trans) {
         const int64_t tiles_k = ceil_div(ceil_div(cols, 32), kBlocks);
-        const int64_t grid = ceil_div(rows, kRows) * tiles_k;
+        const int64_t grid = ceil_div(rows, kWave * kPerLane<T>) * tiles_k;
         if (grid > 0x7fffffff) return hipErrorInvalidValue;
-        quantize_cols_kernel<T><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
+        const bool vec = reinterpret_cast<uintptr_t>(src) % 8 == 0 &&
+                         lds % kPerLane<T> == 0;
+        const bool large = cols * lds * static_cast<int64_t>(sizeof(T)) > (int64_t(192) << 20);
+        auto* const fn = !vec    ? quantize_cols_kernel<T, 0>
+                         : large ? quantize_cols_kernel<T, 2>
+                                 : quantize_cols_kernel<T, 1>;
+        fn<<<dim3(static_cast<unsigned>(grid)), dim3(kBlocks * kWave), 0, s>>>(
             rows, cols, p, lds, data, ldd, scales, ldsc, tiles_k);
         return hipGetLastError();
     }
