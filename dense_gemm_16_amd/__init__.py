@@ -31,6 +31,7 @@ EXPORTS = ("migemm_gemm", "migemm_gemm_variant", "migemm_gemm_ex", "migemm_gemm_
            "migemm_gemm_ws", "migemm_gemm_noalloc", "migemm_workspace_size", "migemm_describe",
            "migemm_describe_ex",
            "migemm_convert", "migemm_quantize_mx", "migemm_dequantize_mx", "migemm_gemm_mx",
+           "migemm_mx_config_count", "migemm_mx_config_name",
            "migemm_linear_loss_workspace_size", "migemm_linear_ce_forward",
            "migemm_linear_ce_backward", "migemm_linear_kd_forward", "migemm_linear_kd_backward",
            "migemm_variant_count", "migemm_variant_name",
@@ -90,9 +91,13 @@ def lib():
     L.migemm_quantize_mx.restype = i32
     L.migemm_dequantize_mx.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp]
     L.migemm_dequantize_mx.restype = i32
-    L.migemm_gemm_mx.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, f32, f32, i32,
+    L.migemm_gemm_mx.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, f32, f32, i32,
                                  vp, i64, vp]
     L.migemm_gemm_mx.restype = i32
+    L.migemm_mx_config_count.argtypes = []
+    L.migemm_mx_config_count.restype = i32
+    L.migemm_mx_config_name.argtypes = [i32]
+    L.migemm_mx_config_name.restype = cp
     layer = [i64, i64, i64, i32, vp, i64, vp, i64]  # T, V, D, dtype, X, ldx, W, ldw
     kd = [i64, i64, i64, i64, i32, vp, i64, vp, i64, i32, vp, i64, vp, i64, f32]
     L.migemm_linear_loss_workspace_size.argtypes = [i32, i64, i64, i64, i64, i32, vp, i64, vp, i64,
@@ -222,10 +227,19 @@ def migemm_dequantize_mx(dst_dtype, rows, cols, data, ldd, scales, ldsc, dst, ld
                                       stream)
 
 
-def migemm_gemm_mx(M, N, K, A, lda, a_scales, ldas, B, ldb, b_scales, ldbs, alpha, beta, c_dtype,
-                   C, ldc, stream=None) -> int:
-    return lib().migemm_gemm_mx(M, N, K, A, lda, a_scales, ldas, B, ldb, b_scales, ldbs, alpha,
-                                beta, c_dtype, C, ldc, stream)
+def migemm_gemm_mx(config, M, N, K, A, lda, a_scales, ldas, B, ldb, b_scales, ldbs, alpha, beta,
+                   c_dtype, C, ldc, stream=None) -> int:
+    return lib().migemm_gemm_mx(config, M, N, K, A, lda, a_scales, ldas, B, ldb, b_scales, ldbs,
+                                alpha, beta, c_dtype, C, ldc, stream)
+
+
+def migemm_mx_config_count() -> int:
+    return lib().migemm_mx_config_count()
+
+
+def migemm_mx_config_name(config: int) -> str | None:
+    s = lib().migemm_mx_config_name(config)
+    return s.decode() if s is not None else None
 
 
 def migemm_linear_loss_workspace_size(backward, T, V, D, top, dtype, X, ldx, W, ldw):
@@ -469,17 +483,20 @@ def _mx_operand(name, m, device):
     import torch
     data, scales, cols = m
     u8, blocks = torch.uint8, (cols + 31) // 32
-    for what, t, need in (("data", data, 16 * blocks), ("scales", scales, blocks)):
-        if not t.is_cuda or t.device != device:
-            _check_device(f"{name}.{what}", t, device)
-        if t.dtype != u8 or t.dim() != 2 or t.shape[0] != data.shape[0] or t.shape[1] < need:
-            raise ValueError(f"{name}.{what} must be a uint8 matrix of {data.shape[0]} rows of at "
-                             f"least {need} bytes (got {t.dtype}, {tuple(t.shape)})")
-    ldd, ldsc, rows = _ld(data), _ld(scales), data.shape[0]
+    shape, sshape = data.shape, scales.shape
+    if not (data.is_cuda and scales.is_cuda and data.device == device == scales.device):
+        _check_device(f"{name}.data", data, device)
+        _check_device(f"{name}.scales", scales, device)
+    if not (data.dtype == u8 == scales.dtype and len(shape) == 2 == len(sshape) and
+            sshape[0] == shape[0] and shape[1] >= 16 * blocks and sshape[1] >= blocks):
+        raise ValueError(f"{name} must hold uint8 data and scales of as many rows, of at least "
+                         f"{16 * blocks} and {blocks} bytes (got {data.dtype}, {tuple(shape)} and "
+                         f"{scales.dtype}, {tuple(sshape)})")
+    ldd, ldsc, rows = _ld(data), _ld(scales), shape[0]
     # a row occupies its whole stride, the last one too
-    if (data.untyped_storage().nbytes() - data.storage_offset() < rows * ldd or
-            scales.untyped_storage().nbytes() - scales.storage_offset() < rows * ldsc):
-        raise ValueError(f"{name}: the storage ends inside the last row's stride")
+    for t, ld in ((data, ldd), (scales, ldsc)):
+        if ld != t.shape[1] and t.untyped_storage().nbytes() - t.storage_offset() < rows * ld:
+            raise ValueError(f"{name}: the storage ends inside the last row's stride")
     return data.data_ptr() or None, ldd, scales.data_ptr() or None, ldsc
 
 
@@ -576,7 +593,7 @@ def dequantize_mx(m, dtype, out=None, *, stream=None):
 
 
 def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=None,
-            stream=None):
+            config: int = -1, stream=None):
     """out = alpha * (A x B^T) + beta * out for two ``MxMatrix`` operands: ``a`` is
     M x K, ``b`` N x K (quantised along k).  ``out`` (M x N, row-major, float32,
     float16 or bfloat16) is allocated with ``out_dtype`` (default float32) if not
@@ -599,9 +616,9 @@ def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=
             _check_device("out", out, device)
             if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
                 raise ValueError("out must have shape (M, N) (and out_dtype, if given)")
-        st = migemm_gemm_mx(M, N, (K + 31) // 32 * 32, pa, lda, psa, ldsa, pb, ldb, psb, ldsb,
-                            float(alpha), float(beta), _dtype_code(out), out.data_ptr() or None,
-                            _ld(out), stream)
+        st = migemm_gemm_mx(config, M, N, (K + 31) // 32 * 32, pa, lda, psa, ldsa, pb, ldb, psb,
+                            ldsb, float(alpha), float(beta), _dtype_code(out),
+                            out.data_ptr() or None, _ld(out), stream)
         if st != OK:
             raise MigemmError(st, "migemm_gemm_mx")
         if fresh and other:

@@ -338,7 +338,10 @@ struct MxArgs {
     hipStream_t stream;
     bool whole_lines;  // c_whole_lines(out)
 };
-hipError_t launch_gemm_mx(const MxArgs& p);
+// config: -1 for the kernel that suits the sizes, or one of mx_config_count's.
+hipError_t launch_gemm_mx(const MxArgs& p, int config);
+int mx_config_count();
+const char* mx_config_name(int c);
 
 // Argument checks shared by the entry points (api.cpp).  Sizes are limited so
 // that every index product fits in 64 bits: a dimension below 2^31 times a

@@ -76,12 +76,12 @@ int migemm_dequantize_mx(int dst_dtype, int64_t rows, int64_t cols, const void* 
                                            static_cast<hipStream_t>(stream)));
 }
 
-int migemm_gemm_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+int migemm_gemm_mx(int config, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                    const void* a_scales, int64_t ldas, const void* B, int64_t ldb,
                    const void* b_scales, int64_t ldbs, float alpha, float beta, int c_dtype,
                    void* C, int64_t ldc, void* stream) {
     if (!known_dtype(c_dtype) || !mx_shape_ok(M, K, lda, ldas) || !mx_shape_ok(N, K, ldb, ldbs) ||
-        K % 32 != 0)
+        K % 32 != 0 || config < -1 || config >= mx_config_count())
         return MIGEMM_ERR_INVALID_ARG;
     if (ldc < (N > 1 ? N : 1) || ldc >= kMaxLd) return MIGEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return MIGEMM_OK;
@@ -98,7 +98,11 @@ int migemm_gemm_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
              static_cast<const uint8_t*>(B), ldb, static_cast<const uint8_t*>(b_scales), ldbs,
              Epi{C, ldc, alpha, beta, c_dtype}, static_cast<hipStream_t>(stream), false};
     p.whole_lines = c_whole_lines(p.out);
-    return hip_status(launch_gemm_mx(p));
+    return hip_status(launch_gemm_mx(p, config));
 }
+
+int migemm_mx_config_count(void) { return mx_config_count(); }
+
+const char* migemm_mx_config_name(int config) { return mx_config_name(config); }
 
 }  // extern "C"

@@ -460,71 +460,89 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
 // ------------------------------------------------------------------ few rows of A
 //
 // M of at most 16 TM rows: nothing is reused but A, which the caches hold, so the
-// time is that of reading B once.  A workgroup takes 16 rows of B (columns of C);
-// its waves split k in groups of 16 chunks (512 elements: four matrix
-// instructions, and the 16 scale bytes of a row in one load), taken in turn, and
-// add their sums through LDS in wave order, so the result does not depend on
-// timing.  A 64-column tile would leave most CUs idle at N = 8192 and walk all of
-// K in each.
-template <int TM, int WAVES>
+// time is that of reading B once.  A workgroup takes 16 TN rows of B (columns of
+// C); its waves split k in groups of 16 blocks (512 elements: four matrix
+// instructions per fragment pair, and the 16 scale bytes of a row in one load),
+// taken in turn, and add their sums through LDS in wave order, so the result does
+// not depend on timing.
+template <int TM, int TN, int WAVES>
 __global__ __launch_bounds__(WAVES * kWave) void mx_rows_kernel(MxArgs p) {
-    __shared__ f32x4 part[WAVES][TM][kWave];
+    __shared__ f32x4 part[WAVES][TM * TN][kWave];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const int r = lane % 16, g = lane / 16;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
-    const int64_t nrow = min(n0 + r, p.N - 1);
-    const uint8_t* const b_row = p.B + nrow * p.ldb;
-    const uint8_t* const sb_row = p.sb + nrow * p.ldsb;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * TN);
     const int64_t chunks = p.K / 32, groups = ceil_div(chunks, 16);
-    f32x4 acc[TM] = {};
-    for (int64_t k = wave; k < groups; k += WAVES) {
-        u32x4 b[4], a[TM][4];
-        const u32x4 wb = *reinterpret_cast<const u32x4*>(sb_row + 16 * k);
-        u32x4 wa[TM];
+    const uint8_t *b_row[TN], *sb_row[TN], *a_row[TM], *sa_row[TM];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int64_t c = 16 * k + 4 * s + g;
-            b[s] = u32x4{0u, 0u, 0u, 0u};
-            if (c < chunks) b[s] = *reinterpret_cast<const u32x4*>(b_row + 16 * c);
+    for (int j = 0; j < TN; ++j) {
+        const int64_t row = min(n0 + 16 * j + r, p.N - 1);
+        b_row[j] = p.B + row * p.ldb + 16 * g;
+        sb_row[j] = p.sb + row * p.ldsb;
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        const int64_t row = min(int64_t(16 * i + r), p.M - 1);
+        a_row[i] = p.A + row * p.lda + 16 * g;
+        sa_row[i] = p.sa + row * p.ldsa;
+    }
+    f32x4 acc[TM][TN] = {};
+    for (int64_t k = wave; k < groups; k += WAVES) {
+        // step s of the group takes block 16 k + 4 s + g in this lane
+        const int left = static_cast<int>(min(chunks - 16 * k, int64_t(16))) - g;
+        u32x4 b[TN][4], a[TM][4], wb[TN], wa[TM];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            wb[j] = *reinterpret_cast<const u32x4*>(sb_row[j] + 16 * k);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                b[j][s] = u32x4{0u, 0u, 0u, 0u};
+                if (4 * s < left)
+                    b[j][s] = *reinterpret_cast<const u32x4*>(b_row[j] + 256 * k + 64 * s);
+            }
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            const int64_t mrow = min(int64_t(16 * i + r), p.M - 1);
-            wa[i] = *reinterpret_cast<const u32x4*>(p.sa + mrow * p.ldsa + 16 * k);
+            wa[i] = *reinterpret_cast<const u32x4*>(sa_row[i] + 16 * k);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                const int64_t c = 16 * k + 4 * s + g;
                 a[i][s] = u32x4{0u, 0u, 0u, 0u};
-                if (c < chunks)
-                    a[i][s] = *reinterpret_cast<const u32x4*>(p.A + mrow * p.lda + 16 * c);
+                if (4 * s < left)
+                    a[i][s] = *reinterpret_cast<const u32x4*>(a_row[i] + 256 * k + 64 * s);
             }
         }
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            // byte g of the four blocks' scales; 0 past K
-            const bool in = 16 * k + 4 * s + g < chunks;
-            const uint32_t sb = in ? wb[s] >> (8 * g) : 0u;
+            // byte g of the step's four scales; 0 past K, whatever the padding holds
+            const bool in = 4 * s < left;
+            uint32_t ea[TM], eb[TN];
+#pragma unroll
+            for (int i = 0; i < TM; ++i) ea[i] = in ? wa[i][s] >> (8 * g) : 0u;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) eb[j] = in ? wb[j][s] >> (8 * g) : 0u;
 #pragma unroll
             for (int i = 0; i < TM; ++i)
-                mfma_mx<0>(acc[i], a[i][s], b[s], in ? wa[i][s] >> (8 * g) : 0u, sb);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) mfma_mx<0>(acc[i][j], a[i][s], b[j][s], ea[i], eb[j]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < TM; ++i) part[wave][i][lane] = acc[i];
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) part[wave][i * TN + j][lane] = acc[i][j];
     __syncthreads();
     using L = AccLayout<16>;
-    for (int i = wave; i < TM; i += WAVES) {
-        f32x4 sum = part[0][i][lane];
+    for (int q = wave; q < TM * TN; q += WAVES) {
+        f32x4 sum = part[0][q][lane];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) {
-            const f32x4 q = part[w][i][lane];
+            const f32x4 x = part[w][q][lane];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] += q[e];
+            for (int e = 0; e < 4; ++e) sum[e] += x[e];
         }
-        const int64_t col = n0 + L::col(lane);
+        const int64_t col = n0 + 16 * (q % TN) + L::col(lane);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int64_t row = 16 * i + L::row(lane, e);
+            const int64_t row = 16 * (q / TN) + L::row(lane, e);
             if (row < p.M && col < p.N)
                 store_out<true>(p.out, row * p.out.ldc + col, sum[e]);
         }
@@ -542,16 +560,62 @@ hipError_t launch_tile(const MxArgs& p) {
     return hipGetLastError();
 }
 
-template <int TM>
+template <int TM, int TN>
 hipError_t launch_rows(const MxArgs& p) {
-    mx_rows_kernel<TM, 8><<<dim3(static_cast<unsigned>(ceil_div(p.N, 16))), dim3(8 * kWave), 0,
-                            p.stream>>>(p);
+    mx_rows_kernel<TM, TN, 8><<<dim3(static_cast<unsigned>(ceil_div(p.N, 16 * TN))),
+                                dim3(8 * kWave), 0, p.stream>>>(p);
     return hipGetLastError();
+}
+
+// Rows of A 64 at a time through the few-rows kernel: any leading dimension.  32
+// columns per workgroup, which read A half as often, where that still makes 256
+// workgroups (us at K = 8192, N = 8192, 32 against 16 columns: M = 1 8.1 / 8.4, 16
+// 10.0 / 12.3, 64 17.6 / 27.3; N = 1024, M = 16 9.2 / 7.1, 64 16.5 / 13.9).
+hipError_t launch_rows_any(const MxArgs& p) {
+    const bool two = p.N > 32 * 255;
+    for (int64_t m = 0; m < p.M; m += 64) {
+        MxArgs q = p;
+        q.M = p.M - m < 64 ? p.M - m : 64;
+        q.A = p.A + m * p.lda;
+        q.sa = p.sa + m * p.ldsa;
+        q.out.C = static_cast<char*>(p.out.C) + m * p.out.ldc * (p.out.c_dtype == 0 ? 4 : 2);
+        const hipError_t e = q.M <= 16   ? (two ? launch_rows<1, 2>(q) : launch_rows<1, 1>(q))
+                             : q.M <= 32 ? (two ? launch_rows<2, 2>(q) : launch_rows<2, 1>(q))
+                                         : (two ? launch_rows<4, 2>(q) : launch_rows<4, 1>(q));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+const char* const kNames[] = {"rows: 16 or 32 columns per workgroup, k over 8 waves", "64x64x256 pingpong",
+                              "128x128x256 pingpong", "256x256x256 pingpong"};
+constexpr int kCount = sizeof(kNames) / sizeof(kNames[0]);
+
+// The kernel for these sizes.  Few rows go to the rows kernel.  Of the tiles, the
+// one whose workgroups cost least: `slots` of them fit the 256 CUs together, a
+// full set takes `full` and a lone one `lone` (us at K = 8192, BF16 C, and about in
+// proportion to K), in between in proportion.  Measured there, us on 64 / 128 / 256:
+// 192 x 8192 22.6 / 27.0 / 47.8, 512 x 8192 39.5 / 31.5 / 50.8, 1024 x 8192 79.6 /
+// 47.4 / 55.5, 2048 x 8192 150 / 90.3 / 66.8; and 2048^3 13.9 / 11.3 / 19.7, 3000 x
+// 3000 x 3008 39.0 / 31.9 / 27.9.
+int choose(const MxArgs& p) {
+    if (p.M <= 64) return 0;
+    auto cost = [&](int64_t b, int64_t slots, double lone, double full) {
+        const int64_t t = ceil_div(p.M, b) * ceil_div(p.N, b), part = t % slots;
+        return static_cast<double>(t / slots) * full +
+               (part ? lone + (full - lone) * static_cast<double>(part) / slots : 0.0);
+    };
+    const double c64 = cost(64, 1024, 19.0, 39.0), c128 = cost(128, 512, 25.0, 47.0);
+    const double c256 = cost(256, 256, 46.0, 67.0);
+    return c256 <= c128 && c256 <= c64 ? 3 : c128 <= c64 ? 2 : 1;
 }
 
 }  // namespace
 
-hipError_t launch_gemm_mx(const MxArgs& p) {
+int mx_config_count() { return kCount; }
+const char* mx_config_name(int c) { return c >= 0 && c < kCount ? kNames[c] : nullptr; }
+
+hipError_t launch_gemm_mx(const MxArgs& p, int config) {
     if (p.K == 0) {
         GemmArgs g{};
         g.M = p.M;
@@ -560,27 +624,16 @@ hipError_t launch_gemm_mx(const MxArgs& p) {
         g.stream = p.stream;
         return launch_empty_product(g);
     }
-    if (p.M <= 16) return launch_rows<1>(p);
-    if (p.M <= 32) return launch_rows<2>(p);
-    if (p.M <= 64) return launch_rows<4>(p);
-    // the tile kernel's load offsets are 32 bits, 255 rows: longer rows 64 at a time
+    if (config < 0) config = choose(p);
+    // the tile kernel's load offsets are 32 bits, over 255 rows
     const int64_t far = int64_t(1) << 23;
-    if (p.lda >= far || p.ldb >= far || p.ldsa >= far || p.ldsb >= far) {
-        for (int64_t m = 0; m < p.M; m += 64) {
-            MxArgs q = p;
-            q.M = p.M - m < 64 ? p.M - m : 64;
-            q.A = p.A + m * p.lda;
-            q.sa = p.sa + m * p.ldsa;
-            q.out.C = static_cast<char*>(p.out.C) + m * p.out.ldc * (p.out.c_dtype == 0 ? 4 : 2);
-            const hipError_t e = launch_rows<4>(q);
-            if (e != hipSuccess) return e;
-        }
-        return hipSuccess;
+    if (p.lda >= far || p.ldb >= far || p.ldsa >= far || p.ldsb >= far) config = 0;
+    switch (config) {
+        case 0: return launch_rows_any(p);
+        case 1: return launch_tile<64>(p);
+        case 2: return launch_tile<128>(p);
+        default: return launch_tile<256>(p);
     }
-    auto tiles = [&](int64_t b) { return ceil_div(p.M, b) * ceil_div(p.N, b); };
-    if (tiles(256) >= 128) return launch_tile<256>(p);
-    if (tiles(128) >= 128) return launch_tile<128>(p);
-    return launch_tile<64>(p);
 }
 
 }  // namespace migemm

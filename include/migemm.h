@@ -379,12 +379,19 @@ int migemm_dequantize_mx(int dst_dtype, int64_t rows, int64_t cols, const void* 
  * c_dtype MIGEMM_F32, MIGEMM_F16 or MIGEMM_BF16, beta == 0 leaves C unread,
  * M == 0 or N == 0 is a no-op and K == 0 gives C = beta * C.  A NaN scale makes
  * every sum it takes part in NaN.  C must not overlap the operands.  Same
- * pointer, stream, ownership and error rules as migemm_gemm.
+ * pointer, stream, ownership and error rules as migemm_gemm.  config: -1 picks the
+ * kernel by the sizes; 0 .. migemm_mx_config_count() - 1 forces one (each computes
+ * the same product, in another summation order).
  */
-int migemm_gemm_mx(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+int migemm_gemm_mx(int config, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                    const void* a_scales, int64_t ldas, const void* B, int64_t ldb,
                    const void* b_scales, int64_t ldbs, float alpha, float beta, int c_dtype,
                    void* C, int64_t ldc, void* stream);
+
+/* Number of configurations of migemm_gemm_mx, and a configuration's name (static
+ * storage; NULL for an unknown index). */
+int migemm_mx_config_count(void);
+const char* migemm_mx_config_name(int config);
 
 /*
  * The losses of an output layer, without its logits.

@@ -139,7 +139,8 @@ def _device(op, k):
     return mg.MxMatrix(torch.from_numpy(op[0]).cuda(), torch.from_numpy(op[1]).cuda(), k)
 
 
-def _check_product(M, N, K, c_type, alpha, beta, seed, ldc_extra=0, low=118, high=124):
+def _check_product(M, N, K, c_type, alpha, beta, seed, ldc_extra=0, low=118, high=124,
+                   config=-1):
     rng = np.random.default_rng(seed)
     a, b = _operand(M, K, rng, low, high), _operand(N, K, rng, low, high)
     prev = torch.from_numpy(rng.standard_normal((M, N))).to(TORCH[c_type])
@@ -148,7 +149,7 @@ def _check_product(M, N, K, c_type, alpha, beta, seed, ldc_extra=0, low=118, hig
     if beta != 0.0:
         out.copy_(prev)
     say(f"gemm_mx {M}x{N}x{K} {c_type} alpha={alpha} beta={beta}")
-    mg.gemm_mx(_device(a, K), _device(b, K), out, alpha=alpha, beta=beta)
+    mg.gemm_mx(_device(a, K), _device(b, K), out, alpha=alpha, beta=beta, config=config)
     torch.cuda.synchronize()
     if ldc_extra:
         assert buf[:, N:].isnan().all()
@@ -172,6 +173,15 @@ def _check_product(M, N, K, c_type, alpha, beta, seed, ldc_extra=0, low=118, hig
 @pytest.mark.parametrize("c_type", ["f32", "bf16"])
 def test_product(M, N, K, c_type):
     _check_product(M, N, K, c_type, 1.0, 0.0, M + N + K)
+
+
+@pytest.mark.parametrize("config", [0, 1, 2, 3])
+@pytest.mark.parametrize("M,N,K,c_type,beta", [
+    (1, 1, 32, "f32", 0.0), (5, 300, 1568, "bf16", 1.0), (70, 129, 256, "f16", 0.0),
+    (256, 512, 768, "bf16", 0.0), (257, 255, 544, "f32", -1.0), (300, 700, 2304, "f16", 0.5),
+    (520, 260, 4128, "bf16", 0.0), (128, 64, 480, "f32", 0.0)])
+def test_every_configuration(M, N, K, c_type, beta, config):
+    _check_product(M, N, K, c_type, 1.0, beta, M + N, 4, config=config)
 
 
 @pytest.mark.parametrize("M,N,K,c_type,alpha,beta,extra", [
@@ -216,7 +226,7 @@ def test_product_of_no_columns_and_nan_scales():
     # an empty sum: C = beta C
     c = torch.ones(20, 50, device="cuda")
     p = 1 << 20
-    assert mg.migemm_gemm_mx(20, 50, 0, p, 16, p, 16, p, 16, p, 16, 1.0, 0.5, mg.F32,
+    assert mg.migemm_gemm_mx(-1, 20, 50, 0, p, 16, p, 16, p, 16, p, 16, 1.0, 0.5, mg.F32,
                              c.data_ptr(), 50, torch.cuda.current_stream().cuda_stream) == mg.OK
     assert (c == 0.5).all()
 

@@ -47,7 +47,7 @@ def test_dequantize_refusals(kw):
 
 
 def gemm(**kw):
-    a = dict(M=8, N=24, K=96, A=P, lda=48, sa=P + (1 << 16), ldas=16, B=Q, ldb=48,
+    a = dict(config=-1, M=8, N=24, K=96, A=P, lda=48, sa=P + (1 << 16), ldas=16, B=Q, ldb=48,
              sb=Q + (1 << 16), ldbs=16, alpha=1.0, beta=0.0, c_dtype=mg.F32, C=R, ldc=24) | kw
     return mg.migemm_gemm_mx(*a.values())
 
@@ -56,7 +56,7 @@ def gemm(**kw):
     {"M": -1}, {"N": 1 << 31}, {"K": 95}, {"K": 100}, {"K": 16}, {"K": -32}, {"lda": 47},
     {"lda": 40}, {"ldb": 32}, {"ldas": 8}, {"ldbs": 24 + 1}, {"A": P + 8}, {"B": None},
     {"sa": None}, {"sb": Q + 5}, {"c_dtype": mg.I32}, {"c_dtype": mg.I8}, {"C": None},
-    {"ldc": 23}, {"C": P}, {"C": Q + (1 << 16)}, {"ldc": 1 << 32}])
+    {"config": -2}, {"config": 4}, {"ldc": 23}, {"C": P}, {"C": Q + (1 << 16)}, {"ldc": 1 << 32}])
 def test_gemm_refusals(kw):
     assert gemm(**kw) == BAD
 
@@ -87,3 +87,10 @@ def test_oracle_rule_on_hand_worked_blocks():
     back = mx.decode(mx.pack(codes), byte, 64)
     assert back[0, :8].tolist() == [4.0, -6.0, 0.0, 1.0, 2.0, 4.0, 0.0, 1.0]
     assert back[0, 32:35].tolist() == [96.0, 16.0, -8.0]
+
+
+def test_configurations_have_names():
+    n = mg.migemm_mx_config_count()
+    names = [mg.migemm_mx_config_name(c) for c in range(n)]
+    assert n == 4 and all(names) and len(set(names)) == n
+    assert mg.migemm_mx_config_name(n) is None and mg.migemm_mx_config_name(-1) is None
