@@ -482,21 +482,28 @@ def _mx_operand(name, m, device):
     """(data pointer, ldd, scales pointer, ldsc) of an MxMatrix, checked."""
     import torch
     data, scales, cols = m
-    u8, blocks = torch.uint8, (cols + 31) // 32
-    shape, sshape = data.shape, scales.shape
+    blocks, u8 = (cols + 31) // 32, torch.uint8
     if not (data.is_cuda and scales.is_cuda and data.device == device == scales.device):
         _check_device(f"{name}.data", data, device)
         _check_device(f"{name}.scales", scales, device)
-    if not (data.dtype == u8 == scales.dtype and len(shape) == 2 == len(sshape) and
-            sshape[0] == shape[0] and shape[1] >= 16 * blocks and sshape[1] >= blocks):
-        raise ValueError(f"{name} must hold uint8 data and scales of as many rows, of at least "
-                         f"{16 * blocks} and {blocks} bytes (got {data.dtype}, {tuple(shape)} and "
-                         f"{scales.dtype}, {tuple(sshape)})")
-    ldd, ldsc, rows = _ld(data), _ld(scales), shape[0]
-    # a row occupies its whole stride, the last one too
-    for t, ld in ((data, ldd), (scales, ldsc)):
-        if ld != t.shape[1] and t.untyped_storage().nbytes() - t.storage_offset() < rows * ld:
-            raise ValueError(f"{name}: the storage ends inside the last row's stride")
+    if not (data.dtype is u8 and scales.dtype is u8 and data.dim() == 2 == scales.dim()):
+        raise ValueError(f"{name} must hold uint8 matrices (got {data.dtype}, {tuple(data.shape)} "
+                         f"and {scales.dtype}, {tuple(scales.shape)})")
+    (rows, width), (srows, swidth) = data.shape, scales.shape
+    (ldd, unit), (ldsc, sunit) = data.stride(), scales.stride()
+    if srows != rows or width < 16 * blocks or swidth < blocks or (
+            width > 1 and unit != 1) or (swidth > 1 and sunit != 1):
+        raise ValueError(f"{name} must hold data and scales of as many rows, of at least "
+                         f"{16 * blocks} and {blocks} bytes, with unit column stride (got "
+                         f"{tuple(data.shape)} and {tuple(scales.shape)}, strides {data.stride()} "
+                         f"and {scales.stride()})")
+    if rows <= 1:
+        ldd, ldsc = width, swidth
+    elif ldd != width or ldsc != swidth:
+        # a row occupies its whole stride, the last one too
+        for t, ld in ((data, ldd), (scales, ldsc)):
+            if t.untyped_storage().nbytes() - t.storage_offset() < rows * ld:
+                raise ValueError(f"{name}: the storage ends inside the last row's stride")
     return data.data_ptr() or None, ldd, scales.data_ptr() or None, ldsc
 
 
@@ -558,7 +565,7 @@ def quantize_mx(src, *, out=None, stream=None):
             if out.shape != (rows, cols):
                 raise ValueError("out must have src's shape")
             data, ldd, scales, ldsc = _mx_operand("out", out, device)
-        st = migemm_quantize_mx(_dtype_code(src), op, rows, cols, src.data_ptr() or None, lds,
+        st = lib().migemm_quantize_mx(_dtype_code(src), op, rows, cols, src.data_ptr() or None, lds,
                                 data, ldd, scales, ldsc, stream)
         if st != OK:
             raise MigemmError(st, "migemm_quantize_mx")
@@ -583,7 +590,7 @@ def dequantize_mx(m, dtype, out=None, *, stream=None):
             _check_device("out", out, device)
             if out.dtype != dtype or tuple(out.shape) != (rows, cols):
                 raise ValueError("out must have m's shape and the requested dtype")
-        st = migemm_dequantize_mx(_dtype_code(out), rows, cols, data, ldd, scales, ldsc,
+        st = lib().migemm_dequantize_mx(_dtype_code(out), rows, cols, data, ldd, scales, ldsc,
                                   out.data_ptr() or None, _ld(out), stream)
         if st != OK:
             raise MigemmError(st, "migemm_dequantize_mx")
@@ -616,7 +623,7 @@ def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=
             _check_device("out", out, device)
             if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
                 raise ValueError("out must have shape (M, N) (and out_dtype, if given)")
-        st = migemm_gemm_mx(config, M, N, (K + 31) // 32 * 32, pa, lda, psa, ldsa, pb, ldb, psb,
+        st = lib().migemm_gemm_mx(config, M, N, (K + 31) // 32 * 32, pa, lda, psa, ldsa, pb, ldb, psb,
                             ldsb, float(alpha), float(beta), _dtype_code(out),
                             out.data_ptr() or None, _ld(out), stream)
         if st != OK:

@@ -13,8 +13,9 @@
 // elements with scale byte 0, so whatever lies in a scale row's padding is
 // not used.
 //
-// Two kernels:
-// * mx_tile_kernel: tiles of C through LDS, ping-pong wave groups;
+// Three kernels:
+// * mx_tile_kernel: tiles of C through LDS, ping-pong wave groups, for many tiles;
+// * mx_deep_kernel: the same without turns and with more loads in flight, for few;
 // * mx_rows_kernel: few rows of A, bound by reading B once.
 #include "mfma16_direct.hpp"
 
@@ -75,6 +76,120 @@ template <int B_> struct MxTile {
     static constexpr int GM = 4;
     static_assert(LDS_BYTES <= 160 * 1024 && PB >= 1, "stages and scales fit");
 };
+
+// The output step of the tile kernels.  Every fragment read of the workgroup is
+// done; each wave sends its accumulators (the tile's part at row mw, column nw),
+// one 16-row block at a time, through LDS of its own, so that C is read (beta) and
+// written 16 bytes per lane in whole row pieces.  The 16-byte chunk index of the
+// block's rows is XORed by (row >> 2), which spreads the accumulator writes over
+// the banks.  CT: C's type; RD: beta != 0.  One branch picks the form, so the code
+// that runs is short and straight.
+template <class T>
+__device__ __forceinline__ void mx_store(const MxArgs& p, const f32x4 (&acc)[T::TM][T::TN],
+                                         MIGEMM_LDS char* lds, int wave, int lane, int64_t mw,
+                                         int64_t nw) {
+    constexpr int WTN = T::WTN, TM = T::TM, TN = T::TN;
+    MIGEMM_LDS float* const scr = (MIGEMM_LDS float*)(lds + wave * (16 * WTN * 4));
+    const Epi out = p.out;
+    const int ar = lane % 16, ag = lane / 16;
+    auto store = [&](auto ct_tag, auto rd_tag) __attribute__((always_inline)) {
+        constexpr int CT = decltype(ct_tag)::value;
+        constexpr bool RD = decltype(rd_tag)::value, HALF = CT != 0;
+        constexpr int VE = HALF ? 8 : 4, ES = HALF ? 2 : 4, PIECES = WTN / VE;
+        constexpr int kXor = (WTN / 4 - 1) & 3;  // 16-byte chunks of FP32 in a row, at most 4 used
+        const bool vec = (out.ldc * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(out.C) & 15) == 0;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int c = 16 * j + ar;
+                    scr[(4 * ag + r) * WTN + ((((c >> 2) ^ (ag & kXor)) << 2) | (c & 3))] =
+                        acc[i][j][r];
+                }
+            asm volatile("" : : : "memory");
+#pragma unroll
+            for (int q = 0; q < (16 * PIECES + kWave - 1) / kWave; ++q) {
+                const int piece = lane + q * kWave, row = piece / PIECES, c0 = piece % PIECES * VE;
+                if (16 * PIECES % kWave != 0 && piece >= 16 * PIECES) continue;
+                const int64_t grow = mw + 16 * i + row, gcol = nw + c0;
+                const int x4 = (row >> 2) & kXor;
+                if (grow >= p.M || gcol >= p.N) continue;
+                const int64_t idx = grow * out.ldc + gcol;
+                if (vec && gcol + VE <= p.N) {
+                    u32x4* const dst =
+                        reinterpret_cast<u32x4*>(static_cast<char*>(out.C) + idx * ES);
+                    u32x4 old = {0u, 0u, 0u, 0u}, w = {0u, 0u, 0u, 0u};
+                    if constexpr (RD) old = *dst;
+#pragma unroll
+                    for (int h = 0; h < VE / 4; ++h) {
+                        const f32x4 x = *(const MIGEMM_LDS f32x4*)(scr + row * WTN +
+                                                                   4 * (((c0 >> 2) + h) ^ x4));
+#pragma unroll
+                        for (int e4 = 0; e4 < 4; ++e4) {
+                            const int e = 4 * h + e4;
+                            float prev = 0.0f;
+                            if constexpr (RD && HALF) {
+                                const uint32_t bits = (old[e / 2] >> (16 * (e % 2))) & 0xffffu;
+                                prev = CT == 1 ? static_cast<float>(__builtin_bit_cast(
+                                                     _Float16, static_cast<uint16_t>(bits)))
+                                               : __uint_as_float(bits << 16);
+                            } else if constexpr (RD) {
+                                prev = __uint_as_float(old[e]);
+                            }
+                            const float res = RD ? fmaf(out.alpha, x[e4], out.beta * prev)
+                                                 : out.alpha * x[e4];
+                            if constexpr (HALF) {
+                                const uint32_t b =
+                                    CT == 1 ? static_cast<uint32_t>(__builtin_bit_cast(
+                                                  uint16_t, static_cast<_Float16>(res)))
+                                            : static_cast<uint32_t>(f32_to_bf16_bits(res));
+                                w[e / 2] |= b << (16 * (e % 2));
+                            } else {
+                                w[e] = __float_as_uint(res);
+                            }
+                        }
+                    }
+                    if (p.whole_lines)
+                        __builtin_nontemporal_store(w, dst);
+                    else
+                        *dst = w;
+                } else {
+                    // edges and unaligned C, an element at a time (a rolled loop
+                    // keeps this small)
+#pragma nounroll
+                    for (int e = 0; e < VE; ++e)
+                        if (gcol + e < p.N)
+                            store_update<false>(
+                                out, idx + e,
+                                scr[row * WTN + 4 * (((c0 + e) >> 2) ^ x4) + ((c0 + e) & 3)],
+                                RD ? load_prev(out, idx + e) : 0.0f);
+                }
+            }
+            asm volatile("" : : : "memory");
+        }
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    using F32 = std::integral_constant<int, 0>;
+    using F16 = std::integral_constant<int, 1>;
+    using BF16 = std::integral_constant<int, 2>;
+    if (out.beta != 0.0f) {
+        if (out.c_dtype == 0)
+            store(F32{}, Yes{});
+        else if (out.c_dtype == 1)
+            store(F16{}, Yes{});
+        else
+            store(BF16{}, Yes{});
+    } else if (out.c_dtype == 0) {
+        store(F32{}, No{});
+    } else if (out.c_dtype == 1) {
+        store(F16{}, No{});
+    } else {
+        store(BF16{}, No{});
+    }
+}
 
 template <int BX, bool TAIL>
 __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int tiles_n) {
@@ -348,113 +463,185 @@ __global__ __launch_bounds__(512) void mx_tile_kernel(MxArgs p, int tiles_m, int
         run_ktile(NoBarrier{});
     }
 
-    // Output.  Every fragment read is done; each wave sends its accumulators, one
-    // 16-row block at a time, through LDS of its own, so that C is read (beta) and
-    // written 16 bytes per lane in whole row pieces.  The 16-byte chunk index of
-    // the block's rows is XORed by (row >> 2), which spreads the accumulator writes
-    // over the banks.  CT: C's type; RD: beta != 0.  One branch picks the form, so
-    // the code that runs is short and straight.
-    constexpr int WTN = T::WTN;
-    MIGEMM_LDS float* const scr = (MIGEMM_LDS float*)(lds + wave * (16 * WTN * 4));
-    const Epi out = p.out;
-    const int64_t mw = m0 + wm0, nw = n0 + wx * WTN;
-    auto store = [&](auto ct_tag, auto rd_tag) __attribute__((always_inline)) {
-        constexpr int CT = decltype(ct_tag)::value;
-        constexpr bool RD = decltype(rd_tag)::value, HALF = CT != 0;
-        constexpr int VE = HALF ? 8 : 4, ES = HALF ? 2 : 4, PIECES = WTN / VE;
-        constexpr int kXor = (WTN / 4 - 1) & 3;  // 16-byte chunks of FP32 in a row, at most 4 used
-        const bool vec = (out.ldc * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(out.C) & 15) == 0;
+    mx_store<T>(p, acc, lds, wave, lane, m0 + wm0, n0 + wx * T::WTN);
+}
+
+// ---------------------------------------------------------- few tiles, deep loads
+//
+// Where the tiles do not fill the CUs, a k-tile of the ping-pong schedule costs the
+// latency of its parts (loads, barriers, LDS reads, dependent instructions),
+// about 0.4 us however small the tile.  Here a step is a pair of k-tiles (512
+// elements, and the 16 scale bytes of a row that go with them), one barrier per
+// step, no turns, and S stages keep S - 1 steps of loads in flight.  Every wave
+// issues the same number of loads for every step (the scales at 4 bytes per lane),
+// so the wait can count them.
+template <int B_, int S_> struct MxDeep {
+    static constexpr int BX = B_, S = S_;
+    static constexpr int WTM = BX / 2, WTN = BX / 4, TM = WTM / 16, TN = WTN / 16;
+    static constexpr int IMAGE = BX * 128;            // one operand's k-tile
+    static constexpr int SCALES = 2 * BX * 16;        // both operands
+    static constexpr int STAGE = 4 * IMAGE + SCALES;  // A's two images, B's two, scales
+    static constexpr int PE = BX / 64, PS = BX / 64;  // loads per wave: an image; the scales
+    static constexpr int L = 4 * PE + PS;             // per wave and step
+    static constexpr int LDS_BYTES = S * STAGE;
+    static_assert(LDS_BYTES <= 160 * 1024 && (S - 2) * L < 64, "fits LDS and the wait counter");
+};
+
+// 4 bytes per lane straight into LDS at lds_base + 4 * lane (see dma16).
+__device__ __forceinline__ void dma4(uint32_t lds_base, const void* sbase, uint32_t voff) {
+    asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, %1"
+                 :
+                 : "v"(voff), "s"(uniform_ptr(sbase)), "{m0}"(lds_base)
+                 : "memory");
+}
+
+template <int BX, int S, bool TAIL>
+__global__ __launch_bounds__(512) void mx_deep_kernel(MxArgs p, int tiles_m, int tiles_n) {
+    using T = MxDeep<BX, S>;
+    constexpr int TM = T::TM, TN = T::TN;
+    __shared__ __attribute__((aligned(1024))) char smem[T::LDS_BYTES];
+    MIGEMM_LDS char* const lds = (MIGEMM_LDS char*)smem;
+    const uint32_t lds_addr = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm0 = (wave >> 2) * T::WTM, wn0 = (wave & 3) * T::WTN;
+    int pm, pn;
+    tile_coords<8>(blockIdx.x, tiles_m, tiles_n, pm, pn);
+    const int64_t m0 = static_cast<int64_t>(pm) * BX, n0 = static_cast<int64_t>(pn) * BX;
+    const int chunks = static_cast<int>(p.K / 32), steps = (chunks + 15) / 16;
+    const int left = TAIL ? chunks % 16 : 16;  // blocks in the last step (TAIL: 1 to 15)
+
+    // element load q of a wave: rows 8 (wave + 8 q) + lane / 8, blocks placed and
+    // swizzled as in mx_tile_kernel; scale load q: rows 16 (wave + 8 q) + lane / 4 of
+    // A's rows and then B's
+    const int r0 = 8 * wave + lane / 8;
+    const int at_chunk = (lane % 8) ^ swz_a<8>(r0);
+    const int logical = (at_chunk & 3) * 2 + (at_chunk >> 2);  // and 8 more in the second image
+    const int last_m = static_cast<int>(min(p.M - m0, int64_t(BX))) - 1;
+    const int last_n = static_cast<int>(min(p.N - n0, int64_t(BX))) - 1;
+    const uint8_t* const a_tile = p.A + m0 * p.lda;
+    const uint8_t* const b_tile = p.B + n0 * p.ldb;
+    uint32_t va[T::PE], vb[T::PE], vs[T::PS];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
+    for (int q = 0; q < T::PE; ++q) {
+        va[q] = static_cast<uint32_t>(min(r0 + 64 * q, last_m)) * static_cast<uint32_t>(p.lda);
+        vb[q] = static_cast<uint32_t>(min(r0 + 64 * q, last_n)) * static_cast<uint32_t>(p.ldb);
+    }
+    const uint8_t* s_tile[T::PS];
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+    for (int q = 0; q < T::PS; ++q) {
+        const int first = 16 * (wave + 8 * q);  // uniform: wholly in A's rows or in B's
+        const bool of_a = first < BX;
+        const int row = (of_a ? first : first - BX) + lane / 4;
+        s_tile[q] = of_a ? p.sa + m0 * p.ldsa : p.sb + n0 * p.ldsb;
+        vs[q] = static_cast<uint32_t>(min(row, of_a ? last_m : last_n)) *
+                    static_cast<uint32_t>(of_a ? p.ldsa : p.ldsb) + 4 * (lane % 4);
+    }
+    auto issue = [&](int step, int stage) __attribute__((always_inline)) {
+        const uint32_t st = lds_addr + stage * T::STAGE;
+        const int64_t k = static_cast<int64_t>(step) * 256;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int c = 16 * j + ar;
-                    scr[(4 * ag + r) * WTN + ((((c >> 2) ^ (ag & kXor)) << 2) | (c & 3))] =
-                        acc[i][j][r];
-                }
-            asm volatile("" : : : "memory");
+        for (int h = 0; h < 2; ++h) {
+            const int block = logical + 8 * h;
+            const uint32_t c = 16 * (TAIL && step == steps - 1 ? min(block, left - 1) : block);
 #pragma unroll
-            for (int q = 0; q < (16 * PIECES + kWave - 1) / kWave; ++q) {
-                const int piece = lane + q * kWave, row = piece / PIECES, c0 = piece % PIECES * VE;
-                if (16 * PIECES % kWave != 0 && piece >= 16 * PIECES) continue;
-                const int64_t grow = mw + 16 * i + row, gcol = nw + c0;
-                const int x4 = (row >> 2) & kXor;
-                if (grow >= p.M || gcol >= p.N) continue;
-                const int64_t idx = grow * out.ldc + gcol;
-                if (vec && gcol + VE <= p.N) {
-                    u32x4* const dst =
-                        reinterpret_cast<u32x4*>(static_cast<char*>(out.C) + idx * ES);
-                    u32x4 old = {0u, 0u, 0u, 0u}, w = {0u, 0u, 0u, 0u};
-                    if constexpr (RD) old = *dst;
+            for (int q = 0; q < T::PE; ++q)
+                dma16(st + h * T::IMAGE + (wave + 8 * q) * 1024, a_tile + k, va[q] + c);
 #pragma unroll
-                    for (int h = 0; h < VE / 4; ++h) {
-                        const f32x4 x = *(const MIGEMM_LDS f32x4*)(scr + row * WTN +
-                                                                   4 * (((c0 >> 2) + h) ^ x4));
+            for (int q = 0; q < T::PE; ++q)
+                dma16(st + (2 + h) * T::IMAGE + (wave + 8 * q) * 1024, b_tile + k, vb[q] + c);
+        }
 #pragma unroll
-                        for (int e4 = 0; e4 < 4; ++e4) {
-                            const int e = 4 * h + e4;
-                            float prev = 0.0f;
-                            if constexpr (RD && HALF) {
-                                const uint32_t bits = (old[e / 2] >> (16 * (e % 2))) & 0xffffu;
-                                prev = CT == 1 ? static_cast<float>(__builtin_bit_cast(
-                                                     _Float16, static_cast<uint16_t>(bits)))
-                                               : __uint_as_float(bits << 16);
-                            } else if constexpr (RD) {
-                                prev = __uint_as_float(old[e]);
-                            }
-                            const float res = RD ? fmaf(out.alpha, x[e4], out.beta * prev)
-                                                 : out.alpha * x[e4];
-                            if constexpr (HALF) {
-                                const uint32_t b =
-                                    CT == 1 ? static_cast<uint32_t>(__builtin_bit_cast(
-                                                  uint16_t, static_cast<_Float16>(res)))
-                                            : static_cast<uint32_t>(f32_to_bf16_bits(res));
-                                w[e / 2] |= b << (16 * (e % 2));
-                            } else {
-                                w[e] = __float_as_uint(res);
-                            }
-                        }
-                    }
-                    if (p.whole_lines)
-                        __builtin_nontemporal_store(w, dst);
-                    else
-                        *dst = w;
-                } else {
-                    // edges and unaligned C, an element at a time (a rolled loop
-                    // keeps this small)
-#pragma nounroll
-                    for (int e = 0; e < VE; ++e)
-                        if (gcol + e < p.N)
-                            store_update<false>(
-                                out, idx + e,
-                                scr[row * WTN + 4 * (((c0 + e) >> 2) ^ x4) + ((c0 + e) & 3)],
-                                RD ? load_prev(out, idx + e) : 0.0f);
-                }
+        for (int q = 0; q < T::PS; ++q)
+            dma4(st + 4 * T::IMAGE + (wave + 8 * q) * 256,
+                 s_tile[q] + static_cast<int64_t>(step) * 16, vs[q]);
+    };
+    // as mx_tile_kernel's: what this wave's loads of the last step brought from past
+    // K becomes 0 (A's elements, both operands' scales)
+    auto zero_tail = [&](int stage) __attribute__((always_inline)) {
+        MIGEMM_LDS char* const st = lds + stage * T::STAGE;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (logical + 8 * h >= left) {
+#pragma unroll
+                for (int q = 0; q < T::PE; ++q)
+                    *(MIGEMM_LDS u32x4*)(st + h * T::IMAGE + (wave + 8 * q) * 1024 + 16 * lane) =
+                        u32x4{0u, 0u, 0u, 0u};
             }
-            asm volatile("" : : : "memory");
+        const int n = left - 4 * (lane % 4);  // valid bytes of the word
+        const uint32_t mask = n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u;
+#pragma unroll
+        for (int q = 0; q < T::PS; ++q) {
+            MIGEMM_LDS uint32_t* const w =
+                (MIGEMM_LDS uint32_t*)(st + 4 * T::IMAGE + (wave + 8 * q) * 256 + 4 * lane);
+            *w = *w & mask;
         }
     };
-    using Yes = std::true_type;
-    using No = std::false_type;
-    using F32 = std::integral_constant<int, 0>;
-    using F16 = std::integral_constant<int, 1>;
-    using BF16 = std::integral_constant<int, 2>;
-    if (out.beta != 0.0f) {
-        if (out.c_dtype == 0)
-            store(F32{}, Yes{});
-        else if (out.c_dtype == 1)
-            store(F16{}, Yes{});
+
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int ar = lane % 16, ag = lane / 16;
+#pragma unroll
+    for (int t = 0; t < S - 1; ++t)
+        if (t < steps) issue(t, t);
+    int stage = 0;
+    for (int step = 0; step < steps; ++step) {
+        // this step has landed; the S - 2 after it may still fly
+        if (step + S - 2 < steps)
+            vm_wait<(S - 2) * T::L>();
         else
-            store(BF16{}, Yes{});
-    } else if (out.c_dtype == 0) {
-        store(F32{}, No{});
-    } else if (out.c_dtype == 1) {
-        store(F16{}, No{});
-    } else {
-        store(BF16{}, No{});
+            vm_wait<0>();
+        if (TAIL && step == steps - 1) zero_tail(stage);
+        lds_wait_then_barrier();
+        // every wave has read the step before: its stage takes step + S - 1
+        if (step + S - 1 < steps) issue(step + S - 1, stage == 0 ? S - 1 : stage - 1);
+        const MIGEMM_LDS char* const ia = lds + stage * T::STAGE;
+        const MIGEMM_LDS char* const ib = ia + 2 * T::IMAGE;
+        const MIGEMM_LDS char* const is = ia + 4 * T::IMAGE + 2 * ag;
+        u32x4 fa[4][TM], fb[4][TN];
+        uint32_t sa[2][TM], sb[2][TN];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                sa[h][i] = *(const MIGEMM_LDS uint16_t*)(is + (wm0 + 16 * i + ar) * 16 + 8 * h);
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                sb[h][j] =
+                    *(const MIGEMM_LDS uint16_t*)(is + (BX + wn0 + 16 * j + ar) * 16 + 8 * h);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int off = h * T::IMAGE + ((4 * s + ag) ^ swz_a<8>(ar)) * 16;
+#pragma unroll
+                for (int i = 0; i < TM; ++i)
+                    fa[2 * h + s][i] =
+                        *(const MIGEMM_LDS u32x4*)(ia + (wm0 + 16 * i + ar) * 128 + off);
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    fb[2 * h + s][j] =
+                        *(const MIGEMM_LDS u32x4*)(ib + (wn0 + 16 * j + ar) * 128 + off);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    mfma_mx<0>(acc[i][j], fa[2 * h][i], fb[2 * h][j], sa[h][i], sb[h][j]);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    mfma_mx<1>(acc[i][j], fa[2 * h + 1][i], fb[2 * h + 1][j], sa[h][i], sb[h][j]);
+        }
+        stage = stage == S - 1 ? 0 : stage + 1;
     }
+    lds_wait_then_barrier();  // the last step's stage becomes the output step's scratch
+    mx_store<T>(p, acc, lds, wave, lane, m0 + wm0, n0 + wn0);
 }
 
 // ------------------------------------------------------------------ few rows of A
@@ -560,6 +747,17 @@ hipError_t launch_tile(const MxArgs& p) {
     return hipGetLastError();
 }
 
+template <int BX, int S>
+hipError_t launch_deep(const MxArgs& p) {
+    const int64_t tm = ceil_div(p.M, BX), tn = ceil_div(p.N, BX);
+    if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+    auto* const fn =
+        p.K % 512 != 0 ? mx_deep_kernel<BX, S, true> : mx_deep_kernel<BX, S, false>;
+    fn<<<dim3(static_cast<unsigned>(tm * tn)), dim3(512), 0, p.stream>>>(
+        p, static_cast<int>(tm), static_cast<int>(tn));
+    return hipGetLastError();
+}
+
 template <int TM, int TN>
 hipError_t launch_rows(const MxArgs& p) {
     mx_rows_kernel<TM, TN, 8><<<dim3(static_cast<unsigned>(ceil_div(p.N, 16 * TN))),
@@ -587,27 +785,35 @@ hipError_t launch_rows_any(const MxArgs& p) {
     return hipSuccess;
 }
 
-const char* const kNames[] = {"rows: 16 or 32 columns per workgroup, k over 8 waves", "64x64x256 pingpong",
+const char* const kNames[] = {"rows: 16 or 32 columns per workgroup, k over 8 waves",
+                              "64x64x512 deep s4", "64x64x512 deep s2", "128x128x512 deep s2",
                               "128x128x256 pingpong", "256x256x256 pingpong"};
 constexpr int kCount = sizeof(kNames) / sizeof(kNames[0]);
 
-// The kernel for these sizes.  Few rows go to the rows kernel.  Of the tiles, the
-// one whose workgroups cost least: `slots` of them fit the 256 CUs together, a
-// full set takes `full` and a lone one `lone` (us at K = 8192, BF16 C, and about in
-// proportion to K), in between in proportion.  Measured there, us on 64 / 128 / 256:
-// 192 x 8192 22.6 / 27.0 / 47.8, 512 x 8192 39.5 / 31.5 / 50.8, 1024 x 8192 79.6 /
-// 47.4 / 55.5, 2048 x 8192 150 / 90.3 / 66.8; and 2048^3 13.9 / 11.3 / 19.7, 3000 x
-// 3000 x 3008 39.0 / 31.9 / 27.9.
+// The kernel for these sizes.  Up to 32 rows go to the rows kernel (M = 32 / 48 / 64
+// by N = K = 8192: 12.5 / 16.3 / 17.6 us, 64x64 tiles 12.0 / 12.2 / 12.3; 32 x 1024 x
+// 4096 6.1 against 7.1).  Of the tiles, the one whose workgroups cost least: `slots` of
+// them fit the 256 CUs together, a full set takes `full` and a lone one `lone` (us
+// at K = 8192, BF16 C, and about in proportion to K), in between in proportion.
+// Measured, us for configurations 1 to 5, N = K = 8192:
+//   M = 128   13.0   16.1  24.0   27.0  47.4      M = 1024  87   72   50.6  46.9  51.3
+//   M = 192   23.2   18.4  24.3   26.9  46.9      M = 2048 171  143  100    90    67.6
+//   M = 512   46.0   36.7  26.7   30.0  49.0
+// and 2048^3 17.9 12.9 9.5 10.9 18.8, 3000 x 3000 x 3008 54 39 35 32 27.
 int choose(const MxArgs& p) {
-    if (p.M <= 64) return 0;
+    if (p.M <= 32) return 0;
     auto cost = [&](int64_t b, int64_t slots, double lone, double full) {
         const int64_t t = ceil_div(p.M, b) * ceil_div(p.N, b), part = t % slots;
         return static_cast<double>(t / slots) * full +
                (part ? lone + (full - lone) * static_cast<double>(part) / slots : 0.0);
     };
-    const double c64 = cost(64, 1024, 19.0, 39.0), c128 = cost(128, 512, 25.0, 47.0);
-    const double c256 = cost(256, 256, 46.0, 67.0);
-    return c256 <= c128 && c256 <= c64 ? 3 : c128 <= c64 ? 2 : 1;
+    const double c[] = {cost(64, 256, 12.0, 13.0), cost(64, 512, 13.0, 19.5),
+                        cost(128, 256, 21.5, 26.0), cost(128, 512, 25.0, 46.5),
+                        cost(256, 256, 46.0, 67.0)};
+    int best = 0;
+    for (int i = 1; i < 5; ++i)
+        if (c[i] < c[best]) best = i;
+    return best + 1;
 }
 
 }  // namespace
@@ -630,8 +836,10 @@ hipError_t launch_gemm_mx(const MxArgs& p, int config) {
     if (p.lda >= far || p.ldb >= far || p.ldsa >= far || p.ldsb >= far) config = 0;
     switch (config) {
         case 0: return launch_rows_any(p);
-        case 1: return launch_tile<64>(p);
-        case 2: return launch_tile<128>(p);
+        case 1: return launch_deep<64, 4>(p);
+        case 2: return launch_deep<64, 2>(p);
+        case 3: return launch_deep<128, 2>(p);
+        case 4: return launch_tile<128>(p);
         default: return launch_tile<256>(p);
     }
 }

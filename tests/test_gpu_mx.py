@@ -175,7 +175,7 @@ def test_product(M, N, K, c_type):
     _check_product(M, N, K, c_type, 1.0, 0.0, M + N + K)
 
 
-@pytest.mark.parametrize("config", [0, 1, 2, 3])
+@pytest.mark.parametrize("config", range(6))
 @pytest.mark.parametrize("M,N,K,c_type,beta", [
     (1, 1, 32, "f32", 0.0), (5, 300, 1568, "bf16", 1.0), (70, 129, 256, "f16", 0.0),
     (256, 512, 768, "bf16", 0.0), (257, 255, 544, "f32", -1.0), (300, 700, 2304, "f16", 0.5),

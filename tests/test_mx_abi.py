@@ -56,7 +56,7 @@ def gemm(**kw):
     {"M": -1}, {"N": 1 << 31}, {"K": 95}, {"K": 100}, {"K": 16}, {"K": -32}, {"lda": 47},
     {"lda": 40}, {"ldb": 32}, {"ldas": 8}, {"ldbs": 24 + 1}, {"A": P + 8}, {"B": None},
     {"sa": None}, {"sb": Q + 5}, {"c_dtype": mg.I32}, {"c_dtype": mg.I8}, {"C": None},
-    {"config": -2}, {"config": 4}, {"ldc": 23}, {"C": P}, {"C": Q + (1 << 16)}, {"ldc": 1 << 32}])
+    {"config": -2}, {"config": 6}, {"ldc": 23}, {"C": P}, {"C": Q + (1 << 16)}, {"ldc": 1 << 32}])
 def test_gemm_refusals(kw):
     assert gemm(**kw) == BAD
 
@@ -92,5 +92,5 @@ def test_oracle_rule_on_hand_worked_blocks():
 def test_configurations_have_names():
     n = mg.migemm_mx_config_count()
     names = [mg.migemm_mx_config_name(c) for c in range(n)]
-    assert n == 4 and all(names) and len(set(names)) == n
+    assert n == 6 and all(names) and len(set(names)) == n
     assert mg.migemm_mx_config_name(n) is None and mg.migemm_mx_config_name(-1) is None
