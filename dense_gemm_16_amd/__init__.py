@@ -533,13 +533,17 @@ def _stream_of(stream, device):
     return (current, False) if stream is None else (stream, stream != current)
 
 
-def _used_on(stream, device, *tensors):
-    """Keeps tensors that torch allocated for its current stream from being reused
-    before the work queued on `stream` has finished."""
+def _run_on(stream, device, *tensors):
+    """For a call on another stream than torch's current one: `stream` waits for what
+    is queued on the current stream (new tensors may reuse memory that work there
+    still reads), and the tensors, None apart, are kept from being reused before the
+    work queued on `stream` has finished."""
     import torch
     s = torch.cuda.ExternalStream(stream, device=device)
+    s.wait_stream(torch.cuda.current_stream(device))
     for t in tensors:
-        t.record_stream(s)
+        if t is not None:
+            t.record_stream(s)
 
 
 def quantize_mx(src, *, out=None, stream=None):
@@ -555,8 +559,7 @@ def quantize_mx(src, *, out=None, stream=None):
     blocks = (cols + 31) // 32
     with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
-        fresh = out is None
-        if fresh:
+        if out is None:
             ldd, ldsc = 16 * max(blocks, 1), max(16, (blocks + 15) // 16 * 16)
             out = MxMatrix(torch.empty((rows, ldd), dtype=torch.uint8, device=device),
                            torch.empty((rows, ldsc), dtype=torch.uint8, device=device), cols)
@@ -565,12 +568,12 @@ def quantize_mx(src, *, out=None, stream=None):
             if out.shape != (rows, cols):
                 raise ValueError("out must have src's shape")
             data, ldd, scales, ldsc = _mx_operand("out", out, device)
+        if other:
+            _run_on(stream, device, src, out.data, out.scales)
         st = lib().migemm_quantize_mx(_dtype_code(src), op, rows, cols, src.data_ptr() or None, lds,
                                 data, ldd, scales, ldsc, stream)
         if st != OK:
             raise MigemmError(st, "migemm_quantize_mx")
-        if fresh and other:
-            _used_on(stream, device, out.data, out.scales)
     return out
 
 
@@ -583,19 +586,18 @@ def dequantize_mx(m, dtype, out=None, *, stream=None):
     data, ldd, scales, ldsc = _mx_operand("m", m, device)
     with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
-        fresh = out is None
-        if fresh:
+        if out is None:
             out = torch.empty((rows, cols), dtype=dtype, device=device)
         else:
             _check_device("out", out, device)
             if out.dtype != dtype or tuple(out.shape) != (rows, cols):
                 raise ValueError("out must have m's shape and the requested dtype")
+        if other:
+            _run_on(stream, device, m.data, m.scales, out)
         st = lib().migemm_dequantize_mx(_dtype_code(out), rows, cols, data, ldd, scales, ldsc,
                                   out.data_ptr() or None, _ld(out), stream)
         if st != OK:
             raise MigemmError(st, "migemm_dequantize_mx")
-        if fresh and other:
-            _used_on(stream, device, out)
     return out
 
 
@@ -614,8 +616,7 @@ def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=
     pb, ldb, psb, ldsb = _mx_operand("b", b, device)
     with _DeviceOf(device):
         stream, other = _stream_of(stream, device)
-        fresh = out is None
-        if fresh:
+        if out is None:
             if beta != 0.0:
                 raise ValueError("beta != 0 needs an existing out")
             out = torch.empty((M, N), dtype=out_dtype or torch.float32, device=device)
@@ -623,13 +624,13 @@ def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=
             _check_device("out", out, device)
             if tuple(out.shape) != (M, N) or (out_dtype is not None and out.dtype != out_dtype):
                 raise ValueError("out must have shape (M, N) (and out_dtype, if given)")
+        if other:
+            _run_on(stream, device, a.data, a.scales, b.data, b.scales, out)
         st = lib().migemm_gemm_mx(config, M, N, (K + 31) // 32 * 32, pa, lda, psa, ldsa, pb, ldb, psb,
                             ldsb, float(alpha), float(beta), _dtype_code(out),
                             out.data_ptr() or None, _ld(out), stream)
         if st != OK:
             raise MigemmError(st, "migemm_gemm_mx")
-        if fresh and other:
-            _used_on(stream, device, out)
     return out
 
 
@@ -711,7 +712,9 @@ def linear_cross_entropy(x, w, target, *, ignore_index: int = -100, stream=None)
     logits are never stored.  Rows whose target is ``ignore_index`` have loss 0; a
     target outside the vocabulary gives NaN.  ``x`` and ``w``: CUDA tensors of one
     dtype (float32, float16, bfloat16), unit column stride.  Runs on ``stream``
-    (default: torch's current stream) without synchronising."""
+    (default: torch's current stream; another one first waits for it) without
+    synchronising.  Autograd does not see the call: the gradients come from the
+    backward function."""
     import torch
     device, T, V, D, dt, ptrs = _layer(x, w)
     pt = _row_vector("target", target, device, torch.int64, T)
@@ -721,8 +724,8 @@ def linear_cross_entropy(x, w, target, *, ignore_index: int = -100, stream=None)
         lse = torch.empty(T, dtype=torch.float32, device=device)
         ws = _loss_workspace(0, T, V, D, 0, dt, ptrs, device)
         if other:
-            _used_on(stream, device, loss, lse, ws)
-        st = migemm_linear_ce_forward(T, V, D, dt, *ptrs, pt, ignore_index, loss.data_ptr() or None,
+            _run_on(stream, device, x, w, target, loss, lse, ws)
+        st = lib().migemm_linear_ce_forward(T, V, D, dt, *ptrs, pt, ignore_index, loss.data_ptr() or None,
                                       lse.data_ptr() or None, ws.data_ptr() or None, ws.numel(),
                                       stream)
     if st != OK:
@@ -747,9 +750,8 @@ def linear_cross_entropy_backward(x, w, target, lse, grad, *, ignore_index: int 
         dx, dw = _gradient("dx", need_dx, dx, x), _gradient("dw", need_dw, dw, w)
         ws = _loss_workspace(1, T, V, D, 0, dt, ptrs, device)
         if other:
-            _hand_over(stream, device)
-            _used_on(stream, device, grad, ws, *(t for t in (dx, dw) if t is not None))
-        st = migemm_linear_ce_backward(
+            _run_on(stream, device, x, w, target, lse, grad, dx, dw, ws)
+        st = lib().migemm_linear_ce_backward(
             T, V, D, dt, *ptrs, pt, ignore_index, pl, grad.data_ptr() or None, *_out_matrix(dx),
             *_out_matrix(dw), ws.data_ptr() or None, ws.numel(), stream)
     if st != OK:
@@ -759,13 +761,6 @@ def linear_cross_entropy_backward(x, w, target, lse, grad, *, ignore_index: int 
 
 def _out_matrix(t):
     return (None, 1) if t is None else (t.data_ptr() or None, _ld(t))
-
-
-def _hand_over(stream, device):
-    """`stream` waits for what this call has queued on torch's current stream (the
-    upstream gradient, brought into one float32 per row there)."""
-    import torch
-    torch.cuda.ExternalStream(stream, device=device).wait_stream(torch.cuda.current_stream(device))
 
 
 def linear_distillation(x, w, teacher_logits, teacher_index, *, temperature: float = 1.0,
@@ -788,8 +783,8 @@ def linear_distillation(x, w, teacher_logits, teacher_index, *, temperature: flo
         student = torch.empty((T, top), dtype=torch.float32, device=device)
         ws = _loss_workspace(0, T, V, D, top, dt, ptrs, device)
         if other:
-            _used_on(stream, device, loss, lse, student, ws)
-        st = migemm_linear_kd_forward(
+            _run_on(stream, device, x, w, teacher_logits, teacher_index, loss, lse, student, ws)
+        st = lib().migemm_linear_kd_forward(
             T, V, D, top, dt, *ptrs, *teacher, float(temperature), loss.data_ptr() or None,
             lse.data_ptr() or None, student.data_ptr() or None, max(1, top), ws.data_ptr() or None,
             ws.numel(), stream)
@@ -816,9 +811,9 @@ def linear_distillation_backward(x, w, teacher_logits, teacher_index, lse, stude
         dx, dw = _gradient("dx", need_dx, dx, x), _gradient("dw", need_dw, dw, w)
         ws = _loss_workspace(1, T, V, D, top, dt, ptrs, device)
         if other:
-            _hand_over(stream, device)
-            _used_on(stream, device, grad, ws, *(t for t in (dx, dw) if t is not None))
-        st = migemm_linear_kd_backward(
+            _run_on(stream, device, x, w, teacher_logits, teacher_index, lse, student, grad, dx,
+                    dw, ws)
+        st = lib().migemm_linear_kd_backward(
             T, V, D, top, dt, *ptrs, *teacher, float(temperature), pl, student.data_ptr() or None,
             _ld(student), grad.data_ptr() or None, *_out_matrix(dx), *_out_matrix(dw),
             ws.data_ptr() or None, ws.numel(), stream)

@@ -38,8 +38,6 @@ struct RowStat {
     float largest, sum;
 };
 
-// 2^(a - m) for a running maximum m that may be infinite: the largest element
-// itself counts 1 and, where the maximum is +infinity, the sum is +infinity.
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Maximum and sum over the 16 lanes of a DPP row, left in every lane.
@@ -121,8 +119,9 @@ template <> __device__ __forceinline__ bf16_t narrow<bf16_t>(float x) {
 // Output step of the backward product: dz, rounded once into the operands' type
 // because the two products that follow run on the matrix cores in that type;
 // the rounding is half a step of each dz, independent of the others.  Columns
-// from N to ldz (the piece's width rounded up to 64) and rows from M to `rows`
-// (rounded up to 64) become 0, so the products can run whole k-tiles over them.
+// from N to the end of the last tile (at most ldz, the piece's width rounded up to
+// 64) become 0, so that the products may read whole 16-byte chunks past N, and so do
+// rows from M to `rows` (rounded up to 64), so that dw's product runs whole k-tiles.
 // Each 16-row block of the wave's tile goes through the wave's own LDS to be
 // written 16 bytes per lane in whole row pieces.
 template <typename E>

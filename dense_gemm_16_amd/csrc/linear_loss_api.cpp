@@ -9,19 +9,27 @@
 namespace migemm {
 
 // 256x256 tiles from half a round of them on, else 128x128 from half a round,
-// else 64x64; the ping-pong schedule where every tile and k-tile is whole.
+// else 64x64; the ping-pong schedule where every tile and k-tile is whole.  Forward
+// pass, us on 64 / 128 / 256 (BF16): 64 x 32000 x 1024 18 / 19 / 34, 200 x 50000 x 2048
+// 89 / 78 / 61, 1000 x 8000 x 512 28 / 21 / 24, 2048 x 4096 x 2048 65 / 47 / 50, 4096 x
+// 1000 x 1024 31 / 25 / 41; FP32 100 x 4000 x 512 16 / 38, 500 x 8000 x 512 46 / 42.
+// FP32 on at most half a round of 64x64 tiles takes 64x32 ones, whose k-tile is half
+// as long (33 x 4099 x 520: 10.1 against 13.7).
 LossShape loss_shape(int dtype, int64_t M, int64_t N, int64_t K) {
     auto tiles = [&](int64_t b) { return ceil_div(M, b) * ceil_div(N, b); };
     const bool f32 = dtype == MIGEMM_F32;
     if (!f32 && M > 128 && tiles(256) >= 128)
         return {M % 256 == 0 && N % 256 == 0 && K % 64 == 0 ? 3 : 2, 64, 256};
     if (M > 64 && tiles(128) >= 128) return {1, 32, 128};
+    if (f32 && tiles(64) <= 128) return {2, 16, 32};
     return {0, 16, 64};
 }
 
 hipError_t launch_loss(const LossTile& t, int config) {
     if (t.dtype == MIGEMM_F32)
-        return config == 1 ? launch_loss_tile<float, 1>(t) : launch_loss_tile<float, 0>(t);
+        return config == 2   ? launch_loss_tile<float, 2>(t)
+               : config == 1 ? launch_loss_tile<float, 1>(t)
+                             : launch_loss_tile<float, 0>(t);
 #define MIGEMM_LOSS(E)                                        \
     switch (config) {                                         \
         case 0: return launch_loss_tile<E, 0>(t);             \
@@ -41,13 +49,17 @@ namespace {
 constexpr int64_t kMaxTop = 1024;
 // Entries of dz in one piece of the vocabulary: 2^28, 512 MiB in 16 bits.
 constexpr int64_t kPieceEntries = int64_t(1) << 28;
+// Widest piece: dz's rows stay within the direct kernels' offset limit (2^21).
+constexpr int64_t kPieceMax = int64_t(1) << 20;
+// Multiply-adds below which a launch more costs more than it saves.
+constexpr double kSmallWork = 2147483648.0;  // 2^31
 
 int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
 
 // What one call copies and where its scratch arrays lie (byte offsets into the
 // workspace, 256-byte aligned).
 struct Plan {
-    bool copy_x = false, copy_w = false, wide = false;
+    bool copy_x = false, copy_w = false, wide = false, small_w = false;
     int64_t depth = 0;   // k of the logits' product
     int64_t ld_copy = 0; // leading dimension of copies
     int64_t bytes = 0;
@@ -106,7 +118,7 @@ Plan make_plan(const LossArgs& a, bool backward) {
     p.t_pad = round_up(a.T, 64);
     p.x = p.take(p.t_pad * p.ld_copy * es);
     const int64_t fit = kPieceEntries / p.t_pad / 256 * 256;
-    p.piece = fit < 2048 ? 2048 : fit;
+    p.piece = fit < 2048 ? 2048 : fit > kPieceMax ? kPieceMax : fit;
     if (p.piece > a.V) p.piece = a.V;
     p.pieces = ceil_div(a.V, p.piece);
     p.ldz = round_up(p.piece, 64);
@@ -114,6 +126,11 @@ Plan make_plan(const LossArgs& a, bool backward) {
     // rows that end inside a chunk are computed as whole ones
     p.wide = a.dtype == MIGEMM_F16 || !whole;
     p.cols = whole ? a.D : p.ld_copy;
+    // A small dw takes one launch (launch_grad): the products' own selection splits
+    // ragged bands off, which costs up to two launches more and pays only where the
+    // product outweighs them.
+    p.small_w = static_cast<double>(p.piece) * static_cast<double>(p.cols) *
+                    static_cast<double>(p.t_pad) < kSmallWork;
     p.dx_acc = p.wide || (a.dtype != MIGEMM_F32 && p.pieces > 1);
     p.info = p.take(round_up(a.T, 256) * static_cast<int64_t>(sizeof(LossRow)));
     p.factor = p.take(256);
@@ -130,7 +147,7 @@ Plan make_plan(const LossArgs& a, bool backward) {
                             nullptr, p.ldz, nullptr, p.copy_w ? p.ld_copy : a.ldw, &b, true) == MIGEMM_OK &&
             b > p.gemm_bytes)
             p.gemm_bytes = b;
-        if (!p.wide &&
+        if (!p.wide && !p.small_w &&
             workspace_bytes(-1, -1, MIGEMM_OP_T, MIGEMM_OP_N, n, p.cols, p.t_pad, a.dtype, nullptr,
                             p.ldz, nullptr, p.ld_copy, &b, true) == MIGEMM_OK &&
             b > p.gemm_bytes)
@@ -200,7 +217,8 @@ hipError_t launch_grad(const LossArgs& a, const Plan& p, const void* dz, int64_t
     out.factor = factor;
     LossTile t{n, p.cols, p.t_pad, a.dtype, dz, ldz, x, p.ld_copy, a.stream, nullptr, nullptr,
                &out};
-    const LossShape s = loss_shape(a.dtype, n, p.cols, p.t_pad);
+    LossShape s = loss_shape(a.dtype, n, p.cols, p.t_pad);
+    if (s.bn == 32) s = {0, 16, 64};  // (not for operands with k as their row index)
     const int64_t rest = p.cols % 256;
     if (s.bn != 256 || p.cols < 256 || rest == 0 || rest > 64) return launch_loss(t, s.config);
     t.N -= rest;
@@ -263,7 +281,7 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
         }
         if (dw) {
             char* const to = static_cast<char*>(dw) + v0 * lddw * es;
-            if (!p.wide)
+            if (!p.wide && !p.small_w)
                 MIGEMM_TRY(run_gemm(-1, -1, MIGEMM_OP_T, MIGEMM_OP_N, n, p.cols, p.t_pad, a.dtype,
                                     dz, ldz, x, p.ld_copy, 1.0f, 0.0f, a.dtype, to, lddw, gws,
                                     p.gemm_bytes, a.stream, true));

@@ -28,6 +28,9 @@ template <> struct Tile<float, 0> {
 template <> struct Tile<float, 1> {
     using Cfg = DirectCfg<float, 128, 128, 2, 4, 16, 4, 32, 4, 2, 48>;
 };
+template <> struct Tile<float, 2> {  // 64x32 on four waves: twice the workgroups
+    using Cfg = DirectCfg<float, 64, 32, 2, 2, 16, 4, 32, 8, 2, 48>;
+};
 
 template <class Cfg, bool TRANS, class Out>
 hipError_t launch_with(const LossTile& t, const Out& out) {
@@ -71,7 +74,10 @@ hipError_t launch_loss_tile(const LossTile& t) {
     using Cfg = typename Tile<E, C>::Cfg;
     if (t.lse) return launch_with<Cfg, false>(t, *t.lse);
     if (t.dz) return launch_with<Cfg, false>(t, *static_cast<const DzOut<E>*>(t.dz));
-    return launch_with<Cfg, true>(t, *static_cast<const GradOut<E>*>(t.grad));
+    // (a k-row image is at least 64 FP32 columns wide)
+    if constexpr (Cfg::BN * sizeof(E) >= 128 && Cfg::BN >= 64)
+        return launch_with<Cfg, true>(t, *static_cast<const GradOut<E>*>(t.grad));
+    return hipErrorInvalidValue;
 }
 
 #if defined(MIGEMM_PART_E) && defined(MIGEMM_PART_C)

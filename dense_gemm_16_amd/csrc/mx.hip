@@ -242,7 +242,7 @@ hipError_t quantize_typed(bool trans, int64_t rows, int64_t cols, const void* sr
         if (grid > 0x7fffffff) return hipErrorInvalidValue;
         const bool vec = reinterpret_cast<uintptr_t>(src) % 8 == 0 &&
                          lds % kPerLane<T> == 0;
-        const bool large = cols * lds * static_cast<int64_t>(sizeof(T)) > (int64_t(192) << 20);
+        const bool large = static_cast<double>(cols) * static_cast<double>(lds) * sizeof(T) > 201326592.0;
         auto* const fn = !vec    ? quantize_cols_kernel<T, 0>
                          : large ? quantize_cols_kernel<T, 2>
                                  : quantize_cols_kernel<T, 1>;
