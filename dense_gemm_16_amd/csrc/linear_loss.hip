@@ -180,14 +180,45 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
     }
 }
 
-// Row data of the backward pass, and X's row into the padded copy.
+// factor[0] = f = 2^14 / m, within 2^+-100, and its inverse.
+__device__ __forceinline__ void write_factor(float m, float* factor) {
+    const float f = fminf(fmaxf(m > 0.0f ? 16384.0f / m : 1.0f, 0x1p-100f), 0x1p100f);
+    factor[0] = f;
+    factor[1] = 1.0f / f;
+}
+
+// A cross-entropy row's coefficient: 0 without a loss, NaN for a target outside
+// the vocabulary.
+__device__ __forceinline__ float ce_coef(const LossArgs& a, int64_t row,
+                                         const float* __restrict__ grad) {
+    const int64_t y = a.target[row];
+    return y == a.ignore ? 0.0f : y >= 0 && y < a.V ? grad[row] : NAN;
+}
+
+// Row data of the backward pass, and X's row into the padded copy.  factor (cross
+// entropy only): written by the first workgroup, from all rows' coefficients;
+// non-finite ones do not count.
 template <typename E>
 __global__ __launch_bounds__(kThreads) void loss_prepare_kernel(
     LossArgs a, const float* __restrict__ lse, const float* __restrict__ grad,
     LossRow* __restrict__ info, E* __restrict__ copy, int64_t rows, int64_t ldc,
-    float* __restrict__ tp, bool vec) {
+    float* __restrict__ tp, float* __restrict__ factor, bool vec) {
     constexpr int EPC = 16 / sizeof(E);
-    __shared__ float shared_coef;
+    __shared__ float shared_coef, part[kRowWaves];
+    if (factor != nullptr && blockIdx.x == 0) {
+        float m = 0.0f;
+        for (int64_t i = threadIdx.x; i < a.T; i += kThreads) {
+            const float c = fabsf(ce_coef(a, i, grad));
+            if (c < INFINITY) m = fmaxf(m, c);
+        }
+        m = wave_max(m);
+        if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = m;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kRowWaves; ++w) m = fmaxf(m, part[w]);
+            write_factor(m, factor);
+        }
+    }
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x % kWave;
     if (threadIdx.x < kWave) {
@@ -196,11 +227,8 @@ __global__ __launch_bounds__(kThreads) void loss_prepare_kernel(
             r.lse2 = lse[row] * kLog2e;
             if (a.top == 0) {
                 const int64_t y = a.target[row];
-                if (y != a.ignore) {
-                    const bool known = y >= 0 && y < a.V;
-                    r.coef = known ? grad[row] : NAN;
-                    r.target = known ? static_cast<int32_t>(y) : -1;
-                }
+                r.coef = ce_coef(a, row, grad);
+                if (y != a.ignore && y >= 0 && y < a.V) r.target = static_cast<int32_t>(y);
             } else {
                 const Teacher t = teacher_row(a, row, lane);
                 if (t.held) r.coef = a.tau * grad[row];
@@ -254,12 +282,7 @@ __global__ __launch_bounds__(1024) void loss_factor_kernel(const LossRow* __rest
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int w = 1; w < 16; ++w) m = fmaxf(m, part[w]);
-    // 2^14 / m, within 2^+-100.  Not a power of two: where all rows weigh the same
-    // (a mean), c (q - 1) lies just below 2^14, where FP16's steps are finest
-    // relative to it, and c itself is exact.
-    const float f = fminf(fmaxf(m > 0.0f ? 16384.0f / m : 1.0f, 0x1p-100f), 0x1p100f);
-    factor[0] = f;
-    factor[1] = 1.0f / f;
+    write_factor(m, factor);
 }
 
 // A wavefront per row: dz at the indices inside [v0, v1).  An index that a row
@@ -354,13 +377,13 @@ hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const
 
 hipError_t launch_loss_prepare(const LossArgs& a, const float* lse, const float* grad,
                                LossRow* info, int64_t rows_info, void* copy, int64_t rows,
-                               int64_t ldc, float* tp) {
+                               int64_t ldc, float* tp, float* factor) {
     return by_type(a.dtype, [&](auto tag) {
         using E = decltype(tag);
         const bool vec = aligned16(a.X) && (a.ldx * static_cast<int64_t>(sizeof(E))) % 16 == 0;
         loss_prepare_kernel<E>
             <<<dim3(static_cast<unsigned>(rows_info)), dim3(kThreads), 0, a.stream>>>(
-                a, lse, grad, info, static_cast<E*>(copy), rows, ldc, tp, vec);
+                a, lse, grad, info, static_cast<E*>(copy), rows, ldc, tp, factor, vec);
         return hipGetLastError();
     });
 }

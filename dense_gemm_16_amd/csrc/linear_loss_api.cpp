@@ -122,16 +122,16 @@ Plan make_plan(const LossArgs& a, bool backward) {
     if (p.piece > a.V) p.piece = a.V;
     p.pieces = ceil_div(a.V, p.piece);
     p.ldz = round_up(p.piece, 64);
-    // FP16: dz holds a factor that the gradients' output steps take out again; and
+    // 16-bit dz holds a factor that the gradients' output steps take out again; and
     // rows that end inside a chunk are computed as whole ones
-    p.wide = a.dtype == MIGEMM_F16 || !whole;
+    p.wide = a.dtype != MIGEMM_F32 || !whole;
     p.cols = whole ? a.D : p.ld_copy;
     // A small dw takes one launch (launch_grad): the products' own selection splits
     // ragged bands off, which costs up to two launches more and pays only where the
     // product outweighs them.
     p.small_w = static_cast<double>(p.piece) * static_cast<double>(p.cols) *
                     static_cast<double>(p.t_pad) < kSmallWork;
-    p.dx_acc = p.wide || (a.dtype != MIGEMM_F32 && p.pieces > 1);
+    p.dx_acc = p.wide;
     p.info = p.take(round_up(a.T, 256) * static_cast<int64_t>(sizeof(LossRow)));
     p.factor = p.take(256);
     p.dz = p.take(p.t_pad * p.ldz * es);
@@ -249,13 +249,11 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
     } while (0)
     MIGEMM_TRY(hip_status(operand(a, p.copy_w, a.W, a.ldw, a.V, round_up(a.V, 64), p, at(ws, p.w),
                                   &w, &ldw)));
+    float* const factor =
+        a.dtype == MIGEMM_F32 ? nullptr : reinterpret_cast<float*>(at(ws, p.factor));
     MIGEMM_TRY(hip_status(launch_loss_prepare(a, lse, grad, info, round_up(a.T, 256), x, p.t_pad,
-                                              p.ld_copy, tp)));
-    float* factor = nullptr;
-    if (a.dtype == MIGEMM_F16) {
-        factor = reinterpret_cast<float*>(at(ws, p.factor));
-        MIGEMM_TRY(hip_status(launch_loss_factor(info, a.T, factor, a.stream)));
-    }
+                                              p.ld_copy, tp, a.top ? nullptr : factor)));
+    if (factor && a.top) MIGEMM_TRY(hip_status(launch_loss_factor(info, a.T, factor, a.stream)));
     const float* const inverse = factor ? factor + 1 : nullptr;
     for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
         const int64_t n = a.V - v0 < p.piece ? a.V - v0 : p.piece, ldz = round_up(n, 64);
