@@ -48,15 +48,17 @@ __device__ __forceinline__ void mfma_mx(f32x4& c, u32x4 a, u32x4 b, uint32_t sa,
 //   takes blocks 2 g and 2 g + 1 of the k-tile (in its first and second slab)
 //   rather than g and 4 + g: its two scale bytes are then neighbours, one 2-byte
 //   LDS read per fragment and k-tile, and the two instructions select the byte.
-//   (Reading eight bytes and permuting g and 4 + g together cost twice the LDS
-//   time and a wait per permute.)
+//   (Reading eight bytes and permuting g and 4 + g together costs twice the LDS
+//   time and waits between reads.)
 // * LDS.  Two stages of A, two and a half of B and two pairs of scales fill the 160
 //   KiB of the 256 x 256 tile.  B moves in halves of the tile's columns, half h of
 //   k-tile kt in slot (2 kt + h) mod 5.  While Y reads k-tile kt, four slots hold
 //   k-tiles kt and kt + 1 and Y fills the fifth with the first half of kt + 2; once
 //   it has read, X fills kt's first slot with the second half, and A's stage, in
-//   its own reading turn.  Loading all of B there instead (two whole stages) made
-//   X's reading turn longer than a turn of matrix instructions.
+//   its own reading turn: twelve loads of X's waves and four of Y's.  (With the
+//   second half between Y's matrix instructions instead, or the scales first copied
+//   into the order that the lanes read them in, 8192^3 took 260 to 263 us against
+//   260 to 265.)
 // * Ragged sizes run on the same kernel: every load's row is clamped on the
 //   spot (the address arithmetic hides in the reading turn), and a last k-tile
 //   that K ends inside (TAIL) has A's chunks past K and both operands' scales
@@ -81,7 +83,7 @@ template <int B_> struct MxTile {
 // done; each wave sends its accumulators (the tile's part at row mw, column nw),
 // one 16-row block at a time, through LDS of its own, so that C is read (beta) and
 // written 16 bytes per lane in whole row pieces.  The 16-byte chunk index of the
-// block's rows is XORed by (row >> 2), which spreads the accumulator writes over
+// block's rows is XORed by 4 (row >> 2), which spreads the accumulator writes over
 // the banks.  CT: C's type; RD: beta != 0.  One branch picks the form, so the code
 // that runs is short and straight.
 template <class T>
@@ -96,7 +98,7 @@ __device__ __forceinline__ void mx_store(const MxArgs& p, const f32x4 (&acc)[T::
         constexpr int CT = decltype(ct_tag)::value;
         constexpr bool RD = decltype(rd_tag)::value, HALF = CT != 0;
         constexpr int VE = HALF ? 8 : 4, ES = HALF ? 2 : 4, PIECES = WTN / VE;
-        constexpr int kXor = (WTN / 4 - 1) & 3;  // 16-byte chunks of FP32 in a row, at most 4 used
+        constexpr int kXor = (WTN / 4 - 1) & 12;  // chunks of FP32 in a row: move by whole blocks
         const bool vec = (out.ldc * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(out.C) & 15) == 0;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
@@ -105,7 +107,7 @@ __device__ __forceinline__ void mx_store(const MxArgs& p, const f32x4 (&acc)[T::
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int c = 16 * j + ar;
-                    scr[(4 * ag + r) * WTN + ((((c >> 2) ^ (ag & kXor)) << 2) | (c & 3))] =
+                    scr[(4 * ag + r) * WTN + ((((c >> 2) ^ ((ag << 2) & kXor)) << 2) | (c & 3))] =
                         acc[i][j][r];
                 }
             asm volatile("" : : : "memory");
@@ -114,7 +116,7 @@ __device__ __forceinline__ void mx_store(const MxArgs& p, const f32x4 (&acc)[T::
                 const int piece = lane + q * kWave, row = piece / PIECES, c0 = piece % PIECES * VE;
                 if (16 * PIECES % kWave != 0 && piece >= 16 * PIECES) continue;
                 const int64_t grow = mw + 16 * i + row, gcol = nw + c0;
-                const int x4 = (row >> 2) & kXor;
+                const int x4 = row & kXor;  // (row >> 2) << 2
                 if (grow >= p.M || gcol >= p.N) continue;
                 const int64_t idx = grow * out.ldc + gcol;
                 if (vec && gcol + VE <= p.N) {
