@@ -310,12 +310,17 @@ bool shape_ok(const LossArgs& a, bool kd) {
         return false;
     // copies and the products' offsets: rows of fewer than 2^21 - 64 elements
     if (a.D > (int64_t(1) << 21) - 64) return false;
+    // a launch holds fewer than 2^32 threads: 256 for each row, 512 for each 256x256
+    // tile of the logits (128x128 in FP32; on 64x64 tiles T is at most 64)
+    if (a.T > (int64_t(1) << 23) - 256 || a.V > int64_t(1) << 28 ||
+        a.T * a.V > int64_t(1) << (a.dtype == MIGEMM_F32 ? 36 : 38))
+        return false;
     return !kd || (a.top >= 1 && a.top <= kMaxTop);
 }
 
 bool kd_ok(const LossArgs& a) {
     return known_dtype(a.t_dtype) && ld_ok(a.ldt, a.top) && ld_ok(a.ldi, a.top) &&
-           ld_ok(a.lds, a.top) && a.tau > 0.0f && a.tau < INFINITY;
+           ld_ok(a.lds, a.top) && a.tau >= 0x1p-60f && a.tau <= 0x1p60f;  // tau^2 is finite
 }
 
 struct Range {

@@ -381,7 +381,8 @@ int migemm_dequantize_mx(int dst_dtype, int64_t rows, int64_t cols, const void* 
  * every sum it takes part in NaN.  C must not overlap the operands.  Same
  * pointer, stream, ownership and error rules as migemm_gemm.  config: -1 picks the
  * kernel by the sizes; 0 .. migemm_mx_config_count() - 1 forces one (each computes
- * the same product, in another summation order).
+ * the same product, in another summation order; operands with rows 2^23 bytes or
+ * more apart always take configuration 0).
  */
 int migemm_gemm_mx(int config, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                    const void* a_scales, int64_t ldas, const void* B, int64_t ldb,
@@ -410,7 +411,8 @@ const char* migemm_mx_config_name(int config);
  * Rows.  T may be 0 (losses: a no-op; dW = 0).  A row without a loss (below) has
  * loss 0, a zero row of dX, and adds nothing to dW, whatever its row of X holds;
  * so has a row whose grad is 0, except for its loss.  V and D are at least 1, D at
- * most 2^21 - 64.
+ * most 2^21 - 64, T at most 2^23 - 256, V at most 2^28 and T V at most 2^38 (FP32:
+ * 2^36).
  *
  * Any alignment and leading dimension: rows off 16-byte boundaries, or D not a
  * whole number of 16-byte chunks, are first copied into the workspace.  lse (T
@@ -460,7 +462,9 @@ int migemm_linear_ce_backward(int64_t T, int64_t V, int64_t D, int dtype, const 
  * logits of -infinity, has no loss.  An index of V or more makes its row's loss and
  * gradients NaN.  An index named twice counts with the sum of its weights.
  * student (T x top, leading dimension lds) is written by the forward pass (z at
- * the indices) and read by the backward pass.  temperature is positive and finite.
+ * the indices) and read by the backward pass.  temperature lies between 2^-60 and
+ * 2^60.  The logarithms are FP32, so a loss carries an error of a few 2^-24 log V
+ * temperature^2, which shows at temperatures far above 1.
  */
 int migemm_linear_kd_forward(int64_t T, int64_t V, int64_t D, int64_t top, int dtype,
                              const void* X, int64_t ldx, const void* W, int64_t ldw,

@@ -44,6 +44,7 @@ def kd_backward(**kw):
 
 
 SHARED = [{"T": -1}, {"T": 1 << 31}, {"V": 0}, {"V": 1 << 31}, {"D": 0}, {"D": 1 << 21},
+          {"T": (1 << 23) - 255}, {"V": (1 << 28) + 1}, {"T": 1 << 22, "V": (1 << 16) + 1},
           {"dtype": mg.I8}, {"dtype": 9}, {"ldx": D - 1}, {"ldw": D - 1}, {"ldx": 1 << 32},
           {"X": None}, {"W": None}, {"lse": None}, {"bytes": -1}, {"ws": X}, {"ws": W}]
 
@@ -69,7 +70,7 @@ def test_ce_backward_refusals(kw):
 
 KD = [{"top": 0}, {"top": 1025, "ldt": 1025, "ldi": 1025, "lds": 1025}, {"top": -1},
       {"t_dtype": mg.I32}, {"teacher": None}, {"index": None}, {"ldt": 7}, {"ldi": 7},
-      {"tau": 0.0}, {"tau": -1.0}, {"tau": float("inf")}, {"tau": float("nan")},
+      {"tau": 0.0}, {"tau": -1.0}, {"tau": 1e-19}, {"tau": 2e18}, {"tau": float("inf")}, {"tau": float("nan")},
       {"student": None}, {"lds": 7}]
 
 
@@ -106,6 +107,9 @@ def test_workspace_size():
     assert ws_bytes(0, W=W + 2)[1] >= forward + 320 * 64 * 2
     assert ws_bytes(1, ldw=D + 1)[1] >= backward + 320 * 64 * 2
     assert ws_bytes(0, T=0) == (mg.OK, 0)
+    # FP32 at 2^36 logits and one past it
+    assert ws_bytes(0, dtype=mg.F32, T=1 << 22, V=1 << 14)[0] == mg.OK
+    assert ws_bytes(0, dtype=mg.F32, T=1 << 22, V=(1 << 14) + 1)[0] == BAD
     for kw in ({"T": -1}, {"V": 0}, {"D": 0}, {"dtype": mg.I32}, {"ldx": 1}, {"top": 1025},
                {"top": -1}):
         assert ws_bytes(0, **kw)[0] == BAD
