@@ -211,7 +211,6 @@ struct GradOut : Epi {
         static_assert(Cfg::MF == 16 && Cfg::NW * kBytes <= Cfg::LDS_BYTES, "scratch fits");
         MIGEMM_LDS char* const scr = smem + wave * kBytes;
         const float f = factor ? *factor : 1.0f;
-        const bool vec = (ldg * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(grad) & 15) == 0;
         const int g = lane >> 4, lj = lane & 15;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
@@ -234,8 +233,9 @@ struct GradOut : Epi {
                 const int64_t grow = m + 16 * i + r, gcol = n + c * VE;
                 if (grow >= M || gcol >= cols) continue;
                 E* const to = grad + grow * ldg + gcol;
-                if (vec && gcol + VE <= cols) {
-                    *reinterpret_cast<u32x4*>(to) = *(const MIGEMM_LDS u32x4*)from;
+                if (gcol + VE <= cols) {
+                    const u32x4 w = *(const MIGEMM_LDS u32x4*)from;
+                    __builtin_memcpy(to, &w, 16);  // one store, whatever the alignment
                 } else {
 #pragma nounroll
                     for (int e = 0; e < VE; ++e)

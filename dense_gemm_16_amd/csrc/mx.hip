@@ -52,16 +52,12 @@ __device__ __forceinline__ uint32_t fp4_codes(const float (&y)[8]) {
 }
 
 // Eight consecutive elements from column c of a row, zeros past cols.
-template <typename T, bool VEC>
+template <typename T>
 __device__ __forceinline__ void load8(const T* __restrict__ row, int64_t c, int64_t cols,
                                       float (&v)[8]) {
-    if (VEC && c + 8 <= cols) {
-        u32x4 raw[sizeof(T) / 2];
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            raw[i] = reinterpret_cast<const u32x4*>(row + c)[i];
+    if (c + 8 <= cols) {
         T e[8];
-        __builtin_memcpy(e, raw, sizeof(e));
+        __builtin_memcpy(e, row + c, sizeof(e));  // 16 bytes at a time, whatever the alignment
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
     } else {
@@ -73,7 +69,7 @@ __device__ __forceinline__ void load8(const T* __restrict__ row, int64_t c, int6
 // Rows along k (OP_N).  Four lanes share a block, eight elements each, so loads
 // are 16 bytes per lane and contiguous over a wavefront.  A workgroup takes
 // kThreads / lpr rows (lpr lanes each, a power of two) of one segment of columns.
-template <typename T, bool VEC>
+template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
     int64_t rows, int64_t cols, const T* __restrict__ src, int64_t lds, uint8_t* __restrict__ data,
     int64_t ldd, uint8_t* __restrict__ scales, int64_t ldsc, int lpr, int64_t segs) {
@@ -84,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
     // whole groups of four lanes leave together
     if (row >= rows || piece / 4 >= blocks) return;
     float v[8];
-    load8<T, VEC>(src + row * lds, piece * 8, cols, v);
+    load8<T>(src + row * lds, piece * 8, cols, v);
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = largest_of(m, v[i]);
@@ -106,16 +102,15 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
 // lane, which spreads a wavefront's writes over the banks) to be written 128 bytes
 // to a row.
 //
-// HOW 0: an element at a time (a source off 8-byte boundaries, and the edges); 1:
-// 8-byte loads; 2: the same, non-temporal, for a source that the 256 MB last-level
-// cache cannot hold beside the result (8192 x 8192 FP32, 268 MB: 53.7 us, 5.7 TB/s,
-// and 104 with the decoding after it, against 65.0 and 138 for HOW 1; one that
-// still lies in the cache is read faster with HOW 1, BF16 of that size 34.2 us
-// against 37.2).  One row per lane, 256 bytes of an FP32 source row, took 102.
+// ONCE: non-temporal loads, for a source on 8-byte boundaries that the 256 MB
+// last-level cache cannot hold beside the result (8192 x 8192 FP32, 268 MB: 53.7 us,
+// 5.7 TB/s, and 104 with the decoding after it, against 65.0 and 138 for plain ones;
+// one that still lies in the cache is read faster with those, BF16 of that size 34.2
+// us against 37.2).  One row per lane, 256 bytes of an FP32 source row, took 102.
 constexpr int kBlocks = 8;
 template <typename T> constexpr int kPerLane = 8 / sizeof(T);
 
-template <typename T, int HOW>
+template <typename T, bool ONCE>
 __global__ __launch_bounds__(kBlocks * kWave) void quantize_cols_kernel(
     int64_t rows, int64_t cols, const T* __restrict__ src, int64_t lds, uint8_t* __restrict__ data,
     int64_t ldd, uint8_t* __restrict__ scales, int64_t ldsc, int64_t tiles_k) {
@@ -133,9 +128,12 @@ __global__ __launch_bounds__(kBlocks * kWave) void quantize_cols_kernel(
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const T* const p = src + (k0 + i) * lds + row;
-            if (k0 + i < cols && HOW != 0 && row + P <= rows) {
-                const u32x2* const q = reinterpret_cast<const u32x2*>(p);
-                const u32x2 w = HOW == 2 ? __builtin_nontemporal_load(q) : *q;
+            if (k0 + i < cols && row + P <= rows) {
+                u32x2 w;
+                if constexpr (ONCE)
+                    w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+                else
+                    __builtin_memcpy(&w, p, sizeof(w));
                 __builtin_memcpy(v[i], &w, sizeof(v[i]));
             } else {
 #pragma unroll
@@ -192,7 +190,7 @@ template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float x) {
 }
 
 // Eight elements per lane, as in quantize_rows_kernel.
-template <typename T, bool VEC>
+template <typename T>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(
     int64_t rows, int64_t cols, const uint8_t* __restrict__ data, int64_t ldd,
     const uint8_t* __restrict__ scales, int64_t ldsc, T* __restrict__ dst, int64_t ld, int lpr,
@@ -210,12 +208,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = from_f32<T>(fp4_value((w >> (4 * i)) & 15u) * s);
     T* const p = dst + row * ld + c;
-    if (VEC && c + 8 <= cols) {
-        u32x4 raw[sizeof(T) / 2];
-        __builtin_memcpy(raw, v, sizeof(v));
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            reinterpret_cast<u32x4*>(p)[i] = raw[i];
+    if (c + 8 <= cols) {
+        __builtin_memcpy(p, v, sizeof(v));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -243,9 +237,8 @@ hipError_t quantize_typed(bool trans, int64_t rows, int64_t cols, const void* sr
         const bool vec = reinterpret_cast<uintptr_t>(src) % 8 == 0 &&
                          lds % kPerLane<T> == 0;
         const bool large = static_cast<double>(cols) * static_cast<double>(lds) * sizeof(T) > 201326592.0;
-        auto* const fn = !vec    ? quantize_cols_kernel<T, 0>
-                         : large ? quantize_cols_kernel<T, 2>
-                                 : quantize_cols_kernel<T, 1>;
+        auto* const fn =
+            vec && large ? quantize_cols_kernel<T, true> : quantize_cols_kernel<T, false>;
         fn<<<dim3(static_cast<unsigned>(grid)), dim3(kBlocks * kWave), 0, s>>>(
             rows, cols, p, lds, data, ldd, scales, ldsc, tiles_k);
         return hipGetLastError();
@@ -255,10 +248,8 @@ hipError_t quantize_typed(bool trans, int64_t rows, int64_t cols, const void* sr
     row_shape(4 * ceil_div(cols, 32), lpr, segs);
     const int64_t grid = ceil_div(rows, kThreads / lpr) * segs;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    const bool vec = aligned16(src) && (lds * static_cast<int64_t>(sizeof(T))) % 16 == 0;
-    auto* const fn = vec ? quantize_rows_kernel<T, true> : quantize_rows_kernel<T, false>;
-    fn<<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(rows, cols, p, lds, data, ldd,
-                                                                   scales, ldsc, lpr, segs);
+    quantize_rows_kernel<T><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
+        rows, cols, p, lds, data, ldd, scales, ldsc, lpr, segs);
     return hipGetLastError();
 }
 
@@ -271,9 +262,7 @@ hipError_t dequantize_typed(int64_t rows, int64_t cols, const uint8_t* data, int
     row_shape(ceil_div(cols, 8), lpr, segs);
     const int64_t grid = ceil_div(rows, kThreads / lpr) * segs;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    const bool vec = aligned16(dst) && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0;
-    auto* const fn = vec ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
-    fn<<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
+    dequantize_kernel<T><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
         rows, cols, data, ldd, scales, ldsc, static_cast<T*>(dst), ld, lpr, segs);
     return hipGetLastError();
 }

@@ -99,7 +99,6 @@ __device__ __forceinline__ void mx_store(const MxArgs& p, const f32x4 (&acc)[T::
         constexpr bool RD = decltype(rd_tag)::value, HALF = CT != 0;
         constexpr int VE = HALF ? 8 : 4, ES = HALF ? 2 : 4, PIECES = WTN / VE;
         constexpr int kXor = (WTN / 4 - 1) & 12;  // chunks of FP32 in a row: move by whole blocks
-        const bool vec = (out.ldc * ES) % 16 == 0 && (reinterpret_cast<uintptr_t>(out.C) & 15) == 0;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -119,11 +118,10 @@ __device__ __forceinline__ void mx_store(const MxArgs& p, const f32x4 (&acc)[T::
                 const int x4 = row & kXor;  // (row >> 2) << 2
                 if (grow >= p.M || gcol >= p.N) continue;
                 const int64_t idx = grow * out.ldc + gcol;
-                if (vec && gcol + VE <= p.N) {
-                    u32x4* const dst =
-                        reinterpret_cast<u32x4*>(static_cast<char*>(out.C) + idx * ES);
+                if (gcol + VE <= p.N) {
+                    char* const dst = static_cast<char*>(out.C) + idx * ES;
                     u32x4 old = {0u, 0u, 0u, 0u}, w = {0u, 0u, 0u, 0u};
-                    if constexpr (RD) old = *dst;
+                    if constexpr (RD) __builtin_memcpy(&old, dst, 16);
 #pragma unroll
                     for (int h = 0; h < VE / 4; ++h) {
                         const f32x4 x = *(const MIGEMM_LDS f32x4*)(scr + row * WTN +
@@ -154,12 +152,12 @@ __device__ __forceinline__ void mx_store(const MxArgs& p, const f32x4 (&acc)[T::
                         }
                     }
                     if (p.whole_lines)
-                        __builtin_nontemporal_store(w, dst);
+                        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(dst));
                     else
-                        *dst = w;
+                        __builtin_memcpy(dst, &w, 16);  // one store, whatever the alignment
                 } else {
-                    // edges and unaligned C, an element at a time (a rolled loop
-                    // keeps this small)
+                    // the last columns, an element at a time (a rolled loop keeps
+                    // this small)
 #pragma nounroll
                     for (int e = 0; e < VE; ++e)
                         if (gcol + e < p.N)

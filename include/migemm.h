@@ -349,10 +349,9 @@ int migemm_convert(int src_dtype, int dst_dtype, int64_t rows, int64_t cols,
  * rounded to the nearest code, midpoints to the even code, magnitudes above 6 to
  * 6.  A block with an infinity or a NaN gets scale byte 255 and codes 0.
  *
- * Any alignment of src (16-byte aligned rows take the vector path).  data and
- * scales must not overlap src or each other.  Misaligned or too narrow outputs
- * are MIGEMM_ERR_INVALID_ARG; the pointer, stream, ownership and error rules are
- * migemm_gemm's; rows == 0 or cols == 0 is a no-op.
+ * Any alignment of src.  data and scales must not overlap src or each other.
+ * Misaligned or too narrow outputs are MIGEMM_ERR_INVALID_ARG; the pointer, stream,
+ * ownership and error rules are migemm_gemm's; rows == 0 or cols == 0 is a no-op.
  */
 int migemm_quantize_mx(int src_dtype, int op, int64_t rows, int64_t cols, const void* src,
                        int64_t lds, void* data, int64_t ldd, void* scales, int64_t ldsc,
