@@ -346,20 +346,48 @@ __global__ __launch_bounds__(kThreads) void pad_copy_kernel(int64_t rows, int64_
     }
 }
 
-// Four columns per lane; src rows 16-byte aligned.
-template <typename E>
-__global__ __launch_bounds__(kThreads) void scaled_convert_kernel(
-    int64_t rows, int64_t cols, const float* __restrict__ src, int64_t lds,
-    const float* __restrict__ factor, E* __restrict__ dst, int64_t ldd) {
+// The sum over slices, scaled, four columns at a time.  LANES lanes share a piece of
+// four columns, each adding every LANES-th slice with its loads in flight together;
+// their sums join in a fixed order.
+template <typename E, int LANES>
+__global__ __launch_bounds__(kThreads) void join_kernel(int64_t rows, int64_t cols,
+                                                        const float* __restrict__ src, int64_t lds,
+                                                        int slices,
+                                                        const float* __restrict__ factor,
+                                                        E* __restrict__ dst, int64_t ldd) {
+    constexpr int kPieces = kWave / LANES;  // per wavefront
+    const int lane = threadIdx.x % kWave, sub = lane / kPieces;
     const float f = factor ? *factor : 1.0f;
     const int64_t per = ceil_div(cols, 4), pieces = rows * per;
-    for (int64_t p = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; p < pieces;
-         p += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t r = p / per, c = p % per * 4;
-        const f32x4 v = *reinterpret_cast<const f32x4*>(src + r * lds + c);
+    const int64_t wave = static_cast<int64_t>(blockIdx.x) * kRowWaves + threadIdx.x / kWave;
+    for (int64_t p0 = wave * kPieces; p0 < pieces;
+         p0 += static_cast<int64_t>(gridDim.x) * kRowWaves * kPieces) {
+        const int64_t p = p0 + lane % kPieces;
+        const int64_t r = (p < pieces ? p : p0) / per, c = (p < pieces ? p : p0) % per * 4;
+        const float* const from = src + r * lds + c;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+        for (int s = sub; s < slices; s += LANES) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(from + s * rows * lds);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < cols) dst[r * ldd + c + e] = narrow<E>(v[e] * f);
+            for (int e = 0; e < 4; ++e) v[e] += x[e];
+        }
+#pragma unroll
+        for (int d = kPieces; d < kWave; d *= 2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += __shfl_xor(v[e], d);
+        if (sub != 0 || p >= pieces) continue;
+        E out[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = narrow<E>(v[e] * f);
+        E* const to = dst + r * ldd + c;
+        if (c + 4 <= cols) {
+            __builtin_memcpy(to, out, sizeof(out));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < cols) to[e] = out[e];
+        }
     }
 }
 
@@ -429,14 +457,14 @@ hipError_t launch_pad_copy(int dtype, int64_t rows, int64_t cols, const void* sr
     });
 }
 
-hipError_t launch_scaled_convert(int dtype, int64_t rows, int64_t cols, const float* src,
-                                 int64_t lds, const float* factor, void* dst, int64_t ldd,
-                                 hipStream_t s) {
+hipError_t launch_join(int dtype, int64_t rows, int64_t cols, const float* src, int64_t lds,
+                       int slices, const float* factor, void* dst, int64_t ldd, hipStream_t s) {
     return by_type(dtype, [&](auto tag) {
         using E = decltype(tag);
-        scaled_convert_kernel<E>
-            <<<dim3(grid_for(rows * ceil_div(cols, 4))), dim3(kThreads), 0, s>>>(
-                rows, cols, src, lds, factor, static_cast<E*>(dst), ldd);
+        const int lanes = slices >= 16 ? 8 : 1;
+        auto* const fn = lanes == 8 ? join_kernel<E, 8> : join_kernel<E, 1>;
+        fn<<<dim3(grid_for(rows * ceil_div(cols, 4) * lanes)), dim3(kThreads), 0, s>>>(
+            rows, cols, src, lds, slices, factor, static_cast<E*>(dst), ldd);
         return hipGetLastError();
     });
 }

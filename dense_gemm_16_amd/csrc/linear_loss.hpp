@@ -250,9 +250,11 @@ struct GradOut : Epi {
 };
 
 // One product with one of the output steps: X W^T (M x N, K deep) with lse or dz,
-// or dz^T X (A stored K x M, zero-filled to whole chunks, B stored K x N) with
-// grad.  A and B are 16-byte aligned with leading dimensions in whole 16-byte
-// chunks, and so are K (lse, dz) or N (grad).
+// dz^T X (A stored K x M, zero-filled to whole chunks, B stored K x N) with grad, or
+// the sums of `slices` slices of dz W's k (A M x K, zero-filled to whole chunks, B
+// stored K x N), M x N of FP32 each, one after another at `sums`.  A and B are
+// 16-byte aligned with leading dimensions in whole 16-byte chunks, and so are K (lse,
+// dz) or N (grad, sums).
 struct LossTile {
     int64_t M, N, K;
     int dtype;
@@ -264,6 +266,8 @@ struct LossTile {
     const LseOut* lse;
     const void* dz;    // DzOut of the type
     const void* grad;  // GradOut of the type
+    float* sums = nullptr;
+    int slices = 0;
 };
 
 // The tile configuration for a product of these sizes, its chunk width (columns
@@ -320,9 +324,9 @@ hipError_t launch_loss_scatter(const LossArgs& a, const LossRow* info, const flo
 // dst (rows_out x ldd, zero-padded) = src (rows x cols).
 hipError_t launch_pad_copy(int dtype, int64_t rows, int64_t cols, const void* src, int64_t lds,
                            void* dst, int64_t rows_out, int64_t ldd, hipStream_t s);
-// dst (rows x cols, dtype) = src (FP32) * (factor ? *factor : 1).
-hipError_t launch_scaled_convert(int dtype, int64_t rows, int64_t cols, const float* src,
-                                 int64_t lds, const float* factor, void* dst, int64_t ldd,
-                                 hipStream_t s);
+// dst (rows x cols, dtype) = the sum of `slices` FP32 matrices (rows x lds, whole
+// 16-byte chunks, one after another at src), times (factor ? *factor : 1).
+hipError_t launch_join(int dtype, int64_t rows, int64_t cols, const float* src, int64_t lds,
+                       int slices, const float* factor, void* dst, int64_t ldd, hipStream_t s);
 
 }  // namespace migemm

@@ -56,6 +56,41 @@ constexpr double kSmallWork = 2147483648.0;  // 2^31
 
 int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
 
+// How dx = dz W (T x cols, k deep) is summed where one piece holds the whole
+// vocabulary: slices of k on `config`'s tiles, or (slices 0) the library's product.
+struct LossSlices {
+    int config = 0, slices = 0;
+};
+// Each tile takes as many slices as make 256 workgroups; the tile is the one whose
+// k-tiles (0.27, 0.62, 1.78 us on 64x64, 128x128, 256x256; 0.19 where two workgroups
+// of 64x64 share a CU), prologue and output step, and slices' sums written and read
+// cost least, and the library's product is taken where that one has a single slice.
+// us for dz and then dx, BF16, 64 / 128 / 256, and the library's product (at most 16
+// slices, and a launch more to convert its sums): 1 x 96923 x 256 30 / 34 / - / 67, 64
+// x 8000 x 1024 20 / 25 / - / 27, 200 x 20000 x 2048 78 / 70 / 84 / 74, 3000 x 32000 x
+// 2048 - / - / 725 / 889, 800 x 600 x 4096 - / - / 54 / 40; FP32 15 x 20986 x 320 34 /
+// 44 / - / 49.
+LossSlices dx_slices(int dtype, int64_t T, int64_t cols, int64_t k) {
+    const double step[] = {0.27, 0.62, 1.78}, once[] = {2.0, 5.0, 10.0};
+    LossSlices best;
+    double least = 1e30;
+    for (int c = 0; c < (dtype == MIGEMM_F32 ? 2 : 3); ++c) {
+        if (c == 2 && k % 8 != 0) break;  // (its partial k-tile takes whole chunks)
+        const int64_t b = int64_t(64) << c, tiles = ceil_div(T, b) * ceil_div(cols, b);
+        const int64_t ks = splitk_slice(k, tiles <= 128 ? 256 / tiles : 1);
+        const int64_t slices = ceil_div(k, ks), rounds = ceil_div(tiles, 256);
+        const double rate = c == 0 && rounds > 1 ? 0.19 : step[c];
+        const double cost = static_cast<double>(rounds * (ks / 64)) * rate + once[c] +
+                            (slices < 2 ? 0.0 : static_cast<double>(slices * T * cols) * 8.0 / 3e6);
+        if (cost < least) {
+            least = cost;
+            best.config = c;
+            best.slices = slices < 2 ? 0 : static_cast<int>(slices);
+        }
+    }
+    return best;
+}
+
 // What one call copies and where its scratch arrays lie (byte offsets into the
 // workspace, 256-byte aligned).
 struct Plan {
@@ -69,6 +104,7 @@ struct Plan {
     // backward
     int64_t t_pad = 0, piece = 0, pieces = 0, ldz = 0, cols = 0;
     bool dx_acc = false;
+    LossSlices dx;
     int64_t info = 0, factor = 0, dz = 0, acc_x = 0, tp = 0, gemm = 0, gemm_bytes = 0;
     int64_t take(int64_t n) {
         const int64_t at = bytes;
@@ -131,11 +167,12 @@ Plan make_plan(const LossArgs& a, bool backward) {
     // product outweighs them.
     p.small_w = static_cast<double>(p.piece) * static_cast<double>(p.cols) *
                     static_cast<double>(p.t_pad) < kSmallWork;
-    p.dx_acc = p.wide;
+    if (p.pieces == 1) p.dx = dx_slices(a.dtype, a.T, p.cols, a.V);
+    p.dx_acc = p.wide || p.dx.slices > 0;
     p.info = p.take(round_up(a.T, 256) * static_cast<int64_t>(sizeof(LossRow)));
     p.factor = p.take(256);
     p.dz = p.take(p.t_pad * p.ldz * es);
-    if (p.dx_acc) p.acc_x = p.take(a.T * p.cols * 4);
+    if (p.dx_acc) p.acc_x = p.take(a.T * p.cols * 4 * (p.dx.slices > 0 ? p.dx.slices : 1));
     const int64_t last = a.V - (p.pieces - 1) * p.piece;
     if (a.top) p.tp = p.take(a.T * a.top * 4);
     // what the two products ask for, for a full piece and the last one (their
@@ -143,7 +180,8 @@ Plan make_plan(const LossArgs& a, bool backward) {
     for (int64_t n : {p.piece, last}) {
         int64_t b = 0;
         const Choice c = dx_choice(a.dtype, a.T, p.cols, n);
-        if (workspace_bytes(c.variant, c.config, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, n, a.dtype,
+        if (p.dx.slices == 0 &&
+            workspace_bytes(c.variant, c.config, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, n, a.dtype,
                             nullptr, p.ldz, nullptr, p.copy_w ? p.ld_copy : a.ldw, &b, true) == MIGEMM_OK &&
             b > p.gemm_bytes)
             p.gemm_bytes = b;
@@ -269,7 +307,13 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
         if (a.top)
             MIGEMM_TRY(
                 hip_status(launch_loss_scatter(a, info, tp, factor, dz, ldz, v0, v0 + n)));
-        if (dx) {
+        if (dx && p.dx.slices > 0) {
+            LossTile t{a.T, p.cols, n, a.dtype, dz, ldz, wp, ldw, a.stream, nullptr, nullptr,
+                       nullptr};
+            t.sums = reinterpret_cast<float*>(at(ws, p.acc_x));
+            t.slices = p.dx.slices;
+            MIGEMM_TRY(hip_status(launch_loss(t, p.dx.config)));
+        } else if (dx) {
             void* const c = p.dx_acc ? at(ws, p.acc_x) : dx;
             const int ct = p.dx_acc ? MIGEMM_F32 : a.dtype;
             const Choice ch = dx_choice(a.dtype, a.T, p.cols, n);
@@ -294,9 +338,10 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
         }
     }
     if (dx && p.dx_acc)
-        MIGEMM_TRY(hip_status(launch_scaled_convert(a.dtype, a.T, a.D,
-                                                    reinterpret_cast<float*>(at(ws, p.acc_x)),
-                                                    p.cols, inverse, dx, lddx, a.stream)));
+        MIGEMM_TRY(hip_status(launch_join(a.dtype, a.T, a.D,
+                                          reinterpret_cast<float*>(at(ws, p.acc_x)), p.cols,
+                                          p.dx.slices > 0 ? p.dx.slices : 1, inverse, dx, lddx,
+                                          a.stream)));
 #undef MIGEMM_TRY
     return MIGEMM_OK;
 }

@@ -67,6 +67,40 @@ hipError_t launch_with(const LossTile& t, const Out& out) {
         g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
 }
 
+// Slices of dz W's k: workgroups of one tile and slice each (SPLITK of
+// mfma16_direct.hpp), plain FP32 sums.
+template <class Cfg>
+hipError_t launch_slices(const LossTile& t) {
+    using E = typename Cfg::E;
+    GemmArgs g{};
+    g.pad_a = true;
+    g.M = t.M;
+    g.N = t.N;
+    g.K = t.K;
+    g.A = t.A;
+    g.lda = t.lda;
+    g.B = t.B;
+    g.ldb = t.ldb;
+    g.stream = t.stream;
+    constexpr bool kTail = (Cfg::FLAGS & 32) != 0, kHead = (Cfg::FLAGS & 64) != 0;
+    const bool ragged = g.K % Cfg::BK != 0;
+    if (!direct_fits<Cfg>(g) || (ragged && !kTail && (!kHead || g.K % (16 / sizeof(E)) != 0)))
+        return hipErrorInvalidValue;
+    const int64_t tm = ceil_div(g.M, Cfg::BM), tn = ceil_div(g.N, Cfg::BN);
+    if (tm * tn * t.slices > 0x7fffffff / Cfg::NT) return hipErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>(tm * tn * t.slices)), block(Cfg::NT);
+    const E* A = static_cast<const E*>(g.A);
+    const E* B = static_cast<const E*>(g.B);
+    const int itm = static_cast<int>(tm), itn = static_cast<int>(tn);
+    const Epi out{t.sums, t.N, 1.0f, 0.0f, 0};
+    if (ragged)
+        return launch_kernel(
+            g, mfma16_direct_kernel<Cfg, false, false, false, kTail, kHead, true>, grid, block,
+            g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
+    return launch_kernel(g, mfma16_direct_kernel<Cfg, false, false, false, false, false, true>,
+                         grid, block, g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
+}
+
 }  // namespace
 
 template <typename E, int C>
@@ -75,8 +109,11 @@ hipError_t launch_loss_tile(const LossTile& t) {
     if (t.lse) return launch_with<Cfg, false>(t, *t.lse);
     if (t.dz) return launch_with<Cfg, false>(t, *static_cast<const DzOut<E>*>(t.dz));
     // (a k-row image is at least 64 FP32 columns wide)
-    if constexpr (Cfg::BN * sizeof(E) >= 128 && Cfg::BN >= 64)
-        return launch_with<Cfg, true>(t, *static_cast<const GradOut<E>*>(t.grad));
+    if constexpr (Cfg::BN >= 64) {
+        if (t.grad) return launch_with<Cfg, true>(t, *static_cast<const GradOut<E>*>(t.grad));
+        if constexpr (Cfg::SCHED != 4)
+            if (t.slices > 0) return launch_slices<Cfg>(t);
+    }
     return hipErrorInvalidValue;
 }
 

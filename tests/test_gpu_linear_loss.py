@@ -128,6 +128,19 @@ def test_cross_entropy(T, V, D, dtype):
     assert not got[1][target == IGNORE].any() and not got[0][target == IGNORE].any()
 
 
+# dx summed over slices of the vocabulary: 64x64 tiles (more slices than 16), 128x128,
+# 256x256 with the vocabulary ending inside a k-tile; each ending anywhere
+@pytest.mark.parametrize("T,V,D,dtype", [(1, 20011, 264, "f32"), (3, 20011, 264, "f16"),
+                                         (40, 9999, 72, "bf16"), (200, 8003, 1032, "bf16"),
+                                         (300, 5001, 768, "f32"), (1500, 16392, 1496, "bf16")])
+def test_cross_entropy_over_slices_of_the_vocabulary(T, V, D, dtype):
+    x, w, target, grad = ce_case(T, V, D, dtype, T + V + D)
+    say(f"ce {T}x{V}x{D} {dtype}")
+    got = run_ce(x, w, target, grad)
+    index = torch.where(target == IGNORE, -1, target)[:, None]
+    check(got, *reference(x, w, index, None, 1.0, grad, True))
+
+
 # whole 256x256 tiles, ragged ones, K ending inside a k-tile, 128x128 tiles of FP32;
 # dw's last eight columns, past whole 256-wide tiles
 @pytest.mark.parametrize("T,V,D,dtype", [(512, 16384, 128, "bf16"), (500, 16391, 72, "bf16"),
