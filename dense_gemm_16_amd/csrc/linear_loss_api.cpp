@@ -53,6 +53,8 @@ constexpr int64_t kPieceEntries = int64_t(1) << 28;
 constexpr int64_t kPieceMax = int64_t(1) << 20;
 // Multiply-adds below which a launch more costs more than it saves.
 constexpr double kSmallWork = 2147483648.0;  // 2^31
+// Multiply-adds of one product from which whole tiles pay (whole_tiles).
+constexpr double kWholeWork = 68719476736.0;  // 2^36
 
 int64_t round_up(int64_t x, int64_t to) { return ceil_div(x, to) * to; }
 
@@ -99,12 +101,16 @@ struct Plan {
     int64_t ld_copy = 0; // leading dimension of copies
     int64_t bytes = 0;
     int64_t x = 0, w = 0;
+    // rows of the products whose other side is the vocabulary: T, or whole tiles of it
+    int64_t rows = 0;
+    bool band = false;  // the vocabulary past whole tiles is a step of its own
     // forward
     int64_t part = 0, chunks = 0;
     // backward
-    int64_t t_pad = 0, piece = 0, pieces = 0, ldz = 0, cols = 0;
+    int64_t t_pad = 0, x_rows = 0, piece = 0, pieces = 0, ldz = 0, cols = 0;
     bool dx_acc = false;
     LossSlices dx;
+    int dx_slabs = 0;  // dx.slices, and one for the band
     int64_t info = 0, factor = 0, dz = 0, acc_x = 0, tp = 0, gemm = 0, gemm_bytes = 0;
     int64_t take(int64_t n) {
         const int64_t at = bytes;
@@ -133,6 +139,27 @@ Choice dx_choice(int dtype, int64_t T, int64_t cols, int64_t k) {
     return {-1, -1};
 }
 
+// The forward statistics' chunks of n columns.
+int64_t chunks_of(const LossShape& s, int64_t n) { return ceil_div(n, s.bn) * (s.bn / s.chunk); }
+
+// Whether ragged sizes are brought to whole 256x256 tiles, for the ping-pong schedule:
+// x copied to whole tiles of rows, the vocabulary past whole tiles as a band of its
+// own, which costs a copy of x and a small launch or three.  Forward and backward
+// pass, us, without and with (BF16): 8190 x 32003 x 4096 1722 / 1495, 5170 / 4544; 2040 x
+// 32001 x 2048 246 / 217, 747 / 687; 500 x 128255 x 2048 260 / 237, 923 / 835; 8000 x
+// 8001 x 1024 149 / 151, 443 / 457; 1500 x 20000 x 768 60 / 65, 168 / 185.
+bool whole_tiles(const LossArgs& a, int64_t depth) {
+    return loss_shape(a.dtype, a.T, a.V, depth).bn == 256 && depth % 64 == 0 && a.V >= 512 &&
+           static_cast<double>(a.T * a.V) * static_cast<double>(a.D) >= kWholeWork;
+}
+
+// Columns [v0, end) of the vocabulary that a step takes: up to `piece`, and whole
+// tiles and what is left past them as steps of their own where `band` is set.
+int64_t step_of(int64_t v0, int64_t end, int64_t piece, bool band) {
+    const int64_t n = end - v0 < piece ? end - v0 : piece;
+    return band && n > 256 ? n - n % 256 : n;
+}
+
 Plan make_plan(const LossArgs& a, bool backward) {
     Plan p;
     const int64_t es = elem_size(a.dtype), epc = 16 / es;
@@ -143,17 +170,26 @@ Plan make_plan(const LossArgs& a, bool backward) {
     // that whatever they hold (NaN from a masked position) stays out of dw
     p.copy_x = backward || !whole || !rows_ok(a.X, a.ldx, epc);
     p.depth = p.copy_w && p.copy_x ? p.ld_copy : a.D;
+    p.rows = a.T;
+    if (whole_tiles(a, p.depth)) {
+        p.rows = round_up(a.T, 256);
+        p.copy_x = p.copy_x || p.rows != a.T;
+        p.band = a.V % 256 != 0;
+    }
     if (p.copy_w) p.w = p.take(round_up(a.V, 64) * p.ld_copy * es);
     if (!backward) {
-        if (p.copy_x) p.x = p.take(a.T * p.ld_copy * es);
-        const LossShape s = loss_shape(a.dtype, a.T, a.V, p.depth);
-        p.chunks = ceil_div(a.V, s.bn) * (s.bn / s.chunk);
-        p.part = p.take(a.T * p.chunks * static_cast<int64_t>(sizeof(RowStat)));
+        if (p.copy_x) p.x = p.take(p.rows * p.ld_copy * es);
+        for (int64_t v0 = 0, n; v0 < a.V; v0 += n) {
+            n = step_of(v0, a.V, a.V, p.band);
+            p.chunks += chunks_of(loss_shape(a.dtype, p.rows, n, p.depth), n);
+        }
+        p.part = p.take(p.rows * p.chunks * static_cast<int64_t>(sizeof(RowStat)));
         return p;
     }
     p.t_pad = round_up(a.T, 64);
-    p.x = p.take(p.t_pad * p.ld_copy * es);
-    const int64_t fit = kPieceEntries / p.t_pad / 256 * 256;
+    p.x_rows = p.rows > p.t_pad ? p.rows : p.t_pad;
+    p.x = p.take(p.x_rows * p.ld_copy * es);
+    const int64_t fit = kPieceEntries / p.x_rows / 256 * 256;
     p.piece = fit < 2048 ? 2048 : fit > kPieceMax ? kPieceMax : fit;
     if (p.piece > a.V) p.piece = a.V;
     p.pieces = ceil_div(a.V, p.piece);
@@ -167,21 +203,25 @@ Plan make_plan(const LossArgs& a, bool backward) {
     // product outweighs them.
     p.small_w = static_cast<double>(p.piece) * static_cast<double>(p.cols) *
                     static_cast<double>(p.t_pad) < kSmallWork;
-    if (p.pieces == 1) p.dx = dx_slices(a.dtype, a.T, p.cols, a.V);
+    if (p.pieces == 1) {
+        p.dx = dx_slices(a.dtype, a.T, p.cols, step_of(0, a.V, p.piece, p.band));
+        p.dx_slabs = p.dx.slices > 0 ? p.dx.slices + p.band : 0;
+    }
     p.dx_acc = p.wide || p.dx.slices > 0;
     p.info = p.take(round_up(a.T, 256) * static_cast<int64_t>(sizeof(LossRow)));
     p.factor = p.take(256);
-    p.dz = p.take(p.t_pad * p.ldz * es);
-    if (p.dx_acc) p.acc_x = p.take(a.T * p.cols * 4 * (p.dx.slices > 0 ? p.dx.slices : 1));
-    const int64_t last = a.V - (p.pieces - 1) * p.piece;
+    p.dz = p.take(p.x_rows * p.ldz * es);
+    if (p.dx_acc) p.acc_x = p.take((p.dx_slabs > 0 ? p.dx_slabs * a.T : p.rows) * p.cols * 4);
     if (a.top) p.tp = p.take(a.T * a.top * 4);
     // what the two products ask for, for a full piece and the last one (their
     // operands are aligned; NULL stands for that)
-    for (int64_t n : {p.piece, last}) {
+    const int64_t dx_rows = p.dx_acc ? p.rows : a.T;
+    for (int64_t v0 = 0, n; v0 < a.V; v0 += n) {
+        n = step_of(v0, a.V, p.piece, p.band);
         int64_t b = 0;
-        const Choice c = dx_choice(a.dtype, a.T, p.cols, n);
+        const Choice c = dx_choice(a.dtype, dx_rows, p.cols, n);
         if (p.dx.slices == 0 &&
-            workspace_bytes(c.variant, c.config, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, n, a.dtype,
+            workspace_bytes(c.variant, c.config, MIGEMM_OP_N, MIGEMM_OP_N, dx_rows, p.cols, n, a.dtype,
                             nullptr, p.ldz, nullptr, p.copy_w ? p.ld_copy : a.ldw, &b, true) == MIGEMM_OK &&
             b > p.gemm_bytes)
             p.gemm_bytes = b;
@@ -197,6 +237,11 @@ Plan make_plan(const LossArgs& a, bool backward) {
 
 char* at(void* ws, int64_t offset) { return static_cast<char*>(ws) + offset; }
 
+// The rows a product's tiles run over: p.rows where they are 256 high.
+int64_t tile_rows(const LossArgs& a, const Plan& p, int64_t n) {
+    return loss_shape(a.dtype, p.rows, n, p.depth).bn == 256 ? p.rows : a.T;
+}
+
 // X or W as the products read them: in place, or the copy made here.
 hipError_t operand(const LossArgs& a, bool copy, const void* src, int64_t lds, int64_t rows,
                    int64_t rows_out, const Plan& p, void* to, const void** out, int64_t* ld) {
@@ -208,22 +253,32 @@ hipError_t operand(const LossArgs& a, bool copy, const void* src, int64_t lds, i
 
 int forward(const LossArgs& a, float* loss, float* lse, void* ws) {
     const Plan p = make_plan(a, false);
+    const int64_t es = elem_size(a.dtype);
     const void *x, *w;
     int64_t ldx, ldw;
-    int st = hip_status(operand(a, p.copy_x, a.X, a.ldx, a.T, a.T, p, at(ws, p.x), &x, &ldx));
+    int st = hip_status(operand(a, p.copy_x, a.X, a.ldx, a.T, p.rows, p, at(ws, p.x), &x,
+                                &ldx));
     if (st != MIGEMM_OK) return st;
     st = hip_status(operand(a, p.copy_w, a.W, a.ldw, a.V, round_up(a.V, 64), p, at(ws, p.w), &w,
                             &ldw));
     if (st != MIGEMM_OK) return st;
+    RowStat* const part = reinterpret_cast<RowStat*>(at(ws, p.part));
     LseOut out{};
-    out.part = reinterpret_cast<RowStat*>(at(ws, p.part));
+    out.part = part;
     out.chunks = p.chunks;
     out.scale = kLog2e / a.tau;
-    const LossTile t{a.T, a.V, p.depth, a.dtype, x, ldx, w, ldw, a.stream, &out, nullptr, nullptr};
-    st = hip_status(launch_loss(t, loss_shape(a.dtype, a.T, a.V, p.depth).config));
-    if (st != MIGEMM_OK) return st;
-    return hip_status(
-        launch_loss_rows(a, x, ldx, w, ldw, p.depth, out.part, p.chunks, loss, lse));
+    for (int64_t v0 = 0, n; v0 < a.V; v0 += n) {
+        n = step_of(v0, a.V, a.V, p.band);
+        const int64_t rows = tile_rows(a, p, n);
+        const LossShape s = loss_shape(a.dtype, rows, n, p.depth);
+        const LossTile t{rows, n, p.depth, a.dtype, x, ldx,
+                         static_cast<const char*>(w) + v0 * ldw * es, ldw, a.stream, &out,
+                         nullptr, nullptr};
+        st = hip_status(launch_loss(t, s.config));
+        if (st != MIGEMM_OK) return st;
+        out.part += chunks_of(s, n);
+    }
+    return hip_status(launch_loss_rows(a, x, ldx, w, ldw, p.depth, part, p.chunks, loss, lse));
 }
 
 template <typename E>
@@ -232,14 +287,15 @@ hipError_t launch_dz(const LossArgs& a, const Plan& p, const void* x, const void
     DzOut<E> out{};
     out.dz = reinterpret_cast<E*>(at(ws, p.dz));
     out.ldz = round_up(n, 64);
-    out.rows = p.t_pad;
+    out.rows = p.x_rows;
     out.v0 = v0;
     out.info = reinterpret_cast<const LossRow*>(at(ws, p.info));
     out.factor = factor;
     out.scale = kLog2e / a.tau;
-    const LossTile t{a.T, n, p.depth, a.dtype, x, p.ld_copy, w, ldw, a.stream, nullptr, &out,
+    const int64_t rows = tile_rows(a, p, n);
+    const LossTile t{rows, n, p.depth, a.dtype, x, p.ld_copy, w, ldw, a.stream, nullptr, &out,
                      nullptr};
-    return launch_loss(t, loss_shape(a.dtype, a.T, n, p.depth).config);
+    return launch_loss(t, loss_shape(a.dtype, rows, n, p.depth).config);
 }
 
 // dw's rows of one piece, through the factor and the column limit.  Columns past
@@ -289,12 +345,14 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
                                   &w, &ldw)));
     float* const factor =
         a.dtype == MIGEMM_F32 ? nullptr : reinterpret_cast<float*>(at(ws, p.factor));
-    MIGEMM_TRY(hip_status(launch_loss_prepare(a, lse, grad, info, round_up(a.T, 256), x, p.t_pad,
+    MIGEMM_TRY(hip_status(launch_loss_prepare(a, lse, grad, info, round_up(a.T, 256), x, p.x_rows,
                                               p.ld_copy, tp, a.top ? nullptr : factor)));
     if (factor && a.top) MIGEMM_TRY(hip_status(launch_loss_factor(info, a.T, factor, a.stream)));
     const float* const inverse = factor ? factor + 1 : nullptr;
-    for (int64_t v0 = 0; v0 < a.V; v0 += p.piece) {
-        const int64_t n = a.V - v0 < p.piece ? a.V - v0 : p.piece, ldz = round_up(n, 64);
+    const int64_t dx_rows = p.dx_acc ? p.rows : a.T;
+    for (int64_t v0 = 0, n; v0 < a.V; v0 += n) {
+        n = step_of(v0, a.V, p.piece, p.band);
+        const int64_t ldz = round_up(n, 64);
         const char* const wp = static_cast<const char*>(w) + v0 * ldw * es;
         hipError_t e;
         if (a.dtype == MIGEMM_F32)
@@ -312,13 +370,17 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
                        nullptr};
             t.sums = reinterpret_cast<float*>(at(ws, p.acc_x));
             t.slices = p.dx.slices;
-            MIGEMM_TRY(hip_status(launch_loss(t, p.dx.config)));
+            if (v0 > 0) {  // the band: the last slab
+                t.sums += p.dx.slices * a.T * p.cols;
+                t.slices = 1;
+            }
+            MIGEMM_TRY(hip_status(launch_loss(t, v0 > 0 ? 1 : p.dx.config)));
         } else if (dx) {
             void* const c = p.dx_acc ? at(ws, p.acc_x) : dx;
             const int ct = p.dx_acc ? MIGEMM_F32 : a.dtype;
-            const Choice ch = dx_choice(a.dtype, a.T, p.cols, n);
-            MIGEMM_TRY(run_gemm(ch.variant, ch.config, MIGEMM_OP_N, MIGEMM_OP_N, a.T, p.cols, n,
-                                a.dtype, dz, ldz, wp, ldw, 1.0f, v0 ? 1.0f : 0.0f, ct, c,
+            const Choice ch = dx_choice(a.dtype, dx_rows, p.cols, n);
+            MIGEMM_TRY(run_gemm(ch.variant, ch.config, MIGEMM_OP_N, MIGEMM_OP_N, dx_rows, p.cols,
+                                n, a.dtype, dz, ldz, wp, ldw, 1.0f, v0 ? 1.0f : 0.0f, ct, c,
                                 p.dx_acc ? p.cols : lddx, gws, p.gemm_bytes, a.stream, true));
         }
         if (dw) {
@@ -340,7 +402,7 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
     if (dx && p.dx_acc)
         MIGEMM_TRY(hip_status(launch_join(a.dtype, a.T, a.D,
                                           reinterpret_cast<float*>(at(ws, p.acc_x)), p.cols,
-                                          p.dx.slices > 0 ? p.dx.slices : 1, inverse, dx, lddx,
+                                          p.dx_slabs > 0 ? p.dx_slabs : 1, inverse, dx, lddx,
                                           a.stream)));
 #undef MIGEMM_TRY
     return MIGEMM_OK;
