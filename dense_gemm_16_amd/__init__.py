@@ -640,9 +640,10 @@ def _layer(x, w):
     """(device, T, V, D, dtype code, (x pointer, ldx, w pointer, ldw)) of an output
     layer's operands, checked."""
     device = x.device
-    _check_device("x", x, device)
-    _check_device("w", w, device)
-    if x.dtype != w.dtype:
+    if not (x.is_cuda and w.device == device):
+        _check_device("x", x, device)
+        _check_device("w", w, device)
+    if x.dtype is not w.dtype:
         raise ValueError(f"dtype mismatch: {x.dtype} vs {w.dtype}")
     dt, ldx, ldw = _dtype_code(x), _ld(x), _ld(w)
     (T, D), (V, D2) = x.shape, w.shape
@@ -653,8 +654,9 @@ def _layer(x, w):
 
 def _row_vector(name, t, device, dtype, rows):
     """Pointer of a contiguous vector of one value per row, checked."""
-    _check_device(name, t, device)
-    if t.dtype != dtype or tuple(t.shape) != (rows,) or not t.is_contiguous():
+    if t.device != device:
+        _check_device(name, t, device)
+    if t.dtype is not dtype or t.shape != (rows,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} vector of {rows} (got {t.dtype}, "
                          f"{tuple(t.shape)}, strides {t.stride()})")
     return t.data_ptr() or None
@@ -666,7 +668,7 @@ def _row_gradient(grad, device, rows):
     if not isinstance(grad, torch.Tensor):
         return torch.full((rows,), float(grad), dtype=torch.float32, device=device)
     _check_device("grad", grad, device)
-    if grad.dtype == torch.float32 and tuple(grad.shape) == (rows,) and grad.is_contiguous():
+    if grad.dtype is torch.float32 and grad.shape == (rows,) and grad.is_contiguous():
         return grad
     if grad.dim() > 1 or (grad.dim() == 1 and grad.shape[0] != rows):
         raise ValueError(f"grad must be a number or a vector of {rows}")
@@ -677,7 +679,7 @@ def _gradient(name, wanted, given, like):
     """The tensor a gradient is written to: `given` (checked), a new one, or None."""
     import torch
     if given is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device) if wanted else None
+        return torch.empty_like(like, memory_format=torch.contiguous_format) if wanted else None
     _check_device(name, given, like.device)
     if given.dtype != like.dtype or given.shape != like.shape:
         raise ValueError(f"{name} must have the shape and dtype of what it is the gradient of")
