@@ -46,7 +46,7 @@ PARTS = ([("mfma16_part.hip", f"mfma16_{et}_{'gen' if gen else 'plain'}_{c}",
          [("mfma_i8_part.hip", f"mfma_i8_{c}", [f"-DMIGEMM_PART_C={c}"]) for c in (0, 1, 2, 3, 4, 6)] +
          [("linear_loss_part.hip", f"linear_loss_{et}_{c}",
            [f"-DMIGEMM_PART_E={e}", f"-DMIGEMM_PART_C={c}"])
-          for et, e, n in (("f32", "float", 3), ("f16", "_Float16", 4), ("bf16", "bf16_t", 4))
+          for et, e, n in (("f32", "float", 4), ("f16", "_Float16", 4), ("bf16", "bf16_t", 4))
           for c in range(n)])
 # Units that take longest, started first (measured compile times, seconds).
 SLOW_FIRST = ("mfma16_f16_gen_14", "mfma16_bf16_gen_14", "mfma_i8_4", "mfma16_f16_gen_4",

@@ -35,24 +35,28 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 
-// The dot product of two rows of `depth` elements (whole 16-byte chunks), over a
-// wavefront, in FP32.
-template <typename E>
-__device__ __forceinline__ float row_dot(const E* __restrict__ x, const E* __restrict__ w,
-                                         int64_t depth, int lane) {
+// The dot products of a row x with U rows w[u], of `depth` elements each (whole
+// 16-byte chunks), over a wavefront, in FP32.
+template <int U, typename E>
+__device__ __forceinline__ void row_dots(const E* __restrict__ x, const E* const (&w)[U],
+                                         int64_t depth, int lane, float (&sum)[U]) {
     constexpr int EPC = 16 / sizeof(E);
-    float s = 0.0f;
-#pragma unroll 4
-    for (int64_t c = static_cast<int64_t>(lane) * EPC; c < depth; c += kWave * EPC) {
-        const u32x4 xr = *reinterpret_cast<const u32x4*>(x + c);
-        const u32x4 wr = *reinterpret_cast<const u32x4*>(w + c);
-        E xe[EPC], we[EPC];
-        __builtin_memcpy(xe, &xr, 16);
-        __builtin_memcpy(we, &wr, 16);
 #pragma unroll
-        for (int e = 0; e < EPC; ++e) s = fmaf(to_f32(xe[e]), to_f32(we[e]), s);
+    for (int u = 0; u < U; ++u) sum[u] = 0.0f;
+#pragma unroll(U == 1 ? 4 : 2)
+    for (int64_t c = static_cast<int64_t>(lane) * EPC; c < depth; c += kWave * EPC) {
+        E xe[EPC], we[U][EPC];
+        __builtin_memcpy(xe, __builtin_assume_aligned(x + c, 16), 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            __builtin_memcpy(we[u], __builtin_assume_aligned(w[u] + c, 16), 16);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < EPC; ++e) sum[u] = fmaf(to_f32(xe[e]), to_f32(we[u][e]), sum[u]);
     }
-    return wave_sum(s);
+#pragma unroll
+    for (int u = 0; u < U; ++u) sum[u] = wave_sum(sum[u]);
 }
 
 // Teacher logit j of a row, in the teacher's type.
@@ -96,7 +100,8 @@ __device__ __forceinline__ Teacher teacher_row(const LossArgs& a, int64_t row, i
 
 // One workgroup per row: its log-sum-exp from the chunks' statistics, the logits
 // at its target or at the teacher's indices, and its loss.
-template <typename E>
+// KD: distillation (cross entropy keeps fewer registers).
+template <typename E, bool KD>
 __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E* __restrict__ X,
                                                              int64_t ldx, const E* __restrict__ W,
                                                              int64_t ldw, int64_t depth,
@@ -105,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
                                                              float* __restrict__ loss,
                                                              float* __restrict__ lse_out) {
     __shared__ RowStat stat[kRowWaves];
-    __shared__ float logit[kMaxTop];
+    __shared__ float logit[KD ? kMaxTop : 1];
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     float m = -INFINITY, s = 0.0f;
@@ -131,19 +136,36 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
     }
     if (lane == 0) stat[wave] = RowStat{m, s};
     const E* const x = X + row * ldx;
-    if (a.top == 0) {
+    if constexpr (!KD) {
         const int64_t y = a.target[row];
         if (wave == 0 && y >= 0 && y < a.V && y != a.ignore) {
-            const float z = row_dot(x, W + y * ldw, depth, lane);
-            if (lane == 0) logit[0] = z;
+            const E* const w[1] = {W + y * ldw};
+            float z[1];
+            row_dots(x, w, depth, lane, z);
+            if (lane == 0) logit[0] = z[0];
         }
     } else {
-        for (int64_t j = wave; j < a.top; j += kRowWaves) {
-            const int64_t v = a.t_index[row * a.ldi + j];
-            const float z = v >= 0 && v < a.V ? row_dot(x, W + v * ldw, depth, lane) : 0.0f;
-            if (lane == 0) {
-                logit[j] = z;
-                a.student[row * a.lds + j] = z;
+        // four entries of a wavefront at a time, their loads in flight together; one
+        // that is not held reads row 0 and counts as 0
+        constexpr int kEntries = 4;
+        for (int64_t j0 = wave; j0 < a.top; j0 += kEntries * kRowWaves) {
+            const E* w[kEntries];
+            bool held[kEntries];
+            float z[kEntries];
+#pragma unroll
+            for (int u = 0; u < kEntries; ++u) {
+                const int64_t j = j0 + u * kRowWaves;
+                const int64_t v = a.t_index[row * a.ldi + (j < a.top ? j : j0)];
+                held[u] = v >= 0 && v < a.V;
+                w[u] = W + (held[u] ? v : 0) * ldw;
+            }
+            row_dots(x, w, depth, lane, z);
+#pragma unroll
+            for (int u = 0; u < kEntries; ++u) {
+                const int64_t j = j0 + u * kRowWaves;
+                if (lane != 0 || j >= a.top) continue;
+                logit[j] = held[u] ? z[u] : 0.0f;
+                a.student[row * a.lds + j] = logit[j];
             }
         }
     }
@@ -155,7 +177,7 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
     for (int w = 1; w < kRowWaves; ++w) join(m, s, stat[w].largest, stat[w].sum);
     const float lse = (m + log2f(s)) * kLn2;
     float out = 0.0f;
-    if (a.top == 0) {
+    if constexpr (!KD) {
         const int64_t y = a.target[row];
         if (y != a.ignore) out = y >= 0 && y < a.V ? lse - logit[0] : NAN;
     } else {
@@ -410,7 +432,8 @@ hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const
                             float* loss, float* lse) {
     return by_type(a.dtype, [&](auto tag) {
         using E = decltype(tag);
-        loss_rows_kernel<E><<<dim3(static_cast<unsigned>(a.T)), dim3(kThreads), 0, a.stream>>>(
+        auto* const fn = a.top ? loss_rows_kernel<E, true> : loss_rows_kernel<E, false>;
+        fn<<<dim3(static_cast<unsigned>(a.T)), dim3(kThreads), 0, a.stream>>>(
             a, static_cast<const E*>(X), ldx, static_cast<const E*>(W), ldw, depth, part, chunks,
             loss, lse);
         return hipGetLastError();

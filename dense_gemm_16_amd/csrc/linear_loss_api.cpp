@@ -13,21 +13,33 @@ namespace migemm {
 // pass, us on 64 / 128 / 256 (BF16): 64 x 32000 x 1024 18 / 19 / 34, 200 x 50000 x 2048
 // 89 / 78 / 61, 1000 x 8000 x 512 28 / 21 / 24, 2048 x 4096 x 2048 65 / 47 / 50, 4096 x
 // 1000 x 1024 31 / 25 / 41; FP32 100 x 4000 x 512 16 / 38, 500 x 8000 x 512 46 / 42.
-// FP32 on at most half a round of 64x64 tiles takes 64x32 ones, whose k-tile is half
-// as long (33 x 4099 x 520: 10.1 against 13.7).
+// FP32, which the matrix cores' rate bounds, takes 64x64 tiles (two to a CU) where a
+// last round of 128x128 ones would stand mostly empty (723 x 5489 x 804: 82 against
+// 108), 64x32 ones on at most half a round, whose k-tile is half as long (33 x 4099 x
+// 520: 10.1 against 13.7), and 32x64 ones for up to 32 rows (5 x 21566 x 1920: 43
+// against 68).
 LossShape loss_shape(int dtype, int64_t M, int64_t N, int64_t K) {
     auto tiles = [&](int64_t b) { return ceil_div(M, b) * ceil_div(N, b); };
     const bool f32 = dtype == MIGEMM_F32;
     if (!f32 && M > 128 && tiles(256) >= 128)
         return {M % 256 == 0 && N % 256 == 0 && K % 64 == 0 ? 3 : 2, 64, 256};
+    if (f32 && M > 64 && tiles(128) >= 128) {
+        const int64_t t = tiles(64) % 512;
+        const double c64 =
+            static_cast<double>(tiles(64) / 512) + (t > 256 ? 1.0 : t > 0 ? 0.63 : 0.0);
+        if (2.0 * static_cast<double>(ceil_div(tiles(128), 256)) <= c64) return {1, 32, 128};
+        return {0, 16, 64};
+    }
     if (M > 64 && tiles(128) >= 128) return {1, 32, 128};
+    if (f32 && M <= 32) return {3, 16, 64};
     if (f32 && tiles(64) <= 128) return {2, 16, 32};
     return {0, 16, 64};
 }
 
 hipError_t launch_loss(const LossTile& t, int config) {
     if (t.dtype == MIGEMM_F32)
-        return config == 2   ? launch_loss_tile<float, 2>(t)
+        return config == 3   ? launch_loss_tile<float, 3>(t)
+               : config == 2 ? launch_loss_tile<float, 2>(t)
                : config == 1 ? launch_loss_tile<float, 1>(t)
                              : launch_loss_tile<float, 0>(t);
 #define MIGEMM_LOSS(E)                                        \
@@ -86,7 +98,7 @@ LossSlices dx_slices(int dtype, int64_t T, int64_t cols, int64_t k) {
                             (slices < 2 ? 0.0 : static_cast<double>(slices * T * cols) * 8.0 / 3e6);
         if (cost < least) {
             least = cost;
-            best.config = c;
+            best.config = c == 0 && dtype == MIGEMM_F32 && T <= 32 ? 3 : c;
             best.slices = slices < 2 ? 0 : static_cast<int>(slices);
         }
     }
@@ -186,7 +198,7 @@ Plan make_plan(const LossArgs& a, bool backward) {
         p.part = p.take(p.rows * p.chunks * static_cast<int64_t>(sizeof(RowStat)));
         return p;
     }
-    p.t_pad = round_up(a.T, 64);
+    p.t_pad = round_up(a.T, a.dtype == MIGEMM_F32 ? 32 : 64);  // whole k-tiles of dw
     p.x_rows = p.rows > p.t_pad ? p.rows : p.t_pad;
     p.x = p.take(p.x_rows * p.ld_copy * es);
     const int64_t fit = kPieceEntries / p.x_rows / 256 * 256;
@@ -312,7 +324,7 @@ hipError_t launch_grad(const LossArgs& a, const Plan& p, const void* dz, int64_t
     LossTile t{n, p.cols, p.t_pad, a.dtype, dz, ldz, x, p.ld_copy, a.stream, nullptr, nullptr,
                &out};
     LossShape s = loss_shape(a.dtype, n, p.cols, p.t_pad);
-    if (s.bn == 32) s = {0, 16, 64};  // (not for operands with k as their row index)
+    if (a.dtype == MIGEMM_F32 && s.config > 1) s = {0, 16, 64};  // (k is their row index)
     const int64_t rest = p.cols % 256;
     if (s.bn != 256 || p.cols < 256 || rest == 0 || rest > 64) return launch_loss(t, s.config);
     t.N -= rest;

@@ -32,6 +32,10 @@ template <> struct Tile<float, 2> {  // 64x32 on four waves: twice the workgroup
     using Cfg = DirectCfg<float, 64, 32, 2, 2, 16, 4, 32, 8, 2, 48>;
 };
 
+template <> struct Tile<float, 3> {  // 32x64 on four waves, for up to 32 rows
+    using Cfg = DirectCfg<float, 32, 64, 1, 4, 16, 4, 32, 8, 2, 48>;
+};
+
 template <class Cfg, bool TRANS, class Out>
 hipError_t launch_with(const LossTile& t, const Out& out) {
     using E = typename Cfg::E;
@@ -109,11 +113,10 @@ hipError_t launch_loss_tile(const LossTile& t) {
     if (t.lse) return launch_with<Cfg, false>(t, *t.lse);
     if (t.dz) return launch_with<Cfg, false>(t, *static_cast<const DzOut<E>*>(t.dz));
     // (a k-row image is at least 64 FP32 columns wide)
-    if constexpr (Cfg::BN >= 64) {
+    if constexpr (Cfg::BM >= 64 && Cfg::BN >= 64)
         if (t.grad) return launch_with<Cfg, true>(t, *static_cast<const GradOut<E>*>(t.grad));
-        if constexpr (Cfg::SCHED != 4)
-            if (t.slices > 0) return launch_slices<Cfg>(t);
-    }
+    if constexpr (Cfg::BN >= 64 && Cfg::SCHED != 4)
+        if (t.slices > 0) return launch_slices<Cfg>(t);
     return hipErrorInvalidValue;
 }
 
