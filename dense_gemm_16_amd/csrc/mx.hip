@@ -104,9 +104,9 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(
 //
 // ONCE: non-temporal loads, for a source on 8-byte boundaries that the 256 MB
 // last-level cache cannot hold beside the result (8192 x 8192 FP32, 268 MB: 53.7 us,
-// 5.7 TB/s, and 104 with the decoding after it, against 65.0 and 138 for plain ones;
-// one that still lies in the cache is read faster with those, BF16 of that size 34.2
-// us against 37.2).  One row per lane, 256 bytes of an FP32 source row, took 102.
+// 5.7 TB/s, against 65.0 for plain ones; one that still lies in the cache is read
+// faster with those, BF16 of that size 34.2 us against 37.2).  One row per lane, 256
+// bytes of an FP32 source row, took 102.
 constexpr int kBlocks = 8;
 template <typename T> constexpr int kPerLane = 8 / sizeof(T);
 
@@ -189,31 +189,54 @@ template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float x) {
     return bf16_t{f32_to_bf16_bits(x)};
 }
 
-// Eight elements per lane, as in quantize_rows_kernel.
-template <typename T>
+// 16 bytes of the result per lane and store, so that each store of a wavefront is
+// contiguous (32 bytes of an FP32 row per lane, as two stores: 8192 x 8192 102 us).  A
+// result that the 32 MiB of the L2 caches hold is written piece by piece: a reader
+// that follows finds it there (4096 x 4096 BF16 and then a negation 23.9 us, 25.9 in the
+// other form).  A larger one four pieces a lane, with non-temporal stores where it is
+// aligned: 8192 x 8192 FP32 44.6 us (6.8 TB/s, part of it into the last-level cache)
+// against 81, 67.8 with plain stores; and a negation 156 against 175.
+template <typename T, int U>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(
     int64_t rows, int64_t cols, const uint8_t* __restrict__ data, int64_t ldd,
     const uint8_t* __restrict__ scales, int64_t ldsc, T* __restrict__ dst, int64_t ld, int lpr,
-    int64_t segs) {
+    int64_t segs, bool once) {
+    constexpr int VE = 16 / sizeof(T);
+    using Codes = std::conditional_t<VE == 8, uint32_t, uint16_t>;
     const int64_t group = blockIdx.x / segs, seg = blockIdx.x % segs;
     const int64_t row = group * (kThreads / lpr) + threadIdx.x / lpr;
-    const int64_t piece = seg * lpr + threadIdx.x % lpr;
-    const int64_t c = piece * 8;
-    if (row >= rows || c >= cols) return;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(data + row * ldd + piece * 4);
-    const uint32_t b = scales[row * ldsc + piece / 4];
-    const float s = b == 255u ? __uint_as_float(0x7fc00000u)
-                              : __uint_as_float(b == 0u ? 0x00400000u : b << 23);
-    T v[8];
+    const int64_t first = seg * lpr * U + threadIdx.x % lpr;
+    if (row >= rows) return;
+    uint32_t w[U], b[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = from_f32<T>(fp4_value((w >> (4 * i)) & 15u) * s);
-    T* const p = dst + row * ld + c;
-    if (c + 8 <= cols) {
-        __builtin_memcpy(p, v, sizeof(v));
-    } else {
+    for (int u = 0; u < U; ++u) {
+        const int64_t piece = first + u * lpr;
+        if (piece * VE >= cols) continue;
+        w[u] = *reinterpret_cast<const Codes*>(data + row * ldd + piece * (VE / 2));
+        b[u] = scales[row * ldsc + piece * VE / 32];
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < cols) p[i] = v[i];
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = (first + u * lpr) * VE;
+        if (c >= cols) continue;
+        const float s = b[u] == 255u ? __uint_as_float(0x7fc00000u)
+                                     : __uint_as_float(b[u] == 0u ? 0x00400000u : b[u] << 23);
+        T v[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[i] = from_f32<T>(fp4_value((w[u] >> (4 * i)) & 15u) * s);
+        T* const p = dst + row * ld + c;
+        if (c + VE <= cols) {
+            u32x4 raw;
+            __builtin_memcpy(&raw, v, 16);
+            if (once)
+                __builtin_nontemporal_store(raw, reinterpret_cast<u32x4*>(p));
+            else
+                __builtin_memcpy(p, &raw, 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+                if (c + i < cols) p[i] = v[i];
+        }
     }
 }
 
@@ -257,13 +280,20 @@ template <typename T>
 hipError_t dequantize_typed(int64_t rows, int64_t cols, const uint8_t* data, int64_t ldd,
                             const uint8_t* scales, int64_t ldsc, void* dst, int64_t ld,
                             hipStream_t s) {
+    const int64_t pieces = ceil_div(cols, 16 / static_cast<int64_t>(sizeof(T)));
     int lpr;
     int64_t segs;
-    row_shape(ceil_div(cols, 8), lpr, segs);
+    row_shape(pieces, lpr, segs);
+    const bool large =
+        static_cast<double>(rows) * static_cast<double>(cols) * sizeof(T) > 33554432.0;
+    const bool wide = segs > 1 && large;
+    if (wide) segs = ceil_div(segs, 4);
     const int64_t grid = ceil_div(rows, kThreads / lpr) * segs;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    dequantize_kernel<T><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
-        rows, cols, data, ldd, scales, ldsc, static_cast<T*>(dst), ld, lpr, segs);
+    const bool once = large && aligned16(dst) && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0;
+    auto* const fn = wide ? dequantize_kernel<T, 4> : dequantize_kernel<T, 1>;
+    fn<<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
+        rows, cols, data, ldd, scales, ldsc, static_cast<T*>(dst), ld, lpr, segs, once);
     return hipGetLastError();
 }
 
