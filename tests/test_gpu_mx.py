@@ -113,6 +113,25 @@ def test_quantize_leaves_row_padding_alone():
         assert (data[:, 16 * blocks:] == 0xAB).all() and (scales[:, blocks:] == 0xCD).all()
 
 
+# results past 32 MiB take wide rows four pieces a lane; a padded `out` with rows off
+# 16-byte boundaries is written by plain stores
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_dequantize_large(dtype, pad):
+    rows, cols = 4099, 5001
+    rng = np.random.default_rng(5)
+    data = rng.integers(0, 256, (rows, 157 * 16), dtype=np.uint8)
+    scales = np.zeros((rows, 160), np.uint8)
+    scales[:, :157] = rng.integers(118, 136, (rows, 157))
+    want = torch.from_numpy(mx.decode(data, scales, cols)).to(TORCH[dtype])
+    out = torch.full((rows, cols + 7 + pad), 7.0, dtype=TORCH[dtype], device="cuda")
+    say(f"dequantize {dtype} {rows}x{cols} ld={out.stride(0)}")
+    q = mg.MxMatrix(torch.from_numpy(data).cuda(), torch.from_numpy(scales).cuda(), cols)
+    mg.dequantize_mx(q, TORCH[dtype], out[:, :cols])
+    assert torch.equal(out[:, :cols].cpu(), want)
+    assert (out[:, cols:] == 7.0).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 def test_dequantize_rounds_and_handles_every_code(dtype):
     rows, blocks = 16, 16
