@@ -374,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void pad_copy_kernel(int64_t rows, int64_
 template <typename E, int LANES>
 __global__ __launch_bounds__(kThreads) void join_kernel(int64_t rows, int64_t cols,
                                                         const float* __restrict__ src, int64_t lds,
-                                                        int slices,
+                                                        int64_t slab, int slices,
                                                         const float* __restrict__ factor,
                                                         E* __restrict__ dst, int64_t ldd) {
     constexpr int kPieces = kWave / LANES;  // per wavefront
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(int64_t rows, int64_t co
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
         for (int s = sub; s < slices; s += LANES) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(from + s * rows * lds);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(from + s * slab);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += x[e];
         }
@@ -481,13 +481,13 @@ hipError_t launch_pad_copy(int dtype, int64_t rows, int64_t cols, const void* sr
 }
 
 hipError_t launch_join(int dtype, int64_t rows, int64_t cols, const float* src, int64_t lds,
-                       int slices, const float* factor, void* dst, int64_t ldd, hipStream_t s) {
+                       int64_t slab, int slices, const float* factor, void* dst, int64_t ldd, hipStream_t s) {
     return by_type(dtype, [&](auto tag) {
         using E = decltype(tag);
         const int lanes = slices >= 16 ? 8 : 1;
         auto* const fn = lanes == 8 ? join_kernel<E, 8> : join_kernel<E, 1>;
         fn<<<dim3(grid_for(rows * ceil_div(cols, 4) * lanes)), dim3(kThreads), 0, s>>>(
-            rows, cols, src, lds, slices, factor, static_cast<E*>(dst), ldd);
+            rows, cols, src, lds, slab, slices, factor, static_cast<E*>(dst), ldd);
         return hipGetLastError();
     });
 }

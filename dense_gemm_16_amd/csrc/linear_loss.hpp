@@ -324,9 +324,10 @@ hipError_t launch_loss_scatter(const LossArgs& a, const LossRow* info, const flo
 // dst (rows_out x ldd, zero-padded) = src (rows x cols).
 hipError_t launch_pad_copy(int dtype, int64_t rows, int64_t cols, const void* src, int64_t lds,
                            void* dst, int64_t rows_out, int64_t ldd, hipStream_t s);
-// dst (rows x cols, dtype) = the sum of `slices` FP32 matrices (rows x lds, whole
-// 16-byte chunks, one after another at src), times (factor ? *factor : 1).
+// dst (rows x cols, dtype) = the sum of `slices` FP32 matrices (leading dimension lds,
+// whole 16-byte chunks, each `slab` elements after the one before), times (factor ?
+// *factor : 1).
 hipError_t launch_join(int dtype, int64_t rows, int64_t cols, const float* src, int64_t lds,
-                       int slices, const float* factor, void* dst, int64_t ldd, hipStream_t s);
+                       int64_t slab, int slices, const float* factor, void* dst, int64_t ldd, hipStream_t s);
 
 }  // namespace migemm

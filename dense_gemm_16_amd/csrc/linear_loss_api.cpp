@@ -83,9 +83,11 @@ struct LossSlices {
 // slices, and a launch more to convert its sums): 1 x 96923 x 256 30 / 34 / - / 67, 64
 // x 8000 x 1024 20 / 25 / - / 27, 200 x 20000 x 2048 78 / 70 / 84 / 74, 3000 x 32000 x
 // 2048 - / - / 725 / 889, 800 x 600 x 4096 - / - / 54 / 40; FP32 15 x 20986 x 320 34 /
-// 44 / - / 49.
+// 44 / - / 49.  256x256 slices run the ping-pong schedule where sizes are whole tiles
+// and k-tiles (1000 x 128255 x 4096, dx alone: 755 against 854).
 LossSlices dx_slices(int dtype, int64_t T, int64_t cols, int64_t k) {
-    const double step[] = {0.27, 0.62, 1.78}, once[] = {2.0, 5.0, 10.0};
+    const bool whole = T % 256 == 0 && cols % 256 == 0 && k % 64 == 0;
+    const double step[] = {0.27, 0.62, whole ? 1.6 : 1.78}, once[] = {2.0, 5.0, 10.0};
     LossSlices best;
     double least = 1e30;
     for (int c = 0; c < (dtype == MIGEMM_F32 ? 2 : 3); ++c) {
@@ -98,7 +100,7 @@ LossSlices dx_slices(int dtype, int64_t T, int64_t cols, int64_t k) {
                             (slices < 2 ? 0.0 : static_cast<double>(slices * T * cols) * 8.0 / 3e6);
         if (cost < least) {
             least = cost;
-            best.config = c == 0 && dtype == MIGEMM_F32 && T <= 32 ? 3 : c;
+            best.config = c == 0 && dtype == MIGEMM_F32 && T <= 32 ? 3 : c == 2 && whole ? 3 : c;
             best.slices = slices < 2 ? 0 : static_cast<int>(slices);
         }
     }
@@ -216,14 +218,14 @@ Plan make_plan(const LossArgs& a, bool backward) {
     p.small_w = static_cast<double>(p.piece) * static_cast<double>(p.cols) *
                     static_cast<double>(p.t_pad) < kSmallWork;
     if (p.pieces == 1) {
-        p.dx = dx_slices(a.dtype, a.T, p.cols, step_of(0, a.V, p.piece, p.band));
+        p.dx = dx_slices(a.dtype, p.rows, p.cols, step_of(0, a.V, p.piece, p.band));
         p.dx_slabs = p.dx.slices > 0 ? p.dx.slices + p.band : 0;
     }
     p.dx_acc = p.wide || p.dx.slices > 0;
     p.info = p.take(round_up(a.T, 256) * static_cast<int64_t>(sizeof(LossRow)));
     p.factor = p.take(256);
     p.dz = p.take(p.x_rows * p.ldz * es);
-    if (p.dx_acc) p.acc_x = p.take((p.dx_slabs > 0 ? p.dx_slabs * a.T : p.rows) * p.cols * 4);
+    if (p.dx_acc) p.acc_x = p.take((p.dx_slabs > 0 ? p.dx_slabs : 1) * p.rows * p.cols * 4);
     if (a.top) p.tp = p.take(a.T * a.top * 4);
     // what the two products ask for, for a full piece and the last one (their
     // operands are aligned; NULL stands for that)
@@ -378,12 +380,12 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
             MIGEMM_TRY(
                 hip_status(launch_loss_scatter(a, info, tp, factor, dz, ldz, v0, v0 + n)));
         if (dx && p.dx.slices > 0) {
-            LossTile t{a.T, p.cols, n, a.dtype, dz, ldz, wp, ldw, a.stream, nullptr, nullptr,
+            LossTile t{p.rows, p.cols, n, a.dtype, dz, ldz, wp, ldw, a.stream, nullptr, nullptr,
                        nullptr};
             t.sums = reinterpret_cast<float*>(at(ws, p.acc_x));
             t.slices = p.dx.slices;
             if (v0 > 0) {  // the band: the last slab
-                t.sums += p.dx.slices * a.T * p.cols;
+                t.sums += p.dx.slices * p.rows * p.cols;
                 t.slices = 1;
             }
             MIGEMM_TRY(hip_status(launch_loss(t, v0 > 0 ? 1 : p.dx.config)));
@@ -414,8 +416,8 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
     if (dx && p.dx_acc)
         MIGEMM_TRY(hip_status(launch_join(a.dtype, a.T, a.D,
                                           reinterpret_cast<float*>(at(ws, p.acc_x)), p.cols,
-                                          p.dx_slabs > 0 ? p.dx_slabs : 1, inverse, dx, lddx,
-                                          a.stream)));
+                                          p.rows * p.cols, p.dx_slabs > 0 ? p.dx_slabs : 1,
+                                          inverse, dx, lddx, a.stream)));
 #undef MIGEMM_TRY
     return MIGEMM_OK;
 }

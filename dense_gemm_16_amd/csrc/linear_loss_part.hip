@@ -90,6 +90,8 @@ hipError_t launch_slices(const LossTile& t) {
     const bool ragged = g.K % Cfg::BK != 0;
     if (!direct_fits<Cfg>(g) || (ragged && !kTail && (!kHead || g.K % (16 / sizeof(E)) != 0)))
         return hipErrorInvalidValue;
+    if (Cfg::SCHED == 4 && (ragged || g.M % Cfg::BM != 0 || g.N % Cfg::BN != 0))
+        return hipErrorInvalidValue;
     const int64_t tm = ceil_div(g.M, Cfg::BM), tn = ceil_div(g.N, Cfg::BN);
     if (tm * tn * t.slices > 0x7fffffff / Cfg::NT) return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(tm * tn * t.slices)), block(Cfg::NT);
@@ -97,10 +99,11 @@ hipError_t launch_slices(const LossTile& t) {
     const E* B = static_cast<const E*>(g.B);
     const int itm = static_cast<int>(tm), itn = static_cast<int>(tn);
     const Epi out{t.sums, t.N, 1.0f, 0.0f, 0};
-    if (ragged)
-        return launch_kernel(
-            g, mfma16_direct_kernel<Cfg, false, false, false, kTail, kHead, true>, grid, block,
-            g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
+    if constexpr (kTail || kHead)
+        if (ragged)
+            return launch_kernel(
+                g, mfma16_direct_kernel<Cfg, false, false, false, kTail, kHead, true>, grid,
+                block, g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
     return launch_kernel(g, mfma16_direct_kernel<Cfg, false, false, false, false, false, true>,
                          grid, block, g.M, g.N, g.K, A, g.lda, B, g.ldb, out, itm, itn);
 }
@@ -115,7 +118,7 @@ hipError_t launch_loss_tile(const LossTile& t) {
     // (a k-row image is at least 64 FP32 columns wide)
     if constexpr (Cfg::BM >= 64 && Cfg::BN >= 64)
         if (t.grad) return launch_with<Cfg, true>(t, *static_cast<const GradOut<E>*>(t.grad));
-    if constexpr (Cfg::BN >= 64 && Cfg::SCHED != 4)
+    if constexpr (Cfg::BN >= 64)
         if (t.slices > 0) return launch_slices<Cfg>(t);
     return hipErrorInvalidValue;
 }
