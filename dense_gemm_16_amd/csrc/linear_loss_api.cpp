@@ -323,6 +323,7 @@ hipError_t launch_grad(const LossArgs& a, const Plan& p, const void* dz, int64_t
     out.ldg = lddw;
     out.cols = a.D;
     out.factor = factor;
+    out.nt = (lddw * sizeof(E)) % 128 == 0 && (reinterpret_cast<uintptr_t>(dw) & 127) == 0;
     LossTile t{n, p.cols, p.t_pad, a.dtype, dz, ldz, x, p.ld_copy, a.stream, nullptr, nullptr,
                &out};
     LossShape s = loss_shape(a.dtype, n, p.cols, p.t_pad);
