@@ -455,6 +455,17 @@ def gemm(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=Non
     return out
 
 
+_torch = None
+
+
+def _load_torch():
+    """torch, kept in a global: an import statement costs a short call 0.2 us."""
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 # ---------------------------------------------------------------------- MXFP4
 
 class MxMatrix(NamedTuple):
@@ -480,7 +491,7 @@ class MxMatrix(NamedTuple):
 
 def _mx_operand(name, m, device):
     """(data pointer, ldd, scales pointer, ldsc) of an MxMatrix, checked."""
-    import torch
+    torch = _torch or _load_torch()
     data, scales, cols = m
     blocks, u8 = (cols + 31) // 32, torch.uint8
     if not (data.is_cuda and scales.is_cuda and data.device == device == scales.device):
@@ -507,28 +518,28 @@ def _mx_operand(name, m, device):
     return data.data_ptr() or None, ldd, scales.data_ptr() or None, ldsc
 
 
-class _DeviceOf:
-    """Makes a tensor's device torch's current one for a call, where it is not."""
-    __slots__ = ("guard",)
-
-    def __init__(self, device):
-        import torch
-        self.guard = None
-        if torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
+class _Here:
+    """The context of a call on torch's current device: nothing to change."""
 
     def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+        pass
 
     def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+        pass
+
+
+_here = _Here()
+
+
+def _device_of(device):
+    """A context that makes `device` torch's current one, where it is not."""
+    torch = _torch or _load_torch()
+    return _here if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
 def _stream_of(stream, device):
     """(stream handle, whether it is another one than torch's current stream)."""
-    import torch
+    torch = _torch or _load_torch()
     current = torch._C._cuda_getCurrentRawStream(device.index)
     return (current, False) if stream is None else (stream, stream != current)
 
@@ -538,7 +549,7 @@ def _run_on(stream, device, *tensors):
     is queued on the current stream (new tensors may reuse memory that work there
     still reads), and the tensors, None apart, are kept from being reused before the
     work queued on `stream` has finished."""
-    import torch
+    torch = _torch or _load_torch()
     s = torch.cuda.ExternalStream(stream, device=device)
     s.wait_stream(torch.cuda.current_stream(device))
     for t in tensors:
@@ -551,13 +562,13 @@ def quantize_mx(src, *, out=None, stream=None):
     transposed view of row-major storage, read as stored) quantised to MXFP4 along
     its rows, as an ``MxMatrix`` (``out``, if given).  Quantise a weight stored K x N
     for ``gemm_mx`` as ``quantize_mx(w.t())``.  Does not synchronise."""
-    import torch
+    torch = _torch or _load_torch()
     device = src.device
     _check_device("src", src, device)
     op, lds = _operand(src)
     rows, cols = src.shape
     blocks = (cols + 31) // 32
-    with _DeviceOf(device):
+    with _device_of(device):
         stream, other = _stream_of(stream, device)
         if out is None:
             ldd, ldsc = 16 * max(blocks, 1), max(16, (blocks + 15) // 16 * 16)
@@ -580,11 +591,11 @@ def quantize_mx(src, *, out=None, stream=None):
 def dequantize_mx(m, dtype, out=None, *, stream=None):
     """The values of an ``MxMatrix`` as a row-major ``dtype`` tensor (float32,
     float16 or bfloat16; ``out``, if given).  Does not synchronise."""
-    import torch
+    torch = _torch or _load_torch()
     device = m.device
     rows, cols = m.shape
     data, ldd, scales, ldsc = _mx_operand("m", m, device)
-    with _DeviceOf(device):
+    with _device_of(device):
         stream, other = _stream_of(stream, device)
         if out is None:
             out = torch.empty((rows, cols), dtype=dtype, device=device)
@@ -607,14 +618,14 @@ def gemm_mx(a, b, out=None, *, alpha: float = 1.0, beta: float = 0.0, out_dtype=
     M x K, ``b`` N x K (quantised along k).  ``out`` (M x N, row-major, float32,
     float16 or bfloat16) is allocated with ``out_dtype`` (default float32) if not
     given, which beta == 0 requires.  Does not synchronise."""
-    import torch
+    torch = _torch or _load_torch()
     device = a.device
     (M, K), (N, K2) = a.shape, b.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {a.shape} x {b.shape} transposed")
     pa, lda, psa, ldsa = _mx_operand("a", a, device)
     pb, ldb, psb, ldsb = _mx_operand("b", b, device)
-    with _DeviceOf(device):
+    with _device_of(device):
         stream, other = _stream_of(stream, device)
         if out is None:
             if beta != 0.0:
@@ -664,7 +675,7 @@ def _row_vector(name, t, device, dtype, rows):
 
 def _row_gradient(grad, device, rows):
     """`grad` as one float32 per row: a number, a 0-d tensor or a vector."""
-    import torch
+    torch = _torch or _load_torch()
     if not isinstance(grad, torch.Tensor):
         return torch.full((rows,), float(grad), dtype=torch.float32, device=device)
     _check_device("grad", grad, device)
@@ -677,7 +688,7 @@ def _row_gradient(grad, device, rows):
 
 def _gradient(name, wanted, given, like):
     """The tensor a gradient is written to: `given` (checked), a new one, or None."""
-    import torch
+    torch = _torch or _load_torch()
     if given is None:
         return torch.empty_like(like, memory_format=torch.contiguous_format) if wanted else None
     _check_device(name, given, like.device)
@@ -687,7 +698,7 @@ def _gradient(name, wanted, given, like):
 
 
 def _loss_workspace(backward, T, V, D, top, dt, ptrs, device):
-    import torch
+    torch = _torch or _load_torch()
     st, n = migemm_linear_loss_workspace_size(backward, T, V, D, top, dt, *ptrs)
     if st != OK:
         raise MigemmError(st, "migemm_linear_loss_workspace_size")
@@ -696,7 +707,7 @@ def _loss_workspace(backward, T, V, D, top, dt, ptrs, device):
 
 def _teacher(logits, index, T, device):
     """(dtype code, pointer, ldt, index pointer, ldi, entries per row), checked."""
-    import torch
+    torch = _torch or _load_torch()
     _check_device("teacher_logits", logits, device)
     _check_device("teacher_index", index, device)
     if logits.dim() != 2 or logits.shape[0] != T or index.shape != logits.shape:
@@ -717,10 +728,10 @@ def linear_cross_entropy(x, w, target, *, ignore_index: int = -100, stream=None)
     (default: torch's current stream; another one first waits for it) without
     synchronising.  Autograd does not see the call: the gradients come from the
     backward function."""
-    import torch
+    torch = _torch or _load_torch()
     device, T, V, D, dt, ptrs = _layer(x, w)
     pt = _row_vector("target", target, device, torch.int64, T)
-    with _DeviceOf(device):
+    with _device_of(device):
         stream, other = _stream_of(stream, device)
         loss = torch.empty(T, dtype=torch.float32, device=device)
         lse = torch.empty(T, dtype=torch.float32, device=device)
@@ -742,11 +753,11 @@ def linear_cross_entropy_backward(x, w, target, lse, grad, *, ignore_index: int 
     in their dtype, for the upstream gradient ``grad`` of each row's loss (a number
     or a vector of T).  ``dx`` and ``dw`` are written into if given; one that is
     neither given nor needed is None."""
-    import torch
+    torch = _torch or _load_torch()
     device, T, V, D, dt, ptrs = _layer(x, w)
     pt = _row_vector("target", target, device, torch.int64, T)
     pl = _row_vector("lse", lse, device, torch.float32, T)
-    with _DeviceOf(device):
+    with _device_of(device):
         stream, other = _stream_of(stream, device)
         grad = _row_gradient(grad, device, T)
         dx, dw = _gradient("dx", need_dx, dx, x), _gradient("dw", need_dw, dw, w)
@@ -775,10 +786,10 @@ def linear_distillation(x, w, teacher_logits, teacher_index, *, temperature: flo
     ``student`` (the student's logits at the indices) are what
     ``linear_distillation_backward`` takes.  All float32.  A row that holds no entry
     has loss 0.  Otherwise as ``linear_cross_entropy``."""
-    import torch
+    torch = _torch or _load_torch()
     device, T, V, D, dt, ptrs = _layer(x, w)
     teacher, top = _teacher(teacher_logits, teacher_index, T, device)
-    with _DeviceOf(device):
+    with _device_of(device):
         stream, other = _stream_of(stream, device)
         loss = torch.empty(T, dtype=torch.float32, device=device)
         lse = torch.empty(T, dtype=torch.float32, device=device)
@@ -800,14 +811,14 @@ def linear_distillation_backward(x, w, teacher_logits, teacher_index, lse, stude
                                  need_dw: bool = True, stream=None):
     """(dx, dw): the gradients of ``linear_distillation``'s losses to ``x`` and ``w``;
     arguments as in ``linear_cross_entropy_backward``."""
-    import torch
+    torch = _torch or _load_torch()
     device, T, V, D, dt, ptrs = _layer(x, w)
     teacher, top = _teacher(teacher_logits, teacher_index, T, device)
     pl = _row_vector("lse", lse, device, torch.float32, T)
     _check_device("student", student, device)
     if student.dtype != torch.float32 or tuple(student.shape) != (T, top):
         raise ValueError(f"student must be float32, {T} x {top}")
-    with _DeviceOf(device):
+    with _device_of(device):
         stream, other = _stream_of(stream, device)
         grad = _row_gradient(grad, device, T)
         dx, dw = _gradient("dx", need_dx, dx, x), _gradient("dw", need_dw, dw, w)
