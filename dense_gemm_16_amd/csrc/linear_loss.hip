@@ -481,7 +481,8 @@ hipError_t launch_pad_copy(int dtype, int64_t rows, int64_t cols, const void* sr
 }
 
 hipError_t launch_join(int dtype, int64_t rows, int64_t cols, const float* src, int64_t lds,
-                       int64_t slab, int slices, const float* factor, void* dst, int64_t ldd, hipStream_t s) {
+                       int64_t slab, int slices, const float* factor, void* dst, int64_t ldd,
+                       hipStream_t s) {
     return by_type(dtype, [&](auto tag) {
         using E = decltype(tag);
         const int lanes = slices >= 16 ? 8 : 1;

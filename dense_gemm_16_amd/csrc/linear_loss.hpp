@@ -334,6 +334,7 @@ hipError_t launch_pad_copy(int dtype, int64_t rows, int64_t cols, const void* sr
 // whole 16-byte chunks, each `slab` elements after the one before), times (factor ?
 // *factor : 1).
 hipError_t launch_join(int dtype, int64_t rows, int64_t cols, const float* src, int64_t lds,
-                       int64_t slab, int slices, const float* factor, void* dst, int64_t ldd, hipStream_t s);
+                       int64_t slab, int slices, const float* factor, void* dst, int64_t ldd,
+                       hipStream_t s);
 
 }  // namespace migemm

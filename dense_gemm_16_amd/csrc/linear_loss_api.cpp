@@ -174,6 +174,17 @@ int64_t step_of(int64_t v0, int64_t end, int64_t piece, bool band) {
     return band && n > 256 ? n - n % 256 : n;
 }
 
+// The tiles of a product with n columns of the vocabulary, and the rows they run
+// over: p.rows where they are 256 high.
+struct Tiling {
+    int64_t rows;
+    LossShape shape;
+};
+Tiling tiling(const LossArgs& a, const Plan& p, int64_t n) {
+    const LossShape s = loss_shape(a.dtype, p.rows, n, p.depth);
+    return s.bn == 256 ? Tiling{p.rows, s} : Tiling{a.T, loss_shape(a.dtype, a.T, n, p.depth)};
+}
+
 Plan make_plan(const LossArgs& a, bool backward) {
     Plan p;
     const int64_t es = elem_size(a.dtype), epc = 16 / es;
@@ -195,7 +206,7 @@ Plan make_plan(const LossArgs& a, bool backward) {
         if (p.copy_x) p.x = p.take(p.rows * p.ld_copy * es);
         for (int64_t v0 = 0, n; v0 < a.V; v0 += n) {
             n = step_of(v0, a.V, a.V, p.band);
-            p.chunks += chunks_of(loss_shape(a.dtype, p.rows, n, p.depth), n);
+            p.chunks += chunks_of(tiling(a, p, n).shape, n);
         }
         p.part = p.take(p.rows * p.chunks * static_cast<int64_t>(sizeof(RowStat)));
         return p;
@@ -235,8 +246,9 @@ Plan make_plan(const LossArgs& a, bool backward) {
         int64_t b = 0;
         const Choice c = dx_choice(a.dtype, dx_rows, p.cols, n);
         if (p.dx.slices == 0 &&
-            workspace_bytes(c.variant, c.config, MIGEMM_OP_N, MIGEMM_OP_N, dx_rows, p.cols, n, a.dtype,
-                            nullptr, p.ldz, nullptr, p.copy_w ? p.ld_copy : a.ldw, &b, true) == MIGEMM_OK &&
+            workspace_bytes(c.variant, c.config, MIGEMM_OP_N, MIGEMM_OP_N, dx_rows, p.cols, n,
+                            a.dtype, nullptr, p.ldz, nullptr, p.copy_w ? p.ld_copy : a.ldw, &b,
+                            true) == MIGEMM_OK &&
             b > p.gemm_bytes)
             p.gemm_bytes = b;
         if (!p.wide && !p.small_w &&
@@ -250,11 +262,6 @@ Plan make_plan(const LossArgs& a, bool backward) {
 }
 
 char* at(void* ws, int64_t offset) { return static_cast<char*>(ws) + offset; }
-
-// The rows a product's tiles run over: p.rows where they are 256 high.
-int64_t tile_rows(const LossArgs& a, const Plan& p, int64_t n) {
-    return loss_shape(a.dtype, p.rows, n, p.depth).bn == 256 ? p.rows : a.T;
-}
 
 // X or W as the products read them: in place, or the copy made here.
 hipError_t operand(const LossArgs& a, bool copy, const void* src, int64_t lds, int64_t rows,
@@ -283,14 +290,13 @@ int forward(const LossArgs& a, float* loss, float* lse, void* ws) {
     out.scale = kLog2e / a.tau;
     for (int64_t v0 = 0, n; v0 < a.V; v0 += n) {
         n = step_of(v0, a.V, a.V, p.band);
-        const int64_t rows = tile_rows(a, p, n);
-        const LossShape s = loss_shape(a.dtype, rows, n, p.depth);
-        const LossTile t{rows, n, p.depth, a.dtype, x, ldx,
+        const Tiling tl = tiling(a, p, n);
+        const LossTile t{tl.rows, n, p.depth, a.dtype, x, ldx,
                          static_cast<const char*>(w) + v0 * ldw * es, ldw, a.stream, &out,
                          nullptr, nullptr};
-        st = hip_status(launch_loss(t, s.config));
+        st = hip_status(launch_loss(t, tl.shape.config));
         if (st != MIGEMM_OK) return st;
-        out.part += chunks_of(s, n);
+        out.part += chunks_of(tl.shape, n);
     }
     return hip_status(launch_loss_rows(a, x, ldx, w, ldw, p.depth, part, p.chunks, loss, lse));
 }
@@ -306,10 +312,10 @@ hipError_t launch_dz(const LossArgs& a, const Plan& p, const void* x, const void
     out.info = reinterpret_cast<const LossRow*>(at(ws, p.info));
     out.factor = factor;
     out.scale = kLog2e / a.tau;
-    const int64_t rows = tile_rows(a, p, n);
-    const LossTile t{rows, n, p.depth, a.dtype, x, p.ld_copy, w, ldw, a.stream, nullptr, &out,
+    const Tiling tl = tiling(a, p, n);
+    const LossTile t{tl.rows, n, p.depth, a.dtype, x, p.ld_copy, w, ldw, a.stream, nullptr, &out,
                      nullptr};
-    return launch_loss(t, loss_shape(a.dtype, rows, n, p.depth).config);
+    return launch_loss(t, tl.shape.config);
 }
 
 // dw's rows of one piece, through the factor and the column limit.  Columns past

@@ -259,7 +259,8 @@ hipError_t quantize_typed(bool trans, int64_t rows, int64_t cols, const void* sr
         if (grid > 0x7fffffff) return hipErrorInvalidValue;
         const bool vec = reinterpret_cast<uintptr_t>(src) % 8 == 0 &&
                          lds % kPerLane<T> == 0;
-        const bool large = static_cast<double>(cols) * static_cast<double>(lds) * sizeof(T) > 201326592.0;
+        const bool large =
+            static_cast<double>(cols) * static_cast<double>(lds) * sizeof(T) > 201326592.0;
         auto* const fn =
             vec && large ? quantize_cols_kernel<T, true> : quantize_cols_kernel<T, false>;
         fn<<<dim3(static_cast<unsigned>(grid)), dim3(kBlocks * kWave), 0, s>>>(

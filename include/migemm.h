@@ -414,7 +414,8 @@ const char* migemm_mx_config_name(int config);
  * 2^36).
  *
  * Any alignment and leading dimension: rows off 16-byte boundaries, or D not a
- * whole number of 16-byte chunks, are first copied into the workspace.  lse (T
+ * whole number of 16-byte chunks, are first copied into the workspace (and X where
+ * whole tiles of rows, or zeroed ones, are needed).  lse (T
  * floats) is written by a forward pass (the natural log of the sum of exp(z /
  * temperature)) and read by its backward pass.  The workspace
  * (migemm_linear_loss_workspace_size bytes for the same arguments, device

@@ -143,11 +143,13 @@ def test_cross_entropy_over_slices_of_the_vocabulary(T, V, D, dtype):
 
 # whole 256x256 tiles, ragged ones, K ending inside a k-tile, 128x128 tiles of FP32;
 # dw's last eight columns, past whole 256-wide tiles; sizes that are brought to whole
-# tiles (2^36 multiply-adds on), dx over slices and as one product
+# tiles (2^36 multiply-adds on), dx over slices and as one product, a last step whose
+# tiles T and its whole-tile rows would choose differently
 @pytest.mark.parametrize("T,V,D,dtype", [(512, 16384, 128, "bf16"), (500, 16391, 72, "bf16"),
                                          (512, 16384, 192, "f16"), (130, 16500, 264, "f16"),
                                          (65, 17001, 520, "bf16"),
                                          (1000, 33003, 2112, "f16"), (4000, 5000, 4096, "bf16"),
+                                         (8000, 8648, 1024, "bf16"),
                                          (700, 12001, 88, "f16"),
                                          (1024, 4096, 100, "f32"), (1025, 4097, 64, "f32")])
 def test_cross_entropy_on_large_tiles(T, V, D, dtype):
