@@ -721,7 +721,7 @@ def _teacher(logits, index, T, device):
 def linear_cross_entropy(x, w, target, *, ignore_index: int = -100, stream=None):
     """(loss, lse): per row of ``x`` (T x D) the softmax cross entropy of the logits
     ``x @ w.t()`` (``w``: V x D) against ``target`` (int64, T), and the logits'
-    log-sum-exp, which ``linear_cross_entropy_backward`` takes; both float32.  The
+    log-sum-exp (float64), which ``linear_cross_entropy_backward`` takes.  The
     logits are never stored.  Rows whose target is ``ignore_index`` have loss 0; a
     target outside the vocabulary gives NaN.  ``x`` and ``w``: CUDA tensors of one
     dtype (float32, float16, bfloat16), unit column stride.  Runs on ``stream``
@@ -734,7 +734,7 @@ def linear_cross_entropy(x, w, target, *, ignore_index: int = -100, stream=None)
     with _device_of(device):
         stream, other = _stream_of(stream, device)
         loss = torch.empty(T, dtype=torch.float32, device=device)
-        lse = torch.empty(T, dtype=torch.float32, device=device)
+        lse = torch.empty(T, dtype=torch.float64, device=device)
         ws = _loss_workspace(0, T, V, D, 0, dt, ptrs, device)
         if other:
             _run_on(stream, device, x, w, target, loss, lse, ws)
@@ -756,7 +756,7 @@ def linear_cross_entropy_backward(x, w, target, lse, grad, *, ignore_index: int 
     torch = _torch or _load_torch()
     device, T, V, D, dt, ptrs = _layer(x, w)
     pt = _row_vector("target", target, device, torch.int64, T)
-    pl = _row_vector("lse", lse, device, torch.float32, T)
+    pl = _row_vector("lse", lse, device, torch.float64, T)
     with _device_of(device):
         stream, other = _stream_of(stream, device)
         grad = _row_gradient(grad, device, T)
@@ -784,7 +784,7 @@ def linear_distillation(x, w, teacher_logits, teacher_index, *, temperature: flo
     entries, at the vocabulary indices ``teacher_index``, int64; a negative index
     marks an entry that is not held), both at ``temperature``.  ``lse`` and
     ``student`` (the student's logits at the indices) are what
-    ``linear_distillation_backward`` takes.  All float32.  A row that holds no entry
+    ``linear_distillation_backward`` takes.  ``lse`` is float64, the others float32.  A row that holds no entry
     has loss 0.  Otherwise as ``linear_cross_entropy``."""
     torch = _torch or _load_torch()
     device, T, V, D, dt, ptrs = _layer(x, w)
@@ -792,7 +792,7 @@ def linear_distillation(x, w, teacher_logits, teacher_index, *, temperature: flo
     with _device_of(device):
         stream, other = _stream_of(stream, device)
         loss = torch.empty(T, dtype=torch.float32, device=device)
-        lse = torch.empty(T, dtype=torch.float32, device=device)
+        lse = torch.empty(T, dtype=torch.float64, device=device)
         student = torch.empty((T, top), dtype=torch.float32, device=device)
         ws = _loss_workspace(0, T, V, D, top, dt, ptrs, device)
         if other:
@@ -814,7 +814,7 @@ def linear_distillation_backward(x, w, teacher_logits, teacher_index, lse, stude
     torch = _torch or _load_torch()
     device, T, V, D, dt, ptrs = _layer(x, w)
     teacher, top = _teacher(teacher_logits, teacher_index, T, device)
-    pl = _row_vector("lse", lse, device, torch.float32, T)
+    pl = _row_vector("lse", lse, device, torch.float64, T)
     _check_device("student", student, device)
     if student.dtype != torch.float32 or tuple(student.shape) != (T, top):
         raise ValueError(f"student must be float32, {T} x {top}")

@@ -108,7 +108,7 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
                                                              const RowStat* __restrict__ part,
                                                              int64_t chunks,
                                                              float* __restrict__ loss,
-                                                             float* __restrict__ lse_out) {
+                                                             double* __restrict__ lse_out) {
     __shared__ RowStat stat[kRowWaves];
     __shared__ float logit[KD ? kMaxTop : 1];
     const int64_t row = blockIdx.x;
@@ -175,22 +175,24 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
     s = stat[0].sum;
 #pragma unroll
     for (int w = 1; w < kRowWaves; ++w) join(m, s, stat[w].largest, stat[w].sum);
-    const float lse = (m + log2f(s)) * kLn2;
+    const double lse = (static_cast<double>(m) + log2(static_cast<double>(s))) * kLn2;
     float out = 0.0f;
     if constexpr (!KD) {
         const int64_t y = a.target[row];
-        if (y != a.ignore) out = y >= 0 && y < a.V ? lse - logit[0] : NAN;
+        if (y != a.ignore) out = y >= 0 && y < a.V ? static_cast<float>(lse - logit[0]) : NAN;
     } else {
         const Teacher t = teacher_row(a, row, lane);
         if (t.held) {
-            const float log_sum = log2f(t.sum) * kLn2, inv = 1.0f / a.tau;
+            const double log_sum = log2(static_cast<double>(t.sum)) * kLn2;
+            const double inv = 1.0 / a.tau;
             float terms = 0.0f;
             for (int64_t j = lane; j < a.top; j += kWave) {
                 if (a.t_index[row * a.ldi + j] < 0) continue;
-                const float log_p = (teacher_logit(a, row, j) - t.largest) * inv - log_sum;
-                const float p = exp2_of(log_p * kLog2e);
+                const double log_p = (teacher_logit(a, row, j) - t.largest) * inv - log_sum;
+                const float p = exp2_of(static_cast<float>(log_p * kLog2e));
                 // no weight, no term: log p may be -infinity there
-                if (p != 0.0f) terms = fmaf(p, log_p - logit[j] * inv + lse, terms);
+                if (p != 0.0f)
+                    terms = fmaf(p, static_cast<float>(log_p - logit[j] * inv + lse), terms);
             }
             out = a.tau * a.tau * wave_sum(terms);
         }
@@ -218,14 +220,15 @@ __device__ __forceinline__ float ce_coef(const LossArgs& a, int64_t row,
     return y == a.ignore ? 0.0f : y >= 0 && y < a.V ? g : NAN;
 }
 
-// Row data of the backward pass, and X's row into the padded copy.  factor (cross
+// Row data of the backward pass, and X's row into the padded copy; rows from `twin` on
+// (if not 0) are those of `twin` before.  factor (cross
 // entropy only): written by the first workgroup, from all rows' coefficients;
 // non-finite ones do not count.
 template <typename E>
 __global__ __launch_bounds__(kThreads) void loss_prepare_kernel(
-    LossArgs a, const float* __restrict__ lse, const float* __restrict__ grad,
+    LossArgs a, const double* __restrict__ lse, const float* __restrict__ grad,
     LossRow* __restrict__ info, E* __restrict__ copy, int64_t rows, int64_t ldc,
-    float* __restrict__ tp, float* __restrict__ factor) {
+    float* __restrict__ tp, float* __restrict__ factor, int64_t twin) {
     constexpr int EPC = 16 / sizeof(E);
     __shared__ float shared_coef, part[kRowWaves];
     if (factor != nullptr && blockIdx.x == 0) {
@@ -252,12 +255,19 @@ __global__ __launch_bounds__(kThreads) void loss_prepare_kernel(
             write_factor(m, factor);
         }
     }
-    const int64_t row = blockIdx.x;
+    const bool second = twin > 0 && blockIdx.x >= twin;
+    const int64_t row = blockIdx.x - (second ? twin : 0);  // of the arguments
+    const int64_t to = blockIdx.x;                         // of info and the copy
     const int lane = threadIdx.x % kWave;
     if (threadIdx.x < kWave) {
         LossRow r{0.0f, 0.0f, -1, 0.0f};
         if (row < a.T) {
-            r.lse2 = lse[row] * kLog2e;
+            const double l = lse[row] * 1.4426950408889634;
+            r.lse2 = static_cast<float>(l);
+            if constexpr (sizeof(E) == 4)
+                r.extra = fabsf(r.lse2) < INFINITY ? static_cast<float>(l - r.lse2) : 0.0f;
+            else
+                r.extra = second ? 1.0f : 0.0f;
             if (a.top == 0) {
                 const int64_t y = a.target[row];
                 r.coef = ce_coef(a, row, grad);
@@ -271,17 +281,17 @@ __global__ __launch_bounds__(kThreads) void loss_prepare_kernel(
                     float p = 0.0f;
                     if (r.coef != 0.0f && a.t_index[row * a.ldi + j] >= 0)
                         p = exp2_of(scale * (teacher_logit(a, row, j) - t.largest)) / t.sum;
-                    tp[row * a.top + j] = r.coef * p;
+                    if (!second) tp[row * a.top + j] = r.coef * p;
                 }
             }
         }
         if (lane == 0) {
-            info[row] = r;
+            info[to] = r;
             shared_coef = r.coef;
         }
     }
     __syncthreads();
-    if (row >= rows) return;
+    if (to >= rows) return;
     const bool live = row < a.T && shared_coef != 0.0f;
     const E* const x = static_cast<const E*>(a.X) + row * a.ldx;
     for (int64_t c = static_cast<int64_t>(threadIdx.x) * EPC; c < ldc; c += kThreads * EPC) {
@@ -296,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void loss_prepare_kernel(
                 if (c + e < a.D) v[e] = x[c + e];
             __builtin_memcpy(&w, v, 16);
         }
-        *reinterpret_cast<u32x4*>(copy + row * ldc + c) = w;
+        *reinterpret_cast<u32x4*>(copy + to * ldc + c) = w;
     }
 }
 
@@ -323,7 +333,8 @@ __global__ __launch_bounds__(1024) void loss_factor_kernel(const LossRow* __rest
 template <typename E>
 __global__ __launch_bounds__(kThreads) void loss_scatter_kernel(
     LossArgs a, const LossRow* __restrict__ info, const float* __restrict__ tp,
-    const float* __restrict__ factor, E* __restrict__ dz, int64_t ldz, int64_t v0, int64_t v1) {
+    const float* __restrict__ factor, E* __restrict__ dz, int64_t ldz, int64_t v0, int64_t v1,
+    int64_t twin) {
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWaves + threadIdx.x / kWave;
     const int lane = threadIdx.x % kWave;
     if (row >= a.T) return;
@@ -337,8 +348,12 @@ __global__ __launch_bounds__(kThreads) void loss_scatter_kernel(
         float weight = 0.0f;
         for (int64_t i = 0; i < a.top; ++i)
             if (index[i] == v) weight += tp[row * a.top + i];
-        const float q = exp2_of(fmaf(a.student[row * a.lds + j], scale, -r.lse2));
-        dz[row * ldz + (v - v0)] = narrow<E>((r.coef * q - weight) * f);
+        const float l = fmaf(a.student[row * a.lds + j], scale, -r.lse2);
+        const float q = exp2_of(sizeof(E) == 4 ? l - r.extra : l);
+        const float d = (r.coef * q - weight) * f;
+        const E first = narrow<E>(d);
+        dz[row * ldz + (v - v0)] = first;
+        if (twin > 0) dz[(row + twin) * ldz + (v - v0)] = narrow<E>(d - to_f32(first));
     }
 }
 
@@ -429,7 +444,7 @@ hipError_t by_type(int dtype, F f) {
 
 hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const void* W,
                             int64_t ldw, int64_t depth, const RowStat* part, int64_t chunks,
-                            float* loss, float* lse) {
+                            float* loss, double* lse) {
     return by_type(a.dtype, [&](auto tag) {
         using E = decltype(tag);
         auto* const fn = a.top ? loss_rows_kernel<E, true> : loss_rows_kernel<E, false>;
@@ -440,14 +455,14 @@ hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const
     });
 }
 
-hipError_t launch_loss_prepare(const LossArgs& a, const float* lse, const float* grad,
+hipError_t launch_loss_prepare(const LossArgs& a, const double* lse, const float* grad,
                                LossRow* info, int64_t rows_info, void* copy, int64_t rows,
-                               int64_t ldc, float* tp, float* factor) {
+                               int64_t ldc, float* tp, float* factor, int64_t twin) {
     return by_type(a.dtype, [&](auto tag) {
         using E = decltype(tag);
         loss_prepare_kernel<E>
             <<<dim3(static_cast<unsigned>(rows_info)), dim3(kThreads), 0, a.stream>>>(
-                a, lse, grad, info, static_cast<E*>(copy), rows, ldc, tp, factor);
+                a, lse, grad, info, static_cast<E*>(copy), rows, ldc, tp, factor, twin);
         return hipGetLastError();
     });
 }
@@ -458,13 +473,13 @@ hipError_t launch_loss_factor(const LossRow* info, int64_t rows, float* factor, 
 }
 
 hipError_t launch_loss_scatter(const LossArgs& a, const LossRow* info, const float* tp,
-                               const float* factor, void* dz, int64_t ldz, int64_t v0,
-                               int64_t v1) {
+                               const float* factor, void* dz, int64_t ldz, int64_t v0, int64_t v1,
+                               int64_t twin) {
     return by_type(a.dtype, [&](auto tag) {
         using E = decltype(tag);
         const unsigned grid = static_cast<unsigned>(ceil_div(a.T, kRowWaves));
         loss_scatter_kernel<E><<<dim3(grid), dim3(kThreads), 0, a.stream>>>(
-            a, info, tp, factor, static_cast<E*>(dz), ldz, v0, v1);
+            a, info, tp, factor, static_cast<E*>(dz), ldz, v0, v1, twin);
         return hipGetLastError();
     });
 }

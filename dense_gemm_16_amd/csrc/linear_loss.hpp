@@ -21,22 +21,33 @@
 //
 // Exponents are kept in base 2: with s = log2(e) / tau, exp(z / tau - lse) =
 // 2^(s z - l), l = lse log2(e), one fused multiply-add and one hardware exp2.
-// All statistics are FP32.
+// Statistics are FP32, except that lse is kept in 64 bits (an FP32 one of 8 to 16 is off
+// by up to 2^-21, and with it every q of the row, and a distillation's loss by tau^2
+// times that).
+//
+// Up to kTwin rows of 16-bit dz are kept as two terms, dz and what its rounding left:
+// row t + kTwin of x is row t again, and the tile of 64 rows has the room.  dw's sum
+// over rows and dx's over a row and its twin then hold dz to 16 (FP16: 22) bits.  With
+// few rows the roundings of dz do not average out (5 tokens, distillation, BF16: dx
+// and dw off by 0.0026 without, of which 0.0017 are the final rounding).
 #pragma once
 
 #include "mfma16_direct.hpp"
 
 namespace migemm {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.6931471805599453;
 
 // What the derivative of a row needs: l, c_t (0: a row without a loss, whose
-// derivative is 0 whatever its logits), and the target's column (-1: none).
+// derivative is 0 whatever its logits), the target's column (-1: none), and in FP32
+// what l lacks of its 64-bit value, in 16 bits whether the row is a twin.
 struct LossRow {
     float lse2, coef;
     int32_t target;
-    float unused;
+    float extra;
 };
+constexpr int64_t kTwin = 32;
 
 // A float2-like pair of one row's statistics over one chunk of columns: the
 // largest s z, and the sum of 2^(s z - largest).
@@ -124,7 +135,8 @@ template <> __device__ __forceinline__ bf16_t narrow<bf16_t>(float x) {
 
 // Output step of the backward product: dz, rounded once into the operands' type
 // because the two products that follow run on the matrix cores in that type;
-// the rounding is half a step of each dz, independent of the others.  Columns
+// the rounding is half a step of each dz, independent of the others (a twin row
+// holds it).  Columns
 // from N to the end of the last tile (at most ldz, the piece's width rounded up to
 // 64) become 0, so that the products may read whole 16-byte chunks past N, and so do
 // rows from M to `rows` (rounded up to 64), so that dw's product runs whole k-tiles.
@@ -166,9 +178,12 @@ struct DzOut : Epi {
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
                     const int64_t col = n + 16 * j + lj;
-                    float v = row.coef * exp2_of(fmaf(acc[i][j][e], scale, -row.lse2));
+                    const float l = fmaf(acc[i][j][e], scale, -row.lse2);
+                    float v = row.coef * exp2_of(ES == 4 ? l - row.extra : l);
                     if (v0 + col == row.target) v -= row.coef;
                     if (row.coef == 0.0f || col >= N) v = 0.0f;
+                    if (ES != 4 && Cfg::BM == 64 && row.extra != 0.0f)  // (twins: 64-row tiles)
+                        v -= to_f32(narrow<E>(v));
                     const int c = 16 * j + lj;
                     const int piece = (c / VE) ^ ((g << 1) & (PIECES - 1));
                     *(MIGEMM_LDS Bits*)(scr + (r * WTN + piece * VE + c % VE) * ES) =
@@ -315,18 +330,19 @@ struct LossArgs {
 // (whole chunks) of them read.
 hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const void* W,
                             int64_t ldw, int64_t depth, const RowStat* part, int64_t chunks,
-                            float* loss, float* lse);
+                            float* loss, double* lse);
 // info for `rows_info` rows, X's rows as a zero-padded copy (rows x ldc; rows
 // without a loss become 0), for distillation tp[t][j] = c_t p_j, and for cross
-// entropy the factor (NULL: none).
-hipError_t launch_loss_prepare(const LossArgs& a, const float* lse, const float* grad,
+// entropy the factor (NULL: none).  twin: kTwin, or 0.
+hipError_t launch_loss_prepare(const LossArgs& a, const double* lse, const float* grad,
                                LossRow* info, int64_t rows_info, void* copy, int64_t rows,
-                               int64_t ldc, float* tp, float* factor);
+                               int64_t ldc, float* tp, float* factor, int64_t twin);
 // factor[0] = what brings the largest |coef| to 2^14, factor[1] its inverse.
 hipError_t launch_loss_factor(const LossRow* info, int64_t rows, float* factor, hipStream_t s);
 // Overwrites the entries of dz that distillation's indices name.
 hipError_t launch_loss_scatter(const LossArgs& a, const LossRow* info, const float* tp,
-                               const float* factor, void* dz, int64_t ldz, int64_t v0, int64_t v1);
+                               const float* factor, void* dz, int64_t ldz, int64_t v0, int64_t v1,
+                               int64_t twin);
 // dst (rows_out x ldd, zero-padded) = src (rows x cols).
 hipError_t launch_pad_copy(int dtype, int64_t rows, int64_t cols, const void* src, int64_t lds,
                            void* dst, int64_t rows_out, int64_t ldd, hipStream_t s);

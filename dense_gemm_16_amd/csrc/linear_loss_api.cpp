@@ -118,6 +118,7 @@ struct Plan {
     // rows of the products whose other side is the vocabulary: T, or whole tiles of it
     int64_t rows = 0;
     bool band = false;  // the vocabulary past whole tiles is a step of its own
+    int64_t twin = 0;   // kTwin where dz is kept as two terms
     // forward
     int64_t part = 0, chunks = 0;
     // backward
@@ -182,7 +183,7 @@ struct Tiling {
 };
 Tiling tiling(const LossArgs& a, const Plan& p, int64_t n) {
     const LossShape s = loss_shape(a.dtype, p.rows, n, p.depth);
-    return s.bn == 256 ? Tiling{p.rows, s} : Tiling{a.T, loss_shape(a.dtype, a.T, n, p.depth)};
+    return s.bn == 256 || p.twin ? Tiling{p.rows, s} : Tiling{a.T, loss_shape(a.dtype, a.T, n, p.depth)};
 }
 
 Plan make_plan(const LossArgs& a, bool backward) {
@@ -210,6 +211,10 @@ Plan make_plan(const LossArgs& a, bool backward) {
         }
         p.part = p.take(p.rows * p.chunks * static_cast<int64_t>(sizeof(RowStat)));
         return p;
+    }
+    if (a.dtype != MIGEMM_F32 && a.T <= kTwin) {
+        p.twin = kTwin;
+        p.rows = 2 * kTwin;
     }
     p.t_pad = round_up(a.T, a.dtype == MIGEMM_F32 ? 32 : 64);  // whole k-tiles of dw
     p.x_rows = p.rows > p.t_pad ? p.rows : p.t_pad;
@@ -272,7 +277,7 @@ hipError_t operand(const LossArgs& a, bool copy, const void* src, int64_t lds, i
     return launch_pad_copy(a.dtype, rows, a.D, src, lds, to, rows_out, p.ld_copy, a.stream);
 }
 
-int forward(const LossArgs& a, float* loss, float* lse, void* ws) {
+int forward(const LossArgs& a, float* loss, double* lse, void* ws) {
     const Plan p = make_plan(a, false);
     const int64_t es = elem_size(a.dtype);
     const void *x, *w;
@@ -346,7 +351,7 @@ hipError_t launch_grad(const LossArgs& a, const Plan& p, const void* dz, int64_t
     return launch_loss(t, 0);
 }
 
-int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, int64_t lddx,
+int backward(const LossArgs& a, const double* lse, const float* grad, void* dx, int64_t lddx,
              void* dw, int64_t lddw, void* ws) {
     const Plan p = make_plan(a, true);
     const int64_t es = elem_size(a.dtype);
@@ -367,7 +372,7 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
     float* const factor =
         a.dtype == MIGEMM_F32 ? nullptr : reinterpret_cast<float*>(at(ws, p.factor));
     MIGEMM_TRY(hip_status(launch_loss_prepare(a, lse, grad, info, round_up(a.T, 256), x, p.x_rows,
-                                              p.ld_copy, tp, a.top ? nullptr : factor)));
+                                              p.ld_copy, tp, a.top ? nullptr : factor, p.twin)));
     if (factor && a.top) MIGEMM_TRY(hip_status(launch_loss_factor(info, a.T, factor, a.stream)));
     const float* const inverse = factor ? factor + 1 : nullptr;
     const int64_t dx_rows = p.dx_acc ? p.rows : a.T;
@@ -385,7 +390,7 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
         MIGEMM_TRY(hip_status(e));
         if (a.top)
             MIGEMM_TRY(
-                hip_status(launch_loss_scatter(a, info, tp, factor, dz, ldz, v0, v0 + n)));
+                hip_status(launch_loss_scatter(a, info, tp, factor, dz, ldz, v0, v0 + n, p.twin)));
         if (dx && p.dx.slices > 0) {
             LossTile t{p.rows, p.cols, n, a.dtype, dz, ldz, wp, ldw, a.stream, nullptr, nullptr,
                        nullptr};
@@ -423,7 +428,8 @@ int backward(const LossArgs& a, const float* lse, const float* grad, void* dx, i
     if (dx && p.dx_acc)
         MIGEMM_TRY(hip_status(launch_join(a.dtype, a.T, a.D,
                                           reinterpret_cast<float*>(at(ws, p.acc_x)), p.cols,
-                                          p.rows * p.cols, p.dx_slabs > 0 ? p.dx_slabs : 1,
+                                          (p.twin ? p.twin : p.rows) * p.cols,
+                                          (p.dx_slabs > 0 ? p.dx_slabs : 1) * (p.twin ? 2 : 1),
                                           inverse, dx, lddx, a.stream)));
 #undef MIGEMM_TRY
     return MIGEMM_OK;
@@ -492,12 +498,12 @@ bool add_inputs(const LossArgs& a, Range* in, int& n) {
            add(in, n, a.t_index, a.T, a.top, a.ldi, 8);
 }
 
-int run_forward(const LossArgs& a, float* loss, float* lse, void* ws, int64_t ws_bytes) {
+int run_forward(const LossArgs& a, float* loss, double* lse, void* ws, int64_t ws_bytes) {
     if (a.T == 0) return ws_bytes < 0 ? MIGEMM_ERR_INVALID_ARG : MIGEMM_OK;
     Range in[8], out[8];
     int n_in = 0, n_out = 0;
     if (!add_inputs(a, in, n_in) || !add(out, n_out, loss, 1, a.T, a.T, 4) ||
-        !add(out, n_out, lse, 1, a.T, a.T, 4))
+        !add(out, n_out, lse, 1, a.T, a.T, 8))
         return MIGEMM_ERR_INVALID_ARG;
     if (a.top && !add(out, n_out, a.student, a.T, a.top, a.lds, 4)) return MIGEMM_ERR_INVALID_ARG;
     const Plan p = make_plan(a, false);
@@ -508,7 +514,7 @@ int run_forward(const LossArgs& a, float* loss, float* lse, void* ws, int64_t ws
     return forward(a, loss, lse, ws);
 }
 
-int run_backward(const LossArgs& a, const float* lse, const float* grad, void* dx, int64_t lddx,
+int run_backward(const LossArgs& a, const double* lse, const float* grad, void* dx, int64_t lddx,
                  void* dw, int64_t lddw, void* ws, int64_t ws_bytes) {
     if ((dx && !ld_ok(lddx, a.D)) || (dw && !ld_ok(lddw, a.D)) || ws_bytes < 0)
         return MIGEMM_ERR_INVALID_ARG;
@@ -523,7 +529,7 @@ int run_backward(const LossArgs& a, const float* lse, const float* grad, void* d
     }
     Range in[8], out[8];
     int n_in = 0, n_out = 0;
-    if (!add_inputs(a, in, n_in) || !add(in, n_in, lse, 1, a.T, a.T, 4) ||
+    if (!add_inputs(a, in, n_in) || !add(in, n_in, lse, 1, a.T, a.T, 8) ||
         !add(in, n_in, grad, 1, a.T, a.T, 4))
         return MIGEMM_ERR_INVALID_ARG;
     if (a.top && !add(in, n_in, a.student, a.T, a.top, a.lds, 4)) return MIGEMM_ERR_INVALID_ARG;
@@ -573,7 +579,7 @@ int migemm_linear_loss_workspace_size(int backward, int64_t T, int64_t V, int64_
 
 int migemm_linear_ce_forward(int64_t T, int64_t V, int64_t D, int dtype, const void* X,
                              int64_t ldx, const void* W, int64_t ldw, const int64_t* target,
-                             int64_t ignore_index, float* loss, float* lse, void* workspace,
+                             int64_t ignore_index, float* loss, double* lse, void* workspace,
                              int64_t workspace_bytes, void* stream) {
     LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, stream);
     a.target = target;
@@ -584,7 +590,7 @@ int migemm_linear_ce_forward(int64_t T, int64_t V, int64_t D, int dtype, const v
 
 int migemm_linear_ce_backward(int64_t T, int64_t V, int64_t D, int dtype, const void* X,
                               int64_t ldx, const void* W, int64_t ldw, const int64_t* target,
-                              int64_t ignore_index, const float* lse, const float* grad, void* dX,
+                              int64_t ignore_index, const double* lse, const float* grad, void* dX,
                               int64_t lddx, void* dW, int64_t lddw, void* workspace,
                               int64_t workspace_bytes, void* stream) {
     LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, stream);
@@ -598,7 +604,7 @@ int migemm_linear_kd_forward(int64_t T, int64_t V, int64_t D, int64_t top, int d
                              const void* X, int64_t ldx, const void* W, int64_t ldw,
                              int teacher_dtype, const void* teacher, int64_t ldt,
                              const int64_t* index, int64_t ldi, float temperature, float* loss,
-                             float* lse, float* student, int64_t lds, void* workspace,
+                             double* lse, float* student, int64_t lds, void* workspace,
                              int64_t workspace_bytes, void* stream) {
     LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, stream);
     a.top = top;
@@ -618,7 +624,7 @@ int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int 
                               const void* X, int64_t ldx, const void* W, int64_t ldw,
                               int teacher_dtype, const void* teacher, int64_t ldt,
                               const int64_t* index, int64_t ldi, float temperature,
-                              const float* lse, const float* student, int64_t lds,
+                              const double* lse, const float* student, int64_t lds,
                               const float* grad, void* dX, int64_t lddx, void* dW, int64_t lddw,
                               void* workspace, int64_t workspace_bytes, void* stream) {
     LossArgs a = layer(T, V, D, dtype, X, ldx, W, ldw, stream);

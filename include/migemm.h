@@ -399,13 +399,14 @@ const char* migemm_mx_config_name(int config);
  * X (T x D) holds T tokens, W (V x D) the layer's weight, one row per entry of the
  * vocabulary; both row-major of `dtype` (MIGEMM_F32, MIGEMM_F16, MIGEMM_BF16).
  * The logits z = X W^T are formed tile by tile and never stored; sums, softmax
- * statistics and losses are FP32.  The backward passes recompute the logits in
+ * statistics and losses are FP32, lse is FP64.  The backward passes recompute the logits in
  * pieces of the vocabulary and write the gradients of X (dX, T x D) and W (dW,
  * V x D) in `dtype`; either may be NULL.  grad (T floats) is the upstream gradient
  * of each row's loss: 1 / n for the mean over n rows, 1 for the sum.  The
  * derivative of the loss to each logit is rounded to `dtype` once, for the
  * matrix cores; 16-bit derivatives are held relative to the largest grad, so that
- * FP16 ones do not vanish and equal grads are held exactly.
+ * FP16 ones do not vanish and equal grads are held exactly, and for up to 32 tokens
+ * as two terms.
  *
  * Rows.  T may be 0 (losses: a no-op; dW = 0).  A row without a loss (below) has
  * loss 0, a zero row of dX, and adds nothing to dW, whatever its row of X holds;
@@ -416,7 +417,7 @@ const char* migemm_mx_config_name(int config);
  * Any alignment and leading dimension: rows off 16-byte boundaries, or D not a
  * whole number of 16-byte chunks, are first copied into the workspace (and X where
  * whole tiles of rows, or zeroed ones, are needed).  lse (T
- * floats) is written by a forward pass (the natural log of the sum of exp(z /
+ * doubles) is written by a forward pass (the natural log of the sum of exp(z /
  * temperature)) and read by its backward pass.  The workspace
  * (migemm_linear_loss_workspace_size bytes for the same arguments, device
  * memory, 256-byte aligned) is lent for the call as in migemm_gemm_ws; NULL, a
@@ -441,11 +442,11 @@ int migemm_linear_loss_workspace_size(int backward, int64_t T, int64_t V, int64_
  */
 int migemm_linear_ce_forward(int64_t T, int64_t V, int64_t D, int dtype, const void* X,
                              int64_t ldx, const void* W, int64_t ldw, const int64_t* target,
-                             int64_t ignore_index, float* loss, float* lse, void* workspace,
+                             int64_t ignore_index, float* loss, double* lse, void* workspace,
                              int64_t workspace_bytes, void* stream);
 int migemm_linear_ce_backward(int64_t T, int64_t V, int64_t D, int dtype, const void* X,
                               int64_t ldx, const void* W, int64_t ldw, const int64_t* target,
-                              int64_t ignore_index, const float* lse, const float* grad, void* dX,
+                              int64_t ignore_index, const double* lse, const float* grad, void* dX,
                               int64_t lddx, void* dW, int64_t lddw, void* workspace,
                               int64_t workspace_bytes, void* stream);
 
@@ -463,20 +464,20 @@ int migemm_linear_ce_backward(int64_t T, int64_t V, int64_t D, int dtype, const 
  * gradients NaN.  An index named twice counts with the sum of its weights.
  * student (T x top, leading dimension lds) is written by the forward pass (z at
  * the indices) and read by the backward pass.  temperature lies between 2^-60 and
- * 2^60.  The logarithms are FP32, so a loss carries an error of a few 2^-24 log V
+ * 2^60.  The sums of exponentials are FP32, so a loss carries an error of a few 2^-24
  * temperature^2, which shows at temperatures far above 1.
  */
 int migemm_linear_kd_forward(int64_t T, int64_t V, int64_t D, int64_t top, int dtype,
                              const void* X, int64_t ldx, const void* W, int64_t ldw,
                              int teacher_dtype, const void* teacher, int64_t ldt,
                              const int64_t* index, int64_t ldi, float temperature, float* loss,
-                             float* lse, float* student, int64_t lds, void* workspace,
+                             double* lse, float* student, int64_t lds, void* workspace,
                              int64_t workspace_bytes, void* stream);
 int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int dtype,
                               const void* X, int64_t ldx, const void* W, int64_t ldw,
                               int teacher_dtype, const void* teacher, int64_t ldt,
                               const int64_t* index, int64_t ldi, float temperature,
-                              const float* lse, const float* student, int64_t lds,
+                              const double* lse, const float* student, int64_t lds,
                               const float* grad, void* dX, int64_t lddx, void* dW, int64_t lddw,
                               void* workspace, int64_t workspace_bytes, void* stream);
 
