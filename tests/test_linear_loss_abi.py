@@ -56,7 +56,7 @@ def test_shared_refusals(call, kw):
 
 
 @pytest.mark.parametrize("kw", [{"target": None}, {"loss": None}, {"loss": LSE}, {"lse": X},
-                                {"loss": TGT}, {"loss": WS}])
+                                {"loss": TGT}, {"loss": WS}, {"loss": LSE + 8 * T - 4}])
 def test_ce_forward_refusals(kw):
     assert ce_forward(**kw) == BAD
 
