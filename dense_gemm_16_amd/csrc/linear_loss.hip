@@ -99,7 +99,9 @@ __device__ __forceinline__ Teacher teacher_row(const LossArgs& a, int64_t row, i
 }
 
 // One workgroup per row: its log-sum-exp from the chunks' statistics, the logits
-// at its target or at the teacher's indices, and its loss.
+// at its target or at the teacher's indices, and its loss.  Bound by reading the rows
+// of W that are named, from memory and caches: 4096 rows of 64 entries, D 4096 BF16, 269
+// us (8 TB/s; 328 with one entry at a time).
 // KD: distillation (cross entropy keeps fewer registers).
 template <typename E, bool KD>
 __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E* __restrict__ X,
@@ -357,7 +359,7 @@ __global__ __launch_bounds__(kThreads) void loss_scatter_kernel(
     }
 }
 
-// 16 bytes of dst per lane.
+// 16 bytes of dst per lane.  65890 x 471 FP16: 27 us, 4.7 TB/s (40 an element at a time).
 template <typename E>
 __global__ __launch_bounds__(kThreads) void pad_copy_kernel(int64_t rows, int64_t cols,
                                                             const E* __restrict__ src, int64_t lds,
@@ -385,7 +387,7 @@ __global__ __launch_bounds__(kThreads) void pad_copy_kernel(int64_t rows, int64_
 
 // The sum over slices, scaled, four columns at a time.  LANES lanes share a piece of
 // four columns, each adding every LANES-th slice with its loads in flight together;
-// their sums join in a fixed order.
+// their sums join in a fixed order.  4096 x 4096, one slice into BF16: 20.5 us, 4.9 TB/s.
 template <typename E, int LANES>
 __global__ __launch_bounds__(kThreads) void join_kernel(int64_t rows, int64_t cols,
                                                         const float* __restrict__ src, int64_t lds,
