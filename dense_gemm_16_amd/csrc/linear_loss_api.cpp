@@ -17,7 +17,8 @@ namespace migemm {
 // last round of 128x128 ones would stand mostly empty (723 x 5489 x 804: 82 against
 // 108), 64x32 ones on at most half a round, whose k-tile is half as long (33 x 4099 x
 // 520: 10.1 against 13.7), and 32x64 ones for up to 32 rows (5 x 21566 x 1920: 43
-// against 68).
+// against 68).  2^23 tiles of 64x64 are more than one launch holds (2^32 threads): so many
+// are always 128x128, where a last round no longer counts.
 LossShape loss_shape(int dtype, int64_t M, int64_t N, int64_t K) {
     auto tiles = [&](int64_t b) { return ceil_div(M, b) * ceil_div(N, b); };
     const bool f32 = dtype == MIGEMM_F32;
@@ -27,7 +28,9 @@ LossShape loss_shape(int dtype, int64_t M, int64_t N, int64_t K) {
         const int64_t t = tiles(64) % 512;
         const double c64 =
             static_cast<double>(tiles(64) / 512) + (t > 256 ? 1.0 : t > 0 ? 0.63 : 0.0);
-        if (2.0 * static_cast<double>(ceil_div(tiles(128), 256)) <= c64) return {1, 32, 128};
+        if (tiles(64) >= int64_t(1) << 23 ||
+            2.0 * static_cast<double>(ceil_div(tiles(128), 256)) <= c64)
+            return {1, 32, 128};
         return {0, 16, 64};
     }
     if (M > 64 && tiles(128) >= 128) return {1, 32, 128};
@@ -444,8 +447,9 @@ bool shape_ok(const LossArgs& a, bool kd) {
         return false;
     // copies and the products' offsets: rows of fewer than 2^21 - 64 elements
     if (a.D > (int64_t(1) << 21) - 64) return false;
-    // a launch holds fewer than 2^32 threads: 256 for each row, 512 for each 256x256
-    // tile of the logits (128x128 in FP32; on 64x64 tiles T is at most 64)
+    // a launch holds fewer than 2^32 threads: 256 for each row, 512 for each tile of
+    // the logits, which are 256x256 (FP32: 128x128) unless T is at most 128 (64 for
+    // 64x64) or they are few (fewer than 2^23, loss_shape)
     if (a.T > (int64_t(1) << 23) - 256 || a.V > int64_t(1) << 28 ||
         a.T * a.V > int64_t(1) << (a.dtype == MIGEMM_F32 ? 36 : 38))
         return false;

@@ -52,7 +52,8 @@ hipError_t launch_with(const LossTile& t, const Out& out) {
     g.stream = t.stream;
     if (!direct_fits<Cfg>(g)) return hipErrorInvalidValue;
     const int64_t tm = ceil_div(g.M, Cfg::BM), tn = ceil_div(g.N, Cfg::BN);
-    if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+    // (a launch holds fewer than 2^32 threads; loss_shape keeps within it)
+    if (tm * tn > 0xffffffff / Cfg::NT) return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(tm * tn)), block(Cfg::NT);
     const E* A = static_cast<const E*>(g.A);
     const E* B = static_cast<const E*>(g.B);

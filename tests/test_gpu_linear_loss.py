@@ -522,3 +522,20 @@ def test_a_layer_quantised_distilled_and_served():
     loss, lse = mg.linear_cross_entropy(xd, wd, target, ignore_index=IGNORE)
     want = torch.logsumexp(served.double(), 1)
     assert ((lse.double() - want).abs() <= 2.0 ** -18 * (1 + want.abs())).all()
+
+
+def test_fp32_logits_past_what_small_tiles_can_launch():
+    """More than 2^35 logits: 64x64 tiles of them would be 2^23 or more, whose 512
+    threads each one launch does not hold.  The rows that are compared lie in the
+    first, the last (ragged) and random tiles."""
+    T, V, D = 600001, 64001, 4
+    x, w, target, _ = ce_case(T, V, D, "f32", 3)
+    say(f"ce {T}x{V}x{D} f32 forward")
+    loss, _ = mg.linear_cross_entropy(x, w, target, ignore_index=IGNORE)
+    assert torch.isfinite(loss).all() and not loss[target == IGNORE].any()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    rows = torch.cat((torch.arange(20, device="cuda"), T - 1 - torch.arange(80, device="cuda"),
+                      torch.randint(0, T, (100,), generator=g, device="cuda")))
+    index = torch.where(target == IGNORE, -1, target)[rows, None]
+    want, tol = reference(x[rows], w, index, None, 1.0, torch.ones(200, device="cuda"), True)
+    check((loss[rows], None, None), want, tol)

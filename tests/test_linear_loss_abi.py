@@ -1,5 +1,7 @@
 """The output-layer losses' entry points refuse what their documentation excludes,
 before any HIP call, and size their workspace (CPU only)."""
+import random
+
 import pytest
 import torch
 
@@ -127,3 +129,33 @@ def test_wrappers_check_their_tensors():
         mg.linear_cross_entropy_backward(x, w, t, torch.zeros(4), 1.0)
     with pytest.raises(ValueError, match="must be on the GPU"):
         mg.linear_distillation(x, w, torch.zeros(4, 2), torch.zeros(4, 2, dtype=torch.long))
+
+
+def _forward_tile(T, V):
+    """(rows, columns) of the FP32 forward product's tiles: its workspace holds 8 bytes
+    for each of a row's chunks, 16 columns wide on 64x64 tiles (four to a tile), 32 on
+    128x128."""
+    st, n = ws_bytes(0, dtype=mg.F32, T=T, V=V, D=64, ldx=64, ldw=64)
+    assert st == mg.OK
+    for tile, chunk in ((64, 16), (128, 32)):
+        if n == -(-8 * T * -(-V // tile) * (tile // chunk) // 256) * 256:
+            return tile
+    raise AssertionError(f"workspace of {n} bytes matches no tile")
+
+
+def test_large_fp32_losses_fit_a_launch():
+    """A launch holds fewer than 2^32 threads, 512 to a tile: every size up to the
+    documented 2^36 logits, ragged ones too, takes tiles that are few enough."""
+    rng = random.Random(1)
+    sizes = [(600000, 64000), (1000000, 65000), (300000, 128256), (524289, 128256),
+             (65, 1 << 28), ((1 << 23) - 256, 8191), (129, (1 << 28) - 1), (8391, 8191777)]
+    for _ in range(2000):
+        V = int(2 ** rng.uniform(13, 28))
+        sizes.append((min((1 << 23) - 256, int(2 ** rng.uniform(34.9, 36)) // V), V))
+    for T, V in sizes:
+        if T * V > 1 << 36:
+            continue
+        b = _forward_tile(T, V)
+        assert -(-T // b) * -(-V // b) * 512 < 1 << 32, (T, V, b)
+    # below it the tile is still chosen by rounds
+    assert _forward_tile(723, 5489) == 64 and _forward_tile(1024, 65536) == 128
