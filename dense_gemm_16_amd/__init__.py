@@ -344,7 +344,19 @@ def _ld(t) -> int:
         raise ValueError("operands must be 2-D")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("operands must have unit stride along rows (row-major)")
-    return max(1, t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    if t.shape[0] <= 1:
+        return max(1, t.shape[1])
+    return _apart(t.stride(0), t.shape[1])
+
+
+def _apart(stride, n) -> int:
+    """The leading dimension of rows of `n` elements that lie `stride` apart.  Packed
+    rows of no elements have stride 0 or 1; rows that share their elements
+    (``expand``) have stride 0 too, but no leading dimension says so."""
+    if stride == 0 and n > 0:
+        raise ValueError("rows that share memory (stride 0) are not supported; copy them "
+                         "with contiguous()")
+    return max(1, stride)
 
 
 def _operand(t):
@@ -354,9 +366,9 @@ def _operand(t):
         raise ValueError("operands must be 2-D")
     rows, cols = t.shape
     if cols <= 1 or t.stride(1) == 1:
-        return OP_N, max(1, t.stride(0) if rows > 1 else cols)
+        return OP_N, _apart(t.stride(0), cols) if rows > 1 else max(1, cols)
     if rows <= 1 or t.stride(0) == 1:
-        return OP_T, max(1, t.stride(1) if cols > 1 else rows)
+        return OP_T, _apart(t.stride(1), rows)  # (cols > 1 here)
     raise ValueError("operands must be row-major or transposed views of row-major storage")
 
 

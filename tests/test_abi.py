@@ -653,3 +653,28 @@ def test_missing_library_fails_loudly(monkeypatch, tmp_path):
     monkeypatch.setattr(mg, "LIBRARY_PATH", str(tmp_path / "absent.so"))
     with pytest.raises(RuntimeError, match="not built"):
         mg.migemm_variant_count()
+
+
+def test_rows_that_share_memory_are_refused():
+    """A broadcast tensor has stride 0: with one element to a row (or one row), taking
+    it for a packed one would read, or write, past its storage."""
+    import torch
+    column, row = torch.ones(1, 1).expand(64, 1), torch.ones(1, 1).expand(1, 64)
+    for t in (column, torch.ones(2, 1, 1).expand(2, 64, 1)[1]):
+        assert t.stride(0) == 0
+        with pytest.raises(ValueError, match="stride"):
+            mg._ld(t)
+        with pytest.raises(ValueError, match="stride"):
+            mg._operand(t)
+        with pytest.raises(ValueError, match="stride"):
+            mg._operand(t.t())
+    with pytest.raises(ValueError, match="stride"):
+        mg._ld(row)
+    with pytest.raises(ValueError, match="stride"):
+        mg._operand(row)
+    # a single element, and rows without elements, have nothing to share
+    one, none = torch.ones(1, 1).expand(1, 1), torch.empty(5, 0)
+    assert mg._ld(one) == 1 and mg._operand(one) == (mg.OP_N, 1)
+    assert mg._ld(none) == 1 and mg._ld(torch.empty(1, 1).expand(0, 1)) == 1
+    # one column of a wider matrix
+    assert mg._ld(torch.ones(64, 7)[:, 2:3]) == 7
