@@ -315,6 +315,10 @@ hipError_t launch_empty_product(const GemmArgs& a);
 hipError_t launch_convert(int src_dtype, int dst_dtype, int64_t rows, int64_t cols,
                           const void* src, int64_t lds, void* dst, int64_t ldd, hipStream_t s);
 
+// The most workgroups of `threads` that one launch takes: it holds fewer than 2^32
+// threads.
+constexpr int64_t launch_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
+
 // MXFP4 (mx.hip, mx_gemm.hip): quantisation (trans: the source holds k as its
 // row index), decoding, and the product C = alpha A B + beta C of A (M x K) and
 // B given transposed (N x K); element and scale rows 16-byte aligned.

@@ -249,33 +249,57 @@ void row_shape(int64_t pieces, int& lpr, int64_t& segs) {
     segs = ceil_div(pieces, lpr);
 }
 
+// Calls launch(first row, rows, workgroups) for parts of the rows, kThreads / lpr rows and
+// `segs` workgroups a group, that one launch holds.
+template <typename F>
+hipError_t by_rows(int64_t rows, int lpr, int64_t segs, F launch) {
+    const int64_t per = kThreads / lpr, step = launch_groups(kThreads) / segs * per;
+    for (int64_t r = 0; r < rows; r += step) {
+        const int64_t n = rows - r < step ? rows - r : step;
+        launch(r, n, static_cast<unsigned>(ceil_div(n, per) * segs));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <typename T>
 hipError_t quantize_typed(bool trans, int64_t rows, int64_t cols, const void* src, int64_t lds,
                           uint8_t* data, int64_t ldd, uint8_t* scales, int64_t ldsc,
                           hipStream_t s) {
     const T* p = static_cast<const T*>(src);
     if (trans) {
-        const int64_t tiles_k = ceil_div(ceil_div(cols, 32), kBlocks);
-        const int64_t grid = ceil_div(rows, kWave * kPerLane<T>) * tiles_k;
-        if (grid > 0x7fffffff) return hipErrorInvalidValue;
         const bool vec = reinterpret_cast<uintptr_t>(src) % 8 == 0 &&
                          lds % kPerLane<T> == 0;
         const bool large =
             static_cast<double>(cols) * static_cast<double>(lds) * sizeof(T) > 201326592.0;
         auto* const fn =
             vec && large ? quantize_cols_kernel<T, true> : quantize_cols_kernel<T, false>;
-        fn<<<dim3(static_cast<unsigned>(grid)), dim3(kBlocks * kWave), 0, s>>>(
-            rows, cols, p, lds, data, ldd, scales, ldsc, tiles_k);
-        return hipGetLastError();
+        // whole tiles of k and of rows, as many as one launch holds
+        constexpr int64_t kRows = kWave * kPerLane<T>, kCols = 32 * kBlocks;
+        constexpr int64_t most = launch_groups(kBlocks * kWave), kMostK = int64_t(1) << 20;
+        for (int64_t k = 0; k < cols; k += kMostK * kCols) {
+            const int64_t nk = cols - k < kMostK * kCols ? cols - k : kMostK * kCols;
+            const int64_t tiles_k = ceil_div(nk, kCols), step = most / tiles_k * kRows;
+            for (int64_t r = 0; r < rows; r += step) {
+                const int64_t nr = rows - r < step ? rows - r : step;
+                fn<<<dim3(static_cast<unsigned>(ceil_div(nr, kRows) * tiles_k)),
+                     dim3(kBlocks * kWave), 0, s>>>(nr, nk, p + k * lds + r, lds,
+                                                    data + r * ldd + k / 2, ldd,
+                                                    scales + r * ldsc + k / 32, ldsc, tiles_k);
+                const hipError_t e = hipGetLastError();
+                if (e != hipSuccess) return e;
+            }
+        }
+        return hipSuccess;
     }
     int lpr;
     int64_t segs;
     row_shape(4 * ceil_div(cols, 32), lpr, segs);
-    const int64_t grid = ceil_div(rows, kThreads / lpr) * segs;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    quantize_rows_kernel<T><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
-        rows, cols, p, lds, data, ldd, scales, ldsc, lpr, segs);
-    return hipGetLastError();
+    return by_rows(rows, lpr, segs, [&](int64_t r, int64_t n, unsigned grid) {
+        quantize_rows_kernel<T><<<dim3(grid), dim3(kThreads), 0, s>>>(
+            n, cols, p + r * lds, lds, data + r * ldd, ldd, scales + r * ldsc, ldsc, lpr, segs);
+    });
 }
 
 template <typename T>
@@ -290,13 +314,13 @@ hipError_t dequantize_typed(int64_t rows, int64_t cols, const uint8_t* data, int
         static_cast<double>(rows) * static_cast<double>(cols) * sizeof(T) > 33554432.0;
     const bool wide = segs > 1 && large;
     if (wide) segs = ceil_div(segs, 4);
-    const int64_t grid = ceil_div(rows, kThreads / lpr) * segs;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
     const bool once = large && aligned16(dst) && (ld * static_cast<int64_t>(sizeof(T))) % 16 == 0;
     auto* const fn = wide ? dequantize_kernel<T, 4> : dequantize_kernel<T, 1>;
-    fn<<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(
-        rows, cols, data, ldd, scales, ldsc, static_cast<T*>(dst), ld, lpr, segs, once);
-    return hipGetLastError();
+    return by_rows(rows, lpr, segs, [&](int64_t r, int64_t n, unsigned grid) {
+        fn<<<dim3(grid), dim3(kThreads), 0, s>>>(n, cols, data + r * ldd, ldd, scales + r * ldsc,
+                                                 ldsc, static_cast<T*>(dst) + r * ld, ld, lpr, segs,
+                                                 once);
+    });
 }
 
 }  // namespace

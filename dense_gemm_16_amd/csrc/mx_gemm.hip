@@ -739,7 +739,7 @@ __global__ __launch_bounds__(WAVES * kWave) void mx_rows_kernel(MxArgs p) {
 template <int BX>
 hipError_t launch_tile(const MxArgs& p) {
     const int64_t tm = ceil_div(p.M, BX), tn = ceil_div(p.N, BX);
-    if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+    if (tm * tn > launch_groups(512)) return hipErrorInvalidValue;
     auto* const fn =
         p.K % 256 != 0 ? mx_tile_kernel<BX, true> : mx_tile_kernel<BX, false>;
     fn<<<dim3(static_cast<unsigned>(tm * tn)), dim3(512), 0, p.stream>>>(
@@ -750,7 +750,7 @@ hipError_t launch_tile(const MxArgs& p) {
 template <int BX, int S>
 hipError_t launch_deep(const MxArgs& p) {
     const int64_t tm = ceil_div(p.M, BX), tn = ceil_div(p.N, BX);
-    if (tm * tn > 0x7fffffff) return hipErrorInvalidValue;
+    if (tm * tn > launch_groups(512)) return hipErrorInvalidValue;
     auto* const fn =
         p.K % 512 != 0 ? mx_deep_kernel<BX, S, true> : mx_deep_kernel<BX, S, false>;
     fn<<<dim3(static_cast<unsigned>(tm * tn)), dim3(512), 0, p.stream>>>(
@@ -816,6 +816,17 @@ int choose(const MxArgs& p) {
     return best + 1;
 }
 
+hipError_t launch_part(const MxArgs& p, int config) {
+    switch (config) {
+        case 0: return launch_rows_any(p);
+        case 1: return launch_deep<64, 4>(p);
+        case 2: return launch_deep<64, 2>(p);
+        case 3: return launch_deep<128, 2>(p);
+        case 4: return launch_tile<128>(p);
+        default: return launch_tile<256>(p);
+    }
+}
+
 }  // namespace
 
 int mx_config_count() { return kCount; }
@@ -834,14 +845,27 @@ hipError_t launch_gemm_mx(const MxArgs& p, int config) {
     // the tile kernel's load offsets are 32 bits, over 255 rows
     const int64_t far = int64_t(1) << 23;
     if (p.lda >= far || p.ldb >= far || p.ldsa >= far || p.ldsb >= far) config = 0;
-    switch (config) {
-        case 0: return launch_rows_any(p);
-        case 1: return launch_deep<64, 4>(p);
-        case 2: return launch_deep<64, 2>(p);
-        case 3: return launch_deep<128, 2>(p);
-        case 4: return launch_tile<128>(p);
-        default: return launch_tile<256>(p);
-    }
+    // one launch where it holds the workgroups (of 512 threads); else parts of C that do
+    const int64_t b = config == 0 ? 16 : config <= 2 ? 64 : config <= 4 ? 128 : 256;
+    const int64_t tm = config == 0 ? 1 : ceil_div(p.M, b), most = launch_groups(512);
+    if (ceil_div(p.N, b) <= most / tm) return launch_part(p, config);
+    const int64_t part_m = tm < 4096 ? tm : 4096, rows = config == 0 ? p.M : part_m * b;
+    const int64_t cols = most / part_m * b;
+    for (int64_t m = 0; m < p.M; m += rows)
+        for (int64_t n = 0; n < p.N; n += cols) {
+            MxArgs q = p;
+            q.M = p.M - m < rows ? p.M - m : rows;
+            q.N = p.N - n < cols ? p.N - n : cols;
+            q.A = p.A + m * p.lda;
+            q.sa = p.sa + m * p.ldsa;
+            q.B = p.B + n * p.ldb;
+            q.sb = p.sb + n * p.ldsb;
+            q.out.C = static_cast<char*>(p.out.C) +
+                      (m * p.out.ldc + n) * (p.out.c_dtype == 0 ? 4 : 2);
+            const hipError_t e = launch_part(q, config);
+            if (e != hipSuccess) return e;
+        }
+    return hipSuccess;
 }
 
 }  // namespace migemm

@@ -294,3 +294,77 @@ def test_product_on_another_stream_and_replayed_in_a_graph():
         assert torch.equal(chained, mg.gemm_mx(mg.quantize_mx(x), cases[0][1]))
         assert all(torch.equal(o, w) for o, (_, _, w) in zip(outs, cases))
     assert warm.shape == chained.shape
+
+
+# ------------------------------------------- past 2^32 threads, one launch's limit
+
+def _spots(n, *borders):
+    """Ranges of 300 at both ends and around the borders that lie inside n."""
+    starts = [0, n - 300] + [b - 150 for b in borders if 150 < b < n - 150]
+    return [slice(s, s + 300) for s in starts]
+
+
+@pytest.mark.parametrize("dtype,trans", [("bf16", False), ("f32", True)])
+def test_quantize_and_decode_more_rows_than_one_launch_takes(dtype, trans):
+    # rows of one element, four threads each: 2^32 at 2^30 rows
+    rows = (1 << 30) + 333
+    say(f"quantize {dtype} {rows}x1 trans={trans}")
+    values = torch.tensor([0.0, 1.0, -1.5, 3.0, -0.25, 96.0, 0.375], device="cuda")
+    pick = torch.randint(0, 7, (rows,), device="cuda", dtype=torch.uint8)
+    x = torch.empty(rows, dtype=TORCH[dtype], device="cuda")
+    for s in range(0, rows, 1 << 27):
+        x[s:s + (1 << 27)] = values[pick[s:s + (1 << 27)].int()].to(x.dtype)
+    del pick
+    if trans:   # stored 1 x rows (the wrapper takes a single column for row-major)
+        q = mg.MxMatrix(torch.empty(rows, 16, dtype=torch.uint8, device="cuda"),
+                        torch.empty(rows, 16, dtype=torch.uint8, device="cuda"), 1)
+        assert mg.migemm_quantize_mx(mg.F32, mg.OP_T, rows, 1, x.data_ptr(), rows,
+                                     q.data.data_ptr(), 16, q.scales.data_ptr(), 16,
+                                     torch.cuda.current_stream().cuda_stream) == mg.OK
+    else:
+        q = mg.quantize_mx(x[:, None])
+    # a block of one element of at most two significant bits holds it exactly
+    back = mg.dequantize_mx(q, x.dtype)
+    assert torch.equal(back[:, 0], x)
+    for s in _spots(rows, 1 << 30):
+        part = mg.quantize_mx(x[s, None])
+        assert torch.equal(q.data[s], part.data) and torch.equal(q.scales[s, 0], part.scales[:, 0])
+
+
+def test_quantize_more_columns_than_one_launch_takes():
+    # k as the source's row index, 512 threads for 256 of k: 2^32 at nearly 2^31
+    cols = ((1 << 23) - 1) * 256 + 33
+    blocks = (cols + 31) // 32
+    say(f"quantize bf16 1x{cols} k as the row index")
+    x = torch.empty(cols, dtype=torch.bfloat16, device="cuda")
+    for s in range(0, cols, 1 << 28):
+        x[s:s + (1 << 28)].normal_()
+    ldd, ldsc = 16 * blocks, (blocks + 15) // 16 * 16
+    data = torch.zeros(1, ldd, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(1, ldsc, dtype=torch.uint8, device="cuda")
+    assert mg.migemm_quantize_mx(mg.BF16, mg.OP_T, 1, cols, x.data_ptr(), 1, data.data_ptr(), ldd,
+                                 scales.data_ptr(), ldsc,
+                                 torch.cuda.current_stream().cuda_stream) == mg.OK
+    want = mg.quantize_mx(x[None])
+    assert torch.equal(data, want.data) and torch.equal(scales[:, :blocks], want.scales[:, :blocks])
+
+
+# 16 columns of C to a workgroup of 512 in the rows kernel (32 from 8161 on), 64 to one of
+# 64x64 tiles
+@pytest.mark.parametrize("M,config,N", [(2, 0, (1 << 28) + 333), (3, 1, (1 << 29) + 333)])
+def test_product_of_more_columns_than_one_launch_takes(M, config, N):
+    say(f"gemm_mx {M}x{N}x32 config {config}")
+    rng = np.random.default_rng(M)
+    a = _device(_operand(M, 32, rng), 32)
+    data = torch.randint(0, 256, (N, 16), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(N, 16, dtype=torch.uint8, device="cuda")
+    scales[:, 0] = torch.randint(118, 124, (N,), dtype=torch.uint8, device="cuda")
+    got = mg.gemm_mx(a, mg.MxMatrix(data, scales, 32), out_dtype=torch.bfloat16, config=config)
+    for s in _spots(N, ((1 << 23) - 1) * 16, 1 << 28, ((1 << 23) - 1) * 64):
+        part = mg.MxMatrix(data[s].contiguous(), scales[s].contiguous(), 32)
+        assert torch.equal(got[:, s], mg.gemm_mx(a, part, out_dtype=torch.bfloat16, config=config))
+    step = 1 << 24
+    for s in range(0, N, step):   # nothing is left out in between
+        part = mg.MxMatrix(data[s:s + step], scales[s:s + step], 32)
+        assert torch.equal(got[:, s:s + step],
+                           mg.gemm_mx(a, part, out_dtype=torch.bfloat16, config=config))
