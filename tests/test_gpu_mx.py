@@ -368,3 +368,27 @@ def test_product_of_more_columns_than_one_launch_takes(M, config, N):
         part = mg.MxMatrix(data[s:s + step], scales[s:s + step], 32)
         assert torch.equal(got[:, s:s + step],
                            mg.gemm_mx(a, part, out_dtype=torch.bfloat16, config=config))
+
+
+# Sources past 192 MiB on 8-byte boundaries are read with non-temporal loads: rows that end
+# inside a lane's group, k that ends inside a block, and (one element off) the plain form
+@pytest.mark.parametrize("dtype,rows,cols,ld", [("f32", 7003, 7337, 7004), ("f32", 7004, 7330, 7005),
+                                                ("bf16", 10007, 10273, 10008),
+                                                ("f16", 10006, 10300, 10012)])
+def test_quantize_large_sources_with_k_as_the_row_index(dtype, rows, cols, ld):
+    say(f"quantize {dtype} {rows}x{cols} ld={ld} k as the row index")
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    stored = torch.full((cols, ld), float("nan"), dtype=TORCH[dtype], device="cuda")
+    x = stored[:, :rows].t()
+    x.copy_(torch.randn(rows, cols, generator=g, device="cuda") *
+            torch.exp(torch.randn(rows, 1, generator=g, device="cuda")))
+    assert cols * ld * x.element_size() > 192 << 20
+    q = mg.quantize_mx(x)
+    # rows along k go through the other kernel, and the last rows through the oracle
+    want = mg.quantize_mx(x.contiguous())
+    blocks = (cols + 31) // 32
+    assert torch.equal(q.data[:, :16 * blocks], want.data[:, :16 * blocks])
+    assert torch.equal(q.scales[:, :blocks], want.scales[:, :blocks])
+    codes, byte = mx.quantize(x[-70:].double().cpu().numpy())
+    assert np.array_equal(q.scales[-70:, :blocks].cpu().numpy(), byte)
+    assert np.array_equal(mx.unpack(q.data[-70:, :16 * blocks].cpu().numpy()), codes)
