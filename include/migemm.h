@@ -374,7 +374,8 @@ int migemm_dequantize_mx(int dst_dtype, int64_t rows, int64_t cols, const void* 
  * a weight stored output-major, or a K x N one quantised with MIGEMM_OP_T).
  * K counts whole blocks and must be a multiple of 32 (a matrix with other cols
  * is multiplied with K rounded up: its padding elements are 0).  Products and
- * scales are exact, sums are FP32, and the output step is migemm_gemm_ex's:
+ * scales are exact, sums are FP32 (subnormal ones kept), and the output step is
+ * migemm_gemm_ex's:
  * c_dtype MIGEMM_F32, MIGEMM_F16 or MIGEMM_BF16, beta == 0 leaves C unread,
  * M == 0 or N == 0 is a no-op and K == 0 gives C = beta * C.  A NaN scale makes
  * every sum it takes part in NaN.  C must not overlap the operands.  Same

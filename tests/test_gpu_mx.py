@@ -392,3 +392,21 @@ def test_quantize_large_sources_with_k_as_the_row_index(dtype, rows, cols, ld):
     codes, byte = mx.quantize(x[-70:].double().cpu().numpy())
     assert np.array_equal(q.scales[-70:, :blocks].cpu().numpy(), byte)
     assert np.array_equal(mx.unpack(q.data[-70:, :16 * blocks].cpu().numpy()), codes)
+
+
+@pytest.mark.parametrize("M,N,K", [(7, 96, 640), (64, 70, 512), (200, 256, 640)])
+def test_product_below_the_normal_range_of_fp32(M, N, K):
+    """Scales of 2^-64 to 2^-62: terms are multiples of 0.25 2^-128 = 2^-130, sums of 640
+    of them below 2^-109, so every partial sum below 2^-106 is a multiple of 2^-130 that
+    FP32 holds exactly, subnormal or not.  With scales of A down to 2^-127 every term lies
+    below 36 2^-187: the sums round to 0, or to the smallest FP32 number."""
+    rng = np.random.default_rng(M + 5)
+    a, b = _operand(M, K, rng, 63, 66), _operand(N, K, rng, 63, 66)
+    say(f"gemm_mx {M}x{N}x{K} below the normal range")
+    want = mx.decode(*a, K) @ mx.decode(*b, K).T
+    got = mg.gemm_mx(_device(a, K), _device(b, K)).double().cpu().numpy()
+    assert np.abs(want).max() < 2.0 ** -106 and (np.abs(want) < 2.0 ** -126).any()
+    assert np.array_equal(got, want)
+    a, b = _operand(M, K, rng, 0, 3), _operand(N, K, rng, 60, 66)
+    got = mg.gemm_mx(_device(a, K), _device(b, K)).double().cpu().numpy()
+    assert (np.abs(got) <= 2.0 ** -149).all()
