@@ -539,3 +539,23 @@ def test_fp32_logits_past_what_small_tiles_can_launch():
     index = torch.where(target == IGNORE, -1, target)[rows, None]
     want, tol = reference(x[rows], w, index, None, 1.0, torch.ones(200, device="cuda"), True)
     check((loss[rows], None, None), want, tol)
+
+
+# Pieces of 32768, 7168 and 65 columns: the vocabulary past whole tiles is a step of its
+# own in a product of several pieces, whose k ends inside a chunk; dx is the library's
+# product added up over the steps, the first of them on slices of k (configuration 17)
+@pytest.mark.parametrize("T,V,D,dtype", [(8192, 40001, 512, "bf16"), (8192, 40001, 512, "f16"),
+                                         (8100, 73729, 264, "bf16"), (8000, 33003, 328, "f16")])
+def test_whole_tiles_and_pieces_together(T, V, D, dtype):
+    x, w, target, grad = ce_case(T, V, D, dtype, T + V + D)
+    target[:40] = torch.arange(V - 40, V, device="cuda")   # targets in every step
+    target[40:60] = torch.arange(32760, 32780, device="cuda")
+    index = torch.where(target == IGNORE, -1, target)[:, None]
+    say(f"ce {T}x{V}x{D} {dtype}")
+    got = run_ce(x, w, target, grad)
+    want, tol = reference(x, w, index, None, 1.0, grad, True)
+    check(got, want, tol)
+    again = run_ce(x, w, target, grad)
+    assert all(torch.equal(p, q) for p, q in zip(got, again))
+    say(f"kd {T}x{V}x{D} {dtype}")
+    check(run_kd(x, w, torch.zeros(T, 1, device="cuda"), index.contiguous(), 1.0, grad), want, tol)
