@@ -2,6 +2,8 @@
 // (linear_loss.hpp): joining the forward statistics, the logits that a loss
 // names, the losses; and the backward pass's row data, its scattered entries and
 // its conversions.
+#include <utility>
+
 #include "linear_loss.hpp"
 
 namespace migemm {
@@ -35,28 +37,120 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 
-// The dot products of a row x with U rows w[u], of `depth` elements each (whole
-// 16-byte chunks), over a wavefront, in FP32.
-template <int U, typename E>
-__device__ __forceinline__ void row_dots(const E* __restrict__ x, const E* const (&w)[U],
-                                         int64_t depth, int lane, float (&sum)[U]) {
-    constexpr int EPC = 16 / sizeof(E);
+// Each lane i of a 16-lane row gets lane (i + N) % 16's value, in the groups of four lanes
+// that BANKS names; the others keep `old`.
+template <int N, int BANKS = 0xf>
+__device__ __forceinline__ u32x4 rotated(u32x4 v, u32x4 old = u32x4{0u, 0u, 0u, 0u}) {
+    if constexpr (N % 16 == 0) return v;
+    u32x4 r;
 #pragma unroll
-    for (int u = 0; u < U; ++u) sum[u] = 0.0f;
-#pragma unroll(U == 1 ? 4 : 2)
-    for (int64_t c = static_cast<int64_t>(lane) * EPC; c < depth; c += kWave * EPC) {
-        E xe[EPC], we[U][EPC];
-        __builtin_memcpy(xe, __builtin_assume_aligned(x + c, 16), 16);
+    for (int e = 0; e < 4; ++e)
+        r[e] = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+            static_cast<int>(old[e]), static_cast<int>(v[e]), 0x120 + (16 - N % 16) % 16, 0xf,
+            BANKS, false));
+    return r;
+}
+
+template <int... N, class F>
+__device__ __forceinline__ void for_each_slab(std::integer_sequence<int, N...>, F f) {
+    (f(std::integral_constant<int, N>{}), ...);
+}
+
+// Logits of row x and PER rows w (w[h]: that of this lane's entry, lane % PER, or 8 h +
+// lane % 8 of 16), in lanes 0 to PER - 1, in the bits that the product's accumulators
+// hold: the same matrix instructions over the same slabs of k (a slab is one 16-byte chunk
+// per lane group, DirectOperand's row images) in the same order, zeros before and past the
+// ends.  lse is a sum over those accumulators, so their roundings cancel in lse - z; an
+// FP32 dot product of another order is off by 1e-4 at logits of 200, which the loss and
+// the derivative of a nearly certain row then consisted of.  head: elements before k = 0
+// in the first slab (a partial first k-tile of the 256x256 product).  `depth` elements,
+// whole chunks.
+//
+// The instruction's block is row x sixteen times by 16 entries.  With fewer than 16 the
+// other lanes of a group load the slabs that follow, and the registers rotate by PER lanes
+// from one slab to the next; 16 entries come as two loads of eight rows by two slabs (whole
+// 128-byte lines), exchanged by halves.  The next U loads are in flight while U run.
+// XS: x lies in LDS (x_slabs), read a slab at a time, which leaves registers for more of
+// w's loads (2048 rows of 32 entries, D 2048 FP16: 56 us against 62).
+template <int PER, bool XS, typename E>
+__device__ __forceinline__ float named_logits(const E* __restrict__ x, const u32x4* xs,
+                                              const E* const (&w)[PER == 16 ? 2 : 1],
+                                              int64_t depth, int head, int lane) {
+    constexpr int EPC = 16 / sizeof(E), kSlab = 4 * EPC;
+    constexpr int H = PER == 16 ? 2 : 1, S = PER == 16 ? 2 : 16 / PER;  // rows, slabs of a load
+    constexpr int U = (XS ? 8 : 4) / H, kLoad = S * kSlab, kStep = U * kLoad;
+    const int64_t k0 = (lane / 16) * EPC + (lane % 16 / (16 / S)) * kSlab - head;
+    const int64_t end = depth + head;
+    struct Batch {
+        u32x4 a[XS ? 1 : U], b[H][U];
+    };
+    auto load = [&](int64_t s, Batch& t) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            __builtin_memcpy(we[u], __builtin_assume_aligned(w[u] + c, 16), 16);
+        for (int u = 0; u < U; ++u) {
+            const int64_t k = k0 + s + u * kLoad;
+            const bool in = k >= 0 && k < depth;
+            if constexpr (!XS) {
+                t.a[u] = u32x4{0u, 0u, 0u, 0u};
+                if (in) t.a[u] = *reinterpret_cast<const u32x4*>(x + k);
+            }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int h = 0; h < H; ++h) {
+                t.b[h][u] = u32x4{0u, 0u, 0u, 0u};
+                if (in) t.b[h][u] = *reinterpret_cast<const u32x4*>(w[h] + k);
+            }
+        }
+    };
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    // slab n of load u, which starts at slab `slab`
+    auto one = [&](int64_t slab, int u, const Batch& t, auto n_tag) __attribute__((always_inline)) {
+        constexpr int N = decltype(n_tag)::value;
+        u32x4 a, b;
+        if constexpr (XS)
+            a = xs[(slab + N) * 4 + lane / 16];
+        else
+            a = rotated<N * (16 / S)>(t.a[u]);
+        if constexpr (PER != 16)
+            b = rotated<N * PER>(t.b[0][u]);
+        else if constexpr (N == 0)
+            b = rotated<8, 0xc>(t.b[1][u], t.b[0][u]);
+        else
+            b = rotated<8, 0x3>(t.b[0][u], t.b[1][u]);
+        MfmaOp<E, 16>::run(acc, a, b);
+    };
+    auto run = [&](int64_t s, const Batch& t) __attribute__((always_inline)) {
 #pragma unroll
-            for (int e = 0; e < EPC; ++e) sum[u] = fmaf(to_f32(xe[e]), to_f32(we[u][e]), sum[u]);
+        for (int u = 0; u < U; ++u) {
+            if (s + u * kLoad >= end) break;
+            for_each_slab(std::make_integer_sequence<int, S>{},
+                          [&](auto n) __attribute__((always_inline)) {
+                              one(s / kSlab + u * S, u, t, n);
+                          });
+        }
+    };
+    Batch t0, t1;
+    load(0, t0);
+    for (int64_t s = 0; s < end; s += 2 * kStep) {
+        load(s + kStep, t1);
+        run(s, t0);
+        load(s + 2 * kStep, t0);
+        run(s + kStep, t1);
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) sum[u] = wave_sum(sum[u]);
+    return acc[0];
+}
+
+// Row x as named_logits reads it from LDS: `head` zeros, x, zeros to the end of the last
+// load.  Up to kSlabBytes of x.
+constexpr int kSlabBytes = 16384, kSlabRoom = kSlabBytes + 2048;
+template <typename E>
+__device__ __forceinline__ void x_slabs(const E* __restrict__ x, int64_t depth, int head,
+                                        u32x4* xs) {
+    constexpr int EPC = 16 / sizeof(E), kMost = 16 * 4;  // chunks of sixteen slabs
+    const int last = static_cast<int>(depth + head) / EPC, first = head / EPC;
+    for (int c = threadIdx.x; c < (last + kMost - 1) / kMost * kMost; c += kThreads) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (c >= first && c < last) v = *reinterpret_cast<const u32x4*>(x + (c - first) * EPC);
+        xs[c] = v;
+    }
 }
 
 // Teacher logit j of a row, in the teacher's type.
@@ -100,73 +194,77 @@ __device__ __forceinline__ Teacher teacher_row(const LossArgs& a, int64_t row, i
 
 // One workgroup per row: its log-sum-exp from the chunks' statistics, the logits
 // at its target or at the teacher's indices, and its loss.  Bound by reading the rows
-// of W that are named, from memory and caches: 4096 rows of 64 entries, D 4096 BF16, 269
-// us (8 TB/s; 328 with one entry at a time).
-// KD: distillation (cross entropy keeps fewer registers).
-template <typename E, bool KD>
+// of W that are named, from memory and caches: 4096 rows of 64 entries, D 4096 BF16, 280
+// us (7.7 TB/s); few rows by the chain of matrix instructions (33 rows of 8 entries, D 520
+// FP32, 130 of them: 11 us).
+// KD: distillation (cross entropy keeps fewer registers).  PER: entries of a wavefront at
+// a time, a power of two up to 16: the fewest that the four need once, or 16.
+template <typename E, bool KD, int PER, bool XS>
 __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E* __restrict__ X,
                                                              int64_t ldx, const E* __restrict__ W,
-                                                             int64_t ldw, int64_t depth,
+                                                             int64_t ldw, int64_t depth, int head,
+                                                             float scale,
                                                              const RowStat* __restrict__ part,
                                                              int64_t chunks,
                                                              float* __restrict__ loss,
                                                              double* __restrict__ lse_out) {
     __shared__ RowStat stat[kRowWaves];
     __shared__ float logit[KD ? kMaxTop : 1];
+    __shared__ u32x4 xs[XS ? kSlabRoom / 16 : 1];
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     float m = -INFINITY, s = 0.0f;
     // eight chunks at a time, their loads in flight together (a row of 8192 chunks
-    // joined one by one took 25 us)
-    constexpr int kAhead = 8;
+    // joined one by one took 25 us); the target's logit is wave 0's meanwhile
+    constexpr int kAhead = 8, kFirst = KD ? 0 : kWave, kOver = kThreads - kFirst;
     const RowStat* const stats = part + row * chunks;
-    for (int64_t c = threadIdx.x; c < chunks; c += kAhead * kThreads) {
-        RowStat r[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int64_t at = c + i * kThreads;
-            r[i] = stats[at < chunks ? at : c];
-            if (at >= chunks) r[i].sum = 0.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) join(m, s, r[i].largest, r[i].sum);
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const float m2 = __shfl_xor(m, d), s2 = __shfl_xor(s, d);
-        join(m, s, m2, s2);
-    }
-    if (lane == 0) stat[wave] = RowStat{m, s};
     const E* const x = X + row * ldx;
-    if constexpr (!KD) {
+    if constexpr (XS) x_slabs(x, depth, head, xs);
+    if (!KD && wave == 0) {
         const int64_t y = a.target[row];
-        if (wave == 0 && y >= 0 && y < a.V && y != a.ignore) {
+        if (y >= 0 && y < a.V && y != a.ignore) {
             const E* const w[1] = {W + y * ldw};
-            float z[1];
-            row_dots(x, w, depth, lane, z);
-            if (lane == 0) logit[0] = z[0];
+            const float z = named_logits<1, false>(x, xs, w, depth, head, lane);
+            if (lane == 0) logit[0] = z;
         }
     } else {
-        // four entries of a wavefront at a time, their loads in flight together; one
-        // that is not held reads row 0 and counts as 0
-        constexpr int kEntries = 4;
-        for (int64_t j0 = wave; j0 < a.top; j0 += kEntries * kRowWaves) {
-            const E* w[kEntries];
-            bool held[kEntries];
-            float z[kEntries];
+        for (int64_t c = static_cast<int>(threadIdx.x) - kFirst; c < chunks; c += kAhead * kOver) {
+            RowStat r[kAhead];
 #pragma unroll
-            for (int u = 0; u < kEntries; ++u) {
-                const int64_t j = j0 + u * kRowWaves;
-                const int64_t v = a.t_index[row * a.ldi + (j < a.top ? j : j0)];
-                held[u] = v >= 0 && v < a.V;
-                w[u] = W + (held[u] ? v : 0) * ldw;
+            for (int i = 0; i < kAhead; ++i) {
+                const int64_t at = c + i * kOver;
+                r[i] = stats[at < chunks ? at : c];
+                if (at >= chunks) r[i].sum = 0.0f;
             }
-            row_dots(x, w, depth, lane, z);
 #pragma unroll
-            for (int u = 0; u < kEntries; ++u) {
-                const int64_t j = j0 + u * kRowWaves;
-                if (lane != 0 || j >= a.top) continue;
-                logit[j] = held[u] ? z[u] : 0.0f;
+            for (int i = 0; i < kAhead; ++i) join(m, s, r[i].largest, r[i].sum);
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d >>= 1) {
+            const float m2 = __shfl_xor(m, d), s2 = __shfl_xor(s, d);
+            join(m, s, m2, s2);
+        }
+    }
+    if (lane == 0) stat[wave] = RowStat{m, s};
+    if constexpr (KD) {
+        if constexpr (XS) __syncthreads();
+        // one that is not held reads row 0 and counts as 0
+        for (int64_t j0 = wave * PER; j0 < a.top; j0 += PER * kRowWaves) {
+            constexpr int H = PER == 16 ? 2 : 1, kRows = PER / H;
+            const E* w[H];
+            bool held = false;
+            const int64_t j = j0 + lane % PER;  // the entry whose logit this lane gets
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int64_t i = j0 + h * kRows + lane % kRows;
+                const int64_t v = a.t_index[row * a.ldi + (i < a.top ? i : j0)];
+                const bool in = v >= 0 && v < a.V;
+                if (i == j) held = in;
+                w[h] = W + (in ? v : 0) * ldw;
+            }
+            const float z = named_logits<PER, XS>(x, xs, w, depth, head, lane);
+            if (lane < PER && j < a.top) {
+                logit[j] = held ? z : 0.0f;
                 a.student[row * a.lds + j] = logit[j];
             }
         }
@@ -177,11 +275,15 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
     s = stat[0].sum;
 #pragma unroll
     for (int w = 1; w < kRowWaves; ++w) join(m, s, stat[w].largest, stat[w].sum);
-    const double lse = (static_cast<double>(m) + log2(static_cast<double>(s))) * kLn2;
+    // in base 2, as the statistics are: s z of a named logit is subtracted from it exactly
+    const double lse2 = static_cast<double>(m) + log2(static_cast<double>(s));
     float out = 0.0f;
     if constexpr (!KD) {
         const int64_t y = a.target[row];
-        if (y != a.ignore) out = y >= 0 && y < a.V ? static_cast<float>(lse - logit[0]) : NAN;
+        if (y != a.ignore)
+            out = y >= 0 && y < a.V
+                      ? static_cast<float>((lse2 - static_cast<double>(scale) * logit[0]) * kLn2)
+                      : NAN;
     } else {
         const Teacher t = teacher_row(a, row, lane);
         if (t.held) {
@@ -194,15 +296,17 @@ __global__ __launch_bounds__(kThreads) void loss_rows_kernel(LossArgs a, const E
                 const float p = exp2_of(static_cast<float>(log_p * kLog2e));
                 // no weight, no term: log p may be -infinity there
                 if (p != 0.0f)
-                    terms = fmaf(p, static_cast<float>(log_p - logit[j] * inv + lse), terms);
+                    terms = fmaf(p, static_cast<float>(log_p + (lse2 - static_cast<double>(scale) *
+                                                                          logit[j]) * kLn2),
+                                 terms);
             }
             out = a.tau * a.tau * wave_sum(terms);
         }
         if (t.bad) out = NAN;
     }
     if (lane == 0) {
-        loss[row] = out;
-        lse_out[row] = lse;
+        loss[row] = out < 0.0f ? 0.0f : out;  // (neither loss is negative but for rounding)
+        lse_out[row] = lse2 * kLn2;
     }
 }
 
@@ -266,10 +370,7 @@ __global__ __launch_bounds__(kThreads) void loss_prepare_kernel(
         if (row < a.T) {
             const double l = lse[row] * 1.4426950408889634;
             r.lse2 = static_cast<float>(l);
-            if constexpr (sizeof(E) == 4)
-                r.extra = fabsf(r.lse2) < INFINITY ? static_cast<float>(l - r.lse2) : 0.0f;
-            else
-                r.extra = second ? 1.0f : 0.0f;
+            r.extra = fabsf(r.lse2) < INFINITY ? static_cast<float>(l - r.lse2) : 0.0f;
             if (a.top == 0) {
                 const int64_t y = a.target[row];
                 r.coef = ce_coef(a, row, grad);
@@ -350,8 +451,7 @@ __global__ __launch_bounds__(kThreads) void loss_scatter_kernel(
         float weight = 0.0f;
         for (int64_t i = 0; i < a.top; ++i)
             if (index[i] == v) weight += tp[row * a.top + i];
-        const float l = fmaf(a.student[row * a.lds + j], scale, -r.lse2);
-        const float q = exp2_of(sizeof(E) == 4 ? l - r.extra : l);
+        const float q = exp2_of(fmaf(a.student[row * a.lds + j], scale, -r.lse2) - r.extra);
         const float d = (r.coef * q - weight) * f;
         const E first = narrow<E>(d);
         dz[row * ldz + (v - v0)] = first;
@@ -445,14 +545,23 @@ hipError_t by_type(int dtype, F f) {
 }  // namespace
 
 hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const void* W,
-                            int64_t ldw, int64_t depth, const RowStat* part, int64_t chunks,
-                            float* loss, double* lse) {
+                            int64_t ldw, int64_t depth, int head, const RowStat* part,
+                            int64_t chunks, float* loss, double* lse) {
     return by_type(a.dtype, [&](auto tag) {
         using E = decltype(tag);
-        auto* const fn = a.top ? loss_rows_kernel<E, true> : loss_rows_kernel<E, false>;
+        const bool xs = depth * static_cast<int64_t>(sizeof(E)) <= kSlabBytes;
+#define MIGEMM_ROWS(PER) \
+    (xs ? loss_rows_kernel<E, true, PER, true> : loss_rows_kernel<E, true, PER, false>)
+        auto* const fn = a.top == 0                ? loss_rows_kernel<E, false, 1, false>
+                         : a.top <= kRowWaves     ? MIGEMM_ROWS(1)
+                         : a.top <= 2 * kRowWaves ? MIGEMM_ROWS(2)
+                         : a.top <= 4 * kRowWaves ? MIGEMM_ROWS(4)
+                         : a.top <= 8 * kRowWaves ? MIGEMM_ROWS(8)
+                                                  : MIGEMM_ROWS(16);
+#undef MIGEMM_ROWS
         fn<<<dim3(static_cast<unsigned>(a.T)), dim3(kThreads), 0, a.stream>>>(
-            a, static_cast<const E*>(X), ldx, static_cast<const E*>(W), ldw, depth, part, chunks,
-            loss, lse);
+            a, static_cast<const E*>(X), ldx, static_cast<const E*>(W), ldw, depth, head,
+            kLog2e / a.tau, part, chunks, loss, lse);
         return hipGetLastError();
     });
 }

@@ -4,8 +4,8 @@
 // z = X W^T (X: T tokens x D, W: V vocabulary rows x D) is never stored.  The
 // forward pass runs the product with an output step that keeps, per row and
 // wave-wide chunk of columns, the largest value m and the sum of exp(z - m)
-// (LseOut); a row kernel joins the chunks into the row's log-sum-exp and
-// computes the few logits the loss names as dot products.  The backward pass
+// (LseOut); a row kernel joins the chunks into the row's log-sum-exp and forms the few
+// logits the loss names as the product forms them, bit for bit.  The backward pass
 // walks the vocabulary in pieces: it recomputes a piece of z with an output step
 // that writes the derivative of the loss to it,
 //     dz[t][v] = c_t (exp(z[t][v] / tau - lse_t) - p[t][v]),  c_t = tau g_t
@@ -40,8 +40,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.6931471805599453;
 
 // What the derivative of a row needs: l, c_t (0: a row without a loss, whose
-// derivative is 0 whatever its logits), the target's column (-1: none), and in FP32
-// what l lacks of its 64-bit value, in 16 bits whether the row is a twin.
+// derivative is 0 whatever its logits), the target's column (-1: none), and what l lacks
+// of its 64-bit value (l of 16 to 32 in FP32 is off by up to 2^-20, which is all there is
+// to 1 - q of a nearly certain row).
 struct LossRow {
     float lse2, coef;
     int32_t target;
@@ -152,6 +153,7 @@ struct DzOut : Epi {
     const LossRow* info;  // padded to whole tiles of rows
     const float* factor;  // f, or NULL
     float scale;          // s
+    int64_t twin;         // rows from here on hold what their twins' rounding left
     template <class Cfg, class Acc>
     __device__ __forceinline__ void store(const Acc (&acc)[Cfg::TM][Cfg::TN],
                                           MIGEMM_LDS char* smem, int64_t m, int64_t n, int wave,
@@ -182,10 +184,10 @@ struct DzOut : Epi {
                 for (int j = 0; j < TN; ++j) {
                     const int64_t col = n + 16 * j + lj;
                     const float l = fmaf(acc[i][j][e], scale, -row.lse2);
-                    float v = row.coef * exp2_of(ES == 4 ? l - row.extra : l);
+                    float v = row.coef * exp2_of(l - row.extra);
                     if (v0 + col == row.target) v -= row.coef;
                     if (row.coef == 0.0f || col >= N) v = 0.0f;
-                    if (ES != 4 && Cfg::BM == 64 && row.extra != 0.0f)  // (twins: 64-row tiles)
+                    if (ES != 4 && Cfg::BM == 64 && m + 16 * i + r >= twin)  // (64-row tiles)
                         v -= to_f32(narrow<E>(v));
                     const int c = 16 * j + lj;
                     const int piece = (c / VE) ^ ((g << 1) & (PIECES - 1));
@@ -331,10 +333,11 @@ struct LossArgs {
 };
 
 // Row kernels (linear_loss.hip).  X and W: 16-byte aligned rows, `depth` elements
-// (whole chunks) of them read.
+// (whole chunks) of them read.  head: how many elements before k = 0 the logits' product
+// starts its first slab of k.
 hipError_t launch_loss_rows(const LossArgs& a, const void* X, int64_t ldx, const void* W,
-                            int64_t ldw, int64_t depth, const RowStat* part, int64_t chunks,
-                            float* loss, double* lse);
+                            int64_t ldw, int64_t depth, int head, const RowStat* part,
+                            int64_t chunks, float* loss, double* lse);
 // info for `rows_info` rows, X's rows as a zero-padded copy (rows x ldc; rows
 // without a loss become 0), for distillation tp[t][j] = c_t p_j, and for cross
 // entropy the factor (NULL: none).  twin: kTwin, or 0.

@@ -184,9 +184,20 @@ struct Tiling {
     int64_t rows;
     LossShape shape;
 };
+// All passes have to form the same bits of a logit.  Every tile adds k in the same order,
+// except that 256x256 ones take a partial k-tile first (head_of): where k ends inside a
+// k-tile, all steps follow the whole vocabulary's choice.
 Tiling tiling(const LossArgs& a, const Plan& p, int64_t n) {
+    if (a.dtype != MIGEMM_F32 && p.depth % 64 != 0) n = a.V;
     const LossShape s = loss_shape(a.dtype, p.rows, n, p.depth);
     return s.bn == 256 || p.twin ? Tiling{p.rows, s} : Tiling{a.T, loss_shape(a.dtype, a.T, n, p.depth)};
+}
+
+// Elements before k = 0 in the first 32-deep slab of the logits' product.
+int head_of(const LossArgs& a, int64_t depth) {
+    const bool head = a.dtype != MIGEMM_F32 && depth % 64 != 0 &&
+                      loss_shape(a.dtype, a.T, a.V, depth).config == 2;
+    return head ? static_cast<int>((32 - depth % 32) % 32) : 0;
 }
 
 Plan make_plan(const LossArgs& a, bool backward) {
@@ -196,9 +207,10 @@ Plan make_plan(const LossArgs& a, bool backward) {
     p.ld_copy = round_up(a.D, 64);
     p.copy_w = !whole || !rows_ok(a.W, a.ldw, epc);
     // the backward pass always copies x: its rows without a loss become 0, so
-    // that whatever they hold (NaN from a masked position) stays out of dw
-    p.copy_x = backward || !whole || !rows_ok(a.X, a.ldx, epc);
-    p.depth = p.copy_w && p.copy_x ? p.ld_copy : a.D;
+    // that whatever they hold (NaN from a masked position) stays out of dw; where w is
+    // copied x is in either pass, so that both see one depth
+    p.copy_x = backward || p.copy_w || !rows_ok(a.X, a.ldx, epc);
+    p.depth = p.copy_w ? p.ld_copy : a.D;
     p.rows = a.T;
     if (whole_tiles(a, p.depth)) {
         p.rows = round_up(a.T, 256);
@@ -306,7 +318,8 @@ int forward(const LossArgs& a, float* loss, double* lse, void* ws) {
         if (st != MIGEMM_OK) return st;
         out.part += chunks_of(tl.shape, n);
     }
-    return hip_status(launch_loss_rows(a, x, ldx, w, ldw, p.depth, part, p.chunks, loss, lse));
+    return hip_status(launch_loss_rows(a, x, ldx, w, ldw, p.depth, head_of(a, p.depth), part,
+                                       p.chunks, loss, lse));
 }
 
 template <typename E>
@@ -320,6 +333,7 @@ hipError_t launch_dz(const LossArgs& a, const Plan& p, const void* x, const void
     out.info = reinterpret_cast<const LossRow*>(at(ws, p.info));
     out.factor = factor;
     out.scale = kLog2e / a.tau;
+    out.twin = p.twin ? p.twin : kMaxDim;
     const Tiling tl = tiling(a, p, n);
     const LossTile t{tl.rows, n, p.depth, a.dtype, x, p.ld_copy, w, ldw, a.stream, nullptr, &out,
                      nullptr};

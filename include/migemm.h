@@ -400,8 +400,10 @@ const char* migemm_mx_config_name(int config);
  * X (T x D) holds T tokens, W (V x D) the layer's weight, one row per entry of the
  * vocabulary; both row-major of `dtype` (MIGEMM_F32, MIGEMM_F16, MIGEMM_BF16).
  * The logits z = X W^T are formed tile by tile and never stored; sums, softmax
- * statistics and losses are FP32, lse is FP64.  The backward passes recompute the logits in
- * pieces of the vocabulary and write the gradients of X (dX, T x D) and W (dW,
+ * statistics and losses are FP32, lse is FP64.  The logits that a loss names are formed in
+ * the order of the sums behind lse, so that their roundings cancel: a nearly certain row's
+ * loss is off by a few 2^-24, and no loss is negative.  The backward passes recompute the
+ * logits in pieces of the vocabulary and write the gradients of X (dX, T x D) and W (dW,
  * V x D) in `dtype`; either may be NULL.  grad (T floats) is the upstream gradient
  * of each row's loss: 1 / n for the mean over n rows, 1 for the sum.  The
  * derivative of the loss to each logit is rounded to `dtype` once, for the

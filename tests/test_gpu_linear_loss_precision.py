@@ -118,3 +118,118 @@ def test_log_sum_exps_are_kept_in_64_bits():
         assert ((got - want).abs() <= tol).all()
         # most are no FP32 numbers: nothing rounds them to 32 bits on the way
         assert int((got.float().double() != got).sum()) > 250
+
+
+# ------------------------------------------------------- rows that are nearly certain
+
+def certain(T, V, D, dtype, size, seed):
+    """x along each row's target (a logit of about `size`, the others of a few), the
+    targets, and the logits in 64 bits."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = (torch.randn(V, D, generator=g, device="cuda") * (2 / math.sqrt(D))).to(dtype)
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    at = w[target].float()
+    x = at * (size / (at * at).sum(1, keepdim=True))
+    x += 0.5 * torch.randn(T, D, generator=g, device="cuda")
+    x = x.to(dtype)
+    return x, w, target, x.double() @ w.double().t(), g
+
+
+def spread_of(z, p, ez):
+    """What logits off by up to ez, the same ones in all of a loss, change in lse - sum p z
+    and in its derivative q - p.  With q the softmax, the first order is sum (q - p) dz,
+    the second half the variance of dz under q, at most 2 ez^2 (1 - max q); q itself is off
+    by q times the difference of its own dz and their mean under q."""
+    q = torch.softmax(z, 1)
+    rest = 1 - q.amax(1)
+    most = ez.amax(1)
+    loss = ((q - p).abs() * ez).sum(1) * (1 + 4 * most) + 4 * rest * most ** 2
+    own = torch.where(q == q.amax(1, keepdim=True), rest[:, None] * 2 * most[:, None],
+                      q * 2 * most[:, None])
+    return loss, own * (1 + 4 * most[:, None])
+
+
+SIZES = [(64, 1000, 256, "f32", 200.0), (20, 3000, 512, "f32", 40.0), (300, 5000, 1024, "f32", 20.0),
+         (16, 1000, 256, "bf16", 200.0), (64, 1000, 520, "f16", 60.0),
+         (100, 20000, 1000, "bf16", 40.0), (300, 17000, 1032, "f16", 40.0),
+         (300, 17001, 200, "bf16", 200.0), (512, 16384, 128, "bf16", 20.0),
+         (1000, 33003, 2112, "bf16", 40.0), (70, 500, 65, "bf16", 100.0),
+         (8192, 40001, 72, "bf16", 100.0), (200, 9000, 256, "f16", 20.0)]
+
+
+@pytest.mark.parametrize("T,V,D,dtype,size", SIZES)
+@pytest.mark.parametrize("misaligned", [False, True])
+def test_nearly_certain_rows_keep_their_small_losses(T, V, D, dtype, size, misaligned):
+    """A loss far below its logits: lse and the named logit have to come from the same
+    sums, whose errors (of up to D 2^-23 sum |x w|, 1e-4 and more here) then cancel.  What
+    is left of them is spread_of's, and the evaluation in FP32: exponentials and some 30
+    roundings of sums near 1, below 2^-19 in all.  As a distillation of one entry too."""
+    if misaligned and (T * V > 1 << 24 or D % 8):
+        pytest.skip("one size of each kind suffices")
+    dt = torch.float32 if dtype == "f32" else TORCH[dtype]
+    x, w, target, z, g = certain(T, V, D, dt, size, T + V)
+    if misaligned:   # w is copied into whole k-tiles first
+        room = torch.empty(V * D + 1, dtype=dt, device="cuda")[1:].view(V, D)
+        w = room.copy_(w)
+    say(f"certain {T}x{V}x{D} {dtype} {size} misaligned={misaligned}")
+    at = target[:, None]
+    # log(1 + sum of the others): exact however small
+    others = (z - z.gather(1, at)).scatter_(1, at, -math.inf)
+    want = torch.log1p(torch.exp(others).sum(1))
+    p = torch.zeros_like(z).scatter_(1, at, 1.0)
+    ez = D * 2.0 ** -23 * (x.double().abs() @ w.double().abs().t())
+    tol, e = spread_of(z, p, ez)
+    del others
+    grad = torch.rand(T, generator=g, device="cuda") + 0.25
+    loss, lse = mg.linear_cross_entropy(x, w, target)
+    kloss, klse, student = mg.linear_distillation(x, w, torch.zeros(T, 1, device="cuda"), at)
+    for name, got in (("ce", loss), ("kd", kloss)):
+        assert (got >= 0).all(), (name, float(got.min()))
+        err = (got.double() - want).abs()
+        worst = (err - tol - 2.0 ** -19 - 2.0 ** -23 * want).max()
+        assert worst <= 0, (name, float(worst), float(err.max()))
+    # the derivative: c (q - 1) at the target, c q elsewhere; a q below FP32's normal range
+    # is 0 or off by as much, 2^-126 at most (e^-200 = 2^-289 lies far below it), and so may
+    # a gradient of the narrower types be
+    c = grad.double()[:, None]
+    q = torch.softmax(z, 1)
+    dz = q.scatter(1, at, -(-torch.expm1(-want))[:, None]) * c
+    u = torch.finfo(dt).eps / 2
+    e = c * (e + 2.0 ** -19 * torch.maximum(q, p) + 2.0 ** -126)
+    if dtype != "f32":
+        e = e + u * dz.abs() + (float(c.max()) * 2.0 ** -37 if dtype == "f16" else 0.0)
+    X, W = x.double(), w.double()
+    dx, dw = dz @ W, dz.t() @ X
+    tol_x = (e + V * 2.0 ** -23 * (dz.abs() + e)) @ W.abs()
+    tol_w = (e + T * 2.0 ** -23 * (dz.abs() + e)).t() @ X.abs()
+    sub = 2.0 ** -25 if dtype == "f16" else 2.0 ** -126
+    for name, got in (("ce", mg.linear_cross_entropy_backward(x, w, target, lse, grad)),
+                      ("kd", mg.linear_distillation_backward(x, w, torch.zeros(T, 1, device="cuda"),
+                                                             at, klse, student, grad))):
+        for which, g_, want_, tol_ in (("dx", got[0], dx, tol_x), ("dw", got[1], dw, tol_w)):
+            bound = tol_ + u * (want_.abs() + tol_) + sub
+            worst = ((g_.double() - want_).abs() / bound).max()
+            assert worst <= 1, (name, which, float(worst))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_student_that_matches_its_teacher_has_almost_no_loss(dtype):
+    """Logits of about 100 at twenty entries of weights 2^-1, 2^-2, ... and the student's
+    own logits as the teacher's: q is p but for the rest of the vocabulary, and the loss
+    nearly 0, whatever the errors that the logits share."""
+    T, V, D, top, tau = 40, 2000, 512, 20, 2.0
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    x, w, target, z, g = certain(T, V, D, dt, 120.0, 5)
+    teacher, index = z.topk(top, 1)
+    teacher = teacher.float().contiguous()
+    say(f"matched student {dtype}")
+    loss, lse, student = mg.linear_distillation(x, w, teacher, index.contiguous(), temperature=tau)
+    p = torch.softmax(teacher.double() / tau, 1)
+    log_q = torch.log_softmax(z / tau, 1).gather(1, index)
+    want = tau * tau * (p * (torch.log_softmax(teacher.double() / tau, 1) - log_q)).sum(1)
+    P = torch.zeros_like(z).scatter_(1, index, p)
+    ez = D * 2.0 ** -23 * (x.double().abs() @ w.double().abs().t()) / tau
+    tol, _ = spread_of(z / tau, P, ez)
+    # teacher and student logs: FP32 exponents and sums, each below 2^-19 as above
+    assert (loss >= 0).all()
+    assert ((loss.double() - want).abs() <= tau * tau * (tol + 2 * 2.0 ** -19)).all()
