@@ -29,9 +29,13 @@ headline it carries:
                 against it;
   by_workload   the other workloads (256^3 to 8192^3; FP32, FP16, BF16, INT8;
                 operand layouts, the general output step, device conversion)
-                and the naive one-work-item-per-output kernel at 1024^3, each
-                with its kernel's resources and, for the plain products, the
-                oracle timed on a bounded sample with the GPU rows checked.
+                and the naive one-work-item-per-output kernel at 1024^3, for
+                the plain products with the oracle timed on a bounded sample
+                and the GPU rows checked.  Their kernels' resources and timing
+                windows, two thirds of the text, go to stderr as a JSON line of
+                their own, so that the printed one stays below 12,000
+                characters and is not cut where only the end of an output is
+                kept.
 
 `--gpus N` with N > 1 exits with an error: the library runs on one GPU.
 """
@@ -56,6 +60,8 @@ HBM_PEAK_GBS = 8000.0
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 RESOURCES_FILE = os.path.join(ROOT, "dense_gemm_16_amd", "kernel_resources.json")
 SETTLE_MS = 200.0
+# What a by_workload entry leaves to the details on stderr.
+DETAILS = ("resources", "launches", "windows_ms")
 # Small, launch-bound workloads also timed as replays of a captured HIP graph.
 GRAPH_TIMED = ("c0-f16-256", "c1-f32-1024", "c2-f16-1024")
 EXTRA = ["c0-f16-256", "c1-f32-1024", "c1-f32-1024-int", "c2-f16-1024", "c3-f16-2048", "c3-bf16-2048",
@@ -410,6 +416,13 @@ def cpu_baseline(p, seconds):
                       f"fp64 ascending-k sums over the same {w.dtype} inputs; {dt:.1f} s",
             "seconds": round(dt, 3), "cpu_model": cpu_model,
             "gpu_rows_vs_oracle": str(chk), "gpu_rows_ok": bool(chk.ok)}
+
+
+def split_details(entries):
+    """(entries without DETAILS, their details): what is printed and what is logged."""
+    short = {n: {k: v for k, v in e.items() if k not in DETAILS} for n, e in entries.items()}
+    rest = {n: {k: e[k] for k in DETAILS if k in e} for n, e in entries.items()}
+    return short, {n: e for n, e in rest.items() if e}
 
 
 def conversion_lines(w):
@@ -803,6 +816,10 @@ def main():
         cpu = cpu_baseline(p, a.cpu_seconds)
         log(f"cpu_baseline: {cpu['value'] * 1e3:.2f} GFLOPS on {cpu['cores']} threads; "
             f"GPU rows {cpu['gpu_rows_vs_oracle']}")
+
+    extra, details = split_details(extra)
+    if details:
+        log("bench: by_workload details " + json.dumps(details))
 
     # INT8 products count integer operations and accumulate and output in INT32
     integer = w.dtype == "i8"

@@ -102,3 +102,13 @@ def test_digest_refuses_a_run_without_the_calibration_copies(tmp_path, monkeypat
     with pytest.raises(SystemExit):
         bench.digest_counters(w, str(tmp_path / "fetch"), str(tmp_path / "write"), 3)
     assert not (tmp_path / "traffic.json").exists()
+
+
+def test_details_of_the_other_workloads_stay_out_of_the_printed_line():
+    full = {"a": {"tflops": 1.5, "ms": 0.1, "launches": 9, "windows_ms": [1, 2, 3],
+                  "resources": {"launches": [{"regs": 1}]}, "oracle": {"gpu_rows_ok": True}},
+            "b": {"gbs": 4.0, "ms": 2.0}}
+    short, details = bench.split_details(full)
+    assert short == {"a": {"tflops": 1.5, "ms": 0.1, "oracle": {"gpu_rows_ok": True}},
+                     "b": {"gbs": 4.0, "ms": 2.0}}
+    assert details == {"a": {k: full["a"][k] for k in bench.DETAILS}}
