@@ -11,8 +11,12 @@ namespace migemm {
 // 256x256 tiles from half a round of them on, else 128x128 from half a round,
 // else 64x64; the ping-pong schedule where every tile and k-tile is whole.  Forward
 // pass, us on 64 / 128 / 256 (BF16): 64 x 32000 x 1024 18 / 19 / 34, 200 x 50000 x 2048
-// 89 / 78 / 61, 1000 x 8000 x 512 28 / 21 / 24, 2048 x 4096 x 2048 65 / 47 / 50, 4096 x
-// 1000 x 1024 31 / 25 / 41; FP32 100 x 4000 x 512 16 / 38, 500 x 8000 x 512 46 / 42.
+// 89 / 78 / 61, 4096 x 1000 x 1024 31 / 25 / 41; FP32 100 x 4000 x 512 16 / 38, 500 x 8000
+// x 512 46 / 42.  At 128 to 160 tiles of 256x256 neither side is always the better:
+// forward and backward pass on 128 / 256, 1000 x 8000 x 512 21 + 55 / 25 + 61, 2048 x 4096 x
+// 2048 50 + 135 / 52 + 134, 200 x 33000 x 1024 36 + 105 / 33 + 98, 500 x 17000 x 1024 37 +
+// 99 / 33 + 98, 1024 x 8192 x 4096 77 + 241 / 77 + 214; 128 where the 256-high tiles stand
+// half empty, 300 x 20000 x 2048 41 + 128 / 54 + 134.
 // FP32, which the matrix cores' rate bounds, takes 64x64 tiles (two to a CU) where a
 // last round of 128x128 ones would stand mostly empty (723 x 5489 x 804: 82 against
 // 108), 64x32 ones on at most half a round, whose k-tile is half as long (33 x 4099 x
@@ -143,10 +147,11 @@ bool rows_ok(const void* p, int64_t ld, int64_t epc) {
     return aligned16(p) && ld % epc == 0 && ld < (int64_t(1) << 21);
 }
 
-// The variant and configuration of dx's product (T x cols, k deep), -1 the
-// selection's.  Where 128x128 tiles just make a round of 256 workgroups the
-// selection walks all of k on them; a long k is better cut into slices on the
-// 256x256 tile (2048 x 2048 x 32000 FP16: 232 us against 310).
+// The variant and configuration of dx's product (T x cols, k deep) where the vocabulary
+// takes several pieces, -1 the selection's.  Where 128x128 tiles just make a round of 256
+// workgroups the selection walks all of k on them; a long k is better cut into slices on
+// the 256x256 tile (dz and dx of 2048 x 200000 x 2048 BF16: 2752 us against 3176; 8192 x
+// 40001 x 512: 868 against 914).
 struct Choice {
     int variant, config;
 };

@@ -196,7 +196,7 @@ template <> __device__ __forceinline__ bf16_t from_f32<bf16_t>(float x) {
 // that follows finds it there (4096 x 4096 BF16 and then a negation 23.9 us, 25.9 in the
 // other form).  A larger one four pieces a lane, with non-temporal stores where it is
 // aligned: 8192 x 8192 FP32 44.6 us (6.8 TB/s, part of it into the last-level cache)
-// against 81, 67.8 with plain stores; and a negation 156 against 175.
+// against 81, 67.8 with plain stores; and a negation 156 against 175.  BF16 27 us (6.2 TB/s).
 template <typename T, int U>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(
     int64_t rows, int64_t cols, const uint8_t* __restrict__ data, int64_t ldd,

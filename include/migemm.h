@@ -407,9 +407,10 @@ const char* migemm_mx_config_name(int config);
  * V x D) in `dtype`; either may be NULL.  grad (T floats) is the upstream gradient
  * of each row's loss: 1 / n for the mean over n rows, 1 for the sum.  The
  * derivative of the loss to each logit is rounded to `dtype` once, for the
- * matrix cores; 16-bit derivatives are held relative to the largest grad, so that
- * FP16 ones do not vanish and equal grads are held exactly, and for up to 32 tokens
- * as two terms.
+ * matrix cores (BF16 gradients are off by up to 1.7 times what their own last rounding
+ * gives); 16-bit derivatives are held relative to the largest grad, so that FP16 ones do
+ * not vanish and that, where all grads are equal, only softmax - target is rounded and
+ * not grad; for up to 32 tokens they are kept as two terms, 16 or 22 bits.
  *
  * Rows.  T may be 0 (losses: a no-op; dW = 0).  A row without a loss (below) has
  * loss 0, a zero row of dX, and adds nothing to dW, whatever its row of X holds;
