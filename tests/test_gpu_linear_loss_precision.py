@@ -233,3 +233,42 @@ def test_a_student_that_matches_its_teacher_has_almost_no_loss(dtype):
     # teacher and student logs: FP32 exponents and sums, each below 2^-19 as above
     assert (loss >= 0).all()
     assert ((loss.double() - want).abs() <= tau * tau * (tol + 2 * 2.0 ** -19)).all()
+
+
+# entries per wavefront 1, 2, 4, 8 and 16 (at once, and more than once); x in LDS up to 16
+# KiB a row and from memory past it; k ending inside a slab; the partial first k-tile
+@pytest.mark.parametrize("top", [1, 3, 7, 13, 30, 60, 150])
+@pytest.mark.parametrize("T,D,dtype", [(5, 72, "f32"), (9, 4104, "f32"), (40, 520, "f16"),
+                                       (7, 8200, "bf16"), (3, 8192, "f16"), (130, 1096, "bf16")])
+def test_named_logits_are_those_behind_the_log_sum_exp(T, D, dtype, top):
+    """With every entry of a vocabulary named, lse is the log-sum-exp of the student's
+    logits as returned, however far their own errors (of up to 1e-4) go: off by the
+    evaluation's 2^-19 and by the rounding of log2(e) / tau, 2^-24 of the largest."""
+    dt = torch.float32 if dtype == "f32" else TORCH[dtype]
+    x, w, _, z, g = certain(T, top, D, dt, 150.0, T + D + top)
+    index = torch.rand(T, top, generator=g, device="cuda").argsort(1).contiguous()
+    say(f"named {T}x{top}x{D} {dtype}")
+    _, lse, student = mg.linear_distillation(x, w, torch.zeros(T, top, device="cuda"), index,
+                                             temperature=2.0)
+    at = z.gather(1, index)
+    ez = D * 2.0 ** -23 * (x.double().abs() @ w.double().abs().t()).gather(1, index)
+    assert ((student.double() - at).abs() <= ez).all()
+    want = torch.logsumexp(student.double() / 2, 1)
+    assert ((lse - want).abs() <= 2.0 ** -19 + 2.0 ** -24 * student.double().abs().amax(1)).all()
+
+
+@pytest.mark.parametrize("T,V,D,dtype", [(300, 17000, 1032, "f16"), (300, 17001, 136, "bf16"),
+                                         (512, 16640, 256, "bf16"), (200, 30000, 72, "f16")])
+def test_named_logits_of_large_tiles(T, V, D, dtype):
+    """The same on 256x256 tiles, a single entry against the softmax's value at it: with
+    logits of about 150 that is 1 less the small rest, as the student's own logit gives it."""
+    x, w, target, z, g = certain(T, V, D, TORCH[dtype], 150.0, V + D)
+    say(f"named {T}x{V}x{D} {dtype}")
+    _, lse, student = mg.linear_distillation(x, w, torch.zeros(T, 1, device="cuda"),
+                                             target[:, None])
+    others = (z - z.gather(1, target[:, None])).scatter_(1, target[:, None], -math.inf)
+    rest = torch.log1p(torch.exp(others).sum(1))
+    sure = rest < 2.0 ** -30
+    assert sure.sum() > T // 2
+    gap = lse - student[:, 0].double()
+    assert (gap[sure].abs() <= 2.0 ** -19 + 2.0 ** -24 * student[sure, 0].double().abs()).all()
