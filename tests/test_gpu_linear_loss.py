@@ -559,3 +559,82 @@ def test_whole_tiles_and_pieces_together(T, V, D, dtype):
     assert all(torch.equal(p, q) for p, q in zip(got, again))
     say(f"kd {T}x{V}x{D} {dtype}")
     check(run_kd(x, w, torch.zeros(T, 1, device="cuda"), index.contiguous(), 1.0, grad), want, tol)
+
+
+# --------------------------------------------------- offsets of more than 32 bits
+
+def test_inputs_and_gradients_of_more_than_2_31_elements_by_tokens():
+    """x, dx, dz and their copies pass 2^31 elements: rows of dx at both ends and around
+    the borders, and dw, the sum over all rows, added up over six parts (each of whose
+    tolerances, six times over, covers sums of six times as many terms)."""
+    T, V, D = 600000, 520, 4096
+    x = torch.empty(T, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for s in range(0, T, 100000):
+        x[s:s + 100000] = torch.randn(100000, D, generator=g, device="cuda").bfloat16()
+    w = (torch.randn(V, D, generator=g, device="cuda") / 32).bfloat16()
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    target[::7] = IGNORE
+    grad = (torch.rand(T, generator=g, device="cuda") + 0.25) / T
+    assert T * D > 1 << 31
+    say(f"ce {T}x{V}x{D} bf16")
+    loss, dx, dw = run_ce(x, w, target, grad)
+    index = torch.where(target == IGNORE, -1, target)[:, None]
+    border = (1 << 31) // D
+    rows = torch.cat([torch.arange(a, a + 60, device="cuda")
+                      for a in (0, border // 2 - 30, border - 30, T - 60)])
+    (l, d, _), (tl, td, _) = reference(x[rows], w, index[rows], None, 1.0, grad[rows], True)
+    check((loss[rows], dx[rows], None), (l, d, None), (tl, td, None))
+    want, tol = torch.zeros(V, D, device="cuda"), torch.zeros(V, D, device="cuda")
+    want, tol = want.double(), tol.double()
+    for s in range(0, T, 100000):
+        p = slice(s, s + 100000)
+        r, t = reference(x[p], w, index[p], None, 1.0, grad[p], True)
+        want += r[2]
+        tol += t[2]
+        del r, t
+    check((None, None, dw), (None, None, want), (None, None, 6 * tol))
+
+
+def test_weights_and_gradients_of_more_than_2_31_elements_by_the_vocabulary():
+    """w, its gradient and the offsets into them pass 2^31 elements, in two pieces of the
+    vocabulary; rows of dw at both ends and around the borders, and all of dx."""
+    T, V, D = 40, 1100000, 2048
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.empty(V, D, dtype=torch.bfloat16, device="cuda")
+    for s in range(0, V, 100000):
+        w[s:s + 100000] = (torch.randn(100000, D, generator=g, device="cuda") / 32).bfloat16()
+    x = torch.randn(T, D, generator=g, device="cuda").bfloat16()
+    border = (1 << 31) // D
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    target[:4] = torch.tensor([0, V - 1, border, border - 1], device="cuda")
+    grad = torch.rand(T, generator=g, device="cuda") + 0.25
+    say(f"ce {T}x{V}x{D} bf16")
+    loss, dx, dw = run_ce(x, w, target, grad)
+    u, X = 2.0 ** -8, x.double()
+    z, ez = (torch.empty(T, V, dtype=torch.double, device="cuda") for _ in range(2))
+    for s in range(0, V, 100000):
+        W = w[s:s + 100000].double()
+        z[:, s:s + 100000], ez[:, s:s + 100000] = X @ W.t(), X.abs() @ W.abs().t()
+    ez *= D * 2.0 ** -23
+    log_q = torch.log_softmax(z, 1)
+    d = ez.amax(1) + 2.0 ** -20 * (1 + z.abs().amax(1) + math.log(V))
+    at = target[:, None]
+    want = -log_q.gather(1, at)[:, 0]
+    assert ((loss.double() - want).abs() <= 2 * d + 2.0 ** -22 * want).all()
+    q, c = log_q.exp(), grad.double()[:, None]
+    p = torch.zeros_like(q).scatter_(1, at, 1.0)
+    dz = c * (q - p)
+    e = (c * (4 * q * d[:, None] + 2.0 ** -20 * p) + u * dz.abs()) * (1 + u)
+    want, tol = (torch.zeros(T, D, dtype=torch.double, device="cuda") for _ in range(2))
+    n = e + V * 2.0 ** -23 * (dz.abs() + e)
+    for s in range(0, V, 100000):
+        W = w[s:s + 100000].double()
+        want += dz[:, s:s + 100000] @ W
+        tol += n[:, s:s + 100000] @ W.abs()
+    check((None, dx, None), (None, want, None), (None, tol + u * (want.abs() + tol), None))
+    rows = torch.cat([torch.arange(a, a + 400, device="cuda")
+                      for a in (0, border // 2 - 200, border - 200, V - 400)])
+    rows = torch.cat((rows, target))
+    want, n = dz[:, rows].t() @ X, (e + T * 2.0 ** -23 * (dz.abs() + e))[:, rows].t() @ X.abs()
+    check((None, None, dw[rows]), (None, None, want), (None, None, n + u * (want.abs() + n)))
