@@ -34,11 +34,28 @@ EXPORTS = ("migemm_gemm", "migemm_gemm_variant", "migemm_gemm_ex", "migemm_gemm_
            "migemm_mx_config_count", "migemm_mx_config_name",
            "migemm_linear_loss_workspace_size", "migemm_linear_ce_forward",
            "migemm_linear_ce_backward", "migemm_linear_kd_forward", "migemm_linear_kd_backward",
+           "migemm_layer_norm_forward", "migemm_layer_norm_workspace_size",
+           "migemm_layer_norm_backward", "migemm_embedding_forward",
+           "migemm_embedding_workspace_size", "migemm_embedding_backward", "migemm_adamw",
            "migemm_variant_count", "migemm_variant_name",
            "migemm_variant_supports", "migemm_config_count", "migemm_config_name",
            "migemm_select", "migemm_status_string", "migemm_last_hip_error", "migemm_version")
 
 _lib = None
+
+
+class AdamwTensor(ctypes.Structure):
+    """``migemm_adamw_tensor``."""
+    _fields_ = [("count", ctypes.c_int64)] + [(name, ctypes.c_void_p) for name in (
+        "param", "grad", "master", "avg", "sq", "avg_scales", "sq_scales")]
+
+
+class AdamwOptions(ctypes.Structure):
+    """``migemm_adamw_options``."""
+    _fields_ = ([(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps",
+                                                      "weight_decay")] +
+                [("step", ctypes.c_int64)] +
+                [(name, ctypes.c_void_p) for name in ("lr_device", "step_device", "grad_scale")])
 
 
 class MigemmError(RuntimeError):
@@ -111,6 +128,23 @@ def lib():
     L.migemm_linear_kd_forward.restype = i32
     L.migemm_linear_kd_backward.argtypes = kd + [vp, vp, i64, vp, vp, i64, vp, i64, vp, i64, vp]
     L.migemm_linear_kd_backward.restype = i32
+    L.migemm_layer_norm_forward.argtypes = [i64, i64, i32, vp, i64, i32, vp, vp, f32, vp, i64, vp,
+                                            vp, vp]
+    L.migemm_layer_norm_forward.restype = i32
+    L.migemm_layer_norm_workspace_size.argtypes = [i64, i64, i32, ctypes.POINTER(i64)]
+    L.migemm_layer_norm_workspace_size.restype = i32
+    L.migemm_layer_norm_backward.argtypes = [i64, i64, i32, vp, i64, vp, i64, i32, vp, vp, vp, vp,
+                                             i64, vp, vp, vp, i64, vp]
+    L.migemm_layer_norm_backward.restype = i32
+    L.migemm_embedding_forward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, f32, vp, i64, vp]
+    L.migemm_embedding_forward.restype = i32
+    L.migemm_embedding_workspace_size.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    L.migemm_embedding_workspace_size.restype = i32
+    L.migemm_embedding_backward.argtypes = [i64, i64, i64, i32, vp, i64, vp, i64, f32, i32, i32,
+                                            vp, i64, vp, i64, vp]
+    L.migemm_embedding_backward.restype = i32
+    L.migemm_adamw.argtypes = [i64, vp, i32, i32, i32, ctypes.POINTER(AdamwOptions), vp]
+    L.migemm_adamw.restype = i32
     L.migemm_variant_count.argtypes = []
     L.migemm_variant_count.restype = i32
     L.migemm_variant_name.argtypes = [i32]
@@ -278,6 +312,52 @@ def migemm_linear_kd_backward(T, V, D, top, dtype, X, ldx, W, ldw, teacher_dtype
                                            teacher, ldt, index, ldi, temperature, lse, student, lds,
                                            grad, dX, lddx, dW, lddw, workspace, workspace_bytes,
                                            stream)
+
+
+def migemm_layer_norm_forward(T, D, dtype, X, ldx, w_dtype, W, B, eps, Y, ldy, mean, rstd,
+                              stream=None) -> int:
+    return lib().migemm_layer_norm_forward(T, D, dtype, X, ldx, w_dtype, W, B, eps, Y, ldy, mean,
+                                           rstd, stream)
+
+
+def migemm_layer_norm_workspace_size(T, D, vectors):
+    """(status, bytes) of the workspace of layer norm's backward pass."""
+    n = ctypes.c_int64(-1)
+    st = lib().migemm_layer_norm_workspace_size(T, D, vectors, ctypes.byref(n))
+    return st, n.value
+
+
+def migemm_layer_norm_backward(T, D, dtype, dY, lddy, X, ldx, w_dtype, W, mean, rstd, dX, lddx,
+                               dW, dB, workspace, workspace_bytes, stream=None) -> int:
+    return lib().migemm_layer_norm_backward(T, D, dtype, dY, lddy, X, ldx, w_dtype, W, mean, rstd,
+                                            dX, lddx, dW, dB, workspace, workspace_bytes, stream)
+
+
+def migemm_embedding_forward(T, V, D, dtype, W, ldw, index, ignore_index, scale, Y, ldy,
+                             stream=None) -> int:
+    return lib().migemm_embedding_forward(T, V, D, dtype, W, ldw, index, ignore_index, scale, Y,
+                                          ldy, stream)
+
+
+def migemm_embedding_workspace_size(T, V, D):
+    """(status, bytes) of the workspace of the embedding's gradient."""
+    n = ctypes.c_int64(-1)
+    st = lib().migemm_embedding_workspace_size(T, V, D, ctypes.byref(n))
+    return st, n.value
+
+
+def migemm_embedding_backward(T, V, D, dtype, dY, lddy, index, ignore_index, scale, accumulate,
+                              dw_dtype, dW, lddw, workspace, workspace_bytes, stream=None) -> int:
+    return lib().migemm_embedding_backward(T, V, D, dtype, dY, lddy, index, ignore_index, scale,
+                                           accumulate, dw_dtype, dW, lddw, workspace,
+                                           workspace_bytes, stream)
+
+
+def migemm_adamw(tensors, list, param_dtype, grad_dtype, state_bits, options, stream=None) -> int:
+    """``list``: an array of AdamwTensor, or of its eight fields in turn as c_int64;
+    ``options``: an AdamwOptions or None."""
+    return lib().migemm_adamw(tensors, list, param_dtype, grad_dtype, state_bits,
+                              None if options is None else ctypes.byref(options), stream)
 
 
 def migemm_variant_count() -> int:
@@ -845,3 +925,317 @@ def linear_distillation_backward(x, w, teacher_logits, teacher_index, lse, stude
     if st != OK:
         raise MigemmError(st, "migemm_linear_kd_backward")
     return dx, dw
+
+
+# ------------------------------------------- around the output layer's losses
+
+def _vector(name, t, device, like, size):
+    """Pointer of a norm's weight or bias (or None), checked against `like`'s dtype."""
+    if t is None:
+        return None
+    if t.device != device:
+        _check_device(name, t, device)
+    if t.dtype is not like or t.shape != (size,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {like} vector of {size} (got {t.dtype}, "
+                         f"{tuple(t.shape)}, strides {t.stride()})")
+    return t.data_ptr() or None
+
+
+def _second_type(name, dtype, x):
+    """The code of `dtype`, x's own or float32."""
+    torch = _torch or _load_torch()
+    code = _dtype_code(x)
+    if dtype is x.dtype:
+        return code
+    if dtype is not torch.float32:
+        raise ValueError(f"{name} must be {x.dtype} or torch.float32 (got {dtype})")
+    return F32
+
+
+def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, stats: bool = True,
+               stream=None):
+    """(y, mean, rstd): layer norm over the rows of ``x`` (T x D), ``(x - mean) * rstd *
+    weight + bias`` with ``rstd = 1 / sqrt(variance + eps)``, in ``x``'s dtype (``out``, if
+    given), and the rows' float32 statistics, which ``layer_norm_backward`` takes (None
+    where ``stats`` is false).  ``x``: a CUDA tensor (float32, float16, bfloat16), unit
+    column stride.  ``weight`` and ``bias``: contiguous vectors of D, both of ``x``'s dtype
+    or both float32; None stands for ones, or zeros.  Runs on ``stream`` (default: torch's
+    current stream; another one first waits for it) without synchronising.  Autograd does
+    not see the call: the gradients come from the backward function."""
+    torch = _torch or _load_torch()
+    device = x.device
+    if not x.is_cuda:
+        _check_device("x", x, device)
+    dt, ldx = _dtype_code(x), _ld(x)
+    T, D = x.shape
+    kind = x.dtype if weight is None and bias is None else (bias if weight is None else weight).dtype
+    wd = _second_type("weight and bias", kind, x)
+    pw, pb = _vector("weight", weight, device, kind, D), _vector("bias", bias, device, kind, D)
+    with _device_of(device):
+        stream, other = _stream_of(stream, device)
+        if out is None:
+            out = torch.empty((T, D), dtype=x.dtype, device=device)
+        else:
+            _gradient("out", True, out, x)
+        mean = rstd = None
+        if stats:
+            mean = torch.empty(T, dtype=torch.float32, device=device)
+            rstd = torch.empty(T, dtype=torch.float32, device=device)
+        if other:
+            _run_on(stream, device, x, weight, bias, out, mean, rstd)
+        st = lib().migemm_layer_norm_forward(
+            T, D, dt, x.data_ptr() or None, ldx, wd, pw, pb, float(eps), out.data_ptr() or None,
+            _ld(out), (mean.data_ptr() or None) if stats else None,
+            (rstd.data_ptr() or None) if stats else None, stream)
+        if st != OK:
+            raise MigemmError(st, "migemm_layer_norm_forward")
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dw=None, db=None,
+                        need_dx: bool = True, need_dw: bool = True, need_db: bool = True,
+                        stream=None):
+    """(dx, dw, db): the gradients of ``layer_norm`` to ``x``, ``weight`` and ``bias`` for
+    the upstream gradient ``dy`` (``x``'s shape and dtype).  ``dw`` and ``db`` are of
+    ``weight``'s dtype (``x``'s where ``weight`` is None, with no ``dw`` then).  Each is
+    written into if given; one that is neither given nor needed is None."""
+    torch = _torch or _load_torch()
+    device = x.device
+    if not (x.is_cuda and dy.device == device):
+        _check_device("x", x, device)
+        _check_device("dy", dy, device)
+    if dy.dtype is not x.dtype or dy.shape != x.shape:
+        raise ValueError("dy must have x's shape and dtype")
+    dt, ldx, lddy = _dtype_code(x), _ld(x), _ld(dy)
+    T, D = x.shape
+    kind = x.dtype if weight is None else weight.dtype
+    wd = _second_type("weight", kind, x)
+    pw = _vector("weight", weight, device, kind, D)
+    pm = _row_vector("mean", mean, device, torch.float32, T)
+    pr = _row_vector("rstd", rstd, device, torch.float32, T)
+    if weight is None:
+        if dw is not None:
+            raise ValueError("dw needs a weight")
+        need_dw = False
+    with _device_of(device):
+        stream, other = _stream_of(stream, device)
+        dx = _gradient("dx", need_dx, dx, x)
+        if dw is None and need_dw:
+            dw = torch.empty(D, dtype=kind, device=device)
+        if db is None and need_db:
+            db = torch.empty(D, dtype=kind, device=device)
+        pdw, pdb = _vector("dw", dw, device, kind, D), _vector("db", db, device, kind, D)
+        st, n = migemm_layer_norm_workspace_size(T, D, dw is not None or db is not None)
+        if st != OK:
+            raise MigemmError(st, "migemm_layer_norm_workspace_size")
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        if other:
+            _run_on(stream, device, dy, x, weight, mean, rstd, dx, dw, db, ws)
+        st = lib().migemm_layer_norm_backward(
+            T, D, dt, dy.data_ptr() or None, lddy, x.data_ptr() or None, ldx, wd, pw, pm, pr,
+            *_out_matrix_of(dx, D), pdw, pdb, ws.data_ptr() or None, n, stream)
+        if st != OK:
+            raise MigemmError(st, "migemm_layer_norm_backward")
+    return dx, dw, db
+
+
+def _out_matrix_of(t, D):
+    return (None, D) if t is None else (t.data_ptr() or None, _ld(t))
+
+
+def embedding(w, index, *, scale: float = 1.0, ignore_index: int = -100, out=None, stream=None):
+    """``scale * w[index]`` (T x D, in ``w``'s dtype; ``out``, if given): rows of the table
+    ``w`` (V x D, a CUDA tensor, float32, float16 or bfloat16, unit column stride) by
+    token (``index``: int64, T).  A token whose index is ``ignore_index`` (padding) has a
+    row of zeros, one outside the table a row of NaN.  Runs on ``stream`` (default:
+    torch's current stream; another one first waits for it) without synchronising.
+    Autograd does not see the call: the gradient comes from ``embedding_backward``."""
+    torch = _torch or _load_torch()
+    device = w.device
+    if not w.is_cuda:
+        _check_device("w", w, device)
+    dt, ldw = _dtype_code(w), _ld(w)
+    V, D = w.shape
+    T = index.numel()
+    pi = _row_vector("index", index, device, torch.int64, T)
+    with _device_of(device):
+        stream, other = _stream_of(stream, device)
+        if out is None:
+            out = torch.empty((T, D), dtype=w.dtype, device=device)
+        else:
+            _check_device("out", out, device)
+            if out.dtype is not w.dtype or out.shape != (T, D):
+                raise ValueError(f"out must be {w.dtype}, {T} x {D}")
+        if other:
+            _run_on(stream, device, w, index, out)
+        st = lib().migemm_embedding_forward(T, V, D, dt, w.data_ptr() or None, ldw, pi,
+                                            ignore_index, float(scale), out.data_ptr() or None,
+                                            _ld(out), stream)
+        if st != OK:
+            raise MigemmError(st, "migemm_embedding_forward")
+    return out
+
+
+def embedding_backward(dy, index, vocab: int, *, scale: float = 1.0, ignore_index: int = -100,
+                       dw=None, accumulate: bool = False, out_dtype=None, stream=None):
+    """The gradient of ``embedding`` to its table, ``vocab`` x D, for the upstream gradient
+    ``dy`` (T x D) of its rows: row v is ``scale`` times the sum of ``dy`` over the tokens of
+    entry v.  ``dw`` (``dy``'s dtype or float32) is written into if given, or added to
+    where ``accumulate`` is set (the gradient that an output layer with the same weight has
+    left, say); otherwise it is allocated with ``out_dtype`` (default: ``dy``'s).  Sums are
+    float32, in an order that does not depend on timing."""
+    torch = _torch or _load_torch()
+    device = dy.device
+    if not dy.is_cuda:
+        _check_device("dy", dy, device)
+    dt, lddy = _dtype_code(dy), _ld(dy)
+    T, D = dy.shape
+    pi = _row_vector("index", index, device, torch.int64, T)
+    if dw is None:
+        if accumulate:
+            raise ValueError("accumulate needs an existing dw")
+        kind = out_dtype or dy.dtype
+    else:
+        _check_device("dw", dw, device)
+        kind = dw.dtype
+        if dw.shape != (vocab, D) or (out_dtype is not None and out_dtype is not kind):
+            raise ValueError(f"dw must have shape ({vocab}, {D}) (and out_dtype, if given)")
+    wd = _second_type("dw", kind, dy)
+    with _device_of(device):
+        stream, other = _stream_of(stream, device)
+        if dw is None:
+            dw = torch.empty((vocab, D), dtype=kind, device=device)
+        st, n = migemm_embedding_workspace_size(T, vocab, D)
+        if st != OK:
+            raise MigemmError(st, "migemm_embedding_workspace_size")
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        if other:
+            _run_on(stream, device, dy, index, dw, ws)
+        st = lib().migemm_embedding_backward(
+            T, vocab, D, dt, dy.data_ptr() or None, lddy, pi, ignore_index, float(scale),
+            int(accumulate), wd, dw.data_ptr() or None, _ld(dw), ws.data_ptr() or None, n, stream)
+        if st != OK:
+            raise MigemmError(st, "migemm_embedding_backward")
+    return dw
+
+
+class AdamState(NamedTuple):
+    """What AdamW keeps of one parameter (the format is described in
+    ``include/migemm.h``).
+
+    32 bits: ``avg`` and ``sq``, float32, as many elements as the parameter, hold the first
+    and the second moment.  8 bits: ``avg`` and ``sq``, float8_e4m3fn (or their bytes,
+    uint8), hold the first moment and the root of the second, in units of ``avg_scales``
+    and ``sq_scales`` (float32, one for each 256 consecutive elements).  ``master``: a
+    float32 copy of a 16-bit parameter, or None."""
+    avg: "torch.Tensor"  # noqa: F821
+    sq: "torch.Tensor"  # noqa: F821
+    avg_scales: "torch.Tensor | None" = None  # noqa: F821
+    sq_scales: "torch.Tensor | None" = None  # noqa: F821
+    master: "torch.Tensor | None" = None  # noqa: F821
+
+
+def adamw_state(param, *, bits: int = 32, master: bool = False) -> AdamState:
+    """The state of ``param`` before its first step; ``bits``: 32 or 8; ``master``: with a
+    float32 copy of the (16-bit) parameter as it is now."""
+    torch = _torch or _load_torch()
+    if bits not in (32, 8):
+        raise ValueError(f"bits must be 32 or 8 (got {bits})")
+    if master and param.dtype is torch.float32:
+        raise ValueError("a float32 parameter needs no master copy")
+    copy = param.detach().to(torch.float32) if master else None
+    shape, device = param.shape, param.device
+    if bits == 32:
+        return AdamState(torch.zeros(shape, device=device), torch.zeros(shape, device=device),
+                         master=copy)
+    blocks = (param.numel() + 255) // 256
+    codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    return AdamState(*codes, torch.zeros(blocks, device=device),
+                     torch.zeros(blocks, device=device), copy)
+
+
+def _step_tensor(name, t, device, dtype):
+    """Pointer of a number on the device, checked."""
+    _check_device(name, t, device)
+    if t.dtype is not dtype or t.numel() != 1:
+        raise ValueError(f"{name} must be a number or one {dtype} on the GPU (got {t.dtype}, "
+                         f"{tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def adamw_(params, grads, states, *, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+           weight_decay: float = 0.01, grad_scale=None, stream=None) -> None:
+    """One AdamW step over lists of parameters, their gradients and their ``AdamState``s,
+    in place (the formulas are in ``include/migemm.h``).
+
+    Parameters are contiguous CUDA tensors of one dtype (float32, float16, bfloat16) on one
+    device, gradients of the same one or all float32, states all of 32 or all of 8 bits,
+    with a master copy in all or in none.  ``step``: the number of this step, from 1.
+    ``step`` (int64), ``lr`` and ``grad_scale`` (float32; gradients are multiplied by it)
+    may be tensors of one element on the GPU: they are read where the step runs, so that a
+    captured step follows them; a ``grad_scale`` of infinity or NaN skips the step.  Runs
+    on ``stream`` (default: torch's current stream; another one first waits for it)
+    without synchronising."""
+    torch = _torch or _load_torch()
+    count = len(params)
+    if len(grads) != count or len(states) != count:
+        raise ValueError(f"{count} parameters, {len(grads)} gradients and {len(states)} states")
+    if count == 0:
+        return
+    device, pd, gd = params[0].device, params[0].dtype, grads[0].dtype
+    _check_device("params", params[0], device)
+    f32, sd = torch.float32, states[0][0].dtype
+    eight = sd is torch.float8_e4m3fn or sd is torch.uint8
+    if not eight and sd is not f32:
+        raise ValueError(f"states must be float32, float8_e4m3fn or uint8 (got {sd})")
+    index = params[0].get_device()
+    master = states[0][4] is not None
+    if master and pd is f32:
+        raise ValueError("float32 parameters take no master copy")
+    pc, gc = _dtype_code(params[0]), _second_type("gradients", gd, params[0])
+    fields = []
+    for p, g, s in zip(params, grads, states):
+        n, (avg, sq, ms, rs, copy) = p.numel(), s
+        held = [(p, pd, n), (g, gd, n), (avg, sd, n), (sq, sd, n)]
+        if eight:
+            held += [(ms, f32, (n + 255) // 256), (rs, f32, (n + 255) // 256)]
+        if master:
+            held.append((copy, f32, n))
+        for t, kind, size in held:
+            if (t is None or t.dtype is not kind or t.numel() != size or t.get_device() != index
+                    or not t.is_contiguous()):
+                raise ValueError(_adamw_refusal(t, kind, size, device))
+        if (copy is not None) != master or (ms is not None) != eight or (rs is not None) != eight:
+            raise ValueError("states must all be of 32 or all of 8 bits, with a master copy in "
+                             "all or in none")
+        fields += (n, p.data_ptr(), g.data_ptr(), copy.data_ptr() if master else 0,
+                   avg.data_ptr(), sq.data_ptr(), ms.data_ptr() if eight else 0,
+                   rs.data_ptr() if eight else 0)
+    numbers = [t if isinstance(t, torch.Tensor) else None for t in (lr, step, grad_scale)]
+    o = AdamwOptions(0.0 if numbers[0] is not None else float(lr), float(betas[0]),
+                     float(betas[1]), float(eps), float(weight_decay),
+                     1 if numbers[1] is not None else int(step))
+    if numbers[0] is not None:
+        o.lr_device = _step_tensor("lr", lr, device, f32)
+    if numbers[1] is not None:
+        o.step_device = _step_tensor("step", step, device, torch.int64)
+    with _device_of(device):
+        stream, other = _stream_of(stream, device)
+        if grad_scale is not None:
+            if numbers[2] is None:
+                numbers[2] = torch.full((), float(grad_scale), dtype=f32, device=device)
+            o.grad_scale = _step_tensor("grad_scale", numbers[2], device, f32)
+        if other:
+            _run_on(stream, device, *params, *grads, *numbers, *(t for s in states for t in s))
+        st = lib().migemm_adamw(count, (ctypes.c_int64 * len(fields))(*fields), pc, gc,
+                                8 if eight else 32, ctypes.byref(o), stream)
+        if st != OK:
+            raise MigemmError(st, "migemm_adamw")
+
+
+def _adamw_refusal(t, kind, size, device):
+    got = "None" if t is None else (f"{t.dtype}, {t.numel()} elements on {t.device}, strides "
+                                    f"{tuple(t.stride())}")
+    return (f"a tensor of the step must be contiguous, {kind}, of {size} elements on {device} "
+            f"(got {got})")

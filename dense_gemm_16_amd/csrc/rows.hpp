@@ -1,0 +1,76 @@
+// rows.hpp -- pieces of rows in registers: what the layer norm, embedding and AdamW
+// kernels share.
+#pragma once
+
+#include "common.hpp"
+
+namespace migemm {
+
+// Elements of type T in one 16-byte access.
+template <typename T> constexpr int kChunk = 16 / static_cast<int>(sizeof(T));
+
+template <typename T> __device__ __forceinline__ T narrow(float x);
+template <> __device__ __forceinline__ float narrow<float>(float x) { return x; }
+template <> __device__ __forceinline__ _Float16 narrow<_Float16>(float x) {
+    return static_cast<_Float16>(x);
+}
+template <> __device__ __forceinline__ bf16_t narrow<bf16_t>(float x) {
+    return bf16_t{f32_to_bf16_bits(x)};
+}
+
+// N consecutive elements, 16 bytes at a time, whatever the alignment.
+template <typename T, int N>
+__device__ __forceinline__ void load_whole(const T* __restrict__ p, T (&e)[N]) {
+    __builtin_memcpy(e, p, sizeof(e));
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_whole(T* __restrict__ p, const T (&e)[N]) {
+    __builtin_memcpy(p, e, sizeof(e));
+}
+
+// N elements of which the first `held` lie inside the row; zeros for the others.
+template <typename T, int N>
+__device__ __forceinline__ void load_part(const T* __restrict__ p, int64_t held, T (&e)[N]) {
+    if (held >= N) {
+        load_whole(p, e);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = i < held ? p[i] : ZeroOf<T>::get();
+    }
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_part(T* __restrict__ p, int64_t held, const T (&e)[N]) {
+    if (held >= N) {
+        store_whole(p, e);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < held) p[i] = e[i];
+    }
+}
+
+// The sum, or largest, over the 16 lanes of a DPP row, in every one of them: rotations by
+// 8, 4, 2 and 1 lanes inside the instruction that adds.
+template <int N> __device__ __forceinline__ float row_rotated(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
+                                                                 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum16(float v) {
+    v += row_rotated<8>(v);
+    v += row_rotated<4>(v);
+    v += row_rotated<2>(v);
+    return v + row_rotated<1>(v);
+}
+
+// The sum over LANES lanes (16 or 64, aligned), in every one of them.
+template <int LANES> __device__ __forceinline__ float sum_lanes(float v) {
+    static_assert(LANES == 16 || LANES == kWave, "a DPP row or a wavefront");
+    v = sum16(v);
+    if constexpr (LANES == kWave) {
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+    }
+    return v;
+}
+
+}  // namespace migemm

@@ -485,6 +485,132 @@ int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int 
                               const float* grad, void* dX, int64_t lddx, void* dW, int64_t lddw,
                               void* workspace, int64_t workspace_bytes, void* stream);
 
+/*
+ * Layer norm over the rows of X (T x D, row-major of `dtype`, MIGEMM_F32, MIGEMM_F16 or
+ * MIGEMM_BF16): with mu and var the mean and variance of row t, r = 1 / sqrt(var + eps)
+ * and h = (x - mu) r,
+ *
+ *     Y[t][j] = h[j] W[j] + B[j]
+ *
+ * W and B are vectors of D of w_dtype (`dtype` or MIGEMM_F32); NULL stands for ones, or
+ * zeros.  Sums and statistics are FP32 (a variance below its range counts as 0), the
+ * variance is the mean of squared distances from mu.  mean and rstd (T floats each, NULL where not wanted) receive mu and r, which the
+ * backward pass reads.  eps is finite and at least 0; a row of equal elements with eps 0
+ * is NaN, and so is a row with a NaN or an infinity.
+ *
+ * Backward, with g = dY W:  dX = r (g - mean(g) - h mean(g h));  dW = the sum over rows of
+ * dY h;  dB = that of dY (dX in `dtype`, the others in w_dtype; each may be NULL where not
+ * wanted).  The sums over rows are FP32 in an order that depends on the sizes alone: no
+ * atomics.  T == 0 is a no-op forwards and gives dW = dB = 0.  D is 1 to 2^24, T below 2^31.
+ *
+ * Any alignment and leading dimensions.  The workspace of the backward pass
+ * (migemm_layer_norm_workspace_size bytes, 256-byte aligned) is lent as in the losses
+ * above; it is 0 bytes when neither dW nor dB is wanted and D is at most 16384.  Outputs
+ * and workspace must not overlap each other or the inputs.  The pointer, stream, ownership
+ * and error rules are migemm_gemm's.
+ */
+int migemm_layer_norm_forward(int64_t T, int64_t D, int dtype, const void* X, int64_t ldx,
+                              int w_dtype, const void* W, const void* B, float eps, void* Y,
+                              int64_t ldy, float* mean, float* rstd, void* stream);
+/* vectors: 1 where dW or dB is wanted, 0 where neither is. */
+int migemm_layer_norm_workspace_size(int64_t T, int64_t D, int vectors, int64_t* bytes);
+int migemm_layer_norm_backward(int64_t T, int64_t D, int dtype, const void* dY, int64_t lddy,
+                               const void* X, int64_t ldx, int w_dtype, const void* W,
+                               const float* mean, const float* rstd, void* dX, int64_t lddx,
+                               void* dW, void* dB, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
+/*
+ * Rows of a table by token (embedding lookup): for the T entries of index,
+ *
+ *     Y[t][j] = scale * W[index[t]][j]
+ *
+ * W is V x D and Y T x D, row-major of `dtype` (MIGEMM_F32, MIGEMM_F16 or MIGEMM_BF16); the
+ * product is FP32, rounded once.  A token whose index is ignore_index (padding) has a row
+ * of zeros; any other index outside 0 .. V - 1 gives a row of NaN (nothing is read for it).
+ *
+ * Backward: dW[v] = scale * (the sum of dY[t] over the tokens t whose index is v), added to
+ * what dW holds where accumulate is 1 (the gradient of a weight that an output layer
+ * shares), else in its place: rows that no token names are then zeroed, and otherwise not
+ * touched.  dW is V x D of dw_dtype (`dtype` or MIGEMM_F32).  Tokens without an entry
+ * (ignored, or outside the table) add nothing.  Sums are FP32, in an order that depends on
+ * the index and the sizes alone: the tokens are sorted by entry, with no atomics on sums.
+ *
+ * T is below 2^31 (0: a no-op, or dW = 0), V 1 to 2^28, D 1 to 2^21.  Any alignment and
+ * leading dimensions.  The workspace (migemm_embedding_workspace_size bytes) and the other
+ * rules are as for the losses above.
+ */
+int migemm_embedding_forward(int64_t T, int64_t V, int64_t D, int dtype, const void* W,
+                             int64_t ldw, const int64_t* index, int64_t ignore_index, float scale,
+                             void* Y, int64_t ldy, void* stream);
+int migemm_embedding_workspace_size(int64_t T, int64_t V, int64_t D, int64_t* bytes);
+int migemm_embedding_backward(int64_t T, int64_t V, int64_t D, int dtype, const void* dY,
+                              int64_t lddy, const int64_t* index, int64_t ignore_index,
+                              float scale, int accumulate, int dw_dtype, void* dW, int64_t lddw,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * One AdamW step over many tensors, in place.  Per element, with g = s grad,
+ *
+ *     m = beta1 m + (1 - beta1) g
+ *     v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay)
+ *         - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *
+ * in FP32, the factors rounded once from FP64 (v too: gradients below 2^-63 lose digits in
+ * it, those below 2^-75 are lost, and it is infinite for those of 2^64).  param is of param_dtype (MIGEMM_F32,
+ * MIGEMM_F16 or MIGEMM_BF16), grad of grad_dtype (param_dtype or MIGEMM_F32).  master, in
+ * all tensors of a call or in none, is an FP32 copy of a 16-bit parameter: p is then read
+ * from and written to it, and param receives it rounded.  Without one a 16-bit parameter
+ * loses steps below half of its own last place.
+ *
+ * state_bits 32: avg holds m and sq holds v, FP32; the scales are NULL.
+ * state_bits 8: avg holds m and sq the root of v as E4M3 bytes (sign, four exponent bits of
+ * bias 7, three mantissa bits; 448 the largest), each element its code times its block's
+ * scale: blocks are 256 consecutive elements of the tensor (the last one shorter), their
+ * FP32 scales avg_scales and sq_scales, ceil(count / 256) each.  A block's scale becomes
+ * its largest magnitude / 448, or 0 (all zeros) below 2^-100; codes are rounded to nearest
+ * even, and a positive root to the smallest code at least.  The update of p uses m and v
+ * before that rounding.  A block that a NaN or an infinity enters becomes NaN.  All-zero
+ * codes and scales are the state before the first step.
+ *
+ * A tensor is `count` (0 or more, below 2^40) consecutive elements; any alignment to its
+ * elements.  What a call writes must not overlap anything else that it names: a tensor
+ * named twice is refused.
+ *
+ * lr_device and step_device (device pointers, NULL: lr and step count) are read where the
+ * kernels run, so that a step captured into a graph follows them; a step on the device
+ * below 1 counts as 1.  grad_scale (device pointer, NULL: 1) is s above: 1 / the loss's
+ * scale, or a clipping factor; where it is infinite or NaN the whole step is skipped.
+ * These are read only, and must not overlap what the call writes.
+ *
+ * lr and weight_decay are finite, beta1 and beta2 lie in [0, 1), eps is finite and at least
+ * 0, step is at least 1 (unless step_device is given).  `list` and `options` are host
+ * memory, read before the call returns.
+ */
+typedef struct {
+    int64_t count;
+    void* param;
+    const void* grad;
+    float* master; /* or NULL */
+    void* avg;
+    void* sq;
+    float* avg_scales; /* state_bits 8, else NULL */
+    float* sq_scales;
+} migemm_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;
+    const float* lr_device;     /* or NULL */
+    const int64_t* step_device; /* or NULL */
+    const float* grad_scale;    /* or NULL */
+} migemm_adamw_options;
+
+int migemm_adamw(int64_t tensors, const migemm_adamw_tensor* list, int param_dtype,
+                 int grad_dtype, int state_bits, const migemm_adamw_options* options,
+                 void* stream);
+
 /* Number of variants (they are numbered 0 .. count-1). */
 int migemm_variant_count(void);
 
