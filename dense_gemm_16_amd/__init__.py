@@ -13,6 +13,7 @@ not been built, every call raises ``RuntimeError``: there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import NamedTuple
@@ -968,25 +969,26 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, stats:
         _check_device("x", x, device)
     dt, ldx = _dtype_code(x), _ld(x)
     T, D = x.shape
-    kind = x.dtype if weight is None and bias is None else (bias if weight is None else weight).dtype
-    wd = _second_type("weight and bias", kind, x)
+    kind = (weight if weight is not None else bias if bias is not None else x).dtype
+    wd = dt if kind is x.dtype else _second_type("weight and bias", kind, x)
     pw, pb = _vector("weight", weight, device, kind, D), _vector("bias", bias, device, kind, D)
     with _device_of(device):
         stream, other = _stream_of(stream, device)
         if out is None:
-            out = torch.empty((T, D), dtype=x.dtype, device=device)
+            # (x.new_empty((T, D)) for a packed x, in less time)
+            out, ldy = (torch.empty_like(x) if ldx == D else x.new_empty((T, D))), D
         else:
             _gradient("out", True, out, x)
-        mean = rstd = None
+            ldy = _ld(out)
+        mean = rstd = pm = pr = None
         if stats:
             mean = torch.empty(T, dtype=torch.float32, device=device)
-            rstd = torch.empty(T, dtype=torch.float32, device=device)
+            rstd = torch.empty_like(mean)
+            pm, pr = mean.data_ptr() or None, rstd.data_ptr() or None
         if other:
             _run_on(stream, device, x, weight, bias, out, mean, rstd)
-        st = lib().migemm_layer_norm_forward(
-            T, D, dt, x.data_ptr() or None, ldx, wd, pw, pb, float(eps), out.data_ptr() or None,
-            _ld(out), (mean.data_ptr() or None) if stats else None,
-            (rstd.data_ptr() or None) if stats else None, stream)
+        st = lib().migemm_layer_norm_forward(T, D, dt, x.data_ptr() or None, ldx, wd, pw, pb, eps,
+                                             out.data_ptr() or None, ldy, pm, pr, stream)
         if st != OK:
             raise MigemmError(st, "migemm_layer_norm_forward")
     return out, mean, rstd
@@ -1009,7 +1011,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dw=None, db=None,
     dt, ldx, lddy = _dtype_code(x), _ld(x), _ld(dy)
     T, D = x.shape
     kind = x.dtype if weight is None else weight.dtype
-    wd = _second_type("weight", kind, x)
+    wd = dt if kind is x.dtype else _second_type("weight", kind, x)
     pw = _vector("weight", weight, device, kind, D)
     pm = _row_vector("mean", mean, device, torch.float32, T)
     pr = _row_vector("rstd", rstd, device, torch.float32, T)
@@ -1020,10 +1022,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dw=None, db=None,
     with _device_of(device):
         stream, other = _stream_of(stream, device)
         dx = _gradient("dx", need_dx, dx, x)
+        like = weight if weight is not None else x.new_empty(D) if need_db and db is None else None
         if dw is None and need_dw:
-            dw = torch.empty(D, dtype=kind, device=device)
+            dw = torch.empty_like(like)
         if db is None and need_db:
-            db = torch.empty(D, dtype=kind, device=device)
+            db = torch.empty_like(like)
         pdw, pdb = _vector("dw", dw, device, kind, D), _vector("db", db, device, kind, D)
         st, n = migemm_layer_norm_workspace_size(T, D, dw is not None or db is not None)
         if st != OK:
@@ -1061,16 +1064,16 @@ def embedding(w, index, *, scale: float = 1.0, ignore_index: int = -100, out=Non
     with _device_of(device):
         stream, other = _stream_of(stream, device)
         if out is None:
-            out = torch.empty((T, D), dtype=w.dtype, device=device)
+            out, ldy = w.new_empty((T, D)), D
         else:
             _check_device("out", out, device)
             if out.dtype is not w.dtype or out.shape != (T, D):
                 raise ValueError(f"out must be {w.dtype}, {T} x {D}")
+            ldy = _ld(out)
         if other:
             _run_on(stream, device, w, index, out)
         st = lib().migemm_embedding_forward(T, V, D, dt, w.data_ptr() or None, ldw, pi,
-                                            ignore_index, float(scale), out.data_ptr() or None,
-                                            _ld(out), stream)
+                                            ignore_index, scale, out.data_ptr() or None, ldy, stream)
         if st != OK:
             raise MigemmError(st, "migemm_embedding_forward")
     return out
@@ -1113,7 +1116,7 @@ def embedding_backward(dy, index, vocab: int, *, scale: float = 1.0, ignore_inde
             _run_on(stream, device, dy, index, dw, ws)
         st = lib().migemm_embedding_backward(
             T, vocab, D, dt, dy.data_ptr() or None, lddy, pi, ignore_index, float(scale),
-            int(accumulate), wd, dw.data_ptr() or None, _ld(dw), ws.data_ptr() or None, n, stream)
+            bool(accumulate), wd, dw.data_ptr() or None, _ld(dw), ws.data_ptr() or None, n, stream)
         if st != OK:
             raise MigemmError(st, "migemm_embedding_backward")
     return dw
@@ -1185,33 +1188,34 @@ def adamw_(params, grads, states, *, step, lr=1e-3, betas=(0.9, 0.999), eps: flo
         return
     device, pd, gd = params[0].device, params[0].dtype, grads[0].dtype
     _check_device("params", params[0], device)
-    f32, sd = torch.float32, states[0][0].dtype
-    eight = sd is torch.float8_e4m3fn or sd is torch.uint8
-    if not eight and sd is not f32:
+    avgs, sqs, avg_scales, sq_scales, masters = zip(*states)
+    f32, sd = torch.float32, avgs[0].dtype
+    eight, master = sd is not f32, masters[0] is not None
+    if eight and sd is not torch.float8_e4m3fn and sd is not torch.uint8:
         raise ValueError(f"states must be float32, float8_e4m3fn or uint8 (got {sd})")
-    index = params[0].get_device()
-    master = states[0][4] is not None
     if master and pd is f32:
         raise ValueError("float32 parameters take no master copy")
-    pc, gc = _dtype_code(params[0]), _second_type("gradients", gd, params[0])
-    fields = []
-    for p, g, s in zip(params, grads, states):
-        n, (avg, sq, ms, rs, copy) = p.numel(), s
-        held = [(p, pd, n), (g, gd, n), (avg, sd, n), (sq, sd, n)]
-        if eight:
-            held += [(ms, f32, (n + 255) // 256), (rs, f32, (n + 255) // 256)]
-        if master:
-            held.append((copy, f32, n))
-        for t, kind, size in held:
-            if (t is None or t.dtype is not kind or t.numel() != size or t.get_device() != index
-                    or not t.is_contiguous()):
-                raise ValueError(_adamw_refusal(t, kind, size, device))
-        if (copy is not None) != master or (ms is not None) != eight or (rs is not None) != eight:
+    for list_, given in ((avg_scales, eight), (sq_scales, eight), (masters, master)):
+        # (by type: `None in` would compare the tensors by value)
+        none = list(map(type, list_)).count(type(None))
+        if none != (0 if given else count):
             raise ValueError("states must all be of 32 or all of 8 bits, with a master copy in "
                              "all or in none")
-        fields += (n, p.data_ptr(), g.data_ptr(), copy.data_ptr() if master else 0,
-                   avg.data_ptr(), sq.data_ptr(), ms.data_ptr() if eight else 0,
-                   rs.data_ptr() if eight else 0)
+    pcode, gcode = _dtype_code(params[0]), _second_type("gradients", gd, params[0])
+    sizes = list(map(torch.Tensor.numel, params))
+    # the fields of each tensor in turn
+    fields = [0] * (8 * count)
+    fields[0::8] = sizes
+    fields[1::8] = _step_pointers(params, pd, sizes, device)
+    fields[2::8] = _step_pointers(grads, gd, sizes, device)
+    if master:
+        fields[3::8] = _step_pointers(masters, f32, sizes, device)
+    fields[4::8] = _step_pointers(avgs, sd, sizes, device)
+    fields[5::8] = _step_pointers(sqs, sd, sizes, device)
+    if eight:
+        blocks = [(n + 255) // 256 for n in sizes]
+        fields[6::8] = _step_pointers(avg_scales, f32, blocks, device)
+        fields[7::8] = _step_pointers(sq_scales, f32, blocks, device)
     numbers = [t if isinstance(t, torch.Tensor) else None for t in (lr, step, grad_scale)]
     o = AdamwOptions(0.0 if numbers[0] is not None else float(lr), float(betas[0]),
                      float(betas[1]), float(eps), float(weight_decay),
@@ -1228,14 +1232,25 @@ def adamw_(params, grads, states, *, step, lr=1e-3, betas=(0.9, 0.999), eps: flo
             o.grad_scale = _step_tensor("grad_scale", numbers[2], device, f32)
         if other:
             _run_on(stream, device, *params, *grads, *numbers, *(t for s in states for t in s))
-        st = lib().migemm_adamw(count, (ctypes.c_int64 * len(fields))(*fields), pc, gc,
-                                8 if eight else 32, ctypes.byref(o), stream)
+        fields = array.array("q", fields)  # (a ctypes array of them takes three times as long)
+        st = lib().migemm_adamw(count, fields.buffer_info()[0], pcode, gcode, 8 if eight else 32,
+                                ctypes.byref(o), stream)
         if st != OK:
             raise MigemmError(st, "migemm_adamw")
 
 
-def _adamw_refusal(t, kind, size, device):
-    got = "None" if t is None else (f"{t.dtype}, {t.numel()} elements on {t.device}, strides "
-                                    f"{tuple(t.stride())}")
-    return (f"a tensor of the step must be contiguous, {kind}, of {size} elements on {device} "
-            f"(got {got})")
+def _step_pointers(tensors, kind, sizes, device):
+    """Pointers of a step's tensors, checked: one dtype and device, contiguous, of the
+    sizes given.  (map over the methods: a loop that names them took twice as long.)"""
+    torch = _torch
+    T = torch.Tensor
+    if not (set(map(T.dtype.__get__, tensors)) == {kind}
+            and set(map(T.get_device, tensors)) == {device.index}
+            and all(map(T.is_contiguous, tensors)) and list(map(T.numel, tensors)) == sizes):
+        for t, size in zip(tensors, sizes):
+            if (t.dtype is not kind or t.numel() != size or t.device != device
+                    or not t.is_contiguous()):
+                raise ValueError(f"a tensor of the step must be contiguous, {kind}, of {size} "
+                                 f"elements on {device} (got {t.dtype}, {t.numel()} on {t.device}, "
+                                 f"strides {tuple(t.stride())})")
+    return map(T.data_ptr, tensors)

@@ -84,12 +84,12 @@ __device__ __forceinline__ float largest16(float v) {
     return __builtin_elementwise_maximum(v, row_rotated<1>(v));
 }
 
-// The values of 16 codes under a scale.
-__device__ __forceinline__ void decode(const uint8_t (&codes)[16], float scale, float (&v)[16]) {
-    uint32_t w[4];
+// The values of eight codes under a scale.
+__device__ __forceinline__ void decode(const uint8_t (&codes)[8], float scale, float (&v)[8]) {
+    uint32_t w[2];
     __builtin_memcpy(w, codes, sizeof(w));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], false);
         const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], true);
         v[4 * i] = lo[0] * scale;
@@ -99,24 +99,97 @@ __device__ __forceinline__ void decode(const uint8_t (&codes)[16], float scale, 
     }
 }
 
-// The codes of 16 values in units of the scale; the hardware rounds to the nearest, ties
-// to even.
-__device__ __forceinline__ void encode(const float (&x)[16], uint8_t (&codes)[16]) {
-    uint32_t w[4];
+// The codes of eight values in units of the scale; the hardware rounds to the nearest,
+// ties to even.
+__device__ __forceinline__ void encode(const float (&x)[8], uint8_t (&codes)[8]) {
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         int c = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i], x[4 * i + 1], 0, false);
         w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * i + 2], x[4 * i + 3], c, true);
     }
     __builtin_memcpy(codes, w, sizeof(w));
 }
 
+// 16- and 8-byte accesses past the caches, at any alignment; wider pieces do not fill whole
+// lines with one access of a wavefront, and go through them.
+template <typename T, int N> __device__ __forceinline__ void load_once(const T* p, T (&e)[N]) {
+    typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(1)));
+    typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(1)));
+    if constexpr (sizeof(e) == 16) {
+        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const v4*>(p));
+        __builtin_memcpy(e, &w, sizeof(e));
+    } else if constexpr (sizeof(e) == 8) {
+        const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const v2*>(p));
+        __builtin_memcpy(e, &w, sizeof(e));
+    } else {
+        load_whole(p, e);
+    }
+}
+template <typename T, int N> __device__ __forceinline__ void store_once(T* p, const T (&e)[N]) {
+    typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(1)));
+    typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(1)));
+    if constexpr (sizeof(e) == 16) {
+        u32x4 w;
+        __builtin_memcpy(&w, e, sizeof(e));
+        __builtin_nontemporal_store(w, reinterpret_cast<v4*>(p));
+    } else if constexpr (sizeof(e) == 8) {
+        u32x2 w;
+        __builtin_memcpy(&w, e, sizeof(e));
+        __builtin_nontemporal_store(w, reinterpret_cast<v2*>(p));
+    } else {
+        store_whole(p, e);
+    }
+}
+
+// How a lane's E elements lie in a tensor: all of them in it (WHOLE); in a tensor's last
+// piece, E elements before its end, of which those past `skip` are the lane's (LAST, no
+// branch around the loads: element by element they took 9 us); or, in a tensor of fewer
+// than E, the `held` first (SHORT).  ONCE is WHOLE with accesses past the caches.
+enum class Lie { WHOLE, ONCE, LAST, SHORT };
+template <Lie L, int E> struct Piece {
+    int64_t at;
+    int skip, held;
+    __device__ __forceinline__ Piece(int64_t i, int64_t count) : at(i), skip(0), held(E) {
+        if constexpr (L == Lie::LAST) {
+            const Span<E> s(i, count);
+            at = s.at;
+            skip = s.skip;
+        }
+        if constexpr (L == Lie::SHORT) {
+            held = i < count ? static_cast<int>(count - i) : 0;
+            at = i < count ? i : 0;
+        }
+    }
+    __device__ __forceinline__ bool own(int e) const { return e >= skip && e < held; }
+    template <typename T> __device__ __forceinline__ void load(const T* p, T (&e)[E]) const {
+        if constexpr (L == Lie::SHORT)
+            load_part(p + at, held, e);
+        else if constexpr (L == Lie::ONCE)
+            load_once(p + at, e);
+        else
+            load_whole(p + at, e);
+    }
+    template <typename T> __device__ __forceinline__ void store(T* p, const T (&e)[E]) const {
+        if constexpr (L == Lie::WHOLE) {
+            store_whole(p + at, e);
+        } else if constexpr (L == Lie::ONCE) {
+            store_once(p + at, e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (own(i)) p[at + i] = e[i];
+        }
+    }
+};
+
 // 32-bit states: four elements a lane at a time, so that every access of a wavefront is
 // contiguous.
-template <typename P, typename G, bool MASTER>
+constexpr int kEach32 = 4;
+template <typename P, typename G, bool MASTER, Lie L>
 __device__ __forceinline__ void step32(const AdamNumbers& n, const migemm_adamw_tensor& t,
                                        int64_t at, float scale) {
-    constexpr int E = 4, U = kPiece / (kThreads * E);
+    constexpr int E = kEach32, U = kPiece / (kThreads * E);
     P* const param = static_cast<P*>(t.param);
     const G* const grad = static_cast<const G*>(t.grad);
     float *const avg = static_cast<float*>(t.avg), *const sq = static_cast<float*>(t.sq);
@@ -125,18 +198,18 @@ __device__ __forceinline__ void step32(const AdamNumbers& n, const migemm_adamw_
     P narrow_p[U][E];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t i = at + (u * kThreads + threadIdx.x) * E, held = t.count - i;
-        load_part(grad + i, held, g[u]);
-        load_part(avg + i, held, m[u]);
-        load_part(sq + i, held, v[u]);
+        const Piece<L, E> piece(at + (u * kThreads + threadIdx.x) * E, t.count);
+        piece.load(grad, g[u]);
+        piece.load(avg, m[u]);
+        piece.load(sq, v[u]);
         if constexpr (MASTER)
-            load_part(t.master + i, held, p[u]);
+            piece.load(t.master, p[u]);
         else
-            load_part(param + i, held, narrow_p[u]);
+            piece.load(param, narrow_p[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t i = at + (u * kThreads + threadIdx.x) * E, held = t.count - i;
+        const Piece<L, E> piece(at + (u * kThreads + threadIdx.x) * E, t.count);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if constexpr (!MASTER) p[u][e] = to_f32(narrow_p[u][e]);
@@ -144,71 +217,89 @@ __device__ __forceinline__ void step32(const AdamNumbers& n, const migemm_adamw_
             p[u][e] = stepped(n, p[u][e], m[u][e], sqrtf(v[u][e]));
             narrow_p[u][e] = narrow<P>(p[u][e]);
         }
-        store_part(avg + i, held, m[u]);
-        store_part(sq + i, held, v[u]);
-        if constexpr (MASTER) store_part(t.master + i, held, p[u]);
-        store_part(param + i, held, narrow_p[u]);
+        piece.store(avg, m[u]);
+        piece.store(sq, v[u]);
+        if constexpr (MASTER) piece.store(t.master, p[u]);
+        piece.store(param, narrow_p[u]);
     }
 }
 
-// 8-bit states: 16 elements a lane, so that the 16 lanes of a DPP row hold one block.
-template <typename P, typename G, bool MASTER>
+// 8-bit states: the 16 lanes of a DPP row hold one block, as two halves of eight elements
+// a lane, so that every access to 16-bit elements and to codes covers whole lines.
+constexpr int kEach8 = 8;
+template <typename P, typename G, bool MASTER, Lie L>
 __device__ __forceinline__ void step8(const AdamNumbers& n, const migemm_adamw_tensor& t,
                                       int64_t at, float scale) {
-    constexpr int E = 16;
-    static_assert(kThreads * E == kPiece && E * 16 == kBlock, "one block to a DPP row");
-    const int64_t i = at + threadIdx.x * E, held = t.count - i, block = i / kBlock;
-    P* const param = static_cast<P*>(t.param) + i;
-    uint8_t *const avg = static_cast<uint8_t*>(t.avg) + i, *const sq = static_cast<uint8_t*>(t.sq) + i;
-    const bool any = t.count > block * kBlock;
-    G g[E];
-    P narrow_p[E];
-    float p[E], m[E], r[E];
-    uint8_t cm[E], cr[E];
-    load_part(static_cast<const G*>(t.grad) + i, held, g);
-    load_part(avg, held, cm);
-    load_part(sq, held, cr);
-    if constexpr (MASTER)
-        load_part(t.master + i, held, p);
-    else
-        load_part(param, held, narrow_p);
-    const float sm = any ? t.avg_scales[block] : 0.0f, sr = any ? t.sq_scales[block] : 0.0f;
-    decode(cm, sm, m);
-    decode(cr, sr, r);
+    constexpr int E = kEach8, H = 2;
+    static_assert(kThreads * E * H == kPiece && E * H * 16 == kBlock, "one block to a DPP row");
+    constexpr bool whole = L == Lie::WHOLE || L == Lie::ONCE;
+    const int64_t start = at + threadIdx.x / 16 * kBlock;  // of the lane's block
+    const bool any = whole || t.count > start;
+    const int64_t block = any ? start / kBlock : 0, i = start + threadIdx.x % 16 * E;
+    P* const param = static_cast<P*>(t.param);
+    const G* const grad = static_cast<const G*>(t.grad);
+    uint8_t *const avg = static_cast<uint8_t*>(t.avg), *const sq = static_cast<uint8_t*>(t.sq);
+    const Piece<L, E> piece[H] = {{i, t.count}, {i + kBlock / H, t.count}};
+    G g[H][E];
+    P narrow_p[H][E];
+    float p[H][E], m[H][E], r[H][E];
+    uint8_t cm[H][E], cr[H][E];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        piece[h].load(grad, g[h]);
+        piece[h].load(avg, cm[h]);
+        piece[h].load(sq, cr[h]);
+        if constexpr (MASTER)
+            piece[h].load(t.master, p[h]);
+        else
+            piece[h].load(param, narrow_p[h]);
+    }
+    const float sm = t.avg_scales[block], sr = t.sq_scales[block];
     float lm = 0.0f, lr = 0.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        if constexpr (!MASTER) p[e] = to_f32(narrow_p[e]);
-        float v = r[e] * r[e];
-        moments(n, to_f32(g[e]) * scale, m[e], v);
-        r[e] = sqrtf(v);
-        p[e] = stepped(n, p[e], m[e], r[e]);
-        narrow_p[e] = narrow<P>(p[e]);
-        lm = largest_of(lm, m[e]);
-        lr = largest_of(lr, r[e]);
+    for (int h = 0; h < H; ++h) {
+        // (elements that are not the lane's may belong to another block: they are dropped)
+        decode(cm[h], sm, m[h]);
+        decode(cr[h], sr, r[h]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if constexpr (!MASTER) p[h][e] = to_f32(narrow_p[h][e]);
+            float v = r[h][e] * r[h][e];
+            moments(n, to_f32(g[h][e]) * scale, m[h][e], v);
+            r[h][e] = sqrtf(v);
+            p[h][e] = stepped(n, p[h][e], m[h][e], r[h][e]);
+            narrow_p[h][e] = narrow<P>(p[h][e]);
+            if (whole || piece[h].own(e)) {
+                lm = largest_of(lm, m[h][e]);
+                lr = largest_of(lr, r[h][e]);
+            }
+        }
+        if constexpr (MASTER) piece[h].store(t.master, p[h]);
+        piece[h].store(param, narrow_p[h]);
     }
-    if constexpr (MASTER) store_part(t.master + i, held, p);
-    store_part(param, held, narrow_p);
     const float nm = block_scale(largest16(lm)), nr = block_scale(largest16(lr));
     const float im = nm > 0.0f ? 1.0f / nm : 0.0f, ir = nr > 0.0f ? 1.0f / nr : 0.0f;
     const float least = nr > 0.0f ? 0x1p-9f : 0.0f;  // E4M3's smallest
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        m[e] *= im;
-        const float x = r[e] * ir;
-        r[e] = r[e] > 0.0f ? fmaxf(x, least) : x;
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            m[h][e] *= im;
+            const float x = r[h][e] * ir;
+            r[h][e] = r[h][e] > 0.0f ? fmaxf(x, least) : x;
+        }
+        encode(m[h], cm[h]);
+        encode(r[h], cr[h]);
+        piece[h].store(avg, cm[h]);
+        piece[h].store(sq, cr[h]);
     }
-    encode(m, cm);
-    encode(r, cr);
-    store_part(avg, held, cm);
-    store_part(sq, held, cr);
     if (any && threadIdx.x % 16 == 0) {
         t.avg_scales[block] = nm;
         t.sq_scales[block] = nr;
     }
 }
 
-template <typename P, typename G, bool EIGHT, bool MASTER>
+template <typename P, typename G, bool EIGHT, bool MASTER, bool ONCE>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(Table a) {
     float scale = 1.0f;
     if (a.grad_scale) {
@@ -239,22 +330,40 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Table a) {
     }
     const migemm_adamw_tensor& t = a.t[lo];
     const int64_t at = static_cast<int64_t>(blockIdx.x - a.first[lo]) * kPiece;
-    if constexpr (EIGHT)
-        step8<P, G, MASTER>(n, t, at, scale);
+    auto run = [&](auto lie) __attribute__((always_inline)) {
+        constexpr Lie L = decltype(lie)::value;
+        if constexpr (EIGHT)
+            step8<P, G, MASTER, L>(n, t, at, scale);
+        else
+            step32<P, G, MASTER, L>(n, t, at, scale);
+    };
+    if (at + kPiece <= t.count)
+        run(std::integral_constant<Lie, ONCE ? Lie::ONCE : Lie::WHOLE>{});
+    else if (t.count >= (EIGHT ? kEach8 : kEach32))
+        run(std::integral_constant<Lie, Lie::LAST>{});
     else
-        step32<P, G, MASTER>(n, t, at, scale);
+        run(std::integral_constant<Lie, Lie::SHORT>{});
 }
 
 using Kernel = void (*)(Table);
 
-template <typename P, typename G> Kernel kernel_of(bool eight, bool master) {
-    if constexpr (std::is_same<P, float>::value) {
-        return eight ? adamw_kernel<P, G, true, false> : adamw_kernel<P, G, false, false>;
-    } else {
-        if (eight) return master ? adamw_kernel<P, G, true, true> : adamw_kernel<P, G, true, false>;
-        return master ? adamw_kernel<P, G, false, true> : adamw_kernel<P, G, false, false>;
+template <typename P, typename G, bool ONCE> Kernel kernel_of(bool eight, bool master) {
+    if constexpr (!std::is_same<P, float>::value) {
+        if (master)
+            return eight ? adamw_kernel<P, G, true, true, ONCE>
+                         : adamw_kernel<P, G, false, true, ONCE>;
     }
+    return eight ? adamw_kernel<P, G, true, false, ONCE> : adamw_kernel<P, G, false, false, ONCE>;
 }
+template <typename P, typename G> Kernel kernel_of(const AdamArgs& a, bool once) {
+    return once ? kernel_of<P, G, true>(a.eight, a.master) : kernel_of<P, G, false>(a.eight, a.master);
+}
+
+// Past this many bytes a step's tensors go past the caches: the last-level one (256 MiB)
+// holds too little of them for the next reader.  738 million BF16 elements with 8-bit
+// states (7.4 GB) 1240 us, 1425 through the caches; 133 million with FP32 states and master
+// copies (3.7 GB) 675 and 708; 40 million with 8-bit states (0.4 GB) 69 and 64.
+constexpr int64_t kOnceBytes = int64_t(512) << 20;
 
 float* moved(float* p, int64_t elements) { return p ? p + elements : p; }
 void* moved(void* p, int64_t bytes) { return static_cast<char*>(p) + bytes; }
@@ -262,16 +371,21 @@ void* moved(void* p, int64_t bytes) { return static_cast<char*>(p) + bytes; }
 }  // namespace
 
 hipError_t launch_adamw(const AdamArgs& a) {
+    const int pb = elem_size(a.param_dtype), gb = elem_size(a.grad_dtype), sb = a.eight ? 1 : 4;
+    double bytes = 0.0;
+    for (int64_t k = 0; k < a.tensors; ++k)
+        bytes += static_cast<double>(a.list[k].count) * (2 * pb + gb + 4 * sb + (a.master ? 8 : 0));
+    const bool once = bytes > static_cast<double>(kOnceBytes);
     Kernel fn;
     switch (a.param_dtype) {
-        case 0: fn = kernel_of<float, float>(a.eight, a.master); break;
+        case 0: fn = kernel_of<float, float>(a, once); break;
         case 1:
-            fn = a.grad_dtype == 0 ? kernel_of<_Float16, float>(a.eight, a.master)
-                                   : kernel_of<_Float16, _Float16>(a.eight, a.master);
+            fn = a.grad_dtype == 0 ? kernel_of<_Float16, float>(a, once)
+                                   : kernel_of<_Float16, _Float16>(a, once);
             break;
         default:
-            fn = a.grad_dtype == 0 ? kernel_of<bf16_t, float>(a.eight, a.master)
-                                   : kernel_of<bf16_t, bf16_t>(a.eight, a.master);
+            fn = a.grad_dtype == 0 ? kernel_of<bf16_t, float>(a, once)
+                                   : kernel_of<bf16_t, bf16_t>(a, once);
     }
     const migemm_adamw_options& o = a.o;
     Table t{};
@@ -289,7 +403,6 @@ hipError_t launch_adamw(const AdamArgs& a) {
     t.lr_device = o.lr_device;
     t.step_device = o.step_device;
     t.grad_scale = o.grad_scale;
-    const int pb = elem_size(a.param_dtype), gb = elem_size(a.grad_dtype), sb = a.eight ? 1 : 4;
     int64_t pieces = 0;
     auto flush = [&]() {
         if (pieces == 0) return hipSuccess;

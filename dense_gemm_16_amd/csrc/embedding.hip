@@ -24,46 +24,35 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------- forwards
 
-// `lpr` lanes (a power of two) take a segment of kUnroll chunks a lane of one row; the
-// loads of all of them are in flight together.
+// `lpr` lanes (a power of two) take a segment of `unroll` chunks a lane of one row, all of
+// whose loads are in flight together.
 constexpr int kUnroll = 4;
-template <typename T>
+constexpr int64_t kFewChunks = 65536;
+template <typename T, int C, int U>
 __global__ __launch_bounds__(kThreads) void gather_kernel(
-    int64_t T_, int64_t V, int64_t D, const T* __restrict__ W, int64_t ldw,
+    int64_t tokens, int64_t V, int64_t D, const T* __restrict__ W, int64_t ldw,
     const int64_t* __restrict__ index, int64_t ignore, float scale, T* __restrict__ Y,
-    int64_t ldy, int lpr, int64_t segs, int64_t groups) {
-    constexpr int C = kChunk<T>;
+    int64_t ldy, int lpr, int64_t segs) {
     const int rows = kThreads / lpr, lane = threadIdx.x % lpr;
-    for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
-        const int64_t t = g / segs * rows + threadIdx.x / lpr;
-        if (t >= T_) continue;
-        const int64_t k0 = (g % segs * kUnroll * lpr + lane) * C, v = index[t];
-        T* const to = Y + t * ldy;
-        if (v != ignore && v >= 0 && v < V) {
-            const T* const from = W + v * ldw;
-            T e[kUnroll][C];
+    const int64_t k0 = (blockIdx.x % segs * U * lpr + lane) * C;
+    for (int64_t t = blockIdx.x / segs * rows + threadIdx.x / lpr; t < tokens;
+         t += gridDim.x / segs * rows) {
+        const int64_t v = index[t];
+        const bool inside = v != ignore && v >= 0 && v < V;
+        const T* const from = W + (inside ? v : 0) * ldw;  // (row 0 is read, and dropped)
+        T e[U][C];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t k = k0 + static_cast<int64_t>(u) * lpr * C;
-                load_part(from + k, D - k, e[u]);
+        for (int u = 0; u < U; ++u)
+            Span<C>(k0 + static_cast<int64_t>(u) * lpr * C, D).load(from, e[u]);
+        const T fill = narrow<T>(v == ignore ? 0.0f : __builtin_nanf(""));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const T o = narrow<T>(scale * to_f32(e[u][i]));
+                e[u][i] = inside ? o : fill;
             }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t k = k0 + static_cast<int64_t>(u) * lpr * C;
-#pragma unroll
-                for (int i = 0; i < C; ++i) e[u][i] = narrow<T>(scale * to_f32(e[u][i]));
-                store_part(to + k, D - k, e[u]);
-            }
-        } else {
-            T e[C];
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                e[i] = narrow<T>(v == ignore ? 0.0f : __builtin_nanf(""));
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t k = k0 + static_cast<int64_t>(u) * lpr * C;
-                store_part(to + k, D - k, e);
-            }
+            Span<C>(k0 + static_cast<int64_t>(u) * lpr * C, D).store(Y + t * ldy, e[u]);
         }
     }
 }
@@ -74,7 +63,7 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(
 // Tokens without an entry (ignored, or outside the table) sort last, as entry V.
 constexpr int kDigit = 9, kBins = 1 << kDigit;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
-constexpr int kTile = 4096;            // pairs of a workgroup where several share a pass
+constexpr int kTile = 1024;            // pairs of a workgroup
 constexpr int kTileEach = kTile / kSortThreads;
 
 __device__ __forceinline__ uint32_t entry_of(const int64_t* index, int64_t t, int64_t ignore,
@@ -110,102 +99,54 @@ __device__ __forceinline__ uint32_t rank_of(uint32_t digit, bool held, N* count)
     return before + static_cast<uint32_t>(__popcll(below));
 }
 
-// Exclusive sums, in place, over count[wave][digit] in the order digit by digit, wavefront
-// by wavefront within a digit.
-__device__ __forceinline__ void scan_counts(uint16_t (&count)[kSortWaves][kBins],
-                                            uint32_t* wave_sum) {
-    // work-item i < kBins owns digit i
-    const int i = threadIdx.x;
-    uint32_t mine = 0;
-    if (i < kBins) {
-#pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) {
-            const uint32_t c = count[w][i];
-            count[w][i] = static_cast<uint16_t>(mine);
-            mine += c;
-        }
-    }
-    uint32_t up = mine;
-    const int lane = i % kWave;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const uint32_t o = __shfl_up(up, d);
-        if (lane >= d) up += o;
-    }
-    if (lane == kWave - 1) wave_sum[i / kWave] = up;
-    __syncthreads();
-    if (i < kBins) {
-        uint32_t before = up - mine;
-        for (int w = 0; w < i / kWave; ++w) before += wave_sum[w];
-#pragma unroll
-        for (int w = 0; w < kSortWaves; ++w)
-            count[w][i] = static_cast<uint16_t>(count[w][i] + before);
-    }
-    __syncthreads();
-}
-
-// Up to kSortOne pairs by one workgroup, in LDS: a pair is its token and what is left of
-// its entry after the digits sorted so far.  The first digit comes straight from the
-// index, so 16 bits of token and 32 - 16 further bits of entry make up a word: V below 2^25.
-constexpr int kOneEach = 32, kSortOne = kOneEach * kSortThreads;
-__global__ __launch_bounds__(kSortThreads) void sort_one_kernel(
-    int T_, int64_t V, const int64_t* __restrict__ index, int64_t ignore, int passes,
+// Up to kRankMost pairs: each workgroup finds the places of kRankKeys of them by counting
+// those that come before, all against all: 32 slices of the list, a work-item to a slice
+// and a pair.  T^2 comparisons, but one short launch over many CUs (1003 pairs XX us against
+// XX by the radix sort below, 4096 XX against XX).
+constexpr int kRankMost = 8192, kRankKeys = 32, kRankSlices = kSortThreads / kRankKeys;
+__global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(
+    int T_, int64_t V, const int64_t* __restrict__ index, int64_t ignore,
     uint32_t* __restrict__ keys, uint32_t* __restrict__ tokens) {
-    __shared__ uint32_t held[kSortOne];
-    __shared__ uint16_t count[kSortWaves][kBins];  // (32-bit ones would not fit beside `held`)
-    __shared__ uint32_t wave_sum[kSortWaves];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
-    // a wavefront owns `each` consecutive groups of 64 pairs
-    const int each = (T_ + kSortThreads - 1) / kSortThreads;
-    const int first = wave * each * kWave + lane;
-    for (int pass = 0; pass < passes; ++pass) {
-        for (int i = threadIdx.x; i < kSortWaves * kBins; i += kSortThreads)
-            (&count[0][0])[i] = 0;
-        __syncthreads();
-        uint32_t word[kOneEach];
-        uint32_t rank[kOneEach];  // the digit above 16 bits of rank
+    __shared__ __attribute__((aligned(16))) uint32_t all[kRankMost];
+    __shared__ uint32_t place[kRankKeys];
+    // whole slices of 16-byte reads; what is past the list comes after everything
+    const int slice = (T_ + 4 * kRankSlices - 1) / (4 * kRankSlices) * 4;
+    for (int i = threadIdx.x; i < slice * kRankSlices; i += kSortThreads)
+        all[i] = i < T_ ? entry_of(index, i, ignore, V) : 0xffffffffu;
+    if (threadIdx.x < kRankKeys) place[threadIdx.x] = 0;
+    __syncthreads();
+    const int mine = threadIdx.x % kRankKeys, s = threadIdx.x / kRankKeys;
+    const int begin = blockIdx.x * kRankKeys, end = begin + kRankKeys;
+    const int at = begin + mine;
+    const uint32_t key = at < T_ ? all[at] : 0;
+    uint32_t before = 0;
+    // those of [from, to) below a bound; both are multiples of 4
+    auto count = [&](int from, int to, uint32_t bound) {
+        for (int j = from; j < to; j += 4) {
+            const u32x4 k = *reinterpret_cast<const u32x4*>(&all[j]);
 #pragma unroll
-        for (int i = 0; i < kOneEach; ++i) {
-            const int at = first + i * kWave;
-            if (i >= each) break;
-            const bool in = at < T_;
-            uint32_t digit = 0;
-            word[i] = 0;
-            if (in) {
-                if (pass == 0) {
-                    const uint32_t e = entry_of(index, at, ignore, V);
-                    digit = e & (kBins - 1);
-                    word[i] = (e >> kDigit) << 16 | static_cast<uint32_t>(at);
-                } else {
-                    const uint32_t w = held[at];
-                    digit = (w >> 16) & (kBins - 1);
-                    word[i] = (w >> 16 >> kDigit) << 16 | (w & 0xffffu);
-                }
-            }
-            rank[i] = digit << 16 | rank_of(digit, in, count[wave]);
+            for (int e = 0; e < 4; ++e) before += k[e] < bound;
         }
-        __syncthreads();
-        scan_counts(count, wave_sum);
-#pragma unroll
-        for (int i = 0; i < kOneEach; ++i) {
-            const int at = first + i * kWave;
-            if (i >= each) break;
-            if (at >= T_) continue;
-            const uint32_t to = count[wave][rank[i] >> 16] + (rank[i] & 0xffffu);
-            if (pass + 1 < passes) {
-                held[to] = word[i];
-            } else {
-                const uint32_t t = word[i] & 0xffffu;
-                tokens[to] = t;
-                keys[to] = entry_of(index, t, ignore, V);
-            }
-        }
-        __syncthreads();
+    };
+    const int lo = s * slice, hi = lo + slice;
+    count(lo, hi < begin ? hi : begin, key + 1);  // earlier tokens of the same entry come first
+    count(lo > end ? lo : end, hi, key);
+    if (s == 0) {
+        for (int j = begin; j < end && j < T_; ++j) before += all[j] < key + (j < at);
+    }
+    atomicAdd(&place[mine], before);  // (a count: its order does not matter)
+    __syncthreads();
+    if (threadIdx.x < kRankKeys && at < T_) {
+        keys[place[mine]] = key;
+        tokens[place[mine]] = static_cast<uint32_t>(at);
     }
 }
 
 // More pairs: each pass counts the digits of every tile, sums the counts over digits and
-// tiles, and moves the pairs.  The first pass reads the index.
+// tiles, and moves the pairs.  The first pass reads the index.  Up to kFewTiles tiles, the
+// workgroups that move the pairs sum all counts themselves, which saves a launch; the
+// counts then lie tile by tile, otherwise digit by digit.
+constexpr int64_t kFewTiles = 64;
 struct Pairs {
     const int64_t* index;  // the first pass's source, NULL afterwards
     int64_t ignore, V;
@@ -221,6 +162,7 @@ struct Pairs {
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(int64_t T_, Pairs from,
                                                                   int shift, int64_t tiles,
                                                                   uint32_t* __restrict__ counts) {
+    const bool few = tiles <= kFewTiles;
     __shared__ uint32_t bins[kBins];
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         if (threadIdx.x < kBins) bins[threadIdx.x] = 0;
@@ -232,7 +174,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(int64_t T_, Pa
             if (at < T_) atomicAdd(&bins[(from.key(at) >> shift) & (kBins - 1)], 1u);
         }
         __syncthreads();
-        if (threadIdx.x < kBins) counts[threadIdx.x * tiles + tile] = bins[threadIdx.x];
+        if (threadIdx.x < kBins)
+            counts[few ? tile * kBins + threadIdx.x : threadIdx.x * tiles + tile] = bins[threadIdx.x];
         __syncthreads();
     }
 }
@@ -278,7 +221,44 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(
     int64_t T_, Pairs from, int shift, int64_t tiles, const uint32_t* __restrict__ offsets,
     uint32_t* __restrict__ keys, uint32_t* __restrict__ tokens) {
     __shared__ uint32_t count[kSortWaves][kBins];
+    __shared__ uint32_t early[2][kBins], wave_sum[kSortWaves];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const bool few = tiles <= kFewTiles;  // (then a workgroup has one tile)
+    uint32_t place = 0;                   // of the tile's first pair of digit threadIdx.x
+    if (few) {
+        // each digit's pairs in the tiles before this one, and in all; even tiles by one half
+        // of the workgroup, odd ones by the other
+        const int digit = threadIdx.x % kBins, half = threadIdx.x / kBins;
+        uint32_t before = 0, all = 0;
+#pragma unroll 8
+        for (int t = half; t < static_cast<int>(tiles); t += 2) {
+            const uint32_t c = offsets[t * kBins + digit];
+            all += c;
+            before += t < static_cast<int>(blockIdx.x) ? c : 0;
+        }
+        if (half) {
+            early[0][digit] = before;
+            early[1][digit] = all;
+        }
+        __syncthreads();
+        uint32_t up = 0;
+        if (!half) {
+            before += early[0][digit];
+            all += early[1][digit];
+            up = all;
+        }
+#pragma unroll
+        for (int d = 1; d < kWave; d <<= 1) {
+            const uint32_t o = __shfl_up(up, d);
+            if (lane >= d) up += o;
+        }
+        if (lane == kWave - 1) wave_sum[wave] = up;
+        __syncthreads();
+        if (!half) {
+            place = up - all + before;
+            for (int w = 0; w < wave; ++w) place += wave_sum[w];
+        }
+    }
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         for (int i = threadIdx.x; i < kSortWaves * kBins; i += kSortThreads)
             (&count[0][0])[i] = 0;
@@ -294,7 +274,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(
         __syncthreads();
         // each digit's place in the whole list, then wavefront by wavefront
         if (threadIdx.x < kBins) {
-            uint32_t at = offsets[threadIdx.x * tiles + tile];
+            uint32_t at = few ? place : offsets[threadIdx.x * tiles + tile];
 #pragma unroll
             for (int w = 0; w < kSortWaves; ++w) {
                 const uint32_t c = count[w][threadIdx.x];
@@ -322,177 +302,231 @@ struct GradArgs {
     const uint32_t *keys, *tokens;  // sorted
     int64_t ldy, ldw;
     float scale;
-    bool accumulate;
-    int stretch;        // pairs of a stretch
+    int stretch;  // pairs of a stretch
     int64_t stretches, pitch;
     float* shared_rows;  // two rows of `pitch` a stretch: of an entry begun before it, of
                          // one that goes on after it
     int lpr;             // lanes of a segment of a row, a power of two up to 64
-    int64_t segs;        // segments of a row: 16 bytes of dy a lane each
-    int64_t zero_groups; // workgroups that zero rows
+    int64_t segs;        // segments of a row: a chunk of dy a lane each
+    int64_t sum_groups;  // workgroups that add; those after them zero rows
 };
 
-// Adds scale times a sum to, or puts it into, a piece of dw.
-template <typename W, int C>
-__device__ __forceinline__ void put(W* to, int64_t held, const float (&sum)[C], float scale,
-                                    bool accumulate) {
-    W e[C];
-    if (accumulate) {
-        load_part(to, held, e);
-#pragma unroll
-        for (int i = 0; i < C; ++i) e[i] = narrow<W>(fmaf(scale, sum[i], to_f32(e[i])));
-    } else {
-#pragma unroll
-        for (int i = 0; i < C; ++i) e[i] = narrow<W>(scale * sum[i]);
+// The first pair of an entry of v or more, by a whole wavefront: 64 places at a time, so
+// three loads one after the other for 2^18 pairs.
+__device__ __forceinline__ int64_t first_of(const GradArgs& a, int64_t v) {
+    const int lane = threadIdx.x % kWave;
+    int64_t lo = 0, n = a.T;
+    while (n > 0) {
+        const int64_t step = ceil_div(n, kWave), at = lo + (lane + 1) * step - 1, end = lo + n;
+        lo += step * __popcll(__ballot(at < end && a.keys[at < end ? at : lo] < v));
+        n = lo < end ? (end - lo < step - 1 ? end - lo : step - 1) : 0;
     }
-    store_part(to, held, e);
+    return lo < a.T ? lo : a.T;
 }
 
 // Zeros the rows of entries v0 .. v0 + kZeroRows - 1 that no token names, by one
-// wavefront: its lanes look for one entry each in the sorted list.
+// wavefront.
 constexpr int kZeroRows = 16;
-template <typename W>
+template <typename W, int C>
 __device__ __forceinline__ void zero_rows(const GradArgs& a, int64_t v0, W* __restrict__ dW) {
     const int lane = threadIdx.x % kWave;
-    const int64_t v = v0 + lane;
-    bool absent = false;
-    if (lane < kZeroRows && v < a.V) {
-        int64_t lo = 0, hi = a.T;
-        while (lo < hi) {
-            const int64_t mid = (lo + hi) / 2;
-            if (a.keys[mid] < v)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        absent = lo == a.T || a.keys[lo] != v;
+    const int64_t v1 = v0 + kZeroRows < a.V ? v0 + kZeroRows : a.V;
+    uint64_t absent = (uint64_t(1) << (v1 - v0)) - 1;
+    for (int64_t v = v0; v < v1;) {
+        // 64 pairs from the first of an entry not seen yet
+        const int64_t at = first_of(a, v) + lane;
+        const int64_t key = at < a.T ? a.keys[at] : a.V;
+#pragma unroll
+        for (int i = 0; i < kZeroRows; ++i)
+            if (__ballot(key == v0 + i)) absent &= ~(uint64_t(1) << i);
+        v = __builtin_amdgcn_readlane(static_cast<uint32_t>(key), kWave - 1) + int64_t(1);
     }
-    constexpr int C = kChunk<W>;
     W zero[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) zero[i] = narrow<W>(0.0f);
-    for (uint64_t todo = __ballot(absent); todo; todo &= todo - 1) {
+    for (uint64_t todo = absent; todo; todo &= todo - 1) {
         W* const row = dW + (v0 + __builtin_ctzll(todo)) * a.ldw;
-        for (int64_t k = lane * C; k < a.D; k += kWave * C) store_part(row + k, a.D - k, zero);
+        for (int64_t k = lane * C; k < a.D; k += kWave * C) Span<C>(k, a.D).store(row, zero);
     }
 }
 
-constexpr int kAhead = 8;  // rows of dy in flight
-template <typename T, typename W>
+// A group of a.lpr lanes sums a segment of columns over one stretch.  An entry that begins
+// in it and ends in the next one is finished here, and left out there: where every other
+// stretch ended inside an entry, the sums left to join took 37 us beside 90 (32768 tokens
+// of 4096 columns).  The group's lanes load the entries and tokens of as many pairs at
+// once; then kAhead rows of dy are in flight together, and, where the gradient is added
+// (ADD), the rows of dw whose entries end among them.  WAVE: the group is a wavefront
+// (pairs come by readlane, and branches are uniform).
+constexpr int kAhead = 8;
+template <typename T, typename W, int C, bool WAVE, bool ADD>
 __global__ __launch_bounds__(kThreads) void scatter_kernel(GradArgs a, const T* __restrict__ dY,
                                                            W* __restrict__ dW) {
-    constexpr int C = kChunk<T>;
-    if (blockIdx.x < a.zero_groups) {
-        const int64_t v0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / kWave) +
+    if (blockIdx.x >= a.sum_groups) {
+        const int64_t v0 = (static_cast<int64_t>(blockIdx.x - a.sum_groups) * (kThreads / kWave) +
                             threadIdx.x / kWave) * kZeroRows;
-        if (v0 < a.V) zero_rows(a, v0, dW);
+        if (v0 < a.V) zero_rows<W, C>(a, v0, dW);
         return;
     }
-    const int64_t group = (blockIdx.x - a.zero_groups) * (kThreads / a.lpr) + threadIdx.x / a.lpr;
+    const int lpr = WAVE ? kWave : a.lpr;
+    const int64_t group = static_cast<int64_t>(blockIdx.x) * (kThreads / lpr) + threadIdx.x / lpr;
     const int64_t s = group / a.segs;
     if (s >= a.stretches) return;
-    const int64_t k = (group % a.segs * a.lpr + threadIdx.x % a.lpr) * C;
-    if (k >= a.D) return;
-    const int64_t first = s * a.stretch;
+    const int lane = threadIdx.x % lpr;
+    const Span<C> piece((group % a.segs * lpr + lane) * C, a.D);
+    int64_t first = s * a.stretch;
     const int64_t end = first + a.stretch < a.T ? first + a.stretch : a.T;
     const uint32_t none = static_cast<uint32_t>(a.V);
-    // the entry that the stretch before ends with: its sum is begun there
-    const uint32_t before = first > 0 ? a.keys[first - 1] : none;
-    const uint32_t after = end < a.T ? a.keys[end] : none;
+    // the entry at i, or one past all of them where the list has ended or not begun
+    auto entry = [&](int64_t i) { return i >= 0 && i < a.T ? a.keys[i] : none + 1; };
+    const uint32_t before = entry(first - 1), head = entry(first), tail = entry(end - 1);
+    const uint32_t after = entry(end), earlier = entry(first - a.stretch - 1);
+    const uint32_t later = entry(end + a.stretch);
+    // pairs of [from, from + stretch) that go on with entry v
+    auto run = [&](int64_t from, uint32_t v) {
+        const int shift = static_cast<int>(threadIdx.x) % kWave / lpr * lpr;
+        int64_t n = 0;
+        while (n < a.stretch) {
+            const uint64_t same = __ballot(n + lane < a.stretch && entry(from + n + lane) == v);
+            const uint64_t mine = same >> shift & (~uint64_t(0) >> (kWave - lpr));
+            n += __popcll(mine);
+            if (__popcll(mine) < lpr) break;
+        }
+        return n;
+    };
+    // whether the sum of its first entry is begun in a stretch before
+    bool begun = before == head && head != none;
+    if (begun && earlier != head && after != head) {  // begun in the last one and ended here
+        first += run(first, head);
+        begun = false;
+    }
+    int64_t stop = end;
+    if (tail != none && after == tail && before != tail && later != tail) stop += run(end, tail);
     float sum[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) sum[i] = 0.0f;
-    uint32_t now = a.keys[first];
-    bool begun = now == before;
-    auto finish = [&](uint32_t v, bool here, bool on) {
-        if (v == none) return;
-        if (here && !on) {
-            put(dW + v * a.ldw + k, a.D - k, sum, a.scale, a.accumulate);
-        } else {
-            // rows of the workspace have room for whole chunks
-            float* const row = a.shared_rows + (2 * s + (here ? 1 : 0)) * a.pitch + k;
-            store_whole(row, sum);
-        }
-    };
-    for (int64_t i = first; i < end; i += kAhead) {
-        uint32_t key[kAhead];
-        T e[kAhead][C];
+    for (int c = 0; c < C; ++c) sum[c] = 0.0f;
+    for (int64_t base = first; base < stop; base += lpr) {
+        // pair base + lane, and the entry after it
+        const int64_t mine = base + lane < a.T ? base + lane : a.T - 1;
+        const uint32_t my_key = a.keys[mine], my_token = a.tokens[mine];
+        const uint32_t my_next = mine + 1 < a.T ? a.keys[mine + 1] : none;
+        const int pairs = static_cast<int>(stop - base < lpr ? stop - base : lpr);
+        for (int i = 0; i < pairs; i += kAhead) {
+            uint32_t key[kAhead], next[kAhead];
+            T e[kAhead][C];
+            W old[ADD ? kAhead : 1][C];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const bool in = i + u < end;
-            key[u] = in ? a.keys[i + u] : none;
-            if (in && key[u] != none)
-                load_part(dY + a.tokens[i + u] * a.ldy + k, a.D - k, e[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            if (i + u >= end) break;
-            if (key[u] != now) {
-                finish(now, !begun, false);
-                now = key[u];
-                begun = false;
-#pragma unroll
-                for (int c = 0; c < C; ++c) sum[c] = 0.0f;
+            for (int u = 0; u < kAhead; ++u) {
+                const int from = i + u < pairs ? i + u : pairs - 1;
+                uint32_t token;
+                if constexpr (WAVE) {
+                    key[u] = __builtin_amdgcn_readlane(my_key, from);
+                    next[u] = __builtin_amdgcn_readlane(my_next, from);
+                    token = __builtin_amdgcn_readlane(my_token, from);
+                } else {
+                    key[u] = __shfl(my_key, from, lpr);
+                    next[u] = __shfl(my_next, from, lpr);
+                    token = __shfl(my_token, from, lpr);
+                }
+                // (the row of a token without an entry is read, and dropped)
+                piece.load(dY + token * a.ldy, e[u]);
+                if constexpr (ADD) {
+                    // the last row stands in for those that are not needed
+                    const uint32_t row = key[u] != next[u] && key[u] != none ? key[u] : key[0];
+                    piece.load(dW + (row != none ? row : 0) * a.ldw, old[u]);
+                }
             }
-            if (key[u] != none) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (i + u >= pairs || key[u] == none) break;
 #pragma unroll
                 for (int c = 0; c < C; ++c) sum[c] += to_f32(e[u][c]);
+                const bool last = key[u] != next[u];
+                if (last && !begun) {
+                    W o[C];
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        if constexpr (ADD)
+                            o[c] = narrow<W>(fmaf(a.scale, sum[c], to_f32(old[u][c])));
+                        else
+                            o[c] = narrow<W>(a.scale * sum[c]);
+                    }
+                    piece.store_own(dW + key[u] * a.ldw, o);
+                } else if (last || base + i + u + 1 == stop) {
+                    piece.store(a.shared_rows + (2 * s + (begun ? 0 : 1)) * a.pitch, sum);
+                }
+                if (last) {
+                    begun = false;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) sum[c] = 0.0f;
+                }
             }
         }
     }
-    finish(now, !begun, now == after);
 }
 
 // Entries that several stretches share: the stretch where one begins adds up the rows
-// that they left.
-constexpr int kJoinWaves = 8, kJoinThreads = kJoinWaves * kWave;
-template <typename T, typename W>
-__global__ __launch_bounds__(kJoinThreads) void scatter_join_kernel(GradArgs a,
-                                                                    W* __restrict__ dW) {
-    constexpr int C = kChunk<T>;
+// that they left.  A workgroup looks at kJoinEach stretches, one lane at each (one to a
+// workgroup, most of which then end at once, took 14 us for 1024 stretches of 4096
+// columns), and adds up to them one after the other, 64 C columns.
+constexpr int64_t kMostStretches = 2048;
+constexpr int kJoinWaves = 8, kJoinThreads = kJoinWaves * kWave, kJoinEach = 8;
+template <typename W, int C, bool ADD>
+__global__ __launch_bounds__(kJoinThreads) void scatter_join_kernel(GradArgs a, W* __restrict__ dW) {
     __shared__ float lds[kJoinWaves][kWave][C + 1];
-    const int64_t s = blockIdx.x;  // (the last stretch shares nothing with a later one)
-    const int64_t end = (s + 1) * a.stretch;
-    const uint32_t v = a.keys[end - 1];
-    // it goes on after this stretch, and begins inside it
-    if (v == static_cast<uint32_t>(a.V) || a.keys[end] != v) return;
-    const int64_t first = s * a.stretch;
-    if (first > 0 && a.keys[first - 1] == v) return;
-    // the last stretch that holds it: the entries are sorted
-    int64_t lo = s + 1, hi = a.stretches;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.keys[mid * a.stretch] == v)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    const int64_t last = lo - 1;
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    for (int64_t k0 = 0; k0 < a.D; k0 += kWave * C) {
-        const int64_t k = k0 + lane * C;
+    const int64_t base = static_cast<int64_t>(blockIdx.x) * kJoinEach;
+    bool open = false;
+    if (lane < kJoinEach && base + lane + 1 < a.stretches) {
+        const int64_t first = (base + lane) * a.stretch, end = first + a.stretch;
+        const uint32_t v = a.keys[end - 1];
+        const uint32_t before = a.keys[first > 0 ? first - 1 : 0];
+        const int64_t far = end + a.stretch < a.T ? end + a.stretch : a.T - 1;
+        // its last entry begins inside it, and goes on past the next one
+        open = v != static_cast<uint32_t>(a.V) && (first == 0 || before != v) &&
+               end + a.stretch < a.T && a.keys[far] == v;
+    }
+    const Span<C> piece((static_cast<int64_t>(blockIdx.y) * kWave + lane) * C, a.D);
+    for (uint64_t todo = __ballot(open); todo; todo &= todo - 1) {
+        const int64_t s = base + __builtin_ctzll(todo);
+        const uint32_t v = a.keys[(s + 1) * a.stretch];
+        // the stretches after it that hold it, 64 x 64 at a time: at most kMostStretches
+        auto held = [&](int64_t from, int64_t by) {
+            const int64_t i = from + lane * by;
+            return static_cast<int64_t>(
+                __popcll(__ballot(i < a.stretches && a.keys[i * a.stretch] == v)));
+        };
+        const int64_t lines = held(s + 1, kWave);
+        const int64_t lo = s + 1 + (lines - 1) * kWave +
+                           held(s + 1 + (lines - 1) * kWave, 1);
         float sum[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) sum[c] = 0.0f;
-        if (k < a.D) {
-            if (wave == 0) load_whole(a.shared_rows + (2 * s + 1) * a.pitch + k, sum);
-#pragma unroll 4
-            for (int64_t i = s + 1 + wave; i <= last; i += kJoinWaves) {
-                float e[C];
-                load_whole(a.shared_rows + 2 * i * a.pitch + k, e);
+        if (wave == 0) piece.load(a.shared_rows + (2 * s + 1) * a.pitch, sum);
+        for (int64_t i = s + 1 + wave; i < lo; i += kJoinWaves * kAhead) {
+            float e[kAhead][C];
 #pragma unroll
-                for (int c = 0; c < C; ++c) sum[c] += e[c];
+            for (int u = 0; u < kAhead; ++u) {
+                const int64_t j = i + u * kJoinWaves < lo ? i + u * kJoinWaves : lo - 1;
+                piece.load(a.shared_rows + 2 * j * a.pitch, e[u]);
             }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+                for (int c = 0; c < C; ++c) sum[c] += i + u * kJoinWaves < lo ? e[u][c] : 0.0f;
         }
 #pragma unroll
         for (int c = 0; c < C; ++c) lds[wave][lane][c] = sum[c];
         __syncthreads();
-        if (wave == 0 && k < a.D) {
+        if (wave == 0) {
+            W o[C];
+            if constexpr (ADD) piece.load(dW + v * a.ldw, o);
 #pragma unroll
-            for (int w = 1; w < kJoinWaves; ++w)
+            for (int c = 0; c < C; ++c) {
 #pragma unroll
-                for (int c = 0; c < C; ++c) sum[c] += lds[w][lane][c];
-            put(dW + v * a.ldw + k, a.D - k, sum, a.scale, a.accumulate);
+                for (int w = 1; w < kJoinWaves; ++w) sum[c] += lds[w][lane][c];
+                o[c] = narrow<W>(ADD ? fmaf(a.scale, sum[c], to_f32(o[c])) : a.scale * sum[c]);
+            }
+            piece.store_own(dW + v * a.ldw, o);
         }
         __syncthreads();
     }
@@ -502,19 +536,13 @@ __global__ __launch_bounds__(kJoinThreads) void scatter_join_kernel(GradArgs a,
 template <typename W>
 __global__ __launch_bounds__(kThreads) void zero_kernel(int64_t V, int64_t D, W* __restrict__ dW,
                                                         int64_t ldw) {
-    constexpr int C = kChunk<W>;
-    W zero[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) zero[i] = narrow<W>(0.0f);
     for (int64_t v = blockIdx.x; v < V; v += gridDim.x)
-        for (int64_t k = threadIdx.x * C; k < D; k += kThreads * C)
-            store_part(dW + v * ldw + k, D - k, zero);
+        for (int64_t k = threadIdx.x; k < D; k += kThreads) dW[v * ldw + k] = narrow<W>(0.0f);
 }
 
 // The workspace: sorted entries and tokens, the other copy of them and the counts where
-// the sort takes several workgroups, and the stretches' shared rows.
+// the sort takes several passes, and the stretches' shared rows.
 struct Plan {
-    bool one;      // one workgroup sorts
     int passes;
     int64_t tiles, stretches, pitch;
     int stretch;
@@ -528,13 +556,14 @@ Plan make_plan(int64_t T, int64_t V, int64_t D) {
     int bits = 1;
     while ((V >> bits) != 0) ++bits;  // the largest key is V
     p.passes = static_cast<int>(ceil_div(bits, kDigit));
-    p.one = T <= kSortOne && V < (int64_t(1) << 25);
     p.tiles = ceil_div(T, kTile);
     p.pitch = ceil_div(D, 64) * 64;
-    // stretches of 8 to 32 pairs, longer ones past 2048 of them: an entry named by every
-    // token leaves a row in each, which one workgroup adds
-    int64_t stretch = ceil_div(T, 2048);
-    stretch = stretch < 32 ? (T >= 8192 ? 32 : T >= 2048 ? 16 : 8) : ceil_div(stretch, kAhead) * kAhead;
+    // stretches of 8 to 32 pairs (16384 tokens of 1024 columns: 12.6 us with 16, 15.4 with
+    // 32), longer ones past kMostStretches: an entry named by every token leaves a row in
+    // each, which one workgroup adds
+    const int64_t stretch = T < 2048    ? 8
+                            : T < 32768 ? 16
+                                        : ceil_div(ceil_div(T, kMostStretches), 32) * 32;
     p.stretch = static_cast<int>(stretch);
     p.stretches = ceil_div(T, stretch);
     int64_t at = 0;
@@ -545,7 +574,7 @@ Plan make_plan(int64_t T, int64_t V, int64_t D) {
     };
     p.keys = take(T * 4);
     p.tokens = take(T * 4);
-    if (!p.one) {
+    if (T > kRankMost) {
         p.keys2 = take(T * 4);
         p.tokens2 = take(T * 4);
         p.counts = take(p.tiles * kBins * 4);
@@ -560,15 +589,22 @@ unsigned grid_of(int64_t groups) {
     return static_cast<unsigned>(groups < most ? groups : most);
 }
 
-template <typename T> hipError_t gather(const EmbedArgs& a) {
-    const int64_t chunks = ceil_div(a.D, kChunk<T>);
+// Rows shorter than a chunk are taken one element a lane.
+template <typename T, int C> hipError_t gather(const EmbedArgs& a) {
+    const int64_t chunks = ceil_div(a.D, C);
+    // few tokens: a chunk a lane, so that many lanes share the latency; else kUnroll
+    const bool few = a.T * chunks <= kFewChunks;
+    const int unroll = few ? 1 : kUnroll;
     int lpr = 1;
-    while (lpr < kThreads && lpr < chunks) lpr *= 2;
-    const int64_t segs = ceil_div(chunks, static_cast<int64_t>(lpr) * kUnroll);
-    const int64_t groups = ceil_div(a.T, kThreads / lpr) * segs;
-    gather_kernel<T><<<dim3(grid_of(groups)), dim3(kThreads), 0, a.stream>>>(
+    while (lpr < kThreads && lpr * unroll < chunks) lpr *= 2;
+    const int64_t segs = ceil_div(chunks, static_cast<int64_t>(lpr) * unroll);
+    int64_t rows = ceil_div(a.T, kThreads / lpr);
+    const int64_t most = launch_groups(kThreads) / segs;  // the kernel strides over the rest
+    if (rows > most) rows = most;
+    const auto fn = few ? gather_kernel<T, C, 1> : gather_kernel<T, C, kUnroll>;
+    fn<<<dim3(static_cast<unsigned>(rows * segs)), dim3(kThreads), 0, a.stream>>>(
         a.T, a.V, a.D, static_cast<const T*>(a.W), a.ldw, a.index, a.ignore, a.scale,
-        static_cast<T*>(a.Y), a.ldy, lpr, segs, groups);
+        static_cast<T*>(a.Y), a.ldy, lpr, segs);
     return hipGetLastError();
 }
 
@@ -578,9 +614,11 @@ hipError_t sort(const EmbedArgs& a, const Plan& p, uint8_t* ws, uint32_t** keys,
     auto at = [&](int64_t offset) { return reinterpret_cast<uint32_t*>(ws + offset); };
     *keys = at(p.keys);
     *tokens = at(p.tokens);
-    if (p.one) {
-        sort_one_kernel<<<dim3(1), dim3(kSortThreads), 0, a.stream>>>(
-            static_cast<int>(a.T), a.V, a.index, a.ignore, p.passes, *keys, *tokens);
+    const int n = static_cast<int>(a.T);
+    if (a.T <= kRankMost) {
+        sort_rank_kernel<<<dim3(static_cast<unsigned>(ceil_div(a.T, kRankKeys))),
+                           dim3(kSortThreads), 0, a.stream>>>(n, a.V, a.index, a.ignore, *keys,
+                                                              *tokens);
         return hipGetLastError();
     }
     Pairs from{a.index, a.ignore, a.V, nullptr, nullptr};
@@ -592,8 +630,9 @@ hipError_t sort(const EmbedArgs& a, const Plan& p, uint8_t* ws, uint32_t** keys,
         uint32_t *const k = at(last ? p.keys : p.keys2), *const t = at(last ? p.tokens : p.tokens2);
         sort_count_kernel<<<dim3(grid), dim3(kSortThreads), 0, a.stream>>>(a.T, from, shift,
                                                                            p.tiles, at(p.counts));
-        sort_scan_kernel<<<dim3(1), dim3(kSortThreads), 0, a.stream>>>(p.tiles * kBins,
-                                                                       at(p.counts));
+        if (p.tiles > kFewTiles)
+            sort_scan_kernel<<<dim3(1), dim3(kSortThreads), 0, a.stream>>>(p.tiles * kBins,
+                                                                           at(p.counts));
         sort_move_kernel<<<dim3(grid), dim3(kSortThreads), 0, a.stream>>>(
             a.T, from, shift, p.tiles, at(p.counts), k, t);
         const hipError_t err = hipGetLastError();
@@ -603,7 +642,7 @@ hipError_t sort(const EmbedArgs& a, const Plan& p, uint8_t* ws, uint32_t** keys,
     return hipSuccess;
 }
 
-template <typename T, typename W> hipError_t scatter(const EmbedArgs& a, void* ws) {
+template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, void* ws) {
     W* const dw = static_cast<W*>(a.dW);
     if (a.T == 0) {
         if (a.accumulate) return hipSuccess;
@@ -624,33 +663,47 @@ template <typename T, typename W> hipError_t scatter(const EmbedArgs& a, void* w
     g.ldy = a.ldy;
     g.ldw = a.ldw;
     g.scale = a.scale;
-    g.accumulate = a.accumulate;
     g.stretch = p.stretch;
     g.stretches = p.stretches;
     g.pitch = p.pitch;
     g.shared_rows = reinterpret_cast<float*>(base + p.rows);
-    const int64_t chunks = ceil_div(a.D, kChunk<T>);
-    g.lpr = 1;
+    const int64_t chunks = ceil_div(a.D, C);
+    g.lpr = kAhead;
     while (g.lpr < kWave && g.lpr < chunks) g.lpr *= 2;
     g.segs = ceil_div(chunks, g.lpr);
-    g.zero_groups = a.accumulate ? 0 : ceil_div(a.V, kZeroRows * (kThreads / kWave));
-    const int64_t groups = g.zero_groups + ceil_div(g.stretches * g.segs, kThreads / g.lpr);
-    scatter_kernel<T, W><<<dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0, a.stream>>>(
-        g, static_cast<const T*>(a.dY), dw);
-    err = hipGetLastError();
-    if (err != hipSuccess || g.stretches < 2) return err;
-    scatter_join_kernel<T, W><<<dim3(static_cast<unsigned>(g.stretches - 1)), dim3(kJoinThreads), 0,
-                                a.stream>>>(g, dw);
-    return hipGetLastError();
+    g.sum_groups = ceil_div(g.stretches * g.segs, kThreads / g.lpr);
+    const int64_t groups = g.sum_groups + (a.accumulate ? 0 : ceil_div(a.V, kZeroRows * (kThreads / kWave)));
+    auto go = [&](auto wave, auto add) {
+        constexpr bool WAVE = decltype(wave)::value, ADD = decltype(add)::value;
+        scatter_kernel<T, W, C, WAVE, ADD><<<dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0,
+                                             a.stream>>>(g, static_cast<const T*>(a.dY), dw);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || g.stretches < 2) return e;
+        scatter_join_kernel<W, C, ADD><<<dim3(static_cast<unsigned>(ceil_div(g.stretches - 1, kJoinEach)),
+                                              static_cast<unsigned>(ceil_div(chunks, kWave))),
+                                         dim3(kJoinThreads), 0, a.stream>>>(g, dw);
+        return hipGetLastError();
+    };
+    using yes = std::true_type;
+    using no = std::false_type;
+    if (g.lpr == kWave) return a.accumulate ? go(yes{}, yes{}) : go(yes{}, no{});
+    return a.accumulate ? go(no{}, yes{}) : go(no{}, no{});
+}
+
+template <typename T> hipError_t gather_any(const EmbedArgs& a) {
+    return a.D < kChunk<T> ? gather<T, 1>(a) : gather<T, kChunk<T>>(a);
+}
+template <typename T, typename W> hipError_t scatter_any(const EmbedArgs& a, void* ws) {
+    return a.D < kChunk<T> ? scatter<T, W, 1>(a, ws) : scatter<T, W, kChunk<T>>(a, ws);
 }
 
 }  // namespace
 
 hipError_t launch_embedding(const EmbedArgs& a) {
     switch (a.dtype) {
-        case 0: return gather<float>(a);
-        case 1: return gather<_Float16>(a);
-        default: return gather<bf16_t>(a);
+        case 0: return gather_any<float>(a);
+        case 1: return gather_any<_Float16>(a);
+        default: return gather_any<bf16_t>(a);
     }
 }
 
@@ -660,11 +713,11 @@ int64_t embedding_workspace(int64_t T, int64_t V, int64_t D) {
 
 hipError_t launch_embedding_backward(const EmbedArgs& a, void* ws) {
     switch (a.dtype) {
-        case 0: return scatter<float, float>(a, ws);
-        case 1: return a.w_dtype == 0 ? scatter<_Float16, float>(a, ws)
-                                      : scatter<_Float16, _Float16>(a, ws);
-        default: return a.w_dtype == 0 ? scatter<bf16_t, float>(a, ws)
-                                       : scatter<bf16_t, bf16_t>(a, ws);
+        case 0: return scatter_any<float, float>(a, ws);
+        case 1: return a.w_dtype == 0 ? scatter_any<_Float16, float>(a, ws)
+                                      : scatter_any<_Float16, _Float16>(a, ws);
+        default: return a.w_dtype == 0 ? scatter_any<bf16_t, float>(a, ws)
+                                       : scatter_any<bf16_t, bf16_t>(a, ws);
     }
 }
 

@@ -19,6 +19,9 @@ namespace {
 
 constexpr int kLongThreads = 1024;  // a row that no register form holds
 constexpr int kColumns = 8;         // its columns per work-item, backwards
+// Work-items of the workgroups that are given rows to walk: four or five wavefronts a SIMD
+// are what the registers leave room for.
+constexpr int64_t kResident = 256 * 1024;
 
 template <int LANES> constexpr int kThreads = LANES <= kWave ? 256 : LANES;
 template <int LANES> constexpr int kRows = kThreads<LANES> / LANES;
@@ -45,47 +48,59 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (&lds)[N][kWaves<L
     }
 }
 
-// A lane's pieces of a row of D: CH chunks of 16 bytes (of T), LANES chunks apart.
-template <typename T, int LANES, int CH> struct Pieces {
-    static constexpr int C = kChunk<T>;
-    static __device__ __forceinline__ int column(int c, int lane) { return (c * LANES + lane) * C; }
-    template <typename E>
-    static __device__ __forceinline__ void load(const E* row, int D, int lane, E (&e)[CH][C]) {
+// A lane's pieces of a row of D: CH chunks of C elements, LANES chunks apart.
+template <int C, int LANES, int CH> struct Pieces {
+    int at[CH], skip[CH];
+    __device__ __forceinline__ Pieces(int D, int lane) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) load_part(row + column(c, lane), D - column(c, lane), e[c]);
+        for (int c = 0; c < CH; ++c) {
+            const Span<C> s((c * LANES + lane) * C, D);
+            at[c] = static_cast<int>(s.at);
+            skip[c] = s.skip;
+        }
+    }
+    template <typename E> __device__ __forceinline__ void load(const E* row, E (&e)[CH][C]) const {
+#pragma unroll
+        for (int c = 0; c < CH; ++c) load_whole(row + at[c], e[c]);
     }
     template <typename E>
-    static __device__ __forceinline__ void store(E* row, int D, int lane, const E (&e)[CH][C]) {
+    __device__ __forceinline__ void store(E* row, const E (&e)[CH][C]) const {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) store_part(row + column(c, lane), D - column(c, lane), e[c]);
+        for (int c = 0; c < CH; ++c) store_whole(row + at[c], e[c]);
     }
 };
 
-template <typename T, typename W, int LANES, int CH>
+// Forwards.  A workgroup walks rows a grid apart, the next row's loads in flight while one
+// is summed; weight and bias stay in registers.  (The last row is loaded once more in place
+// of one past it: loads and the result's stores are under no branch, or the compiler would
+// wait for all stores before the next row.)
+template <typename T, typename W, int C, int LANES, int CH>
 __global__ __launch_bounds__(kThreads<LANES>) void norm_kernel(
     int64_t rows, int D, const T* __restrict__ X, int64_t ldx, const W* __restrict__ weight,
     const W* __restrict__ bias, float eps, T* __restrict__ Y, int64_t ldy,
     float* __restrict__ means, float* __restrict__ rstds) {
-    using P = Pieces<T, LANES, CH>;
-    constexpr int C = P::C;
     __shared__ float lds[2][1][kWaves<LANES>];
     const int lane = threadIdx.x % LANES;
+    const Pieces<C, LANES, CH> piece(D, lane);
     const float d = static_cast<float>(D);
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows<LANES> + threadIdx.x / LANES;
-         row < rows; row += static_cast<int64_t>(gridDim.x) * kRows<LANES>) {
-        T x[CH][C];
-        W w[CH][C], b[CH][C];
-        P::load(X + row * ldx, D, lane, x);
-        if (weight) P::load(weight, D, lane, w);
-        if (bias) P::load(bias, D, lane, b);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRows<LANES>;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * kRows<LANES> + threadIdx.x / LANES;
+    T x[CH][C];
+    W w[CH][C], b[CH][C];
+    piece.load(X + (row < rows ? row : 0) * ldx, x);
+    if (weight) piece.load(weight, w);
+    if (bias) piece.load(bias, b);
+    for (; row < rows; row += step) {
+        const int64_t next = row + step < rows ? row + step : row;
         float v[CH][C], sum[1] = {0.0f};
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 v[c][i] = to_f32(x[c][i]);
-                sum[0] += v[c][i];
+                sum[0] += i >= piece.skip[c] ? v[c][i] : 0.0f;
             }
+        piece.load(X + next * ldx, x);
         row_sums<LANES>(sum, lds[0]);
         const float mean = sum[0] / d;
         sum[0] = 0.0f;
@@ -94,7 +109,7 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_kernel(
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 v[c][i] -= mean;
-                if (P::column(c, lane) + i < D) sum[0] += v[c][i] * v[c][i];
+                sum[0] += i >= piece.skip[c] ? v[c][i] * v[c][i] : 0.0f;
             }
         row_sums<LANES>(sum, lds[1]);
         const float rstd = 1.0f / sqrtf(sum[0] / d + eps);
@@ -108,11 +123,11 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_kernel(
                 if (bias) o += to_f32(b[c][i]);
                 y[c][i] = narrow<T>(o);
             }
-        P::store(Y + row * ldy, D, lane, y);
         if (lane == 0) {
             if (means) means[row] = mean;
             if (rstds) rstds[row] = rstd;
         }
+        piece.store(Y + row * ldy, y);
     }
 }
 
@@ -128,32 +143,35 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const T* const x = X + row * ldx;
         float sum[1] = {0.0f};
-        for (int64_t k = threadIdx.x * C; k < D; k += kLongThreads * C) {
+        for (int64_t k = 0; k < D; k += kLongThreads * C) {
+            const Span<C> piece(k + threadIdx.x * C, D);
             T e[C];
-            load_part(x + k, D - k, e);
+            piece.load(x, e);
 #pragma unroll
-            for (int i = 0; i < C; ++i) sum[0] += to_f32(e[i]);
+            for (int i = 0; i < C; ++i) sum[0] += i >= piece.skip ? to_f32(e[i]) : 0.0f;
         }
         row_sums<kLongThreads>(sum, lds[0]);
         const float mean = sum[0] / d;
         sum[0] = 0.0f;
-        for (int64_t k = threadIdx.x * C; k < D; k += kLongThreads * C) {
+        for (int64_t k = 0; k < D; k += kLongThreads * C) {
+            const Span<C> piece(k + threadIdx.x * C, D);
             T e[C];
-            load_part(x + k, D - k, e);
+            piece.load(x, e);
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 const float v = to_f32(e[i]) - mean;
-                if (k + i < D) sum[0] += v * v;
+                sum[0] += i >= piece.skip ? v * v : 0.0f;
             }
         }
         row_sums<kLongThreads>(sum, lds[1]);
         const float rstd = 1.0f / sqrtf(sum[0] / d + eps);
-        for (int64_t k = threadIdx.x * C; k < D; k += kLongThreads * C) {
+        for (int64_t k = 0; k < D; k += kLongThreads * C) {
+            const Span<C> piece(k + threadIdx.x * C, D);
             T e[C];
             W w[C], b[C];
-            load_part(x + k, D - k, e);
-            if (weight) load_part(weight + k, D - k, w);
-            if (bias) load_part(bias + k, D - k, b);
+            piece.load(x, e);
+            if (weight) piece.load(weight, w);
+            if (bias) piece.load(bias, b);
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 float o = (to_f32(e[i]) - mean) * rstd;
@@ -161,7 +179,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(
                 if (bias) o += to_f32(b[i]);
                 e[i] = narrow<T>(o);
             }
-            store_part(Y + row * ldy + k, D - k, e);
+            piece.store(Y + row * ldy, e);
         }
         if (threadIdx.x == 0) {
             if (means) means[row] = mean;
@@ -172,40 +190,44 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(
 
 // Backwards.  A workgroup walks rows a grid apart, the next row's loads in flight while a
 // row is summed; each lane keeps dw and db of its columns in registers, and the workgroup
-// writes one partial sum of each, which norm_join_kernel adds.  SUMS: dw or db is wanted.
-template <typename T, typename W, int LANES, int CH, bool SUMS>
+// writes one partial sum of each, which norm_join_kernel adds.  SUMS: dw or db is wanted;
+// ROWS: dx is.
+template <typename T, typename W, int C, int LANES, int CH, bool SUMS, bool ROWS>
 __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
     int64_t rows, int D, const T* __restrict__ dY, int64_t lddy, const T* __restrict__ X,
     int64_t ldx, const W* __restrict__ weight, const float* __restrict__ means,
     const float* __restrict__ rstds, T* __restrict__ dX, int64_t lddx,
     float* __restrict__ partial, int64_t pitch) {
-    using P = Pieces<T, LANES, CH>;
-    constexpr int C = P::C, R = kRows<LANES>;
+    constexpr int R = kRows<LANES>;
     __shared__ float lds[2][2][kWaves<LANES>];
     const int lane = threadIdx.x % LANES, part = threadIdx.x / LANES;
+    const Pieces<C, LANES, CH> piece(D, lane);
     const float d = static_cast<float>(D);
-    float w[CH][C], dw[CH][C], db[CH][C];
-    {
-        W e[CH][C];
-        if (weight) P::load(weight, D, lane, e);
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                w[c][i] = weight ? to_f32(e[c][i]) : 1.0f;
-                dw[c][i] = db[c][i] = 0.0f;
-            }
-    }
     const int64_t step = static_cast<int64_t>(gridDim.x) * R;
     int64_t row = static_cast<int64_t>(blockIdx.x) * R + part;
     T x[CH][C], dy[CH][C];
-    float mean = 0.0f, rstd = 0.0f;
-    if (row < rows) {
-        P::load(X + row * ldx, D, lane, x);
-        P::load(dY + row * lddy, D, lane, dy);
-        mean = means[row];
-        rstd = rstds[row];
+    W w[CH][C];
+    float mean, rstd;
+    auto load = [&](int64_t r) __attribute__((always_inline)) {
+        piece.load(X + r * ldx, x);
+        piece.load(dY + r * lddy, dy);
+        mean = means[r];
+        rstd = rstds[r];
+    };
+    load(row < rows ? row : 0);
+    if (weight) {
+        piece.load(weight, w);
+    } else {
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < C; ++i) w[c][i] = narrow<W>(1.0f);
     }
+    float dw[CH][C], db[CH][C];
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < C; ++i) dw[c][i] = db[c][i] = 0.0f;
     for (int turn = 0; row < rows; row += step, turn ^= 1) {
         float h[CH][C], g[CH][C], sum[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -214,8 +236,8 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
             for (int i = 0; i < C; ++i) {
                 const float o = to_f32(dy[c][i]);
                 h[c][i] = (to_f32(x[c][i]) - mean) * rstd;
-                g[c][i] = o * w[c][i];
-                if (P::column(c, lane) + i < D) {
+                g[c][i] = o * to_f32(w[c][i]);
+                if (i >= piece.skip[c]) {
                     sum[0] += g[c][i];
                     sum[1] += g[c][i] * h[c][i];
                 }
@@ -225,13 +247,8 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
                 }
             }
         const float r = rstd;
-        if (row + step < rows) {
-            P::load(X + (row + step) * ldx, D, lane, x);
-            P::load(dY + (row + step) * lddy, D, lane, dy);
-            mean = means[row + step];
-            rstd = rstds[row + step];
-        }
-        if (dX) {
+        load(row + step < rows ? row + step : row);
+        if constexpr (ROWS) {
             row_sums<LANES>(sum, lds[turn]);
             const float a = sum[0] / d, b = sum[1] / d;
             T o[CH][C];
@@ -239,14 +256,14 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
             for (int c = 0; c < CH; ++c)
 #pragma unroll
                 for (int i = 0; i < C; ++i) o[c][i] = narrow<T>(r * (g[c][i] - a - h[c][i] * b));
-            P::store(dX + row * lddx, D, lane, o);
+            piece.store(dX + row * lddx, o);
         }
     }
     if constexpr (SUMS) {
         float* const out = partial + static_cast<int64_t>(blockIdx.x) * 2 * pitch;
         if constexpr (R == 1) {
-            P::store(out, D, lane, dw);
-            P::store(out + pitch, D, lane, db);
+            piece.store(out, dw);
+            piece.store(out + pitch, db);
         } else {
             // the workgroup's rows are joined in order, dw first
             constexpr int kWidth = LANES * CH * C;
@@ -254,9 +271,10 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 if (which) __syncthreads();
-#pragma unroll
-                for (int c = 0; c < CH; ++c)
-                    store_whole(&rows_of[part][P::column(c, lane)], which ? db[c] : dw[c]);
+                if (which)
+                    piece.store(rows_of[part], db);
+                else
+                    piece.store(rows_of[part], dw);
                 __syncthreads();
                 for (int k = threadIdx.x; k < kWidth && k < D; k += kThreads<LANES>) {
                     float s = rows_of[0][k];
@@ -281,17 +299,18 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_sums_kernel(
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
         const float mean = means[row], rstd = rstds[row];
         float sum[2] = {0.0f, 0.0f};
-        for (int64_t k = threadIdx.x * C; k < D; k += kLongThreads * C) {
+        for (int64_t k = 0; k < D; k += kLongThreads * C) {
+            const Span<C> piece(k + threadIdx.x * C, D);
             T x[C], dy[C];
             W w[C];
-            load_part(X + row * ldx + k, D - k, x);
-            load_part(dY + row * lddy + k, D - k, dy);
-            if (weight) load_part(weight + k, D - k, w);
+            piece.load(X + row * ldx, x);
+            piece.load(dY + row * lddy, dy);
+            if (weight) piece.load(weight, w);
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 float g = to_f32(dy[i]);
                 if (weight) g *= to_f32(w[i]);
-                if (k + i < D) {
+                if (i >= piece.skip) {
                     sum[0] += g;
                     sum[1] += g * ((to_f32(x[i]) - mean) * rstd);
                 }
@@ -317,23 +336,22 @@ __global__ __launch_bounds__(256) void norm_long_backward_kernel(
     const int64_t p = blockIdx.x / bands;
     const int64_t k = ((blockIdx.x % bands) * 256 + threadIdx.x) * N;
     if (k >= D) return;
+    const Span<N> piece(k, D);
     const float d = static_cast<float>(D);
-    float w[N], dw[N], db[N];
-    {
-        W e[N];
-        if (weight) load_part(weight + k, D - k, e);
+    W w[N];
+    float dw[N], db[N];
+    if (weight) piece.load(weight, w);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            w[i] = weight ? to_f32(e[i]) : 1.0f;
-            dw[i] = db[i] = 0.0f;
-        }
+    for (int i = 0; i < N; ++i) {
+        if (!weight) w[i] = narrow<W>(1.0f);
+        dw[i] = db[i] = 0.0f;
     }
     const int64_t end = (p + 1) * slab < rows ? (p + 1) * slab : rows;
 #pragma unroll 2
     for (int64_t row = p * slab; row < end; ++row) {
         T x[N], dy[N];
-        load_part(X + row * ldx + k, D - k, x);
-        load_part(dY + row * lddy + k, D - k, dy);
+        piece.load(X + row * ldx, x);
+        piece.load(dY + row * lddy, dy);
         const float mean = means[row], rstd = rstds[row];
         const float a = sums[2 * row] / d, b = sums[2 * row + 1] / d;
 #pragma unroll
@@ -341,13 +359,13 @@ __global__ __launch_bounds__(256) void norm_long_backward_kernel(
             const float o = to_f32(dy[i]), h = (to_f32(x[i]) - mean) * rstd;
             dw[i] += o * h;
             db[i] += o;
-            x[i] = narrow<T>(rstd * (o * w[i] - a - h * b));
+            x[i] = narrow<T>(rstd * (o * to_f32(w[i]) - a - h * b));
         }
-        if (dX) store_part(dX + row * lddx + k, D - k, x);
+        if (dX) piece.store(dX + row * lddx, x);
     }
-    float* const out = partial + p * 2 * pitch + k;
-    store_part(out, D - k, dw);
-    store_part(out + pitch, D - k, db);
+    float* const out = partial + p * 2 * pitch;
+    piece.store(out, dw);
+    piece.store(out + pitch, db);
 }
 
 // dw (blockIdx.y 0) and db (1): the partial sums of 64 columns, every sixteenth of them by
@@ -377,19 +395,23 @@ __global__ __launch_bounds__(kJoin * kWave) void norm_join_kernel(
     }
 }
 
-// How a row of D lies in registers: lanes, and elements of each.  Two elements a lane more
-// than a row needs cost nothing; more than 16 leave too few wavefronts in flight
-// backwards, where five values a column are held.
+// How a row of D lies in registers: C elements a chunk, lanes, and chunks of each.  16
+// elements a lane: more leave too few wavefronts in flight backwards, where five values a
+// column are held.  Rows shorter than a chunk take one element a lane.
 constexpr int64_t kMaxInRegisters = 16384;
 
 template <typename T, typename F> hipError_t with_form(int64_t D, F f) {
-    constexpr int C = kChunk<T>;
     using std::integral_constant;
     auto form = [&](auto lanes, auto elements) {
-        return f(lanes, integral_constant<int, decltype(elements)::value / C>{});
+        constexpr int C = kChunk<T>;
+        return f(integral_constant<int, C>{}, lanes,
+                 integral_constant<int, decltype(elements)::value / C>{});
     };
     using e8 = integral_constant<int, 8>;
     using e16 = integral_constant<int, 16>;
+    if (D < kChunk<T>)
+        return f(integral_constant<int, 1>{}, integral_constant<int, 16>{},
+                 integral_constant<int, 1>{});
     if (D <= 128) return form(integral_constant<int, 16>{}, e8{});
     if (D <= 512) return form(integral_constant<int, 64>{}, e8{});
     if (D <= 1024) return form(integral_constant<int, 64>{}, e16{});
@@ -399,34 +421,45 @@ template <typename T, typename F> hipError_t with_form(int64_t D, F f) {
     return form(integral_constant<int, 1024>{}, e16{});
 }
 
+// Rows, and work-items, of a workgroup of that form.
 int rows_of_form(int64_t D) { return D <= 128 ? 16 : D <= 1024 ? 4 : 1; }
+int threads_of_form(int64_t D) {
+    return D <= 1024 ? 256 : D <= 2048 ? 128 : D <= 4096 ? 256 : D <= 8192 ? 512 : 1024;
+}
+
+// Workgroups for `groups` of rows, `most` at a time, each with as many as the others.
+int64_t even_groups(int64_t groups, int64_t most) {
+    return ceil_div(groups, ceil_div(groups, most));
+}
 
 template <typename T, typename W> hipError_t forward(const NormArgs& a) {
     const T* const x = static_cast<const T*>(a.X);
     const W *const w = static_cast<const W*>(a.W), *const b = static_cast<const W*>(a.B);
     T* const y = static_cast<T*>(a.Y);
-    const int64_t most = int64_t(1) << 20;  // workgroups; they stride over the rest
     if (a.D > kMaxInRegisters) {
+        const int64_t most = int64_t(1) << 20;  // workgroups; they stride over the rest
         norm_long_kernel<T, W><<<dim3(static_cast<unsigned>(a.T < most ? a.T : most)),
                                  dim3(kLongThreads), 0, a.stream>>>(
             a.T, a.D, x, a.ldx, w, b, a.eps, y, a.ldy, a.mean, a.rstd);
         return hipGetLastError();
     }
-    return with_form<T>(a.D, [&](auto lanes, auto chunks) {
-        constexpr int L = decltype(lanes)::value, CH = decltype(chunks)::value;
-        int64_t blocks = ceil_div(a.T, kRows<L>);
-        if (blocks > most) blocks = most;
-        norm_kernel<T, W, L, CH><<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads<L>), 0,
-                                   a.stream>>>(a.T, static_cast<int>(a.D), x, a.ldx, w, b, a.eps,
-                                               y, a.ldy, a.mean, a.rstd);
+    return with_form<T>(a.D, [&](auto chunk, auto lanes, auto chunks) {
+        constexpr int C = decltype(chunk)::value, L = decltype(lanes)::value,
+                      CH = decltype(chunks)::value;
+        const int64_t blocks = even_groups(ceil_div(a.T, kRows<L>), kResident / kThreads<L>);
+        norm_kernel<T, W, C, L, CH><<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads<L>), 0,
+                                      a.stream>>>(a.T, static_cast<int>(a.D), x, a.ldx, w, b,
+                                                  a.eps, y, a.ldy, a.mean, a.rstd);
         return hipGetLastError();
     });
 }
 
 // Workgroups of the backward pass, each of which writes partial sums.
 int64_t backward_parts(int64_t T, int64_t D) {
-    const int64_t groups = ceil_div(T, 4 * rows_of_form(D));
-    return groups < 512 ? groups : 512;
+    const int64_t groups = ceil_div(T, rows_of_form(D));
+    const int64_t most = kResident / threads_of_form(D);
+    const int64_t parts = ceil_div(groups, 4);  // four rows to a partial sum at least
+    return even_groups(groups, parts < most ? (parts < 512 ? parts : 512) : most < 512 ? most : 512);
 }
 int64_t long_slab(int64_t T) { return ceil_div(T, T < 64 * 32 ? ceil_div(T, 32) : 64); }
 int64_t pitch_of(int64_t D) { return ceil_div(D, 64) * 64; }
@@ -456,10 +489,11 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, void* w
         err = hipGetLastError();
     } else {
         const bool sums = a.dW || a.dB;
-        err = with_form<T>(a.D, [&](auto lanes, auto chunks) {
-            constexpr int L = decltype(lanes)::value, CH = decltype(chunks)::value;
-            auto go = [&](auto want) {
-                norm_backward_kernel<T, W, L, CH, decltype(want)::value>
+        err = with_form<T>(a.D, [&](auto chunk, auto lanes, auto chunks) {
+            constexpr int C = decltype(chunk)::value, L = decltype(lanes)::value,
+                          CH = decltype(chunks)::value;
+            auto go = [&](auto want, auto to_x) {
+                norm_backward_kernel<T, W, C, L, CH, decltype(want)::value, decltype(to_x)::value>
                     <<<dim3(static_cast<unsigned>(parts)), dim3(kThreads<L>), 0, a.stream>>>(
                         a.T, static_cast<int>(a.D), dy, a.lddy, x, a.ldx, w, a.mean, a.rstd, dx,
                         a.ldy, partial, pitch);
@@ -467,12 +501,11 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, void* w
             };
             if (sums) {
                 parts = backward_parts(a.T, a.D);
-                return go(std::true_type{});
+                return dx ? go(std::true_type{}, std::true_type{})
+                          : go(std::true_type{}, std::false_type{});
             }
-            const int64_t most = int64_t(1) << 20;
-            parts = ceil_div(a.T, kRows<L>);
-            if (parts > most) parts = most;
-            return go(std::false_type{});
+            parts = even_groups(ceil_div(a.T, kRows<L>), kResident / kThreads<L>);
+            return go(std::false_type{}, std::true_type{});
         });
     }
     if (err != hipSuccess || (!a.dW && !a.dB)) return err;

@@ -28,25 +28,51 @@ __device__ __forceinline__ void store_whole(T* __restrict__ p, const T (&e)[N]) 
     __builtin_memcpy(p, e, sizeof(e));
 }
 
-// N elements of which the first `held` lie inside the row; zeros for the others.
+// Where a lane reads its N elements from `column` on, in a row of `length` (N at least): at
+// the column itself, or, where the row ends sooner, N elements before its end.  So every
+// load is one whole access without a branch, whatever the length; with a branch around the
+// last elements the compiler waits for each load before the next.  The first `skip` of the
+// elements are then another lane's (all of them where the column is past the row): they
+// stay out of sums, and store_own leaves them to that lane.  store writes them too, for
+// values that come out as the same bits in both lanes: a store under no branch can stay in
+// flight while the next loads are waited for.
+template <int N> struct Span {
+    int64_t at;
+    int skip;
+    __device__ __forceinline__ Span(int64_t column, int64_t length) {
+        at = column < length - N ? column : length - N;
+        skip = static_cast<int>(column - at < N ? column - at : N);
+    }
+    template <typename T> __device__ __forceinline__ void load(const T* row, T (&e)[N]) const {
+        load_whole(row + at, e);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* row, const T (&e)[N]) const {
+        store_whole(row + at, e);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store_own(T* row, const T (&e)[N]) const {
+        if (skip == 0) {
+            store_whole(row + at, e);
+        } else {
+#pragma unroll
+            for (int i = 1; i < N; ++i)
+                if (i >= skip) row[at + i] = e[i];
+        }
+    }
+};
+
+// N elements of an array's last ones, `held` of them (zeros for the others).
 template <typename T, int N>
 __device__ __forceinline__ void load_part(const T* __restrict__ p, int64_t held, T (&e)[N]) {
-    if (held >= N) {
-        load_whole(p, e);
-    } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) e[i] = i < held ? p[i] : ZeroOf<T>::get();
-    }
+    for (int i = 0; i < N; ++i) e[i] = i < held ? p[i] : ZeroOf<T>::get();
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_part(T* __restrict__ p, int64_t held, const T (&e)[N]) {
-    if (held >= N) {
-        store_whole(p, e);
-    } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (i < held) p[i] = e[i];
-    }
+    for (int i = 0; i < N; ++i)
+        if (i < held) p[i] = e[i];
 }
 
 // The sum, or largest, over the 16 lanes of a DPP row, in every one of them: rotations by
