@@ -1021,13 +1021,22 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dw=None, db=None,
         need_dw = False
     with _device_of(device):
         stream, other = _stream_of(stream, device)
-        dx = _gradient("dx", need_dx, dx, x)
-        like = weight if weight is not None else x.new_empty(D) if need_db and db is None else None
-        if dw is None and need_dw:
-            dw = torch.empty_like(like)
-        if db is None and need_db:
-            db = torch.empty_like(like)
-        pdw, pdb = _vector("dw", dw, device, kind, D), _vector("db", db, device, kind, D)
+        pdx, lddx, pdw, pdb = None, D, None, None
+        if dx is not None:
+            pdx, lddx = _out_matrix(_gradient("dx", True, dx, x))
+        elif need_dx:
+            dx = torch.empty_like(x) if ldx == D else x.new_empty((T, D))
+            pdx = dx.data_ptr() or None
+        if dw is not None:
+            pdw = _vector("dw", dw, device, kind, D)
+        elif need_dw:
+            dw = torch.empty_like(weight)
+            pdw = dw.data_ptr()
+        if db is not None:
+            pdb = _vector("db", db, device, kind, D)
+        elif need_db:
+            db = x.new_empty(D, dtype=kind) if weight is None else torch.empty_like(weight)
+            pdb = db.data_ptr()
         st, n = migemm_layer_norm_workspace_size(T, D, dw is not None or db is not None)
         if st != OK:
             raise MigemmError(st, "migemm_layer_norm_workspace_size")
@@ -1035,15 +1044,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dw=None, db=None,
         if other:
             _run_on(stream, device, dy, x, weight, mean, rstd, dx, dw, db, ws)
         st = lib().migemm_layer_norm_backward(
-            T, D, dt, dy.data_ptr() or None, lddy, x.data_ptr() or None, ldx, wd, pw, pm, pr,
-            *_out_matrix_of(dx, D), pdw, pdb, ws.data_ptr() or None, n, stream)
+            T, D, dt, dy.data_ptr() or None, lddy, x.data_ptr() or None, ldx, wd, pw, pm, pr, pdx,
+            lddx, pdw, pdb, ws.data_ptr() or None, n, stream)
         if st != OK:
             raise MigemmError(st, "migemm_layer_norm_backward")
     return dx, dw, db
-
-
-def _out_matrix_of(t, D):
-    return (None, D) if t is None else (t.data_ptr() or None, _ld(t))
 
 
 def embedding(w, index, *, scale: float = 1.0, ignore_index: int = -100, out=None, stream=None):

@@ -111,37 +111,6 @@ __device__ __forceinline__ void encode(const float (&x)[8], uint8_t (&codes)[8])
     __builtin_memcpy(codes, w, sizeof(w));
 }
 
-// 16- and 8-byte accesses past the caches, at any alignment; wider pieces do not fill whole
-// lines with one access of a wavefront, and go through them.
-template <typename T, int N> __device__ __forceinline__ void load_once(const T* p, T (&e)[N]) {
-    typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(1)));
-    typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(1)));
-    if constexpr (sizeof(e) == 16) {
-        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const v4*>(p));
-        __builtin_memcpy(e, &w, sizeof(e));
-    } else if constexpr (sizeof(e) == 8) {
-        const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const v2*>(p));
-        __builtin_memcpy(e, &w, sizeof(e));
-    } else {
-        load_whole(p, e);
-    }
-}
-template <typename T, int N> __device__ __forceinline__ void store_once(T* p, const T (&e)[N]) {
-    typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(1)));
-    typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(1)));
-    if constexpr (sizeof(e) == 16) {
-        u32x4 w;
-        __builtin_memcpy(&w, e, sizeof(e));
-        __builtin_nontemporal_store(w, reinterpret_cast<v4*>(p));
-    } else if constexpr (sizeof(e) == 8) {
-        u32x2 w;
-        __builtin_memcpy(&w, e, sizeof(e));
-        __builtin_nontemporal_store(w, reinterpret_cast<v2*>(p));
-    } else {
-        store_whole(p, e);
-    }
-}
-
 // How a lane's E elements lie in a tensor: all of them in it (WHOLE); in a tensor's last
 // piece, E elements before its end, of which those past `skip` are the lane's (LAST, no
 // branch around the loads: element by element they took 9 us); or, in a tensor of fewer

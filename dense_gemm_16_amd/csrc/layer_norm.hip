@@ -22,6 +22,9 @@ constexpr int kColumns = 8;         // its columns per work-item, backwards
 // Work-items of the workgroups that are given rows to walk: four or five wavefronts a SIMD
 // are what the registers leave room for.
 constexpr int64_t kResident = 256 * 1024;
+// Past this many bytes of x, dy and dx, backwards, x and dy are read past the caches, whose
+// last level (256 MiB) holds too little of them for the next reader.
+constexpr double kOnceBytes = 256 << 20;
 
 template <int LANES> constexpr int kThreads = LANES <= kWave ? 256 : LANES;
 template <int LANES> constexpr int kRows = kThreads<LANES> / LANES;
@@ -59,9 +62,15 @@ template <int C, int LANES, int CH> struct Pieces {
             skip[c] = s.skip;
         }
     }
-    template <typename E> __device__ __forceinline__ void load(const E* row, E (&e)[CH][C]) const {
+    template <bool ONCE = false, typename E>
+    __device__ __forceinline__ void load(const E* row, E (&e)[CH][C]) const {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) load_whole(row + at[c], e[c]);
+        for (int c = 0; c < CH; ++c) {
+            if constexpr (ONCE)
+                load_once(row + at[c], e[c]);
+            else
+                load_whole(row + at[c], e[c]);
+        }
     }
     template <typename E>
     __device__ __forceinline__ void store(E* row, const E (&e)[CH][C]) const {
@@ -190,31 +199,38 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(
 
 // Backwards.  A workgroup walks rows a grid apart, the next row's loads in flight while a
 // row is summed; each lane keeps dw and db of its columns in registers, and the workgroup
-// writes one partial sum of each, which norm_join_kernel adds.  SUMS: dw or db is wanted;
-// ROWS: dx is.
-template <typename T, typename W, int C, int LANES, int CH, bool SUMS, bool ROWS>
+// writes one partial sum of each, which norm_join_kernel adds.  Rows stay in registers as
+// they were loaded, and h and g are formed twice: kept in FP32 they left one workgroup less
+// to a CU, and spilled in the form of 1024 lanes.  FP32 rows of that form leave no room for
+// the next one's.  SUMS: dw or db is wanted; ROWS: dx is; ONCE: x and dy are read past the
+// caches.
+template <typename T, typename W, int C, int LANES, int CH, bool SUMS, bool ROWS, bool ONCE>
 __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
     int64_t rows, int D, const T* __restrict__ dY, int64_t lddy, const T* __restrict__ X,
     int64_t ldx, const W* __restrict__ weight, const float* __restrict__ means,
     const float* __restrict__ rstds, T* __restrict__ dX, int64_t lddx,
     float* __restrict__ partial, int64_t pitch) {
     constexpr int R = kRows<LANES>;
+    constexpr bool AHEAD = !(LANES == 1024 && sizeof(T) == 4);
     __shared__ float lds[2][2][kWaves<LANES>];
     const int lane = threadIdx.x % LANES, part = threadIdx.x / LANES;
     const Pieces<C, LANES, CH> piece(D, lane);
     const float d = static_cast<float>(D);
     const int64_t step = static_cast<int64_t>(gridDim.x) * R;
     int64_t row = static_cast<int64_t>(blockIdx.x) * R + part;
-    T x[CH][C], dy[CH][C];
-    W w[CH][C];
-    float mean, rstd;
-    auto load = [&](int64_t r) __attribute__((always_inline)) {
-        piece.load(X + r * ldx, x);
-        piece.load(dY + r * lddy, dy);
-        mean = means[r];
-        rstd = rstds[r];
+    struct Row {
+        T x[CH][C], dy[CH][C];
+        float mean, rstd;
     };
-    load(row < rows ? row : 0);
+    auto load = [&](int64_t r, Row& t) __attribute__((always_inline)) {
+        piece.template load<ONCE>(X + r * ldx, t.x);
+        piece.template load<ONCE>(dY + r * lddy, t.dy);
+        t.mean = means[r];
+        t.rstd = rstds[r];
+    };
+    Row now;
+    if constexpr (AHEAD) load(row < rows ? row : 0, now);
+    W w[CH][C];
     if (weight) {
         piece.load(weight, w);
     } else {
@@ -229,25 +245,28 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
 #pragma unroll
         for (int i = 0; i < C; ++i) dw[c][i] = db[c][i] = 0.0f;
     for (int turn = 0; row < rows; row += step, turn ^= 1) {
-        float h[CH][C], g[CH][C], sum[2] = {0.0f, 0.0f};
+        Row next;
+        if constexpr (AHEAD)
+            load(row + step < rows ? row + step : row, next);
+        else
+            load(row, now);
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                const float o = to_f32(dy[c][i]);
-                h[c][i] = (to_f32(x[c][i]) - mean) * rstd;
-                g[c][i] = o * to_f32(w[c][i]);
+                const float o = to_f32(now.dy[c][i]);
+                const float h = (to_f32(now.x[c][i]) - now.mean) * now.rstd;
+                const float g = o * to_f32(w[c][i]);
                 if (i >= piece.skip[c]) {
-                    sum[0] += g[c][i];
-                    sum[1] += g[c][i] * h[c][i];
+                    sum[0] += g;
+                    sum[1] += g * h;
                 }
                 if constexpr (SUMS) {
-                    dw[c][i] += o * h[c][i];
+                    dw[c][i] += o * h;
                     db[c][i] += o;
                 }
             }
-        const float r = rstd;
-        load(row + step < rows ? row + step : row);
         if constexpr (ROWS) {
             row_sums<LANES>(sum, lds[turn]);
             const float a = sum[0] / d, b = sum[1] / d;
@@ -255,9 +274,14 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int i = 0; i < C; ++i) o[c][i] = narrow<T>(r * (g[c][i] - a - h[c][i] * b));
+                for (int i = 0; i < C; ++i) {
+                    const float h = (to_f32(now.x[c][i]) - now.mean) * now.rstd;
+                    const float g = to_f32(now.dy[c][i]) * to_f32(w[c][i]);
+                    o[c][i] = narrow<T>(now.rstd * (g - a - h * b));
+                }
             piece.store(dX + row * lddx, o);
         }
+        if constexpr (AHEAD) now = next;
     }
     if constexpr (SUMS) {
         float* const out = partial + static_cast<int64_t>(blockIdx.x) * 2 * pitch;
@@ -458,7 +482,8 @@ template <typename T, typename W> hipError_t forward(const NormArgs& a) {
 int64_t backward_parts(int64_t T, int64_t D) {
     const int64_t groups = ceil_div(T, rows_of_form(D));
     const int64_t most = kResident / threads_of_form(D);
-    const int64_t parts = ceil_div(groups, 4);  // four rows to a partial sum at least
+    // four rows to a partial sum at least, two where there are few
+    const int64_t parts = ceil_div(groups, groups <= 256 ? 2 : 4);
     return even_groups(groups, parts < most ? (parts < 512 ? parts : 512) : most < 512 ? most : 512);
 }
 int64_t long_slab(int64_t T) { return ceil_div(T, T < 64 * 32 ? ceil_div(T, 32) : 64); }
@@ -489,11 +514,15 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, void* w
         err = hipGetLastError();
     } else {
         const bool sums = a.dW || a.dB;
+        const bool once = 3.0 * sizeof(T) * a.T * a.D > kOnceBytes;
+        using yes = std::true_type;
+        using no = std::false_type;
         err = with_form<T>(a.D, [&](auto chunk, auto lanes, auto chunks) {
             constexpr int C = decltype(chunk)::value, L = decltype(lanes)::value,
                           CH = decltype(chunks)::value;
-            auto go = [&](auto want, auto to_x) {
-                norm_backward_kernel<T, W, C, L, CH, decltype(want)::value, decltype(to_x)::value>
+            auto go = [&](auto want, auto to_x, auto past) {
+                norm_backward_kernel<T, W, C, L, CH, decltype(want)::value, decltype(to_x)::value,
+                                     decltype(past)::value>
                     <<<dim3(static_cast<unsigned>(parts)), dim3(kThreads<L>), 0, a.stream>>>(
                         a.T, static_cast<int>(a.D), dy, a.lddy, x, a.ldx, w, a.mean, a.rstd, dx,
                         a.ldy, partial, pitch);
@@ -501,11 +530,11 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, void* w
             };
             if (sums) {
                 parts = backward_parts(a.T, a.D);
-                return dx ? go(std::true_type{}, std::true_type{})
-                          : go(std::true_type{}, std::false_type{});
+                if (!dx) return go(yes{}, no{}, no{});
+                return once ? go(yes{}, yes{}, yes{}) : go(yes{}, yes{}, no{});
             }
             parts = even_groups(ceil_div(a.T, kRows<L>), kResident / kThreads<L>);
-            return go(std::false_type{}, std::true_type{});
+            return go(no{}, yes{}, no{});
         });
     }
     if (err != hipSuccess || (!a.dW && !a.dB)) return err;

@@ -28,6 +28,37 @@ __device__ __forceinline__ void store_whole(T* __restrict__ p, const T (&e)[N]) 
     __builtin_memcpy(p, e, sizeof(e));
 }
 
+// 16- and 8-byte accesses past the caches, at any alignment; wider pieces do not fill whole
+// lines with one access of a wavefront, and go through them.
+template <typename T, int N> __device__ __forceinline__ void load_once(const T* p, T (&e)[N]) {
+    typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(1)));
+    typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(1)));
+    if constexpr (sizeof(e) == 16) {
+        const u32x4 w = __builtin_nontemporal_load(reinterpret_cast<const v4*>(p));
+        __builtin_memcpy(e, &w, sizeof(e));
+    } else if constexpr (sizeof(e) == 8) {
+        const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const v2*>(p));
+        __builtin_memcpy(e, &w, sizeof(e));
+    } else {
+        load_whole(p, e);
+    }
+}
+template <typename T, int N> __device__ __forceinline__ void store_once(T* p, const T (&e)[N]) {
+    typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(1)));
+    typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(1)));
+    if constexpr (sizeof(e) == 16) {
+        u32x4 w;
+        __builtin_memcpy(&w, e, sizeof(e));
+        __builtin_nontemporal_store(w, reinterpret_cast<v4*>(p));
+    } else if constexpr (sizeof(e) == 8) {
+        u32x2 w;
+        __builtin_memcpy(&w, e, sizeof(e));
+        __builtin_nontemporal_store(w, reinterpret_cast<v2*>(p));
+    } else {
+        store_whole(p, e);
+    }
+}
+
 // Where a lane reads its N elements from `column` on, in a row of `length` (N at least): at
 // the column itself, or, where the row ends sooner, N elements before its end.  So every
 // load is one whole access without a branch, whatever the length; with a branch around the
