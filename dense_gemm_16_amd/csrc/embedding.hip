@@ -327,7 +327,7 @@ __device__ __forceinline__ int64_t first_of(const GradArgs& a, int64_t v) {
 // Zeros the rows of entries v0 .. v0 + kZeroRows - 1 that no token names, by one
 // wavefront.
 constexpr int kZeroRows = 16;
-template <typename W, int C>
+template <typename W, int C, bool ONCE>
 __device__ __forceinline__ void zero_rows(const GradArgs& a, int64_t v0, W* __restrict__ dW) {
     const int lane = threadIdx.x % kWave;
     const int64_t v1 = v0 + kZeroRows < a.V ? v0 + kZeroRows : a.V;
@@ -346,7 +346,13 @@ __device__ __forceinline__ void zero_rows(const GradArgs& a, int64_t v0, W* __re
     for (int i = 0; i < C; ++i) zero[i] = narrow<W>(0.0f);
     for (uint64_t todo = absent; todo; todo &= todo - 1) {
         W* const row = dW + (v0 + __builtin_ctzll(todo)) * a.ldw;
-        for (int64_t k = lane * C; k < a.D; k += kWave * C) Span<C>(k, a.D).store(row, zero);
+        for (int64_t k = lane * C; k < a.D; k += kWave * C) {
+            const Span<C> piece(k, a.D);
+            if constexpr (ONCE)
+                store_once(row + piece.at, zero);
+            else
+                store_whole(row + piece.at, zero);
+        }
     }
 }
 
@@ -356,15 +362,16 @@ __device__ __forceinline__ void zero_rows(const GradArgs& a, int64_t v0, W* __re
 // of 4096 columns).  The group's lanes load the entries and tokens of as many pairs at
 // once; then kAhead rows of dy are in flight together, and, where the gradient is added
 // (ADD), the rows of dw whose entries end among them.  WAVE: the group is a wavefront
-// (pairs come by readlane, and branches are uniform).
+// (pairs come by readlane, and branches are uniform).  ONCE: dy is read, and zeros are
+// written, past the caches.
 constexpr int kAhead = 8;
-template <typename T, typename W, int C, bool WAVE, bool ADD>
+template <typename T, typename W, int C, bool WAVE, bool ADD, bool ONCE>
 __global__ __launch_bounds__(kThreads) void scatter_kernel(GradArgs a, const T* __restrict__ dY,
                                                            W* __restrict__ dW) {
     if (blockIdx.x >= a.sum_groups) {
         const int64_t v0 = (static_cast<int64_t>(blockIdx.x - a.sum_groups) * (kThreads / kWave) +
                             threadIdx.x / kWave) * kZeroRows;
-        if (v0 < a.V) zero_rows<W, C>(a, v0, dW);
+        if (v0 < a.V) zero_rows<W, C, ONCE>(a, v0, dW);
         return;
     }
     const int lpr = WAVE ? kWave : a.lpr;
@@ -428,7 +435,10 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(GradArgs a, const T* 
                     token = __shfl(my_token, from, lpr);
                 }
                 // (the row of a token without an entry is read, and dropped)
-                piece.load(dY + token * a.ldy, e[u]);
+                if constexpr (ONCE)
+                    load_once(dY + token * a.ldy + piece.at, e[u]);
+                else
+                    piece.load(dY + token * a.ldy, e[u]);
                 if constexpr (ADD) {
                     // the last row stands in for those that are not needed
                     const uint32_t row = key[u] != next[u] && key[u] != none ? key[u] : key[0];
@@ -642,6 +652,12 @@ hipError_t sort(const EmbedArgs& a, const Plan& p, uint8_t* ws, uint32_t** keys,
     return hipSuccess;
 }
 
+// From this many bytes of dy and of rows to zero, both go past the caches, whose last level
+// (256 MiB) holds too little of them for the next reader: 65536 tokens of 50001 x 2048 FP32
+// 192 us instead of 207, 32768 of 131072 x 4096 BF16, added, 99 instead of 105; 8192 of
+// those 35 instead of 32.
+constexpr double kOnceBytes = 256 << 20;
+
 template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, void* ws) {
     W* const dw = static_cast<W*>(a.dW);
     if (a.T == 0) {
@@ -673,9 +689,10 @@ template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, 
     g.segs = ceil_div(chunks, g.lpr);
     g.sum_groups = ceil_div(g.stretches * g.segs, kThreads / g.lpr);
     const int64_t groups = g.sum_groups + (a.accumulate ? 0 : ceil_div(a.V, kZeroRows * (kThreads / kWave)));
-    auto go = [&](auto wave, auto add) {
-        constexpr bool WAVE = decltype(wave)::value, ADD = decltype(add)::value;
-        scatter_kernel<T, W, C, WAVE, ADD><<<dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0,
+    auto go = [&](auto wave, auto add, auto past) {
+        constexpr bool WAVE = decltype(wave)::value, ADD = decltype(add)::value,
+                       ONCE = decltype(past)::value;
+        scatter_kernel<T, W, C, WAVE, ADD, ONCE><<<dim3(static_cast<unsigned>(groups)), dim3(kThreads), 0,
                                              a.stream>>>(g, static_cast<const T*>(a.dY), dw);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || g.stretches < 2) return e;
@@ -686,8 +703,12 @@ template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, 
     };
     using yes = std::true_type;
     using no = std::false_type;
-    if (g.lpr == kWave) return a.accumulate ? go(yes{}, yes{}) : go(yes{}, no{});
-    return a.accumulate ? go(no{}, yes{}) : go(no{}, no{});
+    const double bytes = static_cast<double>(sizeof(T)) * a.T * a.D +
+                         (a.accumulate ? 0.0 : static_cast<double>(sizeof(W)) * a.V * a.D);
+    const bool once = bytes >= kOnceBytes;
+    if (g.lpr < kWave) return a.accumulate ? go(no{}, yes{}, no{}) : go(no{}, no{}, no{});
+    if (once) return a.accumulate ? go(yes{}, yes{}, yes{}) : go(yes{}, no{}, yes{});
+    return a.accumulate ? go(yes{}, yes{}, no{}) : go(yes{}, no{}, no{});
 }
 
 template <typename T> hipError_t gather_any(const EmbedArgs& a) {
