@@ -63,8 +63,10 @@ __global__ __launch_bounds__(kThreads) void gather_kernel(
 // Tokens without an entry (ignored, or outside the table) sort last, as entry V.
 constexpr int kDigit = 9, kBins = 1 << kDigit;
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
-constexpr int kTile = 1024;            // pairs of a workgroup
-constexpr int kTileEach = kTile / kSortThreads;
+// Pairs of a work-item: one up to 65536 pairs, where there are few workgroups, two in
+// longer lists (2^20 pairs 60 us against 69 with one, 55 us against 52 for 2^18).
+constexpr int kEachFew = 1, kEachMany = 2;
+constexpr int64_t kManyPairs = 65536;
 
 __device__ __forceinline__ uint32_t entry_of(const int64_t* index, int64_t t, int64_t ignore,
                                              int64_t V) {
@@ -145,8 +147,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(
 // More pairs: each pass counts the digits of every tile, sums the counts over digits and
 // tiles, and moves the pairs.  The first pass reads the index.  Up to kFewTiles tiles, the
 // workgroups that move the pairs sum all counts themselves, which saves a launch; the
-// counts then lie tile by tile, otherwise digit by digit.
-constexpr int64_t kFewTiles = 64;
+// counts then lie tile by tile.  Otherwise they lie digit by digit, a workgroup to a digit
+// sums them over the tiles, and the digits' totals follow them.
+constexpr int64_t kFewTiles = 128;
 struct Pairs {
     const int64_t* index;  // the first pass's source, NULL afterwards
     int64_t ignore, V;
@@ -159,16 +162,29 @@ struct Pairs {
     }
 };
 
+// The sum of the lanes up to this one.
+__device__ __forceinline__ uint32_t sum_up(uint32_t v) {
+    const int lane = threadIdx.x % kWave;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const uint32_t o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+template <int EACH>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(int64_t T_, Pairs from,
                                                                   int shift, int64_t tiles,
                                                                   uint32_t* __restrict__ counts) {
+    constexpr int kTile = EACH * kSortThreads;
     const bool few = tiles <= kFewTiles;
     __shared__ uint32_t bins[kBins];
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         if (threadIdx.x < kBins) bins[threadIdx.x] = 0;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kTileEach; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             const int64_t at = tile * kTile + i * kSortThreads + threadIdx.x;
             // counts alone: their order does not matter
             if (at < T_) atomicAdd(&bins[(from.key(at) >> shift) & (kBins - 1)], 1u);
@@ -180,93 +196,85 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(int64_t T_, Pa
     }
 }
 
-// Exclusive sums of n values in place, by one workgroup.
-__global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(int64_t n,
+// Exclusive sums over the tiles, in place, of the digit blockIdx.x, and its total.
+__global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(int64_t tiles,
                                                                  uint32_t* __restrict__ counts) {
-    constexpr int kEach = 8;
+    constexpr int kEach = 4;
     __shared__ uint32_t wave_sum[2][kSortWaves];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    uint32_t* const mine = counts + blockIdx.x * tiles;
     uint32_t before = 0;
     int turn = 0;
-    for (int64_t base = 0; base < n; base += kSortThreads * kEach, turn ^= 1) {
+    for (int64_t base = 0; base < tiles; base += kSortThreads * kEach, turn ^= 1) {
         const int64_t at = base + threadIdx.x * kEach;
-        uint32_t c[kEach], mine = 0;
+        uint32_t c[kEach], sum = 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-            const uint32_t v = at + i < n ? counts[at + i] : 0;
-            c[i] = mine;
-            mine += v;
+            const uint32_t v = at + i < tiles ? mine[at + i] : 0;
+            c[i] = sum;
+            sum += v;
         }
-        uint32_t up = mine;
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const uint32_t o = __shfl_up(up, d);
-            if (lane >= d) up += o;
-        }
+        const uint32_t up = sum_up(sum);
         if (lane == kWave - 1) wave_sum[turn][wave] = up;
         __syncthreads();
-        uint32_t mybase = before + up - mine;
+        uint32_t here = before + up - sum;
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) {
-            if (w < wave) mybase += wave_sum[turn][w];
+            if (w < wave) here += wave_sum[turn][w];
             before += wave_sum[turn][w];
         }
 #pragma unroll
         for (int i = 0; i < kEach; ++i)
-            if (at + i < n) counts[at + i] = mybase + c[i];
+            if (at + i < tiles) mine[at + i] = here + c[i];
     }
+    if (threadIdx.x == 0) counts[kBins * tiles + blockIdx.x] = before;
 }
 
+template <int EACH>
 __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(
     int64_t T_, Pairs from, int shift, int64_t tiles, const uint32_t* __restrict__ offsets,
     uint32_t* __restrict__ keys, uint32_t* __restrict__ tokens) {
+    constexpr int kTile = EACH * kSortThreads;
     __shared__ uint32_t count[kSortWaves][kBins];
     __shared__ uint32_t early[2][kBins], wave_sum[kSortWaves];
     const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     const bool few = tiles <= kFewTiles;  // (then a workgroup has one tile)
-    uint32_t place = 0;                   // of the tile's first pair of digit threadIdx.x
+    // `place`: of the first pair of digit threadIdx.x, in the tile (few) or in the list
+    const int digit = threadIdx.x % kBins, half = threadIdx.x / kBins;
+    uint32_t place = 0, all = 0;
     if (few) {
         // each digit's pairs in the tiles before this one, and in all; even tiles by one half
         // of the workgroup, odd ones by the other
-        const int digit = threadIdx.x % kBins, half = threadIdx.x / kBins;
-        uint32_t before = 0, all = 0;
 #pragma unroll 8
         for (int t = half; t < static_cast<int>(tiles); t += 2) {
             const uint32_t c = offsets[t * kBins + digit];
             all += c;
-            before += t < static_cast<int>(blockIdx.x) ? c : 0;
+            place += t < static_cast<int>(blockIdx.x) ? c : 0;
         }
         if (half) {
-            early[0][digit] = before;
+            early[0][digit] = place;
             early[1][digit] = all;
         }
         __syncthreads();
-        uint32_t up = 0;
-        if (!half) {
-            before += early[0][digit];
-            all += early[1][digit];
-            up = all;
-        }
-#pragma unroll
-        for (int d = 1; d < kWave; d <<= 1) {
-            const uint32_t o = __shfl_up(up, d);
-            if (lane >= d) up += o;
-        }
-        if (lane == kWave - 1) wave_sum[wave] = up;
-        __syncthreads();
-        if (!half) {
-            place = up - all + before;
-            for (int w = 0; w < wave; ++w) place += wave_sum[w];
-        }
+        place += early[0][digit];
+        all += early[1][digit];
+    } else {
+        all = offsets[kBins * tiles + digit];
     }
+    // (the second half of the workgroup drops what it sums up)
+    const uint32_t up = sum_up(all);
+    if (lane == kWave - 1) wave_sum[wave] = up;
+    __syncthreads();
+    place += up - all;
+    for (int w = 0; w < wave; ++w) place += wave_sum[w];
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         for (int i = threadIdx.x; i < kSortWaves * kBins; i += kSortThreads)
             (&count[0][0])[i] = 0;
         __syncthreads();
-        const int64_t first = tile * kTile + wave * kTileEach * kWave + lane;
-        uint32_t key[kTileEach], rank[kTileEach];
+        const int64_t first = tile * kTile + wave * EACH * kWave + lane;
+        uint32_t key[EACH], rank[EACH];
 #pragma unroll
-        for (int i = 0; i < kTileEach; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             const int64_t at = first + i * kWave;
             key[i] = at < T_ ? from.key(at) : 0;
             rank[i] = rank_of((key[i] >> shift) & (kBins - 1), at < T_, count[wave]);
@@ -274,7 +282,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(
         __syncthreads();
         // each digit's place in the whole list, then wavefront by wavefront
         if (threadIdx.x < kBins) {
-            uint32_t at = few ? place : offsets[threadIdx.x * tiles + tile];
+            uint32_t at = place + (few ? 0 : offsets[digit * tiles + tile]);
 #pragma unroll
             for (int w = 0; w < kSortWaves; ++w) {
                 const uint32_t c = count[w][threadIdx.x];
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_move_kernel(
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kTileEach; ++i) {
+        for (int i = 0; i < EACH; ++i) {
             const int64_t at = first + i * kWave;
             if (at >= T_) continue;
             const uint32_t to = count[wave][(key[i] >> shift) & (kBins - 1)] + rank[i];
@@ -478,7 +486,6 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(GradArgs a, const T* 
 // that they left.  A workgroup looks at kJoinEach stretches, one lane at each (one to a
 // workgroup, most of which then end at once, took 14 us for 1024 stretches of 4096
 // columns), and adds up to them one after the other, 64 C columns.
-constexpr int64_t kMostStretches = 2048;
 constexpr int kJoinWaves = 8, kJoinThreads = kJoinWaves * kWave, kJoinEach = 8;
 template <typename W, int C, bool ADD>
 __global__ __launch_bounds__(kJoinThreads) void scatter_join_kernel(GradArgs a, W* __restrict__ dW) {
@@ -499,15 +506,14 @@ __global__ __launch_bounds__(kJoinThreads) void scatter_join_kernel(GradArgs a, 
     for (uint64_t todo = __ballot(open); todo; todo &= todo - 1) {
         const int64_t s = base + __builtin_ctzll(todo);
         const uint32_t v = a.keys[(s + 1) * a.stretch];
-        // the stretches after it that hold it, 64 x 64 at a time: at most kMostStretches
-        auto held = [&](int64_t from, int64_t by) {
-            const int64_t i = from + lane * by;
-            return static_cast<int64_t>(
-                __popcll(__ballot(i < a.stretches && a.keys[i * a.stretch] == v)));
-        };
-        const int64_t lines = held(s + 1, kWave);
-        const int64_t lo = s + 1 + (lines - 1) * kWave +
-                           held(s + 1 + (lines - 1) * kWave, 1);
+        // the last stretch that holds it: 64 of them are looked at together, ever closer ones
+        int64_t lo = s + 1;
+        for (int64_t by = kWave * kWave; by > 0; by /= kWave) {
+            const int64_t at = lo + lane * by;
+            const bool holds = at < a.stretches && a.keys[at * a.stretch] == v;
+            lo += (__popcll(__ballot(holds)) - 1) * by;
+        }
+        ++lo;
         float sum[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) sum[c] = 0.0f;
@@ -566,14 +572,18 @@ Plan make_plan(int64_t T, int64_t V, int64_t D) {
     int bits = 1;
     while ((V >> bits) != 0) ++bits;  // the largest key is V
     p.passes = static_cast<int>(ceil_div(bits, kDigit));
-    p.tiles = ceil_div(T, kTile);
+    p.tiles = ceil_div(T, (T <= kManyPairs ? kEachFew : kEachMany) * kSortThreads);
     p.pitch = ceil_div(D, 64) * 64;
     // stretches of 8 to 32 pairs (16384 tokens of 1024 columns: 12.6 us with 16, 15.4 with
-    // 32), longer ones past kMostStretches: an entry named by every token leaves a row in
-    // each, which one workgroup adds
+    // 32), longer ones past some number of them: an entry named by every token leaves a row
+    // in each, which one workgroup adds.  The narrower the rows, the more of them: 2^22
+    // tokens of 128 columns 570 us with 8192, 1520 with 2048; with 32768 475, but 920
+    // instead of 460 where all tokens name one entry
+    int64_t most = (int64_t(1) << 22) / D;
+    most = most < 2048 ? 2048 : most > 8192 ? 8192 : most;
     const int64_t stretch = T < 2048    ? 8
                             : T < 32768 ? 16
-                                        : ceil_div(ceil_div(T, kMostStretches), 32) * 32;
+                                        : ceil_div(ceil_div(T, most), 32) * 32;
     p.stretch = static_cast<int>(stretch);
     p.stretches = ceil_div(T, stretch);
     int64_t at = 0;
@@ -587,7 +597,7 @@ Plan make_plan(int64_t T, int64_t V, int64_t D) {
     if (T > kRankMost) {
         p.keys2 = take(T * 4);
         p.tokens2 = take(T * 4);
-        p.counts = take(p.tiles * kBins * 4);
+        p.counts = take((p.tiles + 1) * kBins * 4);
     }
     p.rows = take(p.stretches * 2 * p.pitch * 4);
     p.bytes = at;
@@ -632,19 +642,20 @@ hipError_t sort(const EmbedArgs& a, const Plan& p, uint8_t* ws, uint32_t** keys,
         return hipGetLastError();
     }
     Pairs from{a.index, a.ignore, a.V, nullptr, nullptr};
-    const unsigned grid = grid_of(p.tiles);
+    uint32_t* const counts = at(p.counts);
+    const dim3 grid(grid_of(p.tiles)), block(kSortThreads);
+    const bool many = a.T > kManyPairs;
+    const auto count = many ? sort_count_kernel<kEachMany> : sort_count_kernel<kEachFew>;
+    const auto move = many ? sort_move_kernel<kEachMany> : sort_move_kernel<kEachFew>;
     for (int pass = 0; pass < p.passes; ++pass) {
         const int shift = pass * kDigit;
         // the last pass ends in keys and tokens
         const bool last = (p.passes - 1 - pass) % 2 == 0;
         uint32_t *const k = at(last ? p.keys : p.keys2), *const t = at(last ? p.tokens : p.tokens2);
-        sort_count_kernel<<<dim3(grid), dim3(kSortThreads), 0, a.stream>>>(a.T, from, shift,
-                                                                           p.tiles, at(p.counts));
+        count<<<grid, block, 0, a.stream>>>(a.T, from, shift, p.tiles, counts);
         if (p.tiles > kFewTiles)
-            sort_scan_kernel<<<dim3(1), dim3(kSortThreads), 0, a.stream>>>(p.tiles * kBins,
-                                                                           at(p.counts));
-        sort_move_kernel<<<dim3(grid), dim3(kSortThreads), 0, a.stream>>>(
-            a.T, from, shift, p.tiles, at(p.counts), k, t);
+            sort_scan_kernel<<<dim3(kBins), block, 0, a.stream>>>(p.tiles, counts);
+        move<<<grid, block, 0, a.stream>>>(a.T, from, shift, p.tiles, counts, k, t);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
         from = Pairs{nullptr, 0, 0, k, t};

@@ -410,6 +410,48 @@ def test_refusals():
     assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("bits,param,grad,master", [(32, "f32", "f32", False), (32, "bf16", "bf16", True),
+                                                    (8, "f16", "f32", True), (8, "bf16", "bf16", False)])
+def test_steps_past_the_caches(bits, param, grad, master):
+    """Past 512 MiB read and written, two tensors, the second off 16-byte boundaries in every
+    array: the bits of the same tensors in steps of their own, which go through the caches."""
+    n = 31_000_003
+    (p, q), (g, h), states = tensors([n, n], param, grad, bits, master, 7, 3)
+
+    def moved(t):
+        return None if t is None else torch.cat((t[:1], t))[1:]
+
+    def moved_codes(t):
+        return torch.cat((t[:1].view(torch.uint8), t.view(torch.uint8)))[1:].view(t.dtype)
+
+    s = states[1]
+    codes = moved if bits == 32 else moved_codes
+    second = (moved(q), moved(h), mg.AdamState(codes(s.avg), codes(s.sq), moved(s.avg_scales),
+                                               moved(s.sq_scales), moved(s.master)))
+    whole = [p, second[0]], [g, second[1]], [states[0], second[2]]
+    written = whole[0] + [t for s in whole[2] for t in s if t is not None]
+    size = sum(t.numel() * t.element_size() for t in whole[1] + 2 * written)  # read and written
+    assert size > 512 << 20
+    parts = [copied([p], [g], [states[0]]), copied([q], [h], [states[1]])]
+    cut = 16 * 4096 * 50
+    say(f"adamw {n} twice {param} {bits} bits")
+    mg.adamw_(*whole, step=4, **HYPER)
+    for (a,), (b,), (t,) in parts:
+        for c in range(0, n, cut):
+            e, k = slice(c, min(n, c + cut)), slice(c // 256, (min(n, c + cut) + 255) // 256)
+            piece = mg.AdamState(t.avg[e], t.sq[e], None if bits == 32 else t.avg_scales[k],
+                                 None if bits == 32 else t.sq_scales[k],
+                                 None if t.master is None else t.master[e])
+            mg.adamw_([a[e]], [b[e]], [piece], step=4, **HYPER)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(whole[0][i], parts[i][0][0])
+        for x, y in zip(whole[2][i], parts[i][2][0]):
+            if x is not None:
+                assert torch.equal(x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x,
+                                   y.view(torch.uint8) if y.dtype == torch.float8_e4m3fn else y)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_more_than_2_31_elements(bits):
     n = (1 << 31) + 4096 * 3 + 77

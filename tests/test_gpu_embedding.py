@@ -302,6 +302,33 @@ def test_repeatable_side_stream_and_graph_replay():
             assert torch.equal(added, once)
 
 
+@pytest.mark.parametrize("T,V,D,dtype", [(40000, 900, 2001, "f32"), (3000, 40000, 2001, "f32"),
+                                         (70000, 3000, 2003, "bf16")])
+def test_rows_past_the_caches(T, V, D, dtype):
+    """From 256 MiB of dy and of rows to zero, which lie off 16-byte boundaries."""
+    both(T, V, D, dtype, T)
+
+
+@pytest.mark.parametrize("run", [15, 16, 17, 32, 33, 47, 48, 49, 64, 65, 200])
+@pytest.mark.parametrize("T", [5000, 40000])
+def test_entries_over_several_stretches(T, run):
+    """Entries of `run` tokens each, so that they begin and end everywhere in the stretches
+    of 16 and 32 pairs, and one more of the rest."""
+    V, D = 4000, 24
+    g = torch.Generator(device="cuda").manual_seed(run)
+    index = (torch.arange(T, device="cuda") // run).clamp(max=V - 1)
+    index = index[torch.randperm(T, generator=g, device="cuda")]
+    dy = torch.randn(T, D, generator=g, device="cuda")
+    say(f"{T} tokens, {run} to an entry")
+    dw = mg.embedding_backward(dy, index, V)
+    wide = mg.embedding_backward(dy.repeat(1, 12), index, V)
+    torch.cuda.synchronize()
+    want = gradient_reference(dy, index, V, 1.0, torch.float32)
+    check(dw, want)
+    # a wavefront to a segment of columns sums in the same order
+    assert torch.equal(wide, dw.repeat(1, 12))
+
+
 def test_more_than_2_31_elements():
     V, D, T = (1 << 31) // 2048 + 300, 2048, 1500
     g = torch.Generator(device="cuda").manual_seed(3)

@@ -301,6 +301,24 @@ def test_repeatable_side_stream_and_graph_replay():
         assert all(torch.equal(a["long" + k], long[k]) for k in ("y", "dx", "dw", "db"))
 
 
+@pytest.mark.parametrize("T,D", [(4, 2), (37, 3), (20, 5), (9, 7)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_rows_shorter_than_a_chunk(T, D, dtype):
+    x, w, b, dy = case(T, D, dtype, "f32", T * D)
+    say(f"layer norm {T}x{D} {dtype}")
+    check(both(x, w, b, dy, 0.1), reference(x, w, b, dy, 0.1))
+
+
+@pytest.mark.parametrize("T,D,dtype", [(24000, 2001, "bf16"), (90000, 515, "f16"), (9000, 4099, "f32"),
+                                       (400000, 120, "bf16"), (1500, 16383, "f32")])
+def test_rows_read_past_the_caches(T, D, dtype):
+    """Past 256 MiB of x, dy and dx: rows off 16-byte boundaries, each form of a row."""
+    x, w, b, dy = case(T, D, dtype, "f32", T)
+    assert 3 * x.numel() * x.element_size() > 256 << 20
+    say(f"layer norm {T}x{D} {dtype}, long")
+    check(both(x, w, b, dy), reference(x, w, b, dy, 1e-5))
+
+
 def test_more_than_2_31_elements():
     T, D = (1 << 31) // 4096 + 700, 4096
     g = torch.Generator(device="cuda").manual_seed(3)
