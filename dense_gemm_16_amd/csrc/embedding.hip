@@ -102,10 +102,11 @@ __device__ __forceinline__ uint32_t rank_of(uint32_t digit, bool held, N* count)
 }
 
 // Up to kRankMost pairs: each workgroup finds the places of kRankKeys of them by counting
-// those that come before, all against all: 32 slices of the list, a work-item to a slice
-// and a pair.  T^2 comparisons, but one short launch over many CUs (1003 pairs XX us against
-// XX by the radix sort below, 4096 XX against XX).
-constexpr int kRankMost = 8192, kRankKeys = 32, kRankSlices = kSortThreads / kRankKeys;
+// those that come before, all against all: 64 slices of the list, a work-item to a slice
+// and a pair.  T^2 comparisons, but one short launch over many CUs: 1003 pairs 3.2 us, 4096
+// 5.2 and 8192 11, against 13, 17 and 20 by the launches of the radix sort below; 16384 take
+// four times as long as 8192, and 18 there.
+constexpr int kRankMost = 8192, kRankKeys = 16, kRankSlices = kSortThreads / kRankKeys;
 __global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(
     int T_, int64_t V, const int64_t* __restrict__ index, int64_t ignore,
     uint32_t* __restrict__ keys, uint32_t* __restrict__ tokens) {
@@ -118,24 +119,24 @@ __global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(
     if (threadIdx.x < kRankKeys) place[threadIdx.x] = 0;
     __syncthreads();
     const int mine = threadIdx.x % kRankKeys, s = threadIdx.x / kRankKeys;
-    const int begin = blockIdx.x * kRankKeys, end = begin + kRankKeys;
-    const int at = begin + mine;
-    const uint32_t key = at < T_ ? all[at] : 0;
+    const int begin = blockIdx.x * kRankKeys, end = begin + kRankKeys, at = begin + mine;
+    const uint32_t key = all[at];
     uint32_t before = 0;
-    // those of [from, to) below a bound; both are multiples of 4
-    auto count = [&](int from, int to, uint32_t bound) {
+    // those of [from, to) that come before it; `bound(j)`: how far up the entry of pair j may
+    // go.  Both ends are multiples of 4.
+    auto count = [&](int from, int to, auto bound) __attribute__((always_inline)) {
+#pragma unroll 4
         for (int j = from; j < to; j += 4) {
             const u32x4 k = *reinterpret_cast<const u32x4*>(&all[j]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) before += k[e] < bound;
+            for (int e = 0; e < 4; ++e) before += k[e] < bound(j + e);
         }
     };
     const int lo = s * slice, hi = lo + slice;
-    count(lo, hi < begin ? hi : begin, key + 1);  // earlier tokens of the same entry come first
-    count(lo > end ? lo : end, hi, key);
-    if (s == 0) {
-        for (int j = begin; j < end && j < T_; ++j) before += all[j] < key + (j < at);
-    }
+    // earlier tokens of the same entry come first
+    count(lo, hi < begin ? hi : begin, [&](int) { return key + 1; });
+    count(lo > end ? lo : end, hi, [&](int) { return key; });
+    if (s == 0) count(begin, end, [&](int j) { return key + (j < at); });
     atomicAdd(&place[mine], before);  // (a count: its order does not matter)
     __syncthreads();
     if (threadIdx.x < kRankKeys && at < T_) {
