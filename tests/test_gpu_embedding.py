@@ -120,6 +120,12 @@ def test_long_lists(T, V, D):
     both(T, V, D, "f32" if T % 2 else "bf16", T)
 
 
+@pytest.mark.parametrize("kind", ["mixed", "one"])
+def test_a_list_of_2_24(kind):
+    """Counts over thousands of tiles, stretches longer than a wavefront, rows of one element."""
+    both((1 << 24) + 3, 70000, 1, "f32", 1, kind)
+
+
 @pytest.mark.parametrize("kind", ["one", "ignored", "bad"])
 @pytest.mark.parametrize("T,V,D", [(1, 40, 16), (31, 1, 24), (700, 900, 520), (33000, 700, 64)])
 def test_special_lists(T, V, D, kind):

@@ -319,6 +319,12 @@ def test_rows_read_past_the_caches(T, D, dtype):
     check(both(x, w, b, dy), reference(x, w, b, dy, 1e-5))
 
 
+def test_the_longest_row():
+    x, w, b, dy = case(2, 1 << 24, "bf16", "f32", 1)
+    say("layer norm 2x2^24")
+    check(both(x, w, b, dy), reference(x, w, b, dy, 1e-5))
+
+
 def test_more_than_2_31_elements():
     T, D = (1 << 31) // 4096 + 700, 4096
     g = torch.Generator(device="cuda").manual_seed(3)
