@@ -978,7 +978,9 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, stats:
             # (x.new_empty((T, D)) for a packed x, in less time)
             out, ldy = (torch.empty_like(x) if ldx == D else x.new_empty((T, D))), D
         else:
-            _gradient("out", True, out, x)
+            _check_device("out", out, device)
+            if out.dtype is not x.dtype or out.shape != x.shape:
+                raise ValueError(f"out must be {x.dtype}, {T} x {D}")
             ldy = _ld(out)
         mean = rstd = pm = pr = None
         if stats:
@@ -1078,7 +1080,8 @@ def embedding(w, index, *, scale: float = 1.0, ignore_index: int = -100, out=Non
         if other:
             _run_on(stream, device, w, index, out)
         st = lib().migemm_embedding_forward(T, V, D, dt, w.data_ptr() or None, ldw, pi,
-                                            ignore_index, scale, out.data_ptr() or None, ldy, stream)
+                                            ignore_index, scale, out.data_ptr() or None, ldy,
+                                            stream)
         if st != OK:
             raise MigemmError(st, "migemm_embedding_forward")
     return out
@@ -1184,7 +1187,8 @@ def adamw_(params, grads, states, *, step, lr=1e-3, betas=(0.9, 0.999), eps: flo
     may be tensors of one element on the GPU: they are read where the step runs, so that a
     captured step follows them; a ``grad_scale`` of infinity or NaN skips the step.  Runs
     on ``stream`` (default: torch's current stream; another one first waits for it)
-    without synchronising."""
+    without synchronising.  Autograd does not see the call, which writes the parameters
+    past its version counters."""
     torch = _torch or _load_torch()
     count = len(params)
     if len(grads) != count or len(states) != count:

@@ -9,16 +9,17 @@
 //
 // 8-bit states.  m and r = sqrt(v) are E4M3 codes times one FP32 scale for each block of
 // 256 consecutive elements: the block's largest magnitude / 448 (E4M3's largest), so that
-// the largest element is exact and a block whose gradients stop decays as it should,
+// the largest element comes back as it was and a block whose gradients stop decays as it should,
 // which it would not under a power of two.  The root is kept instead of v because its
 // range is the square root of v's.  A positive root never becomes code 0: the element's
 // next step would be divided by little more than eps.  The update uses m and r as they
 // were before rounding to codes.
 //
-// Bound by memory: 28 bytes an element with FP32 parameters and states, 10.06 with 16-bit
-// parameters and 8-bit states.  A workgroup takes a piece of 4096 elements of one tensor,
-// found in a table of tensors that the launch carries in its arguments: no copy of it to
-// the device, and a captured launch keeps it.
+// Bound by memory: 28 bytes an element with FP32 parameters and states (5.5 TB/s), 10.06
+// with 16-bit parameters and 8-bit states (738 million elements 1240 us, 6.0 TB/s).  A
+// workgroup takes a piece of 4096 elements of one tensor, found in a table of tensors that
+// the launch carries in its arguments: no copy of it to the device, and a captured launch
+// keeps it.
 #include <math.h>
 
 #include "rows.hpp"
@@ -325,7 +326,8 @@ template <typename P, typename G, bool ONCE> Kernel kernel_of(bool eight, bool m
     return eight ? adamw_kernel<P, G, true, false, ONCE> : adamw_kernel<P, G, false, false, ONCE>;
 }
 template <typename P, typename G> Kernel kernel_of(const AdamArgs& a, bool once) {
-    return once ? kernel_of<P, G, true>(a.eight, a.master) : kernel_of<P, G, false>(a.eight, a.master);
+    return once ? kernel_of<P, G, true>(a.eight, a.master)
+                : kernel_of<P, G, false>(a.eight, a.master);
 }
 
 // Past this many bytes a step's tensors go past the caches: the last-level one (256 MiB)

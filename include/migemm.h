@@ -494,9 +494,10 @@ int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int 
  *
  * W and B are vectors of D of w_dtype (`dtype` or MIGEMM_F32); NULL stands for ones, or
  * zeros.  Sums and statistics are FP32 (a variance below its range counts as 0), the
- * variance is the mean of squared distances from mu.  mean and rstd (T floats each, NULL where not wanted) receive mu and r, which the
- * backward pass reads.  eps is finite and at least 0; a row of equal elements with eps 0
- * is NaN, and so is a row with a NaN or an infinity.
+ * variance is the mean of squared distances from mu.  mean and rstd (T floats each, NULL
+ * where not wanted) receive mu and r, which the backward pass reads.  eps is finite and at
+ * least 0; a row of equal elements with eps 0 is NaN, and so is a row with a NaN or an
+ * infinity.
  *
  * Backward, with g = dY W:  dX = r (g - mean(g) - h mean(g h));  dW = the sum over rows of
  * dY h;  dB = that of dY (dX in `dtype`, the others in w_dtype; each may be NULL where not
@@ -558,11 +559,11 @@ int migemm_embedding_backward(int64_t T, int64_t V, int64_t D, int dtype, const 
  *         - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  *
  * in FP32, the factors rounded once from FP64 (v too: gradients below 2^-63 lose digits in
- * it, those below 2^-75 are lost, and it is infinite for those of 2^64).  param is of param_dtype (MIGEMM_F32,
- * MIGEMM_F16 or MIGEMM_BF16), grad of grad_dtype (param_dtype or MIGEMM_F32).  master, in
- * all tensors of a call or in none, is an FP32 copy of a 16-bit parameter: p is then read
- * from and written to it, and param receives it rounded.  Without one a 16-bit parameter
- * loses steps below half of its own last place.
+ * it, those below 2^-75 are lost, and it is infinite for those of 2^64).  param is of
+ * param_dtype (MIGEMM_F32, MIGEMM_F16 or MIGEMM_BF16), grad of grad_dtype (param_dtype or
+ * MIGEMM_F32).  master, in all tensors of a call or in none, is an FP32 copy of a 16-bit
+ * parameter: p is then read from and written to it, and param receives it rounded.  Without
+ * one a 16-bit parameter loses steps below half of its own last place.
  *
  * state_bits 32: avg holds m and sq holds v, FP32; the scales are NULL.
  * state_bits 8: avg holds m and sq the root of v as E4M3 bytes (sign, four exponent bits of
