@@ -13,13 +13,13 @@ not been built, every call raises ``RuntimeError``: there is no fallback.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import os
 from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(_HERE, "libmigemm.so")
+BINDING_PATH = os.path.join(_HERE, "_binding.so")
 
 F32, F16, BF16, I8, I32 = 0, 1, 2, 3, 4
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE = 0, 1, 2, 3, 4
@@ -930,27 +930,46 @@ def linear_distillation_backward(x, w, teacher_logits, teacher_index, lse, stude
 
 # ------------------------------------------- around the output layer's losses
 
-def _vector(name, t, device, like, size):
-    """Pointer of a norm's weight or bias (or None), checked against `like`'s dtype."""
-    if t is None:
-        return None
-    if t.device != device:
-        _check_device(name, t, device)
-    if t.dtype is not like or t.shape != (size,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {like} vector of {size} (got {t.dtype}, "
-                         f"{tuple(t.shape)}, strides {t.stride()})")
-    return t.data_ptr() or None
+_native = None
 
 
-def _second_type(name, dtype, x):
-    """The code of `dtype`, x's own or float32."""
-    torch = _torch or _load_torch()
-    code = _dtype_code(x)
-    if dtype is x.dtype:
-        return code
-    if dtype is not torch.float32:
-        raise ValueError(f"{name} must be {x.dtype} or torch.float32 (got {dtype})")
-    return F32
+def _load_native():
+    """The calls over torch tensors in C++ (csrc/binding.cpp), kept in a global; raises
+    RuntimeError if they are not built."""
+    global _native
+    if _native is None:
+        lib()
+        _torch or _load_torch()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"_binding.so is not built ({BINDING_PATH}); run "
+                               "`python dense_gemm_16_amd/build.py` or __graft_entry__.build()")
+        from . import _binding
+        _native = _binding
+    return _native
+
+
+def _call(where, function, anchor, stream, *args):
+    """The tuple of tensors of a native call on `stream` (None: torch's current one on
+    `anchor`'s device).  On another stream the call waits for what is queued on the
+    current one, and its tensors, the workspace among them, are kept from being reused before
+    the work queued there has finished."""
+    torch = _torch
+    index = anchor.get_device()  # (-1 on the host: the call refuses it)
+    current = torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
+    if stream is None or stream == current or index < 0:
+        r = function(*args, current, False)
+    else:
+        device = anchor.device
+        _run_on(stream, device, *(t for t in args if isinstance(t, torch.Tensor)))
+        r = function(*args, stream, True)
+        if type(r) is tuple:
+            s = torch.cuda.ExternalStream(stream, device=device)
+            for t in r:
+                if t is not None:
+                    t.record_stream(s)
+    if type(r) is not tuple:
+        raise MigemmError(r, where)
+    return r
 
 
 def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, stats: bool = True,
@@ -963,37 +982,8 @@ def layer_norm(x, weight=None, bias=None, *, eps: float = 1e-5, out=None, stats:
     or both float32; None stands for ones, or zeros.  Runs on ``stream`` (default: torch's
     current stream; another one first waits for it) without synchronising.  Autograd does
     not see the call: the gradients come from the backward function."""
-    torch = _torch or _load_torch()
-    device = x.device
-    if not x.is_cuda:
-        _check_device("x", x, device)
-    dt, ldx = _dtype_code(x), _ld(x)
-    T, D = x.shape
-    kind = (weight if weight is not None else bias if bias is not None else x).dtype
-    wd = dt if kind is x.dtype else _second_type("weight and bias", kind, x)
-    pw, pb = _vector("weight", weight, device, kind, D), _vector("bias", bias, device, kind, D)
-    with _device_of(device):
-        stream, other = _stream_of(stream, device)
-        if out is None:
-            # (x.new_empty((T, D)) for a packed x, in less time)
-            out, ldy = (torch.empty_like(x) if ldx == D else x.new_empty((T, D))), D
-        else:
-            _check_device("out", out, device)
-            if out.dtype is not x.dtype or out.shape != x.shape:
-                raise ValueError(f"out must be {x.dtype}, {T} x {D}")
-            ldy = _ld(out)
-        mean = rstd = pm = pr = None
-        if stats:
-            mean = torch.empty(T, dtype=torch.float32, device=device)
-            rstd = torch.empty_like(mean)
-            pm, pr = mean.data_ptr() or None, rstd.data_ptr() or None
-        if other:
-            _run_on(stream, device, x, weight, bias, out, mean, rstd)
-        st = lib().migemm_layer_norm_forward(T, D, dt, x.data_ptr() or None, ldx, wd, pw, pb, eps,
-                                             out.data_ptr() or None, ldy, pm, pr, stream)
-        if st != OK:
-            raise MigemmError(st, "migemm_layer_norm_forward")
-    return out, mean, rstd
+    return _call("migemm_layer_norm_forward", (_native or _load_native()).layer_norm, x, stream,
+                 x, weight, bias, eps, out, stats)[:3]
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dw=None, db=None,
@@ -1003,54 +993,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, dx=None, dw=None, db=None,
     the upstream gradient ``dy`` (``x``'s shape and dtype).  ``dw`` and ``db`` are of
     ``weight``'s dtype (``x``'s where ``weight`` is None, with no ``dw`` then).  Each is
     written into if given; one that is neither given nor needed is None."""
-    torch = _torch or _load_torch()
-    device = x.device
-    if not (x.is_cuda and dy.device == device):
-        _check_device("x", x, device)
-        _check_device("dy", dy, device)
-    if dy.dtype is not x.dtype or dy.shape != x.shape:
-        raise ValueError("dy must have x's shape and dtype")
-    dt, ldx, lddy = _dtype_code(x), _ld(x), _ld(dy)
-    T, D = x.shape
-    kind = x.dtype if weight is None else weight.dtype
-    wd = dt if kind is x.dtype else _second_type("weight", kind, x)
-    pw = _vector("weight", weight, device, kind, D)
-    pm = _row_vector("mean", mean, device, torch.float32, T)
-    pr = _row_vector("rstd", rstd, device, torch.float32, T)
-    if weight is None:
-        if dw is not None:
-            raise ValueError("dw needs a weight")
-        need_dw = False
-    with _device_of(device):
-        stream, other = _stream_of(stream, device)
-        pdx, lddx, pdw, pdb = None, D, None, None
-        if dx is not None:
-            pdx, lddx = _out_matrix(_gradient("dx", True, dx, x))
-        elif need_dx:
-            dx = torch.empty_like(x) if ldx == D else x.new_empty((T, D))
-            pdx = dx.data_ptr() or None
-        if dw is not None:
-            pdw = _vector("dw", dw, device, kind, D)
-        elif need_dw:
-            dw = torch.empty_like(weight)
-            pdw = dw.data_ptr()
-        if db is not None:
-            pdb = _vector("db", db, device, kind, D)
-        elif need_db:
-            db = x.new_empty(D, dtype=kind) if weight is None else torch.empty_like(weight)
-            pdb = db.data_ptr()
-        st, n = migemm_layer_norm_workspace_size(T, D, dw is not None or db is not None)
-        if st != OK:
-            raise MigemmError(st, "migemm_layer_norm_workspace_size")
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        if other:
-            _run_on(stream, device, dy, x, weight, mean, rstd, dx, dw, db, ws)
-        st = lib().migemm_layer_norm_backward(
-            T, D, dt, dy.data_ptr() or None, lddy, x.data_ptr() or None, ldx, wd, pw, pm, pr, pdx,
-            lddx, pdw, pdb, ws.data_ptr() or None, n, stream)
-        if st != OK:
-            raise MigemmError(st, "migemm_layer_norm_backward")
-    return dx, dw, db
+    return _call("migemm_layer_norm_backward", (_native or _load_native()).layer_norm_backward, x,
+                 stream, dy, x, weight, mean, rstd, dx, dw, db, need_dx, need_dw, need_db)[:3]
 
 
 def embedding(w, index, *, scale: float = 1.0, ignore_index: int = -100, out=None, stream=None):
@@ -1060,31 +1004,8 @@ def embedding(w, index, *, scale: float = 1.0, ignore_index: int = -100, out=Non
     row of zeros, one outside the table a row of NaN.  Runs on ``stream`` (default:
     torch's current stream; another one first waits for it) without synchronising.
     Autograd does not see the call: the gradient comes from ``embedding_backward``."""
-    torch = _torch or _load_torch()
-    device = w.device
-    if not w.is_cuda:
-        _check_device("w", w, device)
-    dt, ldw = _dtype_code(w), _ld(w)
-    V, D = w.shape
-    T = index.numel()
-    pi = _row_vector("index", index, device, torch.int64, T)
-    with _device_of(device):
-        stream, other = _stream_of(stream, device)
-        if out is None:
-            out, ldy = w.new_empty((T, D)), D
-        else:
-            _check_device("out", out, device)
-            if out.dtype is not w.dtype or out.shape != (T, D):
-                raise ValueError(f"out must be {w.dtype}, {T} x {D}")
-            ldy = _ld(out)
-        if other:
-            _run_on(stream, device, w, index, out)
-        st = lib().migemm_embedding_forward(T, V, D, dt, w.data_ptr() or None, ldw, pi,
-                                            ignore_index, scale, out.data_ptr() or None, ldy,
-                                            stream)
-        if st != OK:
-            raise MigemmError(st, "migemm_embedding_forward")
-    return out
+    return _call("migemm_embedding_forward", (_native or _load_native()).embedding, w, stream, w,
+                 index, scale, ignore_index, out)[0]
 
 
 def embedding_backward(dy, index, vocab: int, *, scale: float = 1.0, ignore_index: int = -100,
@@ -1095,39 +1016,8 @@ def embedding_backward(dy, index, vocab: int, *, scale: float = 1.0, ignore_inde
     where ``accumulate`` is set (the gradient that an output layer with the same weight has
     left, say); otherwise it is allocated with ``out_dtype`` (default: ``dy``'s).  Sums are
     float32, in an order that does not depend on timing."""
-    torch = _torch or _load_torch()
-    device = dy.device
-    if not dy.is_cuda:
-        _check_device("dy", dy, device)
-    dt, lddy = _dtype_code(dy), _ld(dy)
-    T, D = dy.shape
-    pi = _row_vector("index", index, device, torch.int64, T)
-    if dw is None:
-        if accumulate:
-            raise ValueError("accumulate needs an existing dw")
-        kind = out_dtype or dy.dtype
-    else:
-        _check_device("dw", dw, device)
-        kind = dw.dtype
-        if dw.shape != (vocab, D) or (out_dtype is not None and out_dtype is not kind):
-            raise ValueError(f"dw must have shape ({vocab}, {D}) (and out_dtype, if given)")
-    wd = _second_type("dw", kind, dy)
-    with _device_of(device):
-        stream, other = _stream_of(stream, device)
-        if dw is None:
-            dw = torch.empty((vocab, D), dtype=kind, device=device)
-        st, n = migemm_embedding_workspace_size(T, vocab, D)
-        if st != OK:
-            raise MigemmError(st, "migemm_embedding_workspace_size")
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        if other:
-            _run_on(stream, device, dy, index, dw, ws)
-        st = lib().migemm_embedding_backward(
-            T, vocab, D, dt, dy.data_ptr() or None, lddy, pi, ignore_index, float(scale),
-            bool(accumulate), wd, dw.data_ptr() or None, _ld(dw), ws.data_ptr() or None, n, stream)
-        if st != OK:
-            raise MigemmError(st, "migemm_embedding_backward")
-    return dw
+    return _call("migemm_embedding_backward", (_native or _load_native()).embedding_backward, dy,
+                 stream, dy, index, vocab, scale, ignore_index, dw, accumulate, out_dtype)[0]
 
 
 class AdamState(NamedTuple):
@@ -1166,15 +1056,6 @@ def adamw_state(param, *, bits: int = 32, master: bool = False) -> AdamState:
                      torch.zeros(blocks, device=device), copy)
 
 
-def _step_tensor(name, t, device, dtype):
-    """Pointer of a number on the device, checked."""
-    _check_device(name, t, device)
-    if t.dtype is not dtype or t.numel() != 1:
-        raise ValueError(f"{name} must be a number or one {dtype} on the GPU (got {t.dtype}, "
-                         f"{tuple(t.shape)})")
-    return t.data_ptr()
-
-
 def adamw_(params, grads, states, *, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
            weight_decay: float = 0.01, grad_scale=None, stream=None) -> None:
     """One AdamW step over lists of parameters, their gradients and their ``AdamState``s,
@@ -1189,77 +1070,21 @@ def adamw_(params, grads, states, *, step, lr=1e-3, betas=(0.9, 0.999), eps: flo
     on ``stream`` (default: torch's current stream; another one first waits for it)
     without synchronising.  Autograd does not see the call, which writes the parameters
     past its version counters."""
-    torch = _torch or _load_torch()
-    count = len(params)
-    if len(grads) != count or len(states) != count:
-        raise ValueError(f"{count} parameters, {len(grads)} gradients and {len(states)} states")
-    if count == 0:
-        return
-    device, pd, gd = params[0].device, params[0].dtype, grads[0].dtype
-    _check_device("params", params[0], device)
-    avgs, sqs, avg_scales, sq_scales, masters = zip(*states)
-    f32, sd = torch.float32, avgs[0].dtype
-    eight, master = sd is not f32, masters[0] is not None
-    if eight and sd is not torch.float8_e4m3fn and sd is not torch.uint8:
-        raise ValueError(f"states must be float32, float8_e4m3fn or uint8 (got {sd})")
-    if master and pd is f32:
-        raise ValueError("float32 parameters take no master copy")
-    for list_, given in ((avg_scales, eight), (sq_scales, eight), (masters, master)):
-        # (by type: `None in` would compare the tensors by value)
-        none = list(map(type, list_)).count(type(None))
-        if none != (0 if given else count):
-            raise ValueError("states must all be of 32 or all of 8 bits, with a master copy in "
-                             "all or in none")
-    pcode, gcode = _dtype_code(params[0]), _second_type("gradients", gd, params[0])
-    sizes = list(map(torch.Tensor.numel, params))
-    # the fields of each tensor in turn
-    fields = [0] * (8 * count)
-    fields[0::8] = sizes
-    fields[1::8] = _step_pointers(params, pd, sizes, device)
-    fields[2::8] = _step_pointers(grads, gd, sizes, device)
-    if master:
-        fields[3::8] = _step_pointers(masters, f32, sizes, device)
-    fields[4::8] = _step_pointers(avgs, sd, sizes, device)
-    fields[5::8] = _step_pointers(sqs, sd, sizes, device)
-    if eight:
-        blocks = [(n + 255) // 256 for n in sizes]
-        fields[6::8] = _step_pointers(avg_scales, f32, blocks, device)
-        fields[7::8] = _step_pointers(sq_scales, f32, blocks, device)
-    numbers = [t if isinstance(t, torch.Tensor) else None for t in (lr, step, grad_scale)]
-    o = AdamwOptions(0.0 if numbers[0] is not None else float(lr), float(betas[0]),
-                     float(betas[1]), float(eps), float(weight_decay),
-                     1 if numbers[1] is not None else int(step))
-    if numbers[0] is not None:
-        o.lr_device = _step_tensor("lr", lr, device, f32)
-    if numbers[1] is not None:
-        o.step_device = _step_tensor("step", step, device, torch.int64)
-    with _device_of(device):
-        stream, other = _stream_of(stream, device)
-        if grad_scale is not None:
-            if numbers[2] is None:
-                numbers[2] = torch.full((), float(grad_scale), dtype=f32, device=device)
-            o.grad_scale = _step_tensor("grad_scale", numbers[2], device, f32)
-        if other:
-            _run_on(stream, device, *params, *grads, *numbers, *(t for s in states for t in s))
-        fields = array.array("q", fields)  # (a ctypes array of them takes three times as long)
-        st = lib().migemm_adamw(count, fields.buffer_info()[0], pcode, gcode, 8 if eight else 32,
-                                ctypes.byref(o), stream)
-        if st != OK:
-            raise MigemmError(st, "migemm_adamw")
-
-
-def _step_pointers(tensors, kind, sizes, device):
-    """Pointers of a step's tensors, checked: one dtype and device, contiguous, of the
-    sizes given.  (map over the methods: a loop that names them took twice as long.)"""
+    native = _native or _load_native()
     torch = _torch
-    T = torch.Tensor
-    if not (set(map(T.dtype.__get__, tensors)) == {kind}
-            and set(map(T.get_device, tensors)) == {device.index}
-            and all(map(T.is_contiguous, tensors)) and list(map(T.numel, tensors)) == sizes):
-        for t, size in zip(tensors, sizes):
-            if (t.dtype is not kind or t.numel() != size or t.device != device
-                    or not t.is_contiguous()):
-                raise ValueError(f"a tensor of the step must be contiguous, {kind}, of {size} "
-                                 f"elements on {device} (got {t.dtype}, {t.numel()} on {t.device}, "
-                                 f"strides {tuple(t.stride())})")
-    return map(T.data_ptr, tensors)
+    if len(params) == 0 and len(grads) == 0 and len(states) == 0:
+        return
+    anchor = params[0] if len(params) else grads[0] if len(grads) else states[0][0]
+    index = anchor.get_device()
+    current = torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
+    other = stream is not None and stream != current and index >= 0
+    if grad_scale is not None and not isinstance(grad_scale, torch.Tensor) and index >= 0:
+        grad_scale = torch.full((), float(grad_scale), dtype=torch.float32, device=anchor.device)
+    if other:
+        numbers = (t for t in (lr, step, grad_scale) if isinstance(t, torch.Tensor) and t.is_cuda)
+        held = (t for s in states for t in s if t is not None)
+        _run_on(stream, anchor.device, *params, *grads, *held, *numbers)
+    st = native.adamw(params, grads, states, step, lr, *betas, eps, weight_decay, grad_scale,
+                      stream if other else current, False)
+    if st != OK:
+        raise MigemmError(st, "migemm_adamw")

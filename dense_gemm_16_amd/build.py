@@ -1,7 +1,8 @@
 """Builds libmigemm.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
 
 Every source is compiled separately (in parallel) into ``_build/`` and linked
-into ``libmigemm.so`` next to this file.  Flags:
+into ``libmigemm.so`` next to this file; ``binding.cpp``, host code against torch's
+headers, becomes ``_binding.so`` there.  Flags:
 
 * ``--offload-arch=gfx950``: MI355X only, no other targets;
 * ``-Xclang -target-feature -Xclang -packed-fp32-ops``: no packed FP32
@@ -26,6 +27,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmigemm.so")
+BINDING = os.path.join(PKG, "_binding.so")
 RESOURCES = os.path.join(PKG, "kernel_resources.json")
 SOURCES = ["api.cpp", "mfma16.hip", "mfma_i8.hip", "regtile_mfma.hip", "naive.hip",
            "lds_tiled.hip", "regtile_valu.hip", "fill.hip", "convert.hip", "pack.hip",
@@ -55,6 +57,7 @@ SLOW_FIRST = ("mfma16_f16_gen_14", "mfma16_bf16_gen_14", "mfma_i8_4", "mfma16_f1
               "mfma16_f16_plain_14", "mfma16_bf16_gen_1", "mfma16_f16_gen_0",
               "mfma16_bf16_plain_14", "mfma16_bf16_gen_0", "mfma16_bf16_gen_4")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CXX = os.environ.get("CXX", "g++")
 FLAGS = ["-x", "hip", "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]
@@ -134,6 +137,40 @@ def _up_to_date(obj: str, src: str) -> bool:
     return all(os.path.getmtime(d) < t for d in deps)
 
 
+def _build_binding(force: bool) -> str:
+    """Compiles binding.cpp; the object."""
+    import sysconfig
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+    if not force and _up_to_date(obj, src):
+        return obj
+    inc = os.path.join(_torch_dir(), "include")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1",
+           "-I", os.path.join(ROOT, "include"), "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-c", src, "-o", obj]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"{CXX} failed on binding.cpp:\n{p.stdout}{p.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    """Links _binding.so against torch's libraries (loaded by then) and libmigemm.so."""
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [CXX, "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-lc10",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python", "-L", PKG, "-l:libmigemm.so",
+           "-Wl,-rpath,$ORIGIN"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"link of _binding.so failed:\n{p.stdout}{p.stderr}")
+    os.replace(tmp, BINDING)
+
+
+def _torch_dir() -> str:
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
 def units():
     """(source, object name, defines) of every compile, slowest first."""
     u = PARTS + [(src, os.path.splitext(src)[0], []) for src in SOURCES]
@@ -149,6 +186,7 @@ def build(jobs: int | None = None, force: bool = True) -> str:
     us = units()
     jobs = jobs or max(1, len(os.sched_getaffinity(0)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_build_binding, force)
         objs = list(ex.map(lambda u: _compile(u, force), us))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
@@ -156,6 +194,7 @@ def build(jobs: int | None = None, force: bool = True) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{p.stdout}{p.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding.result())
     _write_resources(objs)
     return LIB
 
