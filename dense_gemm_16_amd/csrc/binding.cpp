@@ -15,9 +15,11 @@
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <exception>
 #include <sstream>
 #include <string>
 #include <vector>
@@ -55,8 +57,9 @@ int code_of(const at::Tensor& t) {
         case at::kChar: return MIGEMM_I8;
         case at::kInt: return MIGEMM_I32;
         default:
-            refuse("unsupported dtype ", name_of(t.scalar_type()), "; expected float32, float16, bfloat16, "
-                   "int8 (operands) or int32 (output of an int8 product)");
+            refuse("unsupported dtype ", name_of(t.scalar_type()),
+                   "; expected float32, float16, bfloat16, int8 (operands) or int32 (output of an "
+                   "int8 product)");
     }
 }
 
@@ -227,11 +230,11 @@ PyObject* layer_norm_backward(PyObject* const* a) {
     if (st != MIGEMM_OK) return status(st);
     const at::Tensor ws = workspace(bytes, x);
     st = migemm_layer_norm_backward(
-        T, D, code_of(x), pointer(dy), lddy, pointer(x), ldx, wd, weight ? pointer(*weight) : nullptr,
-        static_cast<const float*>(pointer(mean)), static_cast<const float*>(pointer(rstd)),
-        dx.defined() ? writable(dx) : nullptr, dx.defined() ? leading(dx) : D,
-        dw.defined() ? writable(dw) : nullptr, db.defined() ? writable(db) : nullptr, writable(ws),
-        bytes, stream_of(a[11]));
+        T, D, code_of(x), pointer(dy), lddy, pointer(x), ldx, wd,
+        weight ? pointer(*weight) : nullptr, static_cast<const float*>(pointer(mean)),
+        static_cast<const float*>(pointer(rstd)), dx.defined() ? writable(dx) : nullptr,
+        dx.defined() ? leading(dx) : D, dw.defined() ? writable(dw) : nullptr,
+        db.defined() ? writable(db) : nullptr, writable(ws), bytes, stream_of(a[11]));
     return st == MIGEMM_OK ? tuple({dx, dw, db, ws}, truth(a[12])) : status(st);
 }
 
@@ -296,7 +299,8 @@ struct Items {
 };
 
 // One element on the GPU, and its address.
-const void* number_on_device(const char* name, PyObject* o, at::Device device, at::ScalarType kind) {
+const void* number_on_device(const char* name, PyObject* o, at::Device device,
+                             at::ScalarType kind) {
     const at::Tensor& t = tensor(name, o);
     check_device(name, t, device);
     if (t.scalar_type() != kind || t.numel() != 1)
@@ -344,7 +348,8 @@ PyObject* adamw(PyObject* const* a) {
         }
         if ((s.at[2] != Py_None) != eight || (s.at[3] != Py_None) != eight ||
             (s.at[4] != Py_None) != master)
-            refuse("states must all be of 32 or all of 8 bits, with a master copy in all or in none");
+            refuse("states must all be of 32 or all of 8 bits, with a master copy in all or in "
+                   "none");
         const int64_t size = tensor("params", params.at[i]).numel(), blocks = (size + 255) / 256;
         migemm_adamw_tensor& t = list[static_cast<size_t>(i)];
         t.count = size;
@@ -358,7 +363,8 @@ PyObject* adamw(PyObject* const* a) {
     }
     migemm_adamw_options o{};
     if (THPVariable_Check(a[3]))
-        o.step_device = static_cast<const int64_t*>(number_on_device("step", a[3], device, at::kLong));
+        o.step_device =
+            static_cast<const int64_t*>(number_on_device("step", a[3], device, at::kLong));
     else
         o.step = whole(a[3]);
     if (THPVariable_Check(a[4]))
@@ -388,12 +394,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t count) {
     } catch (const Refused& e) {
         PyErr_SetString(PyExc_ValueError, e.what.c_str());
     } catch (const PythonError&) {
-    } catch (const c10::OutOfMemoryError& e) {
-        PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
-    } catch (const c10::Error& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // torch's own, its allocator's among them
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }

@@ -367,3 +367,13 @@ def test_more_than_2_31_elements():
     torch.cuda.synchronize()
     assert torch.equal(y[some], small[index[some]]) and torch.equal(y[::9973], small[index[::9973]])
     check(dw, gradient_reference(dy[some], index[some], V, 1.0, dy.dtype))
+
+
+def test_out_of_memory_is_torchs_error():
+    """An output that no allocation can hold (64 TiB) raises what torch's allocator raises; the
+    next call runs."""
+    w = torch.ones(1, 1 << 20, dtype=torch.float32, device="cuda")
+    index = torch.zeros(1 << 24, dtype=torch.int64, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        mg.embedding(w, index)
+    assert torch.equal(mg.embedding(w, index[:1]), w)
