@@ -9,7 +9,8 @@
 // list is cut into stretches of equal length, whatever entries they hold, so that an entry
 // that a tenth of all tokens name is summed by as many wavefronts as its tokens need;
 // what a stretch holds of an entry that it shares with its neighbours goes to the
-// workspace as one FP32 row, and a last kernel adds those.
+// workspace as one FP32 row, and a last kernel adds those.  Up to 1024 tokens take one launch
+// and no sort: each token's workgroup looks for the others of its entry.
 //
 // Bound by memory: dy is read once, a row of dw written once (read too where it is added
 // to).  Rows of dw that no token names are zeroed by workgroups of the same launch, and
@@ -105,9 +106,9 @@ __device__ __forceinline__ uint32_t rank_of(uint32_t digit, bool held, uint32_t*
 
 // Up to kRankMost pairs: each workgroup finds the places of kRankKeys of them by counting
 // those that come before, all against all: 64 slices of the list, a work-item to a slice
-// and a pair.  T^2 comparisons, but one short launch over many CUs: 1003 pairs 3.2 us, 4096
-// 5.2 and 8192 11, against 13, 17 and 20 by the launches of the radix sort below; 16384 take
-// four times as long as 8192, and 18 there.
+// and a pair.  T^2 comparisons, but one short launch over many CUs: 4096 pairs 5.2 us and 8192
+// 11, against 17 and 20 by the launches of the radix sort below; 16384 take four times as long
+// as 8192, and 18 there.
 constexpr int kRankMost = 8192, kRankKeys = 16, kRankSlices = kSortThreads / kRankKeys;
 __global__ __launch_bounds__(kSortThreads) void sort_rank_kernel(
     int total, int64_t V, const int64_t* __restrict__ index, int64_t ignore,
@@ -321,6 +322,8 @@ struct GradArgs {
     int lpr;             // lanes of a segment of a row, a power of two up to 64
     int64_t segs;        // segments of a row: a chunk of dy a lane each
     int64_t sum_groups;  // workgroups that add; those after them zero rows
+    int64_t few_parts;   // of few tokens: workgroups of a token
+    bool once;           // of few tokens: zeros go past the caches
 };
 
 // The first pair of an entry of v or more, by a whole wavefront: 64 places at a time, so
@@ -336,27 +339,18 @@ __device__ __forceinline__ int64_t first_of(const GradArgs& a, int64_t v) {
     return lo < a.T ? lo : a.T;
 }
 
-// Zeros the rows of entries v0 .. v0 + kZeroRows - 1 that no token names, by one
-// wavefront.
+// Zeros rows of entries v0 .. v0 + kZeroRows - 1, those that no bit of `named` stands for,
+// by one wavefront.
 constexpr int kZeroRows = 16;
 template <typename W, int C, bool ONCE>
-__device__ __forceinline__ void zero_rows(const GradArgs& a, int64_t v0, W* __restrict__ dW) {
+__device__ __forceinline__ void zero_rows(const GradArgs& a, int64_t v0, uint64_t named,
+                                          W* __restrict__ dW) {
     const int lane = threadIdx.x % kWave;
-    const int64_t v1 = v0 + kZeroRows < a.V ? v0 + kZeroRows : a.V;
-    uint64_t absent = (uint64_t(1) << (v1 - v0)) - 1;
-    for (int64_t v = v0; v < v1;) {
-        // 64 pairs from the first of an entry not seen yet
-        const int64_t at = first_of(a, v) + lane;
-        const int64_t key = at < a.T ? a.keys[at] : a.V;
-#pragma unroll
-        for (int i = 0; i < kZeroRows; ++i)
-            if (__ballot(key == v0 + i)) absent &= ~(uint64_t(1) << i);
-        v = __builtin_amdgcn_readlane(static_cast<uint32_t>(key), kWave - 1) + int64_t(1);
-    }
+    const int64_t rows = v0 + kZeroRows < a.V ? kZeroRows : a.V - v0;
     W zero[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) zero[i] = narrow<W>(0.0f);
-    for (uint64_t todo = absent; todo; todo &= todo - 1) {
+    for (uint64_t todo = ((uint64_t(1) << rows) - 1) & ~named; todo; todo &= todo - 1) {
         W* const row = dW + (v0 + __builtin_ctzll(todo)) * a.ldw;
         for (int64_t k = lane * C; k < a.D; k += kWave * C) {
             const Span<C> piece(k, a.D);
@@ -366,6 +360,23 @@ __device__ __forceinline__ void zero_rows(const GradArgs& a, int64_t v0, W* __re
                 store_whole(row + piece.at, zero);
         }
     }
+}
+
+// Those of the entries v0 .. v0 + kZeroRows - 1 that sorted tokens name.
+__device__ __forceinline__ uint64_t named_rows(const GradArgs& a, int64_t v0) {
+    const int lane = threadIdx.x % kWave;
+    const int64_t v1 = v0 + kZeroRows < a.V ? v0 + kZeroRows : a.V;
+    uint64_t named = 0;
+    for (int64_t v = v0; v < v1;) {
+        // 64 pairs from the first of an entry not seen yet
+        const int64_t at = first_of(a, v) + lane;
+        const int64_t key = at < a.T ? a.keys[at] : a.V;
+#pragma unroll
+        for (int i = 0; i < kZeroRows; ++i)
+            if (__ballot(key == v0 + i)) named |= uint64_t(1) << i;
+        v = __builtin_amdgcn_readlane(static_cast<uint32_t>(key), kWave - 1) + int64_t(1);
+    }
+    return named;
 }
 
 // A group of a.lpr lanes sums a segment of columns over one stretch.  An entry that begins
@@ -383,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(GradArgs a, const T* 
     if (blockIdx.x >= a.sum_groups) {
         const int64_t v0 = (static_cast<int64_t>(blockIdx.x - a.sum_groups) * (kThreads / kWave) +
                             threadIdx.x / kWave) * kZeroRows;
-        if (v0 < a.V) zero_rows<W, C, ONCE>(a, v0, dW);
+        if (v0 < a.V) zero_rows<W, C, ONCE>(a, v0, named_rows(a, v0), dW);
         return;
     }
     const int lpr = WAVE ? kWave : a.lpr;
@@ -408,7 +419,7 @@ __global__ __launch_bounds__(kThreads) void scatter_kernel(GradArgs a, const T* 
             const uint64_t same = __ballot(n + lane < a.stretch && entry(from + n + lane) == v);
             const uint64_t mine = same >> shift & (~uint64_t(0) >> (kWave - lpr));
             n += __popcll(mine);
-            if (__popcll(mine) < lpr) break;
+            if (static_cast<int>(__popcll(mine)) < lpr) break;
         }
         return n;
     };
@@ -553,6 +564,125 @@ __global__ __launch_bounds__(kJoinThreads) void scatter_join_kernel(GradArgs a,
     }
 }
 
+// Up to kFewTokens tokens, in one launch and without a sort.  A workgroup stands for a token
+// and kFewWaves segments of columns.  It looks at all tokens, KEYS a lane, and lists those of
+// its token's entry, in order; the workgroup of the first of them sums them, a wavefront to a
+// segment.  Where the list is long, those of the first kFewWaves tokens sum a segment each, a
+// wavefront to a part of the list, joined in order.  Workgroups behind all these zero the rows
+// that no token names.  Against the sort, sums and join of longer lists: 16 tokens of 4096
+// BF16 columns, added, 3.1 us instead of 8.5, 256 3.7 instead of 10.5, 1003 7.7 instead of 15;
+// 1003 into 30001 x 1032 FP16 of its own 13.4 instead of 19.6; 1003 of one and the same entry
+// of 4096 columns 21.5 instead of 15.8, four times as many would take four times as long.
+constexpr int64_t kFewTokens = 1024;
+constexpr int kFewAhead = 8, kFewWaves = 4, kFewMany = 16;
+template <typename T, typename W, int C, int KEYS, bool ADD>
+__global__ __launch_bounds__(kFewWaves * kWave) void scatter_few_kernel(
+    GradArgs a, const int64_t* __restrict__ index, int64_t ignore, const T* __restrict__ dY,
+    W* __restrict__ dW) {
+    __shared__ int list[kFewWaves * KEYS * kWave];
+    __shared__ float lds[kFewWaves][kWave][C + 1];
+    __shared__ int found[kFewWaves], earlier[kFewWaves];
+    __shared__ uint32_t rows[kFewWaves * kZeroRows / 32];
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const int tokens = static_cast<int>(a.T), first = wave * KEYS * kWave + lane;
+    const uint32_t none = static_cast<uint32_t>(a.V);
+    uint32_t key[KEYS];
+#pragma unroll
+    for (int k = 0; k < KEYS; ++k) {
+        const int t = first + k * kWave;
+        const uint32_t v = entry_of(index, t < tokens ? t : tokens - 1, ignore, a.V);
+        key[k] = t < tokens ? v : none;
+    }
+    if (blockIdx.x >= a.sum_groups) {
+        const int64_t v0 = static_cast<int64_t>(blockIdx.x - a.sum_groups) * kFewWaves * kZeroRows;
+        if (threadIdx.x < kFewWaves * kZeroRows / 32) rows[threadIdx.x] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < KEYS; ++k) {
+            const uint32_t row = key[k] - static_cast<uint32_t>(v0);  // (2^31 and more: before v0)
+            if (row < kFewWaves * kZeroRows) atomicOr(&rows[row / 32], 1u << row % 32);
+        }
+        __syncthreads();
+        const int mine = wave * kZeroRows;
+        if (v0 + mine >= a.V) return;
+        const uint32_t named = rows[mine / 32] >> mine % 32;
+        if (a.once)
+            zero_rows<W, C, true>(a, v0 + mine, named, dW);
+        else
+            zero_rows<W, C, false>(a, v0 + mine, named, dW);
+        return;
+    }
+    const int token = static_cast<int>(blockIdx.x / a.few_parts);
+    const uint32_t v = entry_of(index, token, ignore, a.V);
+    if (v == none) return;
+    int held = 0, before = 0;
+    uint64_t same[KEYS];
+#pragma unroll
+    for (int k = 0; k < KEYS; ++k) {
+        same[k] = __ballot(key[k] == v);
+        held += static_cast<int>(__popcll(same[k]));
+        before += static_cast<int>(__popcll(__ballot(key[k] == v && first + k * kWave < token)));
+    }
+    if (lane == 0) {
+        found[wave] = held;
+        earlier[wave] = before;
+    }
+    __syncthreads();
+    int count = 0, rank = 0, at = 0;
+#pragma unroll
+    for (int w = 0; w < kFewWaves; ++w) {
+        at += w < wave ? found[w] : 0;
+        count += found[w];
+        rank += earlier[w];
+    }
+    const bool many = count > kFewMany;
+    if (rank >= (many ? kFewWaves : 1)) return;  // (all of the workgroup)
+#pragma unroll
+    for (int k = 0; k < KEYS; ++k) {
+        if (key[k] == v)
+            list[at + __popcll(same[k] & ((uint64_t(1) << lane) - 1))] = first + k * kWave;
+        at += static_cast<int>(__popcll(same[k]));
+    }
+    __syncthreads();
+    const int64_t seg = static_cast<int64_t>(blockIdx.x % a.few_parts) * kFewWaves +
+                        (many ? rank : wave);
+    if (seg >= a.segs) return;  // (many: all of the workgroup)
+    const Span<C> piece((seg * kWave + lane) * C, a.D);
+    const int each = many ? (count + kFewWaves - 1) / kFewWaves : count;
+    const int from = many ? wave * each : 0, to = from + each < count ? from + each : count;
+    W o[C];
+    if constexpr (ADD) piece.load(dW + v * a.ldw, o);
+    float sum[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) sum[c] = 0.0f;
+    for (int i = from; i < to; i += kFewAhead) {
+        T e[kFewAhead][C];
+#pragma unroll
+        for (int u = 0; u < kFewAhead; ++u) {
+            const int t = list[i + u < to ? i + u : to - 1];
+            piece.load(dY + static_cast<int64_t>(t) * a.ldy, e[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kFewAhead; ++u)
+#pragma unroll
+            for (int c = 0; c < C; ++c) sum[c] += i + u < to ? to_f32(e[u][c]) : 0.0f;
+    }
+    if (many) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) lds[wave][lane][c] = sum[c];
+        __syncthreads();
+        if (wave != 0) return;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int w = 1; w < kFewWaves; ++w) sum[c] += lds[w][lane][c];
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        o[c] = narrow<W>(ADD ? fmaf(a.scale, sum[c], to_f32(o[c])) : a.scale * sum[c]);
+    piece.store_own(dW + v * a.ldw, o);
+}
+
 // dw of no tokens: zeros.
 template <typename W>
 __global__ __launch_bounds__(kThreads) void zero_kernel(int64_t V, int64_t D, W* __restrict__ dW,
@@ -674,6 +804,35 @@ hipError_t sort(const EmbedArgs& a, const Plan& p, uint8_t* ws, uint32_t** keys,
 // those 35 instead of 32.
 constexpr double kOnceBytes = 256 << 20;
 
+template <typename T, typename W, int C>
+hipError_t scatter_few(const EmbedArgs& a) {
+    const int64_t zero_groups = a.accumulate ? 0 : ceil_div(a.V, kZeroRows * kFewWaves);
+    GradArgs g{};
+    g.T = a.T;
+    g.V = a.V;
+    g.D = a.D;
+    g.ldy = a.ldy;
+    g.ldw = a.ldw;
+    g.scale = a.scale;
+    g.segs = ceil_div(ceil_div(a.D, C), kWave);
+    g.few_parts = ceil_div(g.segs, kFewWaves);
+    g.sum_groups = a.T * g.few_parts;
+    g.once = static_cast<double>(sizeof(W)) * a.V * a.D >= kOnceBytes;
+    auto go = [&](auto keys, auto add) {
+        scatter_few_kernel<T, W, C, decltype(keys)::value, decltype(add)::value>
+            <<<dim3(static_cast<unsigned>(g.sum_groups + zero_groups)), dim3(kFewWaves * kWave), 0,
+               a.stream>>>(g, a.index, a.ignore, static_cast<const T*>(a.dY),
+                           static_cast<W*>(a.dW));
+        return hipGetLastError();
+    };
+    auto by_keys = [&](auto add) {
+        if (a.T <= kFewWaves * kWave) return go(std::integral_constant<int, 1>{}, add);
+        if (a.T <= 2 * kFewWaves * kWave) return go(std::integral_constant<int, 2>{}, add);
+        return go(std::integral_constant<int, 4>{}, add);
+    };
+    return a.accumulate ? by_keys(std::true_type{}) : by_keys(std::false_type{});
+}
+
 template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, void* ws) {
     W* const dw = static_cast<W*>(a.dW);
     if (a.T == 0) {
@@ -681,6 +840,7 @@ template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, 
         zero_kernel<W><<<dim3(grid_of(a.V)), dim3(kThreads), 0, a.stream>>>(a.V, a.D, dw, a.ldw);
         return hipGetLastError();
     }
+    if (a.T <= kFewTokens) return scatter_few<T, W, C>(a);
     const Plan p = make_plan(a.T, a.V, a.D);
     uint8_t* const base = static_cast<uint8_t*>(ws);
     uint32_t *keys, *tokens;
@@ -714,7 +874,7 @@ template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, 
         scatter_kernel<T, W, C, WAVE, ADD, ONCE>
             <<<groups, threads, 0, a.stream>>>(g, static_cast<const T*>(a.dY), dw);
         const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || g.stretches < 2) return e;
+        if (e != hipSuccess) return e;
         scatter_join_kernel<W, C, ADD><<<joins, dim3(kJoinThreads), 0, a.stream>>>(g, dw);
         return hipGetLastError();
     };
@@ -746,7 +906,7 @@ hipError_t launch_embedding(const EmbedArgs& a) {
 }
 
 int64_t embedding_workspace(int64_t T, int64_t V, int64_t D) {
-    return T == 0 ? 0 : make_plan(T, V, D).bytes;
+    return T <= kFewTokens ? 0 : make_plan(T, V, D).bytes;
 }
 
 hipError_t launch_embedding_backward(const EmbedArgs& a, void* ws) {

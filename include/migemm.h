@@ -538,8 +538,8 @@ int migemm_layer_norm_backward(int64_t T, int64_t D, int dtype, const void* dY, 
  * the index and the sizes alone: the tokens are sorted by entry, with no atomics on sums.
  *
  * T is below 2^31 (0: a no-op, or dW = 0), V 1 to 2^28, D 1 to 2^21.  Any alignment and
- * leading dimensions.  The workspace (migemm_embedding_workspace_size bytes) and the other
- * rules are as for the losses above.
+ * leading dimensions.  The workspace (migemm_embedding_workspace_size bytes, none for few
+ * tokens) and the other rules are as for the losses above.
  */
 int migemm_embedding_forward(int64_t T, int64_t V, int64_t D, int dtype, const void* W,
                              int64_t ldw, const int64_t* index, int64_t ignore_index, float scale,

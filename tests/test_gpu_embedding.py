@@ -377,3 +377,101 @@ def test_out_of_memory_is_torchs_error():
     with pytest.raises(torch.OutOfMemoryError):
         mg.embedding(w, index)
     assert torch.equal(mg.embedding(w, index[:1]), w)
+
+
+# either side of the lists of one launch (1024 tokens; a lane holds one, two or four of
+# them), and the shapes of SIZES in lists that are sorted
+@pytest.mark.parametrize("kind", ["mixed", "one", "ignored", "bad"])
+@pytest.mark.parametrize("T,V,D", [(15, 3, 9), (16, 2, 600), (17, 2, 600), (70, 1, 2056),
+                                   (255, 40, 65), (256, 9, 4104), (257, 300, 24), (511, 70, 3),
+                                   (512, 4000, 136), (513, 65, 1029), (1000, 7, 2500),
+                                   (1024, 16, 264), (1024, 129, 1), (1025, 16, 264)])
+def test_lists_of_one_launch(T, V, D, kind):
+    both(T, V, D, "f32" if D % 2 else "bf16", T + D, kind)
+    both(T, V, D, "f16", T + D, kind)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,V,D", [(1025, 1, 1), (1100, 1000, 64), (1200, 5, 3), (1031, 300, 8),
+                                   (2000, 300, 40), (1500, 511, 129), (1027, 512, 520),
+                                   (1040, 131072, 4096), (1100, 2000, 8200)])
+def test_short_sorted_lists(T, V, D, dtype):
+    both(T, V, D, dtype, T + V + D)
+
+
+@pytest.mark.parametrize("T", [90, 700, 2500])
+def test_strided_and_misaligned_lists(T):
+    """Rows off 16-byte boundaries, with NaN between them, which no sum takes in and no store
+    meets."""
+    V, D = 130, 531
+    for dtype in ("f32", "f16", "bf16"):
+        w, index, dy = case(T, V, D, dtype, T)
+        index[T // 2:] = torch.where(index[T // 2:] >= 0, 5, index[T // 2:])
+        big = torch.full((T, D + 6), float("nan"), dtype=dy.dtype, device="cuda")
+        big[:, 3:3 + D] = dy
+        for accumulate in (False, True):
+            out = torch.full((V, D + 9), float("nan"), dtype=dy.dtype, device="cuda")
+            out[:, 1:1 + D] = w
+            say(f"embedding {T} strided {dtype} {accumulate}")
+            mg.embedding_backward(big[:, 3:3 + D], index, V, scale=0.75, dw=out[:, 1:1 + D],
+                                  accumulate=accumulate)
+            torch.cuda.synchronize()
+            check(out[:, 1:1 + D], gradient_reference(dy, index, V, 0.75, dy.dtype,
+                                                      w if accumulate else None))
+            assert torch.isnan(out[:, 0]).all() and torch.isnan(out[:, 1 + D:]).all()
+
+
+@pytest.mark.parametrize("V", [(1 << 18) - 1, 1 << 18, (1 << 27) - 1, (1 << 27) + 3])
+def test_sorted_lists_of_long_tables(V):
+    """Entries of two, three and four digits."""
+    T, D = 9000, 2
+    g = torch.Generator(device="cuda").manual_seed(V)
+    index = torch.randint(0, V, (T,), generator=g, device="cuda")
+    index[:4] = torch.tensor([V - 1, 0, V // 2, V - 1])
+    dy = torch.randn(T, D, generator=g, device="cuda")
+    say(f"{T} of a table of {V}")
+    for n in (1500, T):  # by counting, by digits
+        dw = mg.embedding_backward(dy[:n], index[:n], V)
+        torch.cuda.synchronize()
+        rows, where = torch.unique(index[:n], return_inverse=True)
+        check(dw[rows], gradient_reference(dy[:n], where, len(rows), 1.0, torch.float32))
+        dw[rows] = 0
+        assert not dw.any()
+
+
+@pytest.mark.parametrize("T", [40, 800])
+def test_one_launch_repeated_and_captured(T):
+    w, index, dy = case(T, 90, 1300, "bf16", T)
+    index[::3] = 7
+    say(f"embedding of {T} captured")
+    want = mg.embedding_backward(dy, index, 90, scale=2.0)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = mg.embedding_backward(dy, index, 90, scale=2.0, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(got, want)
+    g = torch.cuda.CUDAGraph()
+    added = w.clone()
+    with torch.cuda.graph(g):
+        held = mg.embedding_backward(dy, index, 90, scale=2.0)
+        mg.embedding_backward(dy, index, 90, scale=2.0, dw=added, accumulate=True)
+    more = w.clone()
+    for i in range(3):
+        index.copy_(index.roll(i))
+        held.fill_(float("nan"))
+        added.copy_(more)
+        want = mg.embedding_backward(dy, index, 90, scale=2.0)
+        mg.embedding_backward(dy, index, 90, scale=2.0, dw=more, accumulate=True)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, want) and torch.equal(added, more)
+
+
+def test_gradient_rows_of_short_sorted_lists_may_hold_anything():
+    w, index, dy = case(1500, 90, 72, "f16", 6, "bad")
+    inside = (index >= 0) & (index < 90)
+    dy[~inside] = float("nan")
+    say("rows without an entry, sorted")
+    dw = mg.embedding_backward(dy, index, 90)
+    torch.cuda.synchronize()
+    check(dw, gradient_reference(torch.where(inside[:, None], dy, 0.0), index, 90, 1.0, dy.dtype))
