@@ -9,7 +9,7 @@
 // list is cut into stretches of equal length, whatever entries they hold, so that an entry
 // that a tenth of all tokens name is summed by as many wavefronts as its tokens need;
 // what a stretch holds of an entry that it shares with its neighbours goes to the
-// workspace as one FP32 row, and a last kernel adds those.  Up to 1024 tokens take one launch
+// workspace as one FP32 row, and a last kernel adds those.  Up to 2048 tokens take one launch
 // and no sort: each token's workgroup looks for the others of its entry.
 //
 // Bound by memory: dy is read once, a row of dw written once (read too where it is added
@@ -567,20 +567,29 @@ __global__ __launch_bounds__(kJoinThreads) void scatter_join_kernel(GradArgs a,
 // Up to kFewTokens tokens, in one launch and without a sort.  A workgroup stands for a token
 // and kFewWaves segments of columns.  It looks at all tokens, KEYS a lane, and lists those of
 // its token's entry, in order; the workgroup of the first of them sums them, a wavefront to a
-// segment.  Where the list is long, those of the first kFewWaves tokens sum a segment each, a
-// wavefront to a part of the list, joined in order.  Workgroups behind all these zero the rows
-// that no token names.  Against the sort, sums and join of longer lists: 16 tokens of 4096
-// BF16 columns, added, 3.1 us instead of 8.5, 256 3.7 instead of 10.5, 1003 7.7 instead of 15;
-// 1003 into 30001 x 1032 FP16 of its own 13.4 instead of 19.6; 1003 of one and the same entry
-// of 4096 columns 21.5 instead of 15.8, four times as many would take four times as long.
-constexpr int64_t kFewTokens = 1024;
+// segment.  Where the list is long, those of the first kFewGroups tokens sum a quarter of a
+// segment each, 16 lanes to a part of the list, joined in order.  Workgroups behind all these
+// zero the rows that no token names.
+//
+// Each token's workgroups read the whole list, so the work grows with its square, and wide
+// rows take more workgroups: kFewWide of them at most (of 16-bit rows; FP32 rows take twice as
+// many).  Against the sort, sums and join of longer lists, added: 16 tokens of 4096 BF16
+// columns 3.3 us instead of 8.5, 256 3.9 instead of 10.5, 2048 14.5 instead of 21.8, all of one
+// entry 17.8 instead of 18.0; 512 of 16384 FP32 columns 21.7 instead of 24.7.  2048 of 8192
+// BF16 columns would take 31.6 instead of 26.6, 4096 of 4096 30.7 instead of 25.2.
+constexpr int64_t kFewTokens = 2048, kFewWide = 4096;
+bool few_tokens(int64_t T, int64_t D) {
+    return T <= kFewTokens && T * ceil_div(D, 2048) <= kFewWide;
+}
 constexpr int kFewAhead = 8, kFewWaves = 4, kFewMany = 16;
+constexpr int kFewLanes = 16, kFewQuarters = kWave / kFewLanes;
+constexpr int kFewGroups = kFewWaves * kFewQuarters;  // (kFewMany or fewer)
 template <typename T, typename W, int C, int KEYS, bool ADD>
 __global__ __launch_bounds__(kFewWaves * kWave) void scatter_few_kernel(
     GradArgs a, const int64_t* __restrict__ index, int64_t ignore, const T* __restrict__ dY,
     W* __restrict__ dW) {
     __shared__ int list[kFewWaves * KEYS * kWave];
-    __shared__ float lds[kFewWaves][kWave][C + 1];
+    __shared__ float lds[kFewGroups][kFewLanes][C + 1];
     __shared__ int found[kFewWaves], earlier[kFewWaves];
     __shared__ uint32_t rows[kFewWaves * kZeroRows / 32];
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
@@ -636,7 +645,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void scatter_few_kernel(
         rank += earlier[w];
     }
     const bool many = count > kFewMany;
-    if (rank >= (many ? kFewWaves : 1)) return;  // (all of the workgroup)
+    if (rank >= (many ? kFewGroups : 1)) return;  // (all of the workgroup)
 #pragma unroll
     for (int k = 0; k < KEYS; ++k) {
         if (key[k] == v)
@@ -645,11 +654,13 @@ __global__ __launch_bounds__(kFewWaves * kWave) void scatter_few_kernel(
     }
     __syncthreads();
     const int64_t seg = static_cast<int64_t>(blockIdx.x % a.few_parts) * kFewWaves +
-                        (many ? rank : wave);
+                        (many ? rank / kFewQuarters : wave);
     if (seg >= a.segs) return;  // (many: all of the workgroup)
-    const Span<C> piece((seg * kWave + lane) * C, a.D);
-    const int each = many ? (count + kFewWaves - 1) / kFewWaves : count;
-    const int from = many ? wave * each : 0, to = from + each < count ? from + each : count;
+    const int chunk = many ? rank % kFewQuarters * kFewLanes + lane % kFewLanes : lane;
+    const Span<C> piece((seg * kWave + chunk) * C, a.D);
+    const int each = many ? (count + kFewGroups - 1) / kFewGroups : count;
+    const int from = many ? threadIdx.x / kFewLanes * each : 0;
+    const int to = from + each < count ? from + each : count;
     W o[C];
     if constexpr (ADD) piece.load(dW + v * a.ldw, o);
     float sum[C];
@@ -669,13 +680,13 @@ __global__ __launch_bounds__(kFewWaves * kWave) void scatter_few_kernel(
     }
     if (many) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) lds[wave][lane][c] = sum[c];
+        for (int c = 0; c < C; ++c) lds[threadIdx.x / kFewLanes][lane % kFewLanes][c] = sum[c];
         __syncthreads();
-        if (wave != 0) return;
+        if (threadIdx.x >= kFewLanes) return;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int w = 1; w < kFewWaves; ++w) sum[c] += lds[w][lane][c];
+            for (int g = 1; g < kFewGroups; ++g) sum[c] += lds[g][lane][c];
     }
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -828,7 +839,9 @@ hipError_t scatter_few(const EmbedArgs& a) {
     auto by_keys = [&](auto add) {
         if (a.T <= kFewWaves * kWave) return go(std::integral_constant<int, 1>{}, add);
         if (a.T <= 2 * kFewWaves * kWave) return go(std::integral_constant<int, 2>{}, add);
-        return go(std::integral_constant<int, 4>{}, add);
+        if (a.T <= 4 * kFewWaves * kWave) return go(std::integral_constant<int, 4>{}, add);
+        static_assert(kFewTokens == 8 * kFewWaves * kWave, "the longest list fits");
+        return go(std::integral_constant<int, 8>{}, add);
     };
     return a.accumulate ? by_keys(std::true_type{}) : by_keys(std::false_type{});
 }
@@ -840,7 +853,7 @@ template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, 
         zero_kernel<W><<<dim3(grid_of(a.V)), dim3(kThreads), 0, a.stream>>>(a.V, a.D, dw, a.ldw);
         return hipGetLastError();
     }
-    if (a.T <= kFewTokens) return scatter_few<T, W, C>(a);
+    if (few_tokens(a.T, a.D)) return scatter_few<T, W, C>(a);
     const Plan p = make_plan(a.T, a.V, a.D);
     uint8_t* const base = static_cast<uint8_t*>(ws);
     uint32_t *keys, *tokens;
@@ -906,7 +919,7 @@ hipError_t launch_embedding(const EmbedArgs& a) {
 }
 
 int64_t embedding_workspace(int64_t T, int64_t V, int64_t D) {
-    return T <= kFewTokens ? 0 : make_plan(T, V, D).bytes;
+    return few_tokens(T, D) ? 0 : make_plan(T, V, D).bytes;
 }
 
 hipError_t launch_embedding_backward(const EmbedArgs& a, void* ws) {

@@ -475,3 +475,38 @@ def test_gradient_rows_of_short_sorted_lists_may_hold_anything():
     dw = mg.embedding_backward(dy, index, 90)
     torch.cuda.synchronize()
     check(dw, gradient_reference(torch.where(inside[:, None], dy, 0.0), index, 90, 1.0, dy.dtype))
+
+
+# either side of 2048 tokens, and of 4096 workgroups of 2048 columns
+@pytest.mark.parametrize("kind", ["mixed", "one", "bad"])
+@pytest.mark.parametrize("T,V,D", [(1500, 70, 33), (2047, 300, 72), (2048, 5, 520), (2048, 900, 4096),
+                                   (2049, 300, 72), (1365, 40, 6144), (1366, 40, 6144),
+                                   (33, 17, 251903), (2, 3, 1 << 21), (3, 2, (1 << 21) - 5)])
+def test_lists_and_rows_of_one_launch(T, V, D, kind):
+    both(T, V, D, "f32" if D % 2 else "f16", T + D, kind)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,V,D", [(2049, 1, 1), (2100, 1000, 64), (2200, 5, 3), (2050, 300, 8),
+                                   (3000, 300, 40), (2500, 511, 129), (2051, 512, 520),
+                                   (2060, 20000, 4096), (1100, 2000, 8200), (2100, 2000, 8200)])
+def test_sorted_lists(T, V, D, dtype):
+    both(T, V, D, dtype, T + V + D)
+    if D < 1000:
+        both(T, V, D, dtype, T + V + D, "one")
+
+
+def test_gradient_rows_of_sorted_lists_may_hold_anything():
+    w, index, dy = case(2500, 90, 72, "f16", 6, "bad")
+    inside = (index >= 0) & (index < 90)
+    dy[~inside] = float("nan")
+    say("rows without an entry, sorted")
+    dw = mg.embedding_backward(dy, index, 90)
+    torch.cuda.synchronize()
+    check(dw, gradient_reference(torch.where(inside[:, None], dy, 0.0), index, 90, 1.0, dy.dtype))
+    at = int(inside.nonzero()[0])
+    dy[at, 3] = float("-inf")
+    dw = mg.embedding_backward(dy, index, 90)
+    torch.cuda.synchronize()
+    bad = ~torch.isfinite(dw)
+    assert bad[index[at], 3] and int(bad.sum()) == 1
