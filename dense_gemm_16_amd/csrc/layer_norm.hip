@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kLongThreads = 1024;  // a row that no register form holds
 constexpr int kColumns = 8;         // its columns per work-item, backwards
+constexpr int64_t kMaxInRegisters = 16384;  // (and longer ones are those)
 // Work-items of the workgroups that are given rows to walk: four or five wavefronts a SIMD
 // are what the registers leave room for.
 constexpr int64_t kResident = 256 * 1024;
@@ -31,7 +32,8 @@ template <int LANES> constexpr int kThreads = LANES <= kWave ? 256 : LANES;
 template <int LANES> constexpr int kRows = kThreads<LANES> / LANES;
 template <int LANES> constexpr int kWaves = LANES <= kWave ? 1 : LANES / kWave;
 
-// Sums of N values over a row's lanes, in every one of them.  `lds` is free again once
+// Sums of N values over a row's lanes (the workgroup, or LANES of it with an `lds` of their
+// own), in every one of them.  `lds` is free again once
 // the row's work-items have passed the barrier of the call after this one.
 template <int LANES, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (&lds)[N][kWaves<LANES>]) {
@@ -40,7 +42,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (&lds)[N][kWaves<L
     if constexpr (LANES > kWave) {
         if (threadIdx.x % kWave == 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) lds[i][threadIdx.x / kWave] = v[i];
+            for (int i = 0; i < N; ++i) lds[i][threadIdx.x % LANES / kWave] = v[i];
         }
         __syncthreads();
 #pragma unroll
@@ -313,6 +315,115 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
     }
 }
 
+// Few rows, backwards, in one launch: dw and db need no sums over a row, only what the forward
+// pass left.  The first workgroups take rows, one to LANES lanes; those behind them a band of
+// 128 bytes of columns each, eight lanes to a row, and join their rows' sums in order.  x and
+// dy are read twice, the second time from the caches.  Against partial sums and their join:
+// 76 x 1032 FP16 3.1 us instead of 6.4, 1003 8.7 instead of 10.5, 512 x 8192 BF16 8.2 instead
+// of 15.1; past kFewRows rows a band's workgroup is at work too long (2048 x 1032 18.6 instead
+// of 12.8), past kFewBytes of x the second reading costs more than a launch (1024 x 3000 FP32
+// 13.7 instead of 11.4).
+constexpr int64_t kFewRows = 1024, kFewBytes = 8 << 20;
+bool few_rows(int64_t T, int64_t D, int bytes) {
+    return T <= kFewRows && D <= kMaxInRegisters && T * D * bytes <= kFewBytes;
+}
+template <int LANES> constexpr int kFewThreads = LANES <= 512 ? 512 : LANES;
+constexpr int kBandLanes = 8, kBandAhead = 4;
+template <typename T, typename W, int C, int LANES, int CH>
+__global__ __launch_bounds__(kFewThreads<LANES>) void norm_few_kernel(
+    int rows, int D, const T* __restrict__ dY, int64_t lddy, const T* __restrict__ X, int64_t ldx,
+    const W* __restrict__ weight, const float* __restrict__ means,
+    const float* __restrict__ rstds, T* __restrict__ dX, int64_t lddx, W* __restrict__ dW,
+    W* __restrict__ dB, int row_groups) {
+    constexpr int THREADS = kFewThreads<LANES>;
+    if (static_cast<int>(blockIdx.x) < row_groups) {
+        constexpr int R = THREADS / LANES;
+        __shared__ float lds[R][2][kWaves<LANES>];
+        const int lane = threadIdx.x % LANES, part = threadIdx.x / LANES;
+        const Pieces<C, LANES, CH> piece(D, lane);
+        // (past the last row that one again, whose result comes out as the same bits)
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * R + part;
+        const int64_t row = at < rows ? at : rows - 1;
+        T x[CH][C], dy[CH][C];
+        W w[CH][C];
+        piece.load(X + row * ldx, x);
+        piece.load(dY + row * lddy, dy);
+        if (weight) piece.load(weight, w);
+        const float mean = means[row], rstd = rstds[row], d = static_cast<float>(D);
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                if (!weight) w[c][i] = narrow<W>(1.0f);
+                const float h = (to_f32(x[c][i]) - mean) * rstd;
+                const float g = to_f32(dy[c][i]) * to_f32(w[c][i]);
+                if (i >= piece.skip[c]) {
+                    sum[0] += g;
+                    sum[1] += g * h;
+                }
+            }
+        row_sums<LANES>(sum, lds[part]);
+        const float a = sum[0] / d, b = sum[1] / d;
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const float h = (to_f32(x[c][i]) - mean) * rstd;
+                const float g = to_f32(dy[c][i]) * to_f32(w[c][i]);
+                x[c][i] = narrow<T>(rstd * (g - a - h * b));
+            }
+        piece.store(dX + row * lddx, x);
+        return;
+    }
+    constexpr int kBand = kBandLanes * C, kGroups = THREADS / kBandLanes;
+    __shared__ float lds[2][kGroups / 2][kBand + 1];
+    const int first = (blockIdx.x - row_groups) * kBand, lane = threadIdx.x % kBandLanes;
+    const Span<C> piece(first + lane * C, D);
+    float dw[C], db[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) dw[i] = db[i] = 0.0f;
+    for (int row = threadIdx.x / kBandLanes; row < rows; row += kGroups * kBandAhead) {
+        T x[kBandAhead][C], dy[kBandAhead][C];
+        float mean[kBandAhead], rstd[kBandAhead];
+#pragma unroll
+        for (int u = 0; u < kBandAhead; ++u) {
+            const int64_t r = row + u * kGroups < rows ? row + u * kGroups : rows - 1;
+            piece.load(X + r * ldx, x[u]);
+            piece.load(dY + r * lddy, dy[u]);
+            mean[u] = means[r];
+            rstd[u] = rstds[r];
+        }
+#pragma unroll
+        for (int u = 0; u < kBandAhead; ++u)
+            if (row + u * kGroups < rows) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    const float o = to_f32(dy[u][i]);
+                    dw[i] += o * ((to_f32(x[u][i]) - mean[u]) * rstd[u]);
+                    db[i] += o;
+                }
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        dw[i] += row_rotated<8>(dw[i]);  // (the other row of the 16 lanes)
+        db[i] += row_rotated<8>(db[i]);
+        if (threadIdx.x % 16 < kBandLanes && i >= piece.skip) {
+            lds[0][threadIdx.x / 16][piece.at + i - first] = dw[i];
+            lds[1][threadIdx.x / 16][piece.at + i - first] = db[i];
+        }
+    }
+    __syncthreads();
+    const int which = threadIdx.x / kBand, k = threadIdx.x % kBand;
+    W* const out = which ? dB : dW;
+    if (which > 1 || first + k >= D || !out) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int g = 0; g < kGroups / 2; ++g) s += lds[which][g][k];
+    out[first + k] = narrow<W>(s);
+}
+
 // Rows too long for registers, backwards (1024 x 60000 BF16 127 us): first the two sums of
 // each row,
 template <typename T, typename W>
@@ -425,8 +536,6 @@ __global__ __launch_bounds__(kJoin * kWave) void norm_join_kernel(
 // How a row of D lies in registers: C elements a chunk, lanes, and chunks of each.  16
 // elements a lane: more leave too few wavefronts in flight backwards, where five values a
 // column are held.  Rows shorter than a chunk take one element a lane.
-constexpr int64_t kMaxInRegisters = 16384;
-
 template <typename T, typename F> hipError_t with_form(int64_t D, F f) {
     using std::integral_constant;
     auto form = [&](auto lanes, auto elements) {
@@ -499,6 +608,7 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, void* w
     T* const dx = static_cast<T*>(a.Y);
     float* partial = static_cast<float*>(ws);
     const int64_t pitch = pitch_of(a.D);
+    const bool few = (a.dW || a.dB) && few_rows(a.T, a.D, sizeof(T));
     int64_t parts = 0;
     hipError_t err;
     if (a.D > kMaxInRegisters) {
@@ -532,6 +642,17 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, void* w
                         a.ldy, partial, pitch);
                 return hipGetLastError();
             };
+            if (few) {
+                constexpr int R = kFewThreads<L> / L, B = kBandLanes * C;
+                const int groups = dx ? static_cast<int>(ceil_div(a.T, R)) : 0;
+                norm_few_kernel<T, W, C, L, CH>
+                    <<<dim3(static_cast<unsigned>(groups + ceil_div(a.D, B))),
+                       dim3(kFewThreads<L>), 0, a.stream>>>(
+                        static_cast<int>(a.T), static_cast<int>(a.D), dy, a.lddy, x, a.ldx, w,
+                        a.mean, a.rstd, dx, a.ldy, static_cast<W*>(a.dW), static_cast<W*>(a.dB),
+                        groups);
+                return hipGetLastError();
+            }
             if (sums) {
                 parts = backward_parts(a.T, a.D);
                 if (!dx) return go(yes{}, no{}, no{});
@@ -541,7 +662,7 @@ template <typename T, typename W> hipError_t backward(const NormArgs& a, void* w
             return go(no{}, yes{}, no{});
         });
     }
-    if (err != hipSuccess || (!a.dW && !a.dB)) return err;
+    if (err != hipSuccess || (!a.dW && !a.dB) || few) return err;
     norm_join_kernel<W><<<dim3(static_cast<unsigned>(ceil_div(a.D, kWave)), 2), dim3(kJoin * kWave),
                           0, a.stream>>>(parts, a.D, partial, pitch, static_cast<W*>(a.dW),
                                          static_cast<W*>(a.dB));
@@ -565,7 +686,8 @@ hipError_t launch_layer_norm(const NormArgs& a) {
 }
 
 int64_t layer_norm_workspace(int64_t T, int64_t D, bool vectors) {
-    if (T == 0) return 0;
+    // (enough for every type: FP32 rows are few sooner)
+    if (T == 0 || few_rows(T, D, 4)) return 0;
     if (D <= kMaxInRegisters) return vectors ? backward_parts(T, D) * 2 * pitch_of(D) * 4 : 0;
     return (ceil_div(T, long_slab(T)) * 2 * pitch_of(D) + 2 * T) * 4;
 }

@@ -506,8 +506,8 @@ int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int 
  *
  * Any alignment and leading dimensions.  The workspace of the backward pass
  * (migemm_layer_norm_workspace_size bytes, 256-byte aligned) is lent as in the losses
- * above; it is 0 bytes when neither dW nor dB is wanted and D is at most 16384.  Outputs
- * and workspace must not overlap each other or the inputs.  The pointer, stream, ownership
+ * above; it is 0 bytes when neither dW nor dB is wanted and D is at most 16384, and for few
+ * rows.  Outputs and workspace must not overlap each other or the inputs.  The pointer, stream, ownership
  * and error rules are migemm_gemm's.
  */
 int migemm_layer_norm_forward(int64_t T, int64_t D, int dtype, const void* X, int64_t ldx,

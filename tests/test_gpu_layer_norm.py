@@ -348,3 +348,89 @@ def test_more_than_2_31_elements():
     dx[rows] = 0
     assert not dx.any()
     assert math.isfinite(float(y[::4097].float().sum()))
+
+
+# either side of the rows that one launch takes backwards: 1024, and 8 MiB of x
+FEW = [(1, 16384), (127, 16384), (128, 16384), (129, 16384), (256, 16380), (1023, 40), (1024, 2048),
+       (1024, 4096), (1025, 40), (64, 5), (65, 9), (257, 129), (1000, 2049), (500, 8192), (513, 700)]
+# and rows of every form past them
+MANY = [(1025, 1), (1030, 8), (1100, 127), (1400, 129), (1029, 512), (1025, 513), (1031, 1024),
+        (1027, 1025), (1040, 2048), (1050, 1537), (1026, 2049), (1030, 8192), (1025, 8200),
+        (1025, 16384)]
+
+
+@pytest.mark.parametrize("dtype,weight", [("f32", "f32"), ("f16", "f16"), ("bf16", "bf16"),
+                                          ("bf16", "f32")])
+@pytest.mark.parametrize("T,D", FEW + MANY)
+def test_rows_of_one_launch_and_more(T, D, dtype, weight):
+    x, w, b, dy = case(T, D, dtype, weight, T + D)
+    say(f"layer norm {T}x{D} {dtype} {weight}")
+    check(both(x, w, b, dy), reference(x, w, b, dy, 1e-5))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,D", [(90, 77), (300, 1001), (1500, 77), (1200, 1001), (1100, 4003)])
+def test_strided_rows_of_one_launch_and_more(T, D, dtype):
+    """Rows off 16-byte boundaries with NaN between them, and results inside larger buffers."""
+    x, w, b, dy = case(T, D, dtype, dtype, D + T)
+    want = reference(x, w, b, dy, 1e-5)
+
+    def inside(t, offset, extra):
+        buf = torch.full((t.shape[0], t.shape[1] + extra), float("nan"), dtype=t.dtype, device="cuda")
+        buf[:, offset:offset + t.shape[1]] = t
+        return buf, buf[:, offset:offset + t.shape[1]]
+
+    say(f"layer norm {T}x{D} inside buffers {dtype}")
+    xs, dys = inside(x, 3, 8)[1], inside(dy, 1, 5)[1]
+    y, mean, rstd = mg.layer_norm(xs, w, b)
+    xbuf, dx = inside(torch.zeros_like(x), 5, 7)
+    vectors = torch.full((2 * D + 3,), float("nan"), dtype=w.dtype, device="cuda")
+    dw, db = vectors[1:1 + D], vectors[2 + D:2 + 2 * D]
+    mg.layer_norm_backward(dys, xs, w, mean, rstd, dx=dx, dw=dw, db=db)
+    torch.cuda.synchronize()
+    check({"y": y, "mean": mean, "rstd": rstd, "dx": dx, "dw": dw, "db": db}, want)
+    assert torch.isnan(vectors[[0, 1 + D, -1]]).all()
+    dx.zero_()
+    assert int(torch.isnan(xbuf).sum()) == xbuf.numel() - dx.numel()
+    # each result alone
+    for name in ("dx", "dw", "db"):
+        need = {f"need_{n}": n == name for n in ("dx", "dw", "db")}
+        got = dict(zip(("dx", "dw", "db"), mg.layer_norm_backward(dys, xs, w, mean, rstd, **need)))
+        torch.cuda.synchronize()
+        assert all(got[n] is None for n in got if n != name)
+        check({name: got[name]}, want)
+
+
+@pytest.mark.parametrize("T,D", [(200, 1032), (1100, 1032), (30, 16000)])
+def test_backward_captured_and_on_a_side_stream(T, D):
+    x, w, b, dy = case(T, D, "bf16", "f32", 7)
+    y, mean, rstd = mg.layer_norm(x, w, b)
+    say(f"layer norm {T}x{D} captured")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = mg.layer_norm_backward(dy, x, w, mean, rstd)
+    side = torch.cuda.Stream()
+    for i in range(3):
+        dy.copy_(dy.roll(i, 0))
+        want = mg.layer_norm_backward(dy, x, w, mean, rstd)
+        for t in held:
+            t.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        got = mg.layer_norm_backward(dy, x, w, mean, rstd, stream=side.cuda_stream)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [60, 1500])
+def test_infinities_stay_in_their_rows_and_columns(T):
+    x, w, b, dy = case(T, 300, "f32", "f32", T)
+    y, mean, rstd = mg.layer_norm(x, w, b)
+    dy[T // 2, 7] = float("inf")
+    say(f"layer norm {T}x300 with an infinity in dy")
+    dx, dw, db = mg.layer_norm_backward(dy, x, w, mean, rstd)
+    torch.cuda.synchronize()
+    rows, columns = ~torch.isfinite(dx).all(1), ~torch.isfinite(dw)
+    assert rows.nonzero().tolist() == [[T // 2]] and columns.nonzero().tolist() == [[7]]
+    assert (~torch.isfinite(db)).nonzero().tolist() == [[7]]
