@@ -90,7 +90,10 @@ int64_t leading(const at::Tensor& t) {
 }
 
 const void* pointer(const at::Tensor& t) { return t.numel() ? t.const_data_ptr() : nullptr; }
-void* writable(const at::Tensor& t) { return t.numel() ? t.mutable_data_ptr() : nullptr; }
+// (of a tensor that may not be defined, too)
+void* writable(const at::Tensor& t) {
+    return t.defined() && t.numel() ? t.mutable_data_ptr() : nullptr;
+}
 
 void check_vector(const char* name, const at::Tensor& t, at::Device device, at::ScalarType kind,
                   int64_t size) {
@@ -122,7 +125,7 @@ at::Tensor matrix(const char* name, const at::Tensor* given, const at::Tensor& l
 }
 
 at::Tensor workspace(int64_t bytes, const at::Tensor& like) {
-    return at::empty({bytes}, like.options().dtype(at::kByte));
+    return bytes ? at::empty({bytes}, like.options().dtype(at::kByte)) : at::Tensor();
 }
 
 bool truth(PyObject* o) {
@@ -191,8 +194,7 @@ PyObject* layer_norm(PyObject* const* a) {
     const int st = migemm_layer_norm_forward(
         T, D, code_of(x), pointer(x), ldx, wd, weight ? pointer(*weight) : nullptr,
         bias ? pointer(*bias) : nullptr, static_cast<float>(number(a[3])), writable(y), leading(y),
-        mean.defined() ? static_cast<float*>(writable(mean)) : nullptr,
-        rstd.defined() ? static_cast<float*>(writable(rstd)) : nullptr, stream_of(a[6]));
+        static_cast<float*>(writable(mean)), static_cast<float*>(writable(rstd)), stream_of(a[6]));
     return st == MIGEMM_OK ? tuple({y, mean, rstd, {}}, false) : status(st);
 }
 
@@ -232,9 +234,8 @@ PyObject* layer_norm_backward(PyObject* const* a) {
     st = migemm_layer_norm_backward(
         T, D, code_of(x), pointer(dy), lddy, pointer(x), ldx, wd,
         weight ? pointer(*weight) : nullptr, static_cast<const float*>(pointer(mean)),
-        static_cast<const float*>(pointer(rstd)), dx.defined() ? writable(dx) : nullptr,
-        dx.defined() ? leading(dx) : D, dw.defined() ? writable(dw) : nullptr,
-        db.defined() ? writable(db) : nullptr, writable(ws), bytes, stream_of(a[11]));
+        static_cast<const float*>(pointer(rstd)), writable(dx), dx.defined() ? leading(dx) : D,
+        writable(dw), writable(db), writable(ws), bytes, stream_of(a[11]));
     return st == MIGEMM_OK ? tuple({dx, dw, db, ws}, truth(a[12])) : status(st);
 }
 
