@@ -319,8 +319,8 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
 // pass left.  The first workgroups take rows, one to LANES lanes; those behind them a band of
 // 128 bytes of columns each, eight lanes to a row, and join their rows' sums in order.  x and
 // dy are read twice, the second time from the caches.  Against partial sums and their join:
-// 76 x 1032 FP16 3.1 us instead of 6.4, 1003 8.7 instead of 10.5, 512 x 8192 BF16 8.2 instead
-// of 15.1; past kFewRows rows a band's workgroup is at work too long (2048 x 1032 18.6 instead
+// 76 x 1032 FP16 3.5 us instead of 6.4, 1003 7.4 instead of 10.5, 512 x 8192 BF16 8.2 instead
+// of 15.1; past kFewRows rows a band's workgroup is at work too long (2048 x 1032 14.9 instead
 // of 12.8), past kFewBytes of x the second reading costs more than a launch (1024 x 3000 FP32
 // 13.7 instead of 11.4).
 constexpr int64_t kFewRows = 1024, kFewBytes = 8 << 20;
@@ -328,7 +328,9 @@ bool few_rows(int64_t T, int64_t D, int bytes) {
     return T <= kFewRows && D <= kMaxInRegisters && T * D * bytes <= kFewBytes;
 }
 template <int LANES> constexpr int kFewThreads = LANES <= 512 ? 512 : LANES;
-constexpr int kBandLanes = 8, kBandAhead = 4;
+constexpr int kBandLanes = 8;
+// Rows in flight: 1003 x 1032 FP16 7.4 us with 8, 8.7 with 4; 512 x 8192 BF16 9.2 and 8.2.
+template <int LANES> constexpr int kBandAhead = LANES <= 128 ? 8 : 4;
 template <typename T, typename W, int C, int LANES, int CH>
 __global__ __launch_bounds__(kFewThreads<LANES>) void norm_few_kernel(
     int rows, int D, const T* __restrict__ dY, int64_t lddy, const T* __restrict__ X, int64_t ldx,
@@ -377,17 +379,18 @@ __global__ __launch_bounds__(kFewThreads<LANES>) void norm_few_kernel(
         return;
     }
     constexpr int kBand = kBandLanes * C, kGroups = THREADS / kBandLanes;
+    constexpr int AHEAD = kBandAhead<LANES>;
     __shared__ float lds[2][kGroups / 2][kBand + 1];
     const int first = (blockIdx.x - row_groups) * kBand, lane = threadIdx.x % kBandLanes;
     const Span<C> piece(first + lane * C, D);
     float dw[C], db[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) dw[i] = db[i] = 0.0f;
-    for (int row = threadIdx.x / kBandLanes; row < rows; row += kGroups * kBandAhead) {
-        T x[kBandAhead][C], dy[kBandAhead][C];
-        float mean[kBandAhead], rstd[kBandAhead];
+    for (int row = threadIdx.x / kBandLanes; row < rows; row += kGroups * AHEAD) {
+        T x[AHEAD][C], dy[AHEAD][C];
+        float mean[AHEAD], rstd[AHEAD];
 #pragma unroll
-        for (int u = 0; u < kBandAhead; ++u) {
+        for (int u = 0; u < AHEAD; ++u) {
             const int64_t r = row + u * kGroups < rows ? row + u * kGroups : rows - 1;
             piece.load(X + r * ldx, x[u]);
             piece.load(dY + r * lddy, dy[u]);
@@ -395,7 +398,7 @@ __global__ __launch_bounds__(kFewThreads<LANES>) void norm_few_kernel(
             rstd[u] = rstds[r];
         }
 #pragma unroll
-        for (int u = 0; u < kBandAhead; ++u)
+        for (int u = 0; u < AHEAD; ++u)
             if (row + u * kGroups < rows) {
 #pragma unroll
                 for (int i = 0; i < C; ++i) {
