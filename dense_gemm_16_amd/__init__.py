@@ -6,7 +6,9 @@ kernels.  The functions named ``migemm_*`` mirror the C ABI in
 ``gemm`` is a convenience wrapper over torch tensors that derives the sizes,
 leading dimensions, pointers and the current stream, lends the workspace that
 ``migemm_workspace_size`` asks for (a torch allocation on the same stream) and
-calls ``migemm_gemm_ws``.
+calls ``migemm_gemm_ws``.  Layer norm, embeddings and AdamW over torch tensors are
+compiled (``_binding.so``, linked against torch): their kernels take a few microseconds,
+and so did ctypes.
 
 The library is loaded on first use from this package's directory.  If it has
 not been built, every call raises ``RuntimeError``: there is no fallback.
