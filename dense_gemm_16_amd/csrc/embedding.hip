@@ -887,7 +887,8 @@ template <typename T, typename W, int C> hipError_t scatter(const EmbedArgs& a, 
         scatter_kernel<T, W, C, WAVE, ADD, ONCE>
             <<<groups, threads, 0, a.stream>>>(g, static_cast<const T*>(a.dY), dw);
         const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        // (one stretch, of up to 8 pairs of rows past a million columns, shares no entry)
+        if (e != hipSuccess || g.stretches < 2) return e;
         scatter_join_kernel<W, C, ADD><<<joins, dim3(kJoinThreads), 0, a.stream>>>(g, dw);
         return hipGetLastError();
     };

@@ -510,3 +510,12 @@ def test_gradient_rows_of_sorted_lists_may_hold_anything():
     torch.cuda.synchronize()
     bad = ~torch.isfinite(dw)
     assert bad[index[at], 3] and int(bad.sum()) == 1
+
+
+# one stretch of 8 pairs: so few tokens that there is one, of rows so wide (FP32: a workgroup to
+# 1024 columns) that their lists are sorted; and two stretches
+@pytest.mark.parametrize("kind", ["mixed", "one", "bad"])
+@pytest.mark.parametrize("T,D", [(8, (1 << 20) + 1), (7, 1198081), (6, 1396737), (5, 1677313),
+                                 (5, 1 << 21), (8, 1 << 21), (9, (1 << 20) + 1), (4, 1 << 21)])
+def test_lists_of_one_stretch(T, D, kind):
+    both(T, 3, D, "f32" if D % 2 else "bf16", T, kind)
