@@ -1048,14 +1048,13 @@ def adamw_state(param, *, bits: int = 32, master: bool = False) -> AdamState:
         raise ValueError("a float32 parameter needs no master copy")
     copy = param.detach().to(torch.float32) if master else None
     shape, device = param.shape, param.device
+    held = shape if bits == 32 else (param.numel() + 255) // 256
+    floats = [torch.zeros(held, dtype=torch.float32, device=device) for _ in range(2)]
     if bits == 32:
-        return AdamState(torch.zeros(shape, device=device), torch.zeros(shape, device=device),
-                         master=copy)
-    blocks = (param.numel() + 255) // 256
+        return AdamState(*floats, master=copy)
     codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
              for _ in range(2)]
-    return AdamState(*codes, torch.zeros(blocks, device=device),
-                     torch.zeros(blocks, device=device), copy)
+    return AdamState(*codes, *floats, copy)
 
 
 def adamw_(params, grads, states, *, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8,

@@ -238,3 +238,16 @@ def test_adamw_states():
         mg.adamw_state(p, bits=16)
     with pytest.raises(ValueError, match="needs no master"):
         mg.adamw_state(p.float(), master=True)
+
+
+def test_states_do_not_follow_the_default_dtype():
+    p = torch.zeros(300, dtype=torch.bfloat16)
+    kept = torch.get_default_dtype()
+    try:
+        for default in (torch.float64, torch.bfloat16):
+            torch.set_default_dtype(default)
+            wide, eight = mg.adamw_state(p), mg.adamw_state(p, bits=8)
+            assert all(t.dtype == torch.float32
+                       for t in (wide.avg, wide.sq, eight.avg_scales, eight.sq_scales))
+    finally:
+        torch.set_default_dtype(kept)
