@@ -642,13 +642,14 @@ def _stream_of(stream, device):
 def _run_on(stream, device, *tensors):
     """For a call on another stream than torch's current one: `stream` waits for what
     is queued on the current stream (new tensors may reuse memory that work there
-    still reads), and the tensors, None apart, are kept from being reused before the
-    work queued on `stream` has finished."""
+    still reads), and the tensors are kept from being reused before the work queued on
+    `stream` has finished.  None, and what is not on the GPU (the call refuses it), is
+    passed over."""
     torch = _torch or _load_torch()
     s = torch.cuda.ExternalStream(stream, device=device)
     s.wait_stream(torch.cuda.current_stream(device))
     for t in tensors:
-        if t is not None:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(s)
 
 
@@ -956,13 +957,14 @@ def _call(where, function, anchor, stream, *args):
     current one, and its tensors, the workspace among them, are kept from being reused before
     the work queued there has finished."""
     torch = _torch
-    index = anchor.get_device()  # (-1 on the host: the call refuses it)
+    # -1 on the host, or of what is no tensor: the call refuses it
+    index = anchor.get_device() if isinstance(anchor, torch.Tensor) else -1
     current = torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
     if stream is None or stream == current or index < 0:
         r = function(*args, current, False)
     else:
         device = anchor.device
-        _run_on(stream, device, *(t for t in args if isinstance(t, torch.Tensor)))
+        _run_on(stream, device, *args)
         r = function(*args, stream, True)
         if type(r) is tuple:
             s = torch.cuda.ExternalStream(stream, device=device)
@@ -1076,15 +1078,14 @@ def adamw_(params, grads, states, *, step, lr=1e-3, betas=(0.9, 0.999), eps: flo
     if len(params) == 0 and len(grads) == 0 and len(states) == 0:
         return
     anchor = params[0] if len(params) else grads[0] if len(grads) else states[0][0]
-    index = anchor.get_device()
+    index = anchor.get_device() if isinstance(anchor, torch.Tensor) else -1
     current = torch._C._cuda_getCurrentRawStream(index) if index >= 0 else 0
     other = stream is not None and stream != current and index >= 0
     if grad_scale is not None and not isinstance(grad_scale, torch.Tensor) and index >= 0:
         grad_scale = torch.full((), float(grad_scale), dtype=torch.float32, device=anchor.device)
     if other:
-        numbers = (t for t in (lr, step, grad_scale) if isinstance(t, torch.Tensor) and t.is_cuda)
-        held = (t for s in states for t in s if t is not None)
-        _run_on(stream, anchor.device, *params, *grads, *held, *numbers)
+        held = (t for s in states for t in s)
+        _run_on(stream, anchor.device, *params, *grads, *held, lr, step, grad_scale)
     st = native.adamw(params, grads, states, step, lr, *betas, eps, weight_decay, grad_scale,
                       stream if other else current, False)
     if st != OK:

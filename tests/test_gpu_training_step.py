@@ -127,3 +127,25 @@ def test_captured_step_beside_an_eager_one():
         assert torch.equal(loss, want)
         for a, b in zip(eager[0], captured[0]):
             assert torch.equal(a, b)
+
+
+def test_refusals_on_another_stream():
+    """What is not on the GPU is refused as on the current stream."""
+    x = torch.ones(6, 16, device="cuda")
+    w, index = torch.ones(16, device="cuda"), torch.zeros(6, dtype=torch.int64, device="cuda")
+    y, mean, rstd = mg.layer_norm(x, w)
+    state = mg.adamw_state(x)
+    side = torch.cuda.Stream()
+    s = side.cuda_stream
+    say("refusals on another stream")
+    for call in (lambda: mg.layer_norm(x, w.cpu(), stream=s),
+                 lambda: mg.layer_norm_backward(y.cpu(), x, w, mean, rstd, stream=s),
+                 lambda: mg.layer_norm_backward(y, x, w, mean, rstd.cpu(), stream=s),
+                 lambda: mg.embedding(x, index.cpu(), stream=s),
+                 lambda: mg.embedding_backward(y, index.cpu(), 6, stream=s),
+                 lambda: mg.adamw_([x], [y.cpu()], [state], step=1, stream=s),
+                 lambda: mg.adamw_([x], [y], [state._replace(sq=state.sq.cpu())], step=1, stream=s),
+                 lambda: mg.adamw_([x], [None], [state], step=1, stream=s)):
+        with pytest.raises(ValueError):
+            call()
+    torch.cuda.synchronize()

@@ -251,3 +251,13 @@ def test_states_do_not_follow_the_default_dtype():
                        for t in (wide.avg, wide.sq, eight.avg_scales, eight.sq_scales))
     finally:
         torch.set_default_dtype(kept)
+
+
+def test_operands_that_are_no_tensors():
+    x, v, t = torch.zeros(4, 8), torch.zeros(4), torch.zeros(4, dtype=torch.long)
+    rows = [[0.0] * 8] * 4
+    for call in (lambda: mg.layer_norm(rows), lambda: mg.layer_norm_backward(x, rows, None, v, v),
+                 lambda: mg.embedding(rows, t), lambda: mg.embedding_backward(rows, t, 5),
+                 lambda: mg.adamw_([rows], [x], [mg.adamw_state(x)], step=1)):
+        with pytest.raises(ValueError, match="must be a tensor"):
+            call()
