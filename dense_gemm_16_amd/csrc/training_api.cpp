@@ -56,6 +56,11 @@ struct Ranges {
     }
 };
 
+// Kernels read a row's statistics and a token's index by scalar loads, which drop an
+// address's lowest bits: those lie on their elements' boundaries.  (Elements of matrices
+// and vectors are read by vector loads, at any address.)
+bool on_elements(const void* p, int es) { return reinterpret_cast<uintptr_t>(p) % es == 0; }
+
 // The workspace lent is `need` bytes or more, and aligned.
 int check_workspace(int64_t need, const void* ws, int64_t ws_bytes) {
     if (need == 0) return MIGEMM_OK;
@@ -92,8 +97,7 @@ bool name_tensor(const migemm_adamw_tensor& t, int pb, int gb, bool eight, bool 
                  int& n) {
     auto add = [&](const void* p, int64_t count, int es, bool written) {
         Named r{0, 0, written};
-        if (!p || reinterpret_cast<uintptr_t>(p) % es != 0 ||
-            !extent(p, 1, count, count, es, r.lo, r.hi))
+        if (!p || !on_elements(p, es) || !extent(p, 1, count, count, es, r.lo, r.hi))
             return false;
         at[n++] = r;
         return true;
@@ -185,6 +189,7 @@ int migemm_layer_norm_backward(int64_t T, int64_t D, int dtype, const void* dY, 
         r.reads(mean, 1, T, T, 4);
         r.reads(rstd, 1, T, T, 4);
         if (dX) r.writes(dX, T, D, lddx, es);
+        if (!on_elements(mean, 4) || !on_elements(rstd, 4)) return MIGEMM_ERR_INVALID_ARG;
     }
     if (dW) r.writes(dW, 1, D, D, vs);
     if (dB) r.writes(dB, 1, D, D, vs);
@@ -261,6 +266,7 @@ int migemm_embedding_backward(int64_t T, int64_t V, int64_t D, int dtype, const 
     if (T > 0) {
         r.reads(dY, T, D, lddy, elem_size(dtype));
         r.reads(index, 1, T, T, 8);
+        if (!on_elements(index, 8)) return MIGEMM_ERR_INVALID_ARG;
     }
     r.writes(dW, V, D, lddw, elem_size(dw_dtype));
     if (!r.ok()) return MIGEMM_ERR_INVALID_ARG;
@@ -323,7 +329,7 @@ int migemm_adamw(int64_t tensors, const migemm_adamw_tensor* list, int param_dty
     for (const auto& q : numbers) {
         if (!ok || !q.p) continue;
         Named r{0, 0, false};
-        ok = reinterpret_cast<uintptr_t>(q.p) % q.es == 0 && extent(q.p, 1, 1, 1, q.es, r.lo, r.hi);
+        ok = on_elements(q.p, q.es) && extent(q.p, 1, 1, 1, q.es, r.lo, r.hi);
         named[n++] = r;
     }
     ok = ok && !some_meet(named, n);

@@ -504,11 +504,12 @@ int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int 
  * wanted).  The sums over rows are FP32 in an order that depends on the sizes alone: no
  * atomics.  T == 0 is a no-op forwards and gives dW = dB = 0.  D is 1 to 2^24, T below 2^31.
  *
- * Any alignment and leading dimensions.  The workspace of the backward pass
+ * Any alignment and leading dimensions, but for the backward pass's mean and rstd, which lie
+ * on 4-byte boundaries.  The workspace of the backward pass
  * (migemm_layer_norm_workspace_size bytes, 256-byte aligned) is lent as in the losses
  * above; it is 0 bytes when neither dW nor dB is wanted and D is at most 16384, and for few
- * rows.  Outputs and workspace must not overlap each other or the inputs.  The pointer, stream, ownership
- * and error rules are migemm_gemm's.
+ * rows.  Outputs and workspace must not overlap each other or the inputs.  The pointer,
+ * stream, ownership and error rules are migemm_gemm's.
  */
 int migemm_layer_norm_forward(int64_t T, int64_t D, int dtype, const void* X, int64_t ldx,
                               int w_dtype, const void* W, const void* B, float eps, void* Y,
@@ -538,7 +539,8 @@ int migemm_layer_norm_backward(int64_t T, int64_t D, int dtype, const void* dY, 
  * the index and the sizes alone: the tokens are sorted by entry, with no atomics on sums.
  *
  * T is below 2^31 (0: a no-op, or dW = 0), V 1 to 2^28, D 1 to 2^21.  Any alignment and
- * leading dimensions.  The workspace (migemm_embedding_workspace_size bytes, none for few
+ * leading dimensions, but for the backward pass's index, which lies on an 8-byte boundary.
+ * The workspace (migemm_embedding_workspace_size bytes, none for few
  * tokens) and the other rules are as for the losses above.
  */
 int migemm_embedding_forward(int64_t T, int64_t V, int64_t D, int dtype, const void* W,

@@ -261,3 +261,11 @@ def test_operands_that_are_no_tensors():
                  lambda: mg.adamw_([rows], [x], [mg.adamw_state(x)], step=1)):
         with pytest.raises(ValueError, match="must be a tensor"):
             call()
+
+
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_row_statistics_and_tokens_off_their_elements(off):
+    """Workgroups read them by scalar loads, which drop an address's lowest bits."""
+    assert norm_backward(mean=MEAN + off) == BAD and norm_backward(rstd=RSTD + off) == BAD
+    assert norm_backward(T=T, mean=MEAN + off) == BAD
+    assert embed_backward(index=INDEX + off) == BAD and embed_backward(T=T, index=INDEX + 4) == BAD
