@@ -2,7 +2,7 @@
 
 Every source is compiled separately (in parallel) into ``_build/`` and linked
 into ``libmigemm.so`` next to this file; ``binding.cpp``, host code against torch's
-headers, becomes ``_binding.so`` there.  Flags:
+headers, becomes ``_binding.so`` there (nothing else needs torch).  Flags:
 
 * ``--offload-arch=gfx950``: MI355X only, no other targets;
 * ``-Xclang -target-feature -Xclang -packed-fp32-ops``: no packed FP32
@@ -137,38 +137,49 @@ def _up_to_date(obj: str, src: str) -> bool:
     return all(os.path.getmtime(d) < t for d in deps)
 
 
-def _build_binding(force: bool) -> str:
-    """Compiles binding.cpp; the object."""
+def _build_binding(force: bool, torch) -> str:
+    """Compiles binding.cpp against `torch`; the object."""
     import sysconfig
     src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
-    if not force and _up_to_date(obj, src):
-        return obj
-    inc = os.path.join(_torch_dir(), "include")
-    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall", "-D_GLIBCXX_USE_CXX11_ABI=1",
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-I", os.path.join(ROOT, "include"), "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-c", src, "-o", obj]
+    # what the object stands for beside its source: another torch, another object
+    made, how = obj + ".made", "\n".join([torch.__version__, *cmd])
+    if not force and _up_to_date(obj, src) and os.path.exists(made):
+        with open(made) as f:
+            if f.read() == how:
+                return obj
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError(f"{CXX} failed on binding.cpp:\n{p.stdout}{p.stderr}")
+    with open(made, "w") as f:
+        f.write(how)
     return obj
 
 
-def _link_binding(obj: str) -> None:
+def _link_binding(obj: str, torch) -> None:
     """Links _binding.so against torch's libraries (loaded by then) and libmigemm.so."""
     tmp = BINDING + f".tmp{os.getpid()}"
-    cmd = [CXX, "-shared", "-o", tmp, obj, "-L", os.path.join(_torch_dir(), "lib"), "-lc10",
-           "-ltorch_cpu", "-ltorch", "-ltorch_python", "-L", PKG, "-l:libmigemm.so",
-           "-Wl,-rpath,$ORIGIN"]
+    cmd = [CXX, "-shared", "-o", tmp, obj,
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-ltorch_cpu",
+           "-ltorch", "-ltorch_python", "-L", PKG, "-l:libmigemm.so", "-Wl,-rpath,$ORIGIN"]
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
         raise RuntimeError(f"link of _binding.so failed:\n{p.stdout}{p.stderr}")
     os.replace(tmp, BINDING)
 
 
-def _torch_dir() -> str:
-    import importlib.util
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+def _installed_torch():
+    """The torch module, or None: the C library does without."""
+    try:
+        import torch
+        return torch
+    except ImportError:
+        return None
 
 
 def units():
@@ -179,14 +190,17 @@ def units():
 
 
 def build(jobs: int | None = None, force: bool = True) -> str:
-    """Compile all sources and link libmigemm.so; returns the library path.
+    """Compile all sources and link libmigemm.so, and _binding.so where torch is installed;
+    returns the library path.
 
-    force=False recompiles only objects older than their source or any header."""
+    force=False recompiles only objects older than their source or any header (the
+    binding's: made for another torch, too)."""
     os.makedirs(BUILD, exist_ok=True)
     us = units()
     jobs = jobs or max(1, len(os.sched_getaffinity(0)))
+    torch = _installed_torch()
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = ex.submit(_build_binding, force)
+        binding = ex.submit(_build_binding, force, torch) if torch else None
         objs = list(ex.map(lambda u: _compile(u, force), us))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
@@ -194,8 +208,14 @@ def build(jobs: int | None = None, force: bool = True) -> str:
     if p.returncode != 0:
         raise RuntimeError(f"link failed:\n{p.stdout}{p.stderr}")
     os.replace(tmp, LIB)
-    _link_binding(binding.result())
     _write_resources(objs)
+    if binding:
+        _link_binding(binding.result(), torch)
+    else:
+        if os.path.exists(BINDING):  # (of a torch that is gone)
+            os.remove(BINDING)
+        print("torch is not installed: libmigemm.so is built without _binding.so, the calls over "
+              "torch tensors of layer norm, embeddings and AdamW", file=sys.stderr)
     return LIB
 
 
