@@ -519,3 +519,61 @@ def test_gradient_rows_of_sorted_lists_may_hold_anything():
                                  (5, 1 << 21), (8, 1 << 21), (9, (1 << 20) + 1), (4, 1 << 21)])
 def test_lists_of_one_stretch(T, D, kind):
     both(T, 3, D, "f32" if D % 2 else "bf16", T, kind)
+
+
+def whole_case(T, V, D, kind, seed):
+    """Gradients of -1, 0 and 1: as long as their magnitudes add up to less than 2^24, FP32
+    sums of them are exact in any order, and so a stretch that is left out, added twice or
+    joined to another entry shows, however many tokens an entry has."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    if kind == "middle":  # entries of a few tokens on both sides of one of 0.6 T
+        index = torch.randint(0, V, (T,), generator=g, device="cuda")
+        index = torch.where(torch.rand(T, generator=g, device="cuda") < 0.6, V // 2, index)
+    else:
+        index = draw_index(T, V, g, kind)
+    u = torch.rand(T, D, generator=g, device="cuda")
+    dy = (u < 3 / 8).float() - (u > 7 / 8).float()
+    old = torch.randint(-100, 100, (V, D), generator=g, device="cuda").float()
+    assert float(dy.abs().sum(0).max()) + 100 < 2 ** 24
+    inside = ((index >= 0) & (index < V)).cpu()
+    total = torch.zeros(V, D, dtype=torch.int64)
+    total.index_add_(0, index.cpu()[inside], dy.cpu()[inside].long())
+    return index, dy, old, total.cuda()
+
+
+@pytest.mark.parametrize("kind", ["one", "mixed", "middle"])
+@pytest.mark.parametrize("T,V,D", [(12, 3, (1 << 20) + 8), (900, 7, 520), (2048, 300, 72), (2049, 5, 24),
+                                   (8192, 40, 40), (8193, 40, 260), (33000, 700, 64), (70000, 5, 264),
+                                   (300000, 4000, 24), (1 << 20, 1000, 2), ((1 << 24) + 3, 70000, 1)])
+def test_sums_of_whole_numbers_are_exact(T, V, D, kind):
+    index, dy, old, total = whole_case(T, V, D, kind, T)
+    say(f"whole gradients, {T} of {V}x{D} {kind}")
+    dw = mg.embedding_backward(dy, index, V)
+    half = mg.embedding_backward(dy.bfloat16(), index, V, scale=0.5, out_dtype=torch.float32)
+    added = mg.embedding_backward(dy, index, V, scale=2.0, dw=old.clone(), accumulate=True)
+    rounded = mg.embedding_backward(dy.bfloat16(), index, V)
+    torch.cuda.synchronize()
+    assert torch.equal(dw, total.float()) and torch.equal(half, total.float() * 0.5)
+    # (twice a sum and what was there: below 2^25, and a product and a sum of one rounding)
+    assert torch.equal(added, (2 * total.double() + old.double()).float())
+    assert torch.equal(rounded, total.float().bfloat16())
+
+
+# lists that are sorted by counting (2049 to 8192 tokens), and the first one past them
+@pytest.mark.parametrize("T", [2100, 8192, 8193])
+@pytest.mark.parametrize("V", [(1 << 18) - 1, 1 << 18, (1 << 25) - 1, (1 << 25) + 5, (1 << 27) + 3])
+def test_counted_lists_of_long_tables(T, V):
+    D = 2
+    g = torch.Generator(device="cuda").manual_seed(V)
+    index = torch.randint(0, V, (T,), generator=g, device="cuda")
+    index[:4] = torch.tensor([V - 1, 0, V // 2, V - 1])
+    index[100:150] = V - 2
+    dy = torch.randint(-4, 5, (T, D), generator=g, device="cuda").float()
+    say(f"{T} of a table of {V}")
+    dw = mg.embedding_backward(dy, index, V)
+    torch.cuda.synchronize()
+    rows, where = torch.unique(index, return_inverse=True)
+    total = torch.zeros(len(rows), D, dtype=torch.int64).index_add_(0, where.cpu(), dy.cpu().long())
+    assert torch.equal(dw[rows].cpu(), total.float())
+    dw[rows] = 0
+    assert not dw.any()
