@@ -149,3 +149,30 @@ def test_refusals_on_another_stream():
         with pytest.raises(ValueError):
             call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,V,D", [(77, 300, 128), (300, 1000, 264), (500, 400, 96)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_step_of_a_tied_model_within_its_roundings(T, V, D, dtype):
+    """Targets drawn apart from the tokens, so that the sums over tokens do not cancel (where
+    a target is the next token, dbeta's own terms and targets' do).  Seven roundings, of x,
+    y, the losses' derivative, dy, dx and twice the gradient, move each element of theirs by
+    u at most, so the root mean square of what follows by u of its own: the norm's derivative
+    is a projection, and a token's own logit of about sqrt(D) (10 and more here, log V is
+    below 7) leaves its softmax's p (1 - p) below 0.1 for most.  8 u covers the seven added
+    up, the FP32 sums as above."""
+    g = torch.Generator(device="cuda").manual_seed(T + V)
+    w = (torch.randn(V, D, generator=g, device="cuda") / math.sqrt(D)).to(dtype)
+    gamma = (1 + 0.1 * torch.randn(D, generator=g, device="cuda")).to(dtype)
+    beta = (0.1 * torch.randn(D, generator=g, device="cuda")).to(dtype)
+    index, target = torch.randint(0, V, (2, T), generator=g, device="cuda")
+    index[-2:] = IGNORE
+    target[-3:] = IGNORE
+    scale = math.sqrt(D)
+    say(f"training step {T} of {V}x{D} {dtype}, targets apart")
+    got = forward_backward(w, gamma, beta, index, target, scale)
+    torch.cuda.synchronize()
+    tol = 8 * (torch.finfo(dtype).eps / 2 + (V + D) * 2.0 ** -24)
+    for a, b in zip(got, reference(w, gamma, beta, index, target, scale)):
+        error = (a.double().cpu() - b).square().mean().sqrt()
+        assert float(error) <= tol * float(b.square().mean().sqrt())
