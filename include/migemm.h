@@ -493,8 +493,9 @@ int migemm_linear_kd_backward(int64_t T, int64_t V, int64_t D, int64_t top, int 
  *     Y[t][j] = h[j] W[j] + B[j]
  *
  * W and B are vectors of D of w_dtype (`dtype` or MIGEMM_F32); NULL stands for ones, or
- * zeros.  Sums and statistics are FP32 (a variance below its range counts as 0), the
- * variance is the mean of squared distances from mu.  mean and rstd (T floats each, NULL
+ * zeros.  Sums and statistics are FP32, the variance the mean of squared distances from mu: one
+ * below FP32's range counts as 0, one of squares that add up to 2^128 and more as infinite,
+ * and r, h and dX are 0 then.  mean and rstd (T floats each, NULL
  * where not wanted) receive mu and r, which the backward pass reads.  eps is finite and at
  * least 0; a row of equal elements with eps 0 is NaN, and so is a row with a NaN or an
  * infinity.
@@ -529,7 +530,8 @@ int migemm_layer_norm_backward(int64_t T, int64_t D, int dtype, const void* dY, 
  *
  * W is V x D and Y T x D, row-major of `dtype` (MIGEMM_F32, MIGEMM_F16 or MIGEMM_BF16); the
  * product is FP32, rounded once.  A token whose index is ignore_index (padding) has a row
- * of zeros; any other index outside 0 .. V - 1 gives a row of NaN (nothing is read for it).
+ * of zeros; any other index outside 0 .. V - 1 gives a row of NaN (row 0 is read for either,
+ * and dropped).
  *
  * Backward: dW[v] = scale * (the sum of dY[t] over the tokens t whose index is v), added to
  * what dW holds where accumulate is 1 (the gradient of a weight that an output layer

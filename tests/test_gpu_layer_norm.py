@@ -434,3 +434,18 @@ def test_infinities_stay_in_their_rows_and_columns(T):
     rows, columns = ~torch.isfinite(dx).all(1), ~torch.isfinite(dw)
     assert rows.nonzero().tolist() == [[T // 2]] and columns.nonzero().tolist() == [[7]]
     assert (~torch.isfinite(db)).nonzero().tolist() == [[7]]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D", [(6, 40), (6, 700), (6, 5000), (6, 20000), (1100, 700)])
+def test_squares_past_the_range(T, D, dtype):
+    """Distances of 1e20, whose squares FP32 does not hold: an infinite variance, so y is the
+    bias and dx 0, and the row adds nothing to dw; the rows beside it are as without it."""
+    x, w, b, dy = case(T, D, dtype, dtype, D)
+    x[3] = 1e20 * torch.where(torch.arange(D, device="cuda") % 2 == 0, 1.0, -1.0)
+    say(f"layer norm {T}x{D} {dtype} with a row past the squares' range")
+    got = both(x, w, b, dy)
+    assert torch.equal(got["y"][3], b) and not got["rstd"][3] and not got["dx"][3].any()
+    keep = [i for i in range(T) if i != 3]
+    want = reference(x[keep], w, b, dy[keep], 1e-5)
+    check({k: got[k][keep] for k in ("y", "mean", "rstd", "dx")} | {"dw": got["dw"]}, want)
