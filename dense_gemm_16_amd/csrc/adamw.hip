@@ -16,7 +16,8 @@
 // were before rounding to codes.
 //
 // Bound by memory: 28 bytes an element with FP32 parameters and states (5.5 TB/s), 10.06
-// with 16-bit parameters and 8-bit states (738 million elements 1240 us, 6.0 TB/s).  A
+// with 16-bit parameters and 8-bit states (738 million elements 1240 to 1310 us on four
+// boards, 6.0 to 5.7 TB/s).  A
 // workgroup takes a piece of 4096 elements of one tensor, found in a table of tensors that
 // the launch carries in its arguments: no copy of it to the device, and a captured launch
 // keeps it.
@@ -30,7 +31,8 @@ namespace {
 
 constexpr int kThreads = 256, kPiece = 4096;
 constexpr int kBlock = 256;          // elements of one scale
-constexpr int kTensors = 48;         // of one launch: its arguments stay below 4 KiB
+constexpr int kTensors = 48;         // of one launch: its arguments stay below 4 KiB (a last
+                                     // launch of three tensors takes 5 to 6.5 us)
 constexpr int64_t kPieces = int64_t(1) << 23;  // of one launch: fewer than 2^32 threads
 
 struct Table {
@@ -331,8 +333,8 @@ template <typename P, typename G> Kernel kernel_of(const AdamArgs& a, bool once)
 }
 
 // Past this many bytes a step's tensors go past the caches: the last-level one (256 MiB)
-// holds too little of them for the next reader.  738 million BF16 elements with 8-bit
-// states (7.4 GB) 1240 us, 1425 through the caches; 133 million with FP32 states and master
+// holds too little of them for the next reader.  On one board, 738 million BF16 elements with
+// 8-bit states (7.4 GB) 1240 us, 1425 through the caches; 133 million with FP32 states and master
 // copies (3.7 GB) 675 and 708; 40 million with 8-bit states (0.4 GB) 69 and 64.
 constexpr int64_t kOnceBytes = int64_t(512) << 20;
 

@@ -16,7 +16,7 @@
 // to).  Rows of dw that no token names are zeroed by workgroups of the same launch, and
 // not touched where the gradient is added.  32768 tokens, 11000 entries of 131072 x 4096
 // BF16: 64 to 72 us forwards (171 MB read, an entry once by each L2 cache, and 268 written);
-// backwards, added, 21 for the sort, 105 for the sums (432 MB, 4.1 TB/s), 10 for the join.
+// backwards, added, 21 for the sort, 105 for the sums (432 MB, 4.1 TB/s), 12 for the join.
 // 65536 of 50001 x 2048 FP32: 190 us for the sums and zeros (907 MB, 4.8 TB/s).
 #include "rows.hpp"
 #include "training.hpp"
@@ -574,8 +574,8 @@ __global__ __launch_bounds__(kJoinThreads) void scatter_join_kernel(GradArgs a,
 // Each token's workgroups read the whole list, so the work grows with its square, and wide
 // rows take more workgroups: kFewWide of them at most (of 16-bit rows; FP32 rows take twice as
 // many).  Against the sort, sums and join of longer lists, added: 16 tokens of 4096 BF16
-// columns 3.3 us instead of 8.5, 256 3.9 instead of 10.5, 2048 14.5 instead of 21.8, all of one
-// entry 17.8 instead of 18.0; 512 of 16384 FP32 columns 21.7 instead of 24.7.  2048 of 8192
+// columns 3.3 us instead of 8.5, 256 3.9 instead of 10.5, 2048 14.5 instead of 21.8 (16.8 after
+// the lookup of other tokens), all of one entry 17.8 instead of 18.0; 512 of 16384 FP32 columns 21.7 instead of 24.7.  2048 of 8192
 // BF16 columns would take 31.6 instead of 26.6, 4096 of 4096 30.7 instead of 25.2.
 constexpr int64_t kFewTokens = 2048, kFewWide = 4096;
 bool few_tokens(int64_t T, int64_t D) {

@@ -10,8 +10,11 @@
 //
 // Bound by memory: x is read and y written once; backwards dy and x are read and dx
 // written once.  A row lives in the registers of LANES lanes (16 to 1024), 16 elements each.
-// 16384 x 8192 BF16: 98 us forwards (5.5 TB/s), 141 backwards and 7 for the join of 512
-// partial sums (5.7 TB/s); 8191 x 771 FP32, which the last-level cache holds, 10, 14.6 and 4.
+// 16384 x 8192 BF16: 97 to 119 us forwards (5.5 to 4.5 TB/s), 136 to 149 backwards and 7 for the
+// join of 512 partial sums (5.7 to 5.2 TB/s); 8191 x 771 FP32, which the last-level cache holds,
+// 10, 14 and 4.  Forms are 512, 1024, 2048 ... columns wide, and the lanes past a row's end load
+// and store its last chunk again: 2468 x 2624 FP32, in 4096, takes 12, 16 and 5 us, 1.6 times its
+// bytes' time.
 #include "rows.hpp"
 #include "training.hpp"
 
@@ -144,7 +147,7 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_kernel(
 }
 
 // The same for rows of any length: three passes, the later ones from the caches (1024 x
-// 60000 BF16 84 us, 2.9 TB/s).
+// 60000 BF16 84 to 91 us, 2.9 to 2.7 TB/s; its bytes alone take 48).
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(
     int64_t rows, int64_t D, const T* __restrict__ X, int64_t ldx, const W* __restrict__ weight,
@@ -205,9 +208,12 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(
 // row is summed; each lane keeps dw and db of its columns in registers, and the workgroup
 // writes one partial sum of each, which norm_join_kernel adds.  Rows stay in registers as
 // they were loaded, and h and g are formed twice: kept in FP32 they left one workgroup less
-// to a CU, and spilled in the form of 1024 lanes.  FP32 rows of that form leave no room for
-// the next one's.  SUMS: dw or db is wanted; ROWS: dx is; ONCE: x and dy are read past the
-// caches.
+// to a CU.  The form of 1024 lanes has 128 registers a lane: FP32 rows leave no room there for
+// the next one's, and 16-bit ones with sums and dx spill 2 to 4 (17, 48 bytes of scratch a
+// lane, with BF16 weights past the caches; 8192 x 12000 BF16 140 us, 4.2 TB/s).  The last
+// row's loads are repeated in place of one past it: with ONCE from memory, a row of x and dy
+// for each workgroup (16384 x 8192 BF16 17 MB beside 537).  SUMS: dw or db is wanted; ROWS:
+// dx is; ONCE: x and dy are read past the caches.
 template <typename T, typename W, int C, int LANES, int CH, bool SUMS, bool ROWS, bool ONCE>
 __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
     int64_t rows, int D, const T* __restrict__ dY, int64_t lddy, const T* __restrict__ X,
@@ -318,18 +324,25 @@ __global__ __launch_bounds__(kThreads<LANES>) void norm_backward_kernel(
 // Few rows, backwards, in one launch: dw and db need no sums over a row, only what the forward
 // pass left.  The first workgroups take rows, one to LANES lanes; those behind them a band of
 // 128 bytes of columns each, eight lanes to a row, and join their rows' sums in order.  x and
-// dy are read twice, the second time from the caches.  Against partial sums and their join:
-// 76 x 1032 FP16 3.5 us instead of 6.4, 1003 7.4 instead of 10.5, 512 x 8192 BF16 8.2 instead
-// of 15.1; past kFewRows rows a band's workgroup is at work too long (2048 x 1032 14.9 instead
-// of 12.8), past kFewBytes of x the second reading costs more than a launch (1024 x 3000 FP32
-// 13.7 instead of 11.4).
+// dy are read twice, the second time from the caches.  On the same rows over and over, against
+// partial sums and their join: 76 x 1032 FP16 3.5 us instead of 6.4, 1003 7.5 instead of 10.5,
+// 512 x 8192 BF16 8.2 instead of 15.1 (1003 x 1032 after the forward pass 8.8, 512 x 8192
+// 8.9); past kFewRows rows a band's workgroup is at work too long (2048 x 1032 14.9 instead of
+// 12.8), past kFewBytes of x the second reading costs more than a launch (1024 x 3000 FP32 13.7
+// instead of 11.4).
 constexpr int64_t kFewRows = 1024, kFewBytes = 8 << 20;
 bool few_rows(int64_t T, int64_t D, int bytes) {
     return T <= kFewRows && D <= kMaxInRegisters && T * D * bytes <= kFewBytes;
 }
 template <int LANES> constexpr int kFewThreads = LANES <= 512 ? 512 : LANES;
 constexpr int kBandLanes = 8;
-// Rows in flight: 1003 x 1032 FP16 7.4 us with 8, 8.7 with 4; 512 x 8192 BF16 9.2 and 8.2.
+// Rows in flight in a band.  What decides is how many rows there are, 512 work-items having 64
+// lane groups: FP16, with 8 and with 4, 1003 x 1032 7.5 and 8.7 us, 512 x 1032 4.6 and 5.0, 256
+// x 1032 4.0 and 3.7, 100 x 1032 3.7 and 3.3.  The rule goes by the row's form instead, since
+// one kernel holds both: it is right for the forms of 1024 lanes (256 x 16384 10.1 and 8.1) and
+// 512 (512 x 8192 9.6 and 9.6, 512 x 6144 7.9 and 8.8, 100 x 8192 3.9 and 3.5) and for rows up to
+// 2048 columns past 400 of them; in the form of 256 lanes it gains 0.3 us on few rows (100 x
+// 4096 3.4 instead of 3.8) and loses up to 2.3 on many (1024 x 4096 12.8 instead of 10.5).
 template <int LANES> constexpr int kBandAhead = LANES <= 128 ? 8 : 4;
 template <typename T, typename W, int C, int LANES, int CH>
 __global__ __launch_bounds__(kFewThreads<LANES>) void norm_few_kernel(
@@ -427,8 +440,8 @@ __global__ __launch_bounds__(kFewThreads<LANES>) void norm_few_kernel(
     out[first + k] = narrow<W>(s);
 }
 
-// Rows too long for registers, backwards (1024 x 60000 BF16 127 us): first the two sums of
-// each row,
+// Rows too long for registers, backwards (1024 x 60000 BF16 117 to 127 us: 43, 67 and 7 for
+// the join; its bytes alone take 72): first the two sums of each row,
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void norm_long_sums_kernel(
     int64_t rows, int64_t D, const T* __restrict__ dY, int64_t lddy, const T* __restrict__ X,

@@ -102,7 +102,7 @@ def both(T, V, D, dtype, seed, kind="mixed", scale=3.0):
 
 
 # rows below a wavefront's lanes, of several segments, ending inside a chunk; lists shorter
-# than a stretch, ending inside one, past one workgroup's sort (32768)
+# than a stretch, ending inside one, past the sort by counting (8192)
 SIZES = [(1, 1, 1), (1, 1000, 64), (7, 5, 3), (8, 300, 8), (9, 300, 40), (100, 511, 129),
          (100, 512, 520), (1003, 3001, 200), (2048, 50, 1032), (5000, 40000, 72), (8192, 700, 136),
          (16, 131072, 4096), (300, 2000, 8200)]
@@ -379,8 +379,8 @@ def test_out_of_memory_is_torchs_error():
     assert torch.equal(mg.embedding(w, index[:1]), w)
 
 
-# either side of the lists of one launch (1024 tokens; a lane holds one, two or four of
-# them), and the shapes of SIZES in lists that are sorted
+# lists of one launch (up to 2048 tokens; a lane holds one, two, four or eight of them), and
+# the shapes of SIZES in lists that are sorted
 @pytest.mark.parametrize("kind", ["mixed", "one", "ignored", "bad"])
 @pytest.mark.parametrize("T,V,D", [(15, 3, 9), (16, 2, 600), (17, 2, 600), (70, 1, 2056),
                                    (255, 40, 65), (256, 9, 4104), (257, 300, 24), (511, 70, 3),
@@ -559,7 +559,8 @@ def test_sums_of_whole_numbers_are_exact(T, V, D, kind):
     assert torch.equal(rounded, total.float().bfloat16())
 
 
-# lists that are sorted by counting (2049 to 8192 tokens), and the first one past them
+# lists that are sorted by counting (2049 to 8192 tokens; shorter ones take one launch without
+# a sort), and the first one past them
 @pytest.mark.parametrize("T", [2100, 8192, 8193])
 @pytest.mark.parametrize("V", [(1 << 18) - 1, 1 << 18, (1 << 25) - 1, (1 << 25) + 5, (1 << 27) + 3])
 def test_counted_lists_of_long_tables(T, V):
